@@ -6,11 +6,15 @@ first call raises if libbqgemm.so is missing or the device is not sm_100.
 
 Names follow the C ABI: q4_0_dequantize, affine_dequantize, quant_matmul,
 quant_matmul_ex, bf16_matmul, q4_0_quantize, affine_quantize,
-quant_matmul_select_path, quant_matmul_workspace_size, bq_device_status.
+quant_matmul_select_path, quant_matmul_workspace_size, bq_device_status, and the
+products with an epilogue and their gradients: quant_matmul_act,
+quant_matmul_act_backward, quant_matmul_glu, quant_matmul_glu_backward.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
+import functools
 import os
 
 import torch
@@ -58,6 +62,11 @@ def lib() -> ctypes.CDLL:
         "quant_matmul_gemv_kernel": [I64, I64, I64, I, I, I],
         "quant_matmul_select_path": [I64, I64, I64, I, I],
         "bf16_matmul": [P, P, P, I64, I64, I64, P],
+        "quant_matmul_act": [P, P, P, P, P, P, I, P, P, I64, I64, I64, I, I, P, SZ, P],
+        "quant_matmul_act_backward": [P, P, P, P, P, I, P, P, P, I64, I64, I64, I, I, P, SZ, P],
+        "quant_matmul_glu": [P, P, P, P, P, P, I, P, P, P, I64, I64, I64, I, I, P, SZ, P],
+        "quant_matmul_glu_backward": [P, P, P, P, P, P, I, P, P, P, P, P, I64, I64, I64, I, I, P, SZ, P],
+        "quant_matmul_epilogue_workspace_size": [I, I64, I64, I64, I, I],
         "q4_0_quantize": [P, P, P, I64, I64, P],
         "affine_quantize": [P, P, P, P, I64, I64, I, I, P],
         "bq_device_status": [],
@@ -70,6 +79,7 @@ def lib() -> ctypes.CDLL:
         fn.argtypes = args
         fn.restype = I
     L.quant_matmul_workspace_size.restype = SZ
+    L.quant_matmul_epilogue_workspace_size.restype = SZ
     L.bq_status_string.restype = ctypes.c_char_p
     _lib = L
     return L
@@ -325,6 +335,202 @@ def bf16_matmul(x: torch.Tensor, w: torch.Tensor, out: torch.Tensor | None = Non
     _check(lib().bf16_matmul(_arg(x, BF16, M * K, "x"), _arg(w, BF16, N * K, "w"), _arg(out, BF16, M * N, "out"),
                              M, N, K, _stream(stream)), "bf16_matmul")
     return out
+
+
+# ------------------------------------------------- products with an epilogue
+ACTS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
+OP_ACT, OP_ACT_BACKWARD, OP_GLU, OP_GLU_BACKWARD = 0, 1, 2, 3
+
+
+def _act_code(act: str) -> int:
+    if act not in ACTS:
+        raise ValueError(f"act: expected one of {sorted(ACTS)}, got {act!r}")
+    return ACTS[act]
+
+
+@functools.lru_cache(maxsize=4096)
+def _epilogue_ws_bytes(device_index: int, op: int, M: int, N: int, K: int, group_size: int, bits: int) -> int:
+    return lib().quant_matmul_epilogue_workspace_size(op, M, N, K, group_size, bits)
+
+
+def quant_matmul_epilogue_workspace_size(op: int, M: int, N: int, K: int, group_size: int, bits: int) -> int:
+    """Bytes of workspace of OP_ACT, OP_ACT_BACKWARD, OP_GLU or OP_GLU_BACKWARD."""
+    return lib().quant_matmul_epilogue_workspace_size(op, M, N, K, group_size, bits)
+
+
+def _operand(t: torch.Tensor | None, dtypes, shape, name: str, device: torch.device):
+    """The pointer of a contiguous tensor of exactly `shape` on `device` (None: NULL)."""
+    if t is None:
+        return None
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name}: expected one of {[str(d) for d in dtypes]}, got {t.dtype}")
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, the call needs {shape}")
+    if t.device != device:
+        raise ValueError(f"{name}: on {t.device}, the call runs on {device}")
+    return _ptr(t)
+
+
+def _matrix(w, N: int, K: int, group_size: int, bits: int, device: torch.device, name: str):
+    """Checked pointers of one (wq, scales, biases | None) with W [N][K]."""
+    wq, scales, biases = w
+    q4 = biases is None
+    groups = (N, K // (32 if q4 else max(group_size, 1)))
+    sdt = BITS16 if q4 else BF16
+    return (_operand(wq, U8 if q4 else U32, (N, K // 2 if q4 else K * bits // 32), name + ".wq", device),
+            _operand(scales, sdt, groups, name + ".scales", device),
+            _operand(biases, BF16, groups, name + ".biases", device))
+
+
+def _on(device: torch.device, stream):
+    """Makes `device` and `stream` current for the call, so that the outputs and the
+    workspace come from that stream's memory; nothing to do where they are already."""
+    if stream is not None:
+        return torch.cuda.stream(stream)
+    if device.index != torch.cuda.current_device():
+        return torch.cuda.device(device)
+    return contextlib.nullcontext()
+
+
+def _need_cuda(t: torch.Tensor, name: str, stream) -> torch.device:
+    if not t.is_cuda:
+        raise ValueError("tensors must live on a CUDA device")
+    if t.dim() != 2:
+        raise ValueError(f"{name}: expected a matrix, got {t.dim()} dimensions")
+    if stream is not None and stream.device != t.device:
+        raise ValueError(f"stream: on {stream.device}, {name} is on {t.device}")
+    return t.device
+
+
+def _new(M: int, N: int, device) -> torch.Tensor:
+    return torch.empty((M, N), dtype=torch.bfloat16, device=device)
+
+
+def _scratch(op: int, M: int, N: int, K: int, group_size: int, bits: int, device):
+    """(tensor to keep until the call returned, pointer, bytes)"""
+    n = _epilogue_ws_bytes(device.index, op, M, N, K, group_size, bits)
+    if n == 0:
+        return None, None, 0
+    t = torch.empty(n, dtype=torch.uint8, device=device)
+    return t, t.data_ptr(), n
+
+
+def _out(t: torch.Tensor | None, M: int, N: int, device, name: str):
+    if t is None:
+        t = _new(M, N, device)
+        return t, (t.data_ptr() if t.numel() else _EMPTY_TAG)
+    return t, _operand(t, (torch.bfloat16,), (M, N), name, device)
+
+
+def _pair_of(gate, up, N: int, K: int, group_size: int, bits: int, device):
+    """The host arrays (wq, scales, biases | None) of a gate and an up matrix of one format."""
+    if (gate[2] is None) != (up[2] is None):
+        raise ValueError("gate and up must both be Q4_0 (biases None) or both be affine")
+    a = _matrix(gate, N, K, group_size, bits, device, "gate")
+    b = _matrix(up, N, K, group_size, bits, device, "up")
+    VP = ctypes.c_void_p * 2
+    return VP(a[0], b[0]), VP(a[1], b[1]), None if gate[2] is None else VP(a[2], b[2])
+
+
+def quant_matmul_act(x: torch.Tensor, wq: torch.Tensor, scales: torch.Tensor, biases: torch.Tensor | None = None,
+                     out_bias: torch.Tensor | None = None, act: str = "none", residual: torch.Tensor | None = None,
+                     group_size: int = 32, bits: int = 4, save_preact: bool = False, out: torch.Tensor | None = None,
+                     stream=None):
+    """y = residual + act(x . dequant(W)[N][K]^T + out_bias), bf16 [M][N], in the
+    product's own epilogue; act is a key of ACTS.  out may be residual itself.  With
+    save_preact: (y, z), z the bf16 argument of act, for quant_matmul_act_backward."""
+    dev = _need_cuda(x, "x", stream)
+    M, K = x.shape
+    N = wq.shape[0]
+    code = _act_code(act)
+    with _on(dev, stream):
+        w = _matrix((wq, scales, biases), N, K, group_size, bits, dev, "w")
+        xp = _operand(x, BF16, (M, K), "x", dev)
+        bp = _operand(out_bias, BF16, (N,), "out_bias", dev)
+        rp = _operand(residual, BF16, (M, N), "residual", dev)
+        out, yp = _out(out, M, N, dev, "out")
+        z, zp = _out(None, M, N, dev, "z") if save_preact else (None, None)
+        keep, ws, wsb = _scratch(OP_ACT, M, N, K, group_size, bits, dev)
+        _check(lib().quant_matmul_act(xp, w[0], w[1], w[2], bp, rp, code, yp, zp, M, N, K, group_size, bits, ws, wsb,
+                                      torch.cuda.current_stream().cuda_stream), "quant_matmul_act")
+    return (out, z) if save_preact else out
+
+
+def quant_matmul_act_backward(dy: torch.Tensor, wq: torch.Tensor, scales: torch.Tensor,
+                              biases: torch.Tensor | None = None, preact: torch.Tensor | None = None,
+                              act: str = "none", group_size: int = 32, bits: int = 4, need_dbias: bool = False,
+                              stream=None):
+    """The gradients of quant_matmul_act for frozen weights, from dy [M][N] and the
+    saved z: (dx [M][K], dz [M][N]) and with need_dbias also dbias [N], all bf16.
+    For act "none" dz is dy itself and preact is not needed; the residual's gradient is dy."""
+    dev = _need_cuda(dy, "dy", stream)
+    M, N = dy.shape
+    K = _k_of(wq, biases, bits)
+    code = _act_code(act)
+    if code and preact is None:
+        raise ValueError(f"preact: act {act!r} needs the saved z")
+    with _on(dev, stream):
+        w = _matrix((wq, scales, biases), N, K, group_size, bits, dev, "w")
+        dyp = _operand(dy, (torch.bfloat16,), (M, N), "dy", dev)
+        pp = _operand(preact, BF16, (M, N), "preact", dev)
+        dx, dxp = _out(None, M, K, dev, "dx")
+        dz, dzp = _out(None, M, N, dev, "dz") if code else (dy, None)
+        db = torch.empty(N, dtype=torch.bfloat16, device=dev) if need_dbias else None
+        keep, ws, wsb = _scratch(OP_ACT_BACKWARD, M, N, K, group_size, bits, dev)
+        _check(lib().quant_matmul_act_backward(dyp, pp, w[0], w[1], w[2], code, dxp, dzp, _ptr(db), M, N, K, group_size,
+                                               bits, ws, wsb, torch.cuda.current_stream().cuda_stream),
+               "quant_matmul_act_backward")
+    return (dx, dz, db) if need_dbias else (dx, dz)
+
+
+def quant_matmul_glu(x: torch.Tensor, gate, up, gate_bias: torch.Tensor | None = None,
+                     up_bias: torch.Tensor | None = None, act: str = "silu", group_size: int = 32, bits: int = 4,
+                     save_preact: bool = False, out: torch.Tensor | None = None, stream=None):
+    """h = act(x . dequant(gate)^T + gate_bias) * (x . dequant(up)^T + up_bias), bf16
+    [M][N], both projections in one product.  gate and up are (wq, scales, biases | None)
+    of one format.  With save_preact: (h, g, u), the bf16 factors before the activation,
+    for quant_matmul_glu_backward."""
+    dev = _need_cuda(x, "x", stream)
+    M, K = x.shape
+    N = gate[0].shape[0]
+    code = _act_code(act)
+    with _on(dev, stream):
+        w = _pair_of(gate, up, N, K, group_size, bits, dev)
+        xp = _operand(x, BF16, (M, K), "x", dev)
+        gbp = _operand(gate_bias, BF16, (N,), "gate_bias", dev)
+        ubp = _operand(up_bias, BF16, (N,), "up_bias", dev)
+        out, hp = _out(out, M, N, dev, "out")
+        g, gp = _out(None, M, N, dev, "g") if save_preact else (None, None)
+        u, up_ = _out(None, M, N, dev, "u") if save_preact else (None, None)
+        keep, ws, wsb = _scratch(OP_GLU, M, N, K, group_size, bits, dev)
+        _check(lib().quant_matmul_glu(xp, w[0], w[1], w[2], gbp, ubp, code, hp, gp, up_, M, N, K, group_size, bits, ws,
+                                      wsb, torch.cuda.current_stream().cuda_stream), "quant_matmul_glu")
+    return (out, g, u) if save_preact else out
+
+
+def quant_matmul_glu_backward(dh: torch.Tensor, g: torch.Tensor, u: torch.Tensor, gate, up, act: str = "silu",
+                              group_size: int = 32, bits: int = 4, need_dbias: bool = False, stream=None):
+    """The gradients of quant_matmul_glu for frozen weights, from dh [M][N] and the
+    saved g and u: (dx [M][K], dg [M][N], du [M][N]) and with need_dbias also
+    (dgate_bias [N], dup_bias [N]), all bf16."""
+    dev = _need_cuda(dh, "dh", stream)
+    M, N = dh.shape
+    K = _k_of(gate[0], gate[2], bits)
+    code = _act_code(act)
+    with _on(dev, stream):
+        w = _pair_of(gate, up, N, K, group_size, bits, dev)
+        dhp = _operand(dh, BF16, (M, N), "dh", dev)
+        gp = _operand(g, BF16, (M, N), "g", dev)
+        up_ = _operand(u, BF16, (M, N), "u", dev)
+        dx, dxp = _out(None, M, K, dev, "dx")
+        dg, dgp = _out(None, M, N, dev, "dg")
+        du, dup = _out(None, M, N, dev, "du")
+        dgb, dub = (torch.empty(N, dtype=torch.bfloat16, device=dev) for _ in range(2)) if need_dbias else (None, None)
+        keep, ws, wsb = _scratch(OP_GLU_BACKWARD, M, N, K, group_size, bits, dev)
+        _check(lib().quant_matmul_glu_backward(dhp, gp, up_, w[0], w[1], w[2], code, dxp, dgp, dup, _ptr(dgb), _ptr(dub),
+                                               M, N, K, group_size, bits, ws, wsb,
+                                               torch.cuda.current_stream().cuda_stream), "quant_matmul_glu_backward")
+    return (dx, dg, du, dgb, dub) if need_dbias else (dx, dg, du)
 
 
 # ------------------------------------------------------------------- quantize

@@ -20,6 +20,7 @@
 #include "gemv_affine.cuh"
 #include "gemv_stream.cuh"
 #include "tc_gemm.cuh"
+#include "tc_pair.cuh"
 
 namespace bq {
 namespace {
@@ -214,6 +215,21 @@ bool make_scale_map_3d(CUtensorMap* m, const void* ptr, int64_t rows, int64_t gr
     cuuint32_t estride[3] = {1, 1, 1};
     return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, const_cast<void*>(ptr), gdim, gstride, box, estride,
               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Row-major bf16 [rows][cols], rows `pitch` elements apart, 128-byte swizzle.
+bool make_map_pitch(CUtensorMap* m, const void* ptr, int64_t rows, int64_t cols, int64_t pitch, int box_rows,
+                    int box_cols)
+{
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    cuuint64_t gdim[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+    cuuint64_t gstride[1] = {(cuuint64_t)(pitch * 2)};
+    cuuint32_t box[2] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows};
+    cuuint32_t estride[2] = {1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(ptr), gdim, gstride, box, estride,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -1279,6 +1295,8 @@ bq_status noalloc_scratch(void** out)
 }  // namespace
 }  // namespace bq
 
+#include "epi_host.cuh"
+
 using namespace bq;
 
 extern "C" {
@@ -1567,6 +1585,78 @@ bq_status bf16_matmul(const uint16_t* x_bf16, const uint16_t* w_bf16, uint16_t* 
     if (!aligned16(x_bf16) || !aligned16(w_bf16)) return BQ_ERR_ALIGN;
     if ((s = current_device(&dev, &di)) != BQ_OK) return s;
     return launch_tc<kModeBF16>(di, dev, x_bf16, w_bf16, nullptr, nullptr, y_bf16, M, N, K, (cudaStream_t)stream);
+}
+
+bq_status quant_matmul_act(const uint16_t* x_bf16, const void* wq, const void* scales, const void* biases,
+                           const uint16_t* out_bias, const uint16_t* residual, int act, uint16_t* y_bf16,
+                           uint16_t* preact, int64_t M, int64_t N, int64_t K, int group_size, int bits,
+                           void* workspace, size_t workspace_bytes, bq_stream_t stream)
+{
+    const QMat w{wq, scales, biases};
+    EpiParams e;
+    e.bias = out_bias;
+    e.res = residual;
+    e.y = y_bf16;
+    e.pre = preact;
+    e.act = act;
+    return epi_forward<kEpiAct>(x_bf16, &w, e, M, N, K, group_size, bits, workspace, workspace_bytes,
+                                (cudaStream_t)stream);
+}
+
+bq_status quant_matmul_glu(const uint16_t* x_bf16, const void* const* wq, const void* const* scales,
+                           const void* const* biases, const uint16_t* gate_bias, const uint16_t* up_bias, int act,
+                           uint16_t* h_bf16, uint16_t* g_bf16, uint16_t* u_bf16, int64_t M, int64_t N, int64_t K,
+                           int group_size, int bits, void* workspace, size_t workspace_bytes, bq_stream_t stream)
+{
+    if (!wq || !scales) return BQ_ERR_NULL;
+    const QMat w[2] = {{wq[0], scales[0], biases ? biases[0] : nullptr}, {wq[1], scales[1], biases ? biases[1] : nullptr}};
+    EpiParams e;
+    e.bias = gate_bias;
+    e.bias2 = up_bias;
+    e.y = h_bf16;
+    e.pre = g_bf16;
+    e.pre2 = u_bf16;
+    e.act = act;
+    return epi_forward<kEpiGlu>(x_bf16, w, e, M, N, K, group_size, bits, workspace, workspace_bytes,
+                                (cudaStream_t)stream);
+}
+
+bq_status quant_matmul_act_backward(const uint16_t* dy_bf16, const uint16_t* preact, const void* wq,
+                                    const void* scales, const void* biases, int act, uint16_t* dx_bf16,
+                                    uint16_t* dz_bf16, uint16_t* dbias_bf16, int64_t M, int64_t N, int64_t K,
+                                    int group_size, int bits, void* workspace, size_t workspace_bytes,
+                                    bq_stream_t stream)
+{
+    const QMat w{wq, scales, biases};
+    const EpiBackward b{dy_bf16, {preact, nullptr}, dx_bf16, {dz_bf16, nullptr}, {dbias_bf16, nullptr}};
+    return epi_backward<false>(b, &w, act, M, N, K, group_size, bits, workspace, workspace_bytes, (cudaStream_t)stream);
+}
+
+bq_status quant_matmul_glu_backward(const uint16_t* dh_bf16, const uint16_t* g_bf16, const uint16_t* u_bf16,
+                                    const void* const* wq, const void* const* scales, const void* const* biases,
+                                    int act, uint16_t* dx_bf16, uint16_t* dg_bf16, uint16_t* du_bf16,
+                                    uint16_t* dgate_bias_bf16, uint16_t* dup_bias_bf16, int64_t M, int64_t N,
+                                    int64_t K, int group_size, int bits, void* workspace, size_t workspace_bytes,
+                                    bq_stream_t stream)
+{
+    if (!wq || !scales) return BQ_ERR_NULL;
+    const QMat w[2] = {{wq[0], scales[0], biases ? biases[0] : nullptr}, {wq[1], scales[1], biases ? biases[1] : nullptr}};
+    const EpiBackward b{dh_bf16, {g_bf16, u_bf16}, dx_bf16, {dg_bf16, du_bf16}, {dgate_bias_bf16, dup_bias_bf16}};
+    return epi_backward<true>(b, w, act, M, N, K, group_size, bits, workspace, workspace_bytes, (cudaStream_t)stream);
+}
+
+size_t quant_matmul_epilogue_workspace_size(int op, int64_t M, int64_t N, int64_t K, int group_size, int bits)
+{
+    WFmt fmt;
+    if (op < BQ_OP_ACT || op > BQ_OP_GLU_BACKWARD || M < 1 || N < 1 || K < 0 || !sizes_ok(M, N, K) ||
+        check_format(format_tag(group_size, bits), N, K, group_size, bits, &fmt) != BQ_OK)
+        return 0;
+    int num_sms, smem_optin;
+    device_or_b200(&num_sms, &smem_optin);
+    EpiWs ws;
+    const int mats = op == BQ_OP_GLU || op == BQ_OP_GLU_BACKWARD ? 2 : 1;
+    if (op == BQ_OP_ACT || op == BQ_OP_GLU) return K > 0 && plan_forward(mats, M, N, K, num_sms, smem_optin, &ws) ? ws.bytes : 0;
+    return plan_backward(mats, M, N, K, num_sms, smem_optin, &ws) ? ws.bytes : 0;
 }
 
 bq_status q4_0_quantize(const float* w, uint8_t* wq, uint16_t* scales_f16, int64_t N, int64_t K, bq_stream_t stream)

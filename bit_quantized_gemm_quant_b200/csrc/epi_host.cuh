@@ -1,0 +1,375 @@
+// epi_host.cuh -- host side of the products with an epilogue and of their
+// gradients: argument checks, plans, workspaces and launches.  Included by
+// bqgemm.cu, after the helpers it uses.
+#pragma once
+
+namespace bq {
+namespace {
+
+// One quantized matrix [N][K] as an entry point receives it.
+struct QMat {
+    const void* wq;
+    const void* scales;
+    const void* biases;
+};
+
+int bits_of(WFmt f)
+{
+    switch (f) {
+    case WFmt::AFF2: return 2;
+    case WFmt::AFF3: return 3;
+    case WFmt::AFF6: return 6;
+    case WFmt::AFF8: return 8;
+    default: return 4;
+    }
+}
+
+size_t up256(size_t b) { return (b + 255) / 256 * 256; }
+
+// The current device's SM count and shared memory, a B200's without a device.
+void device_or_b200(int* num_sms, int* smem_optin)
+{
+    int dev;
+    DeviceInfo di;
+    *num_sms = 148;
+    *smem_optin = 232448;
+    if (cudaGetDevice(&dev) == cudaSuccess && current_device(&dev, &di) == BQ_OK) {
+        *num_sms = di.num_sms;
+        *smem_optin = di.max_smem_optin;
+    }
+    cudaGetLastError();
+}
+
+// ------------------------------------------------------------------ pair product
+struct PairPlan {
+    int bn = 32, stages = 0, splits = 1;
+    int64_t tiles = 0, dp_tiles = 0;
+    size_t ws_bytes = 0;
+};
+
+// Token tile and reduction splits for `rows` D rows, M tokens and nk 64-element
+// blocks of the reduction.  Cost model in SM clocks, per unit of work: a block costs
+// the larger of the MMA's 2 bn and of the loads' (a 16 KB weight half-tile and bn / 2
+// tokens per SM through L2), plus a fixed start and the drain of the last tile.
+bool plan_pair(int64_t rows, int64_t M, int64_t nk, int num_sms, int smem_optin, PairPlan* pl)
+{
+    const int64_t pairs = std::max(num_sms / 2, 1), rtiles = (rows + 255) / 256;
+    const int64_t maxb = std::min<int64_t>(256, (M + 31) / 32 * 32);
+    double best = 1e300;
+    for (int b = 32; b <= maxb; b += 32) {
+        const int64_t tiles = ((M + b - 1) / b) * rtiles;
+        const double kb = std::max(2.0 * b, 300.0 + 0.5 * b);
+        auto consider = [&](double c, int sp, int64_t dp) {
+            if (c < best) {
+                best = c;
+                pl->bn = b;
+                pl->splits = sp;
+                pl->dp_tiles = dp;
+            }
+        };
+        auto unit = [&](int64_t blocks) { return (double)blocks * kb + 1500.0; };
+        const double drain = 8.0 * b;
+        for (int sp = 1; sp <= 32 && (sp == 1 || nk / sp >= 4); ++sp) {
+            const int64_t rounds = (tiles * sp + pairs - 1) / pairs;
+            const double red = sp > 1 ? 5000.0 + (double)sp * (double)tiles * b * 256.0 * 8.0 / 2500.0 : 0.0;
+            consider((double)rounds * unit((nk + sp - 1) / sp) + drain + red, sp, sp > 1 ? 0 : tiles);
+        }
+        const int64_t dp = tiles / pairs * pairs, tail = tiles - dp;
+        for (int sp = 2; dp > 0 && tail > 0 && tail * sp <= pairs && nk / sp >= 4; ++sp) {
+            const double red = 5000.0 + (double)sp * (double)tail * b * 256.0 * 8.0 / 2500.0;
+            consider(((double)(dp / pairs) * unit(nk) + unit((nk + sp - 1) / sp) + drain + red) * 1.02, sp, dp);
+        }
+    }
+    pl->tiles = ((M + pl->bn - 1) / pl->bn) * rtiles;
+    pl->stages = std::min<int>(8, (smem_optin - 1024 - 512) / (int)pair_stage_bytes(pl->bn));
+    pl->ws_bytes = pl->splits > 1
+                       ? (size_t)pl->splits * (size_t)(pl->tiles - pl->dp_tiles) * (size_t)pl->bn * 256u * 4u : 0u;
+    return pl->stages >= 3 && pl->tiles <= INT32_MAX / 64;
+}
+
+unsigned reduce_grid(int64_t items, const DeviceInfo& di)
+{
+    return (unsigned)std::max<int64_t>(1, std::min<int64_t>((items + 255) / 256, 8 * (int64_t)di.num_sms));
+}
+
+// D = sum over segs of A_i . B_i^T with the epilogue e.  A_i: bf16 weights, a_rows
+// rows (K-major: D rows x red; MN: red x D rows); B_i: tokens [M][red], b_pitch
+// elements apart.  outs: outputs per token (glu: of each of gate and up).
+template <bool MN, int EPI>
+bq_status launch_pair(const DeviceInfo& di, int dev, const PairPlan& pl, const uint16_t* const* A,
+                      const uint16_t* const* B, int segs, int64_t rows, int64_t outs, int64_t M, int64_t red,
+                      int64_t b_pitch, const EpiParams& e, void* ws, cudaStream_t st)
+{
+    auto kern = tc_pair_kernel<MN, EPI>;
+    static bool attr_done[kMaxDevices] = {};
+    if (!attr_done[dev]) {
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, di.max_smem_optin) != cudaSuccess)
+            return BQ_ERR_CUDA;
+        attr_done[dev] = true;
+    }
+    CUtensorMap ta[2], tb[2];
+    for (int i = 0; i < 2; ++i) {
+        const int j = i < segs ? i : 0;
+        const bool a_ok = MN ? make_map(&ta[i], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, A[j], red, rows, 64, 64,
+                                        CU_TENSOR_MAP_SWIZZLE_128B)
+                             : make_map(&ta[i], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, A[j], rows, red, 128, 64,
+                                        CU_TENSOR_MAP_SWIZZLE_128B);
+        if (!a_ok || !make_map_pitch(&tb[i], B[j], M, red, b_pitch, pl.bn / 2, 64)) return BQ_ERR_CUDA;
+    }
+    PairParams p;
+    p.e = e;
+    p.M = (int)M;
+    p.N = (int)outs;
+    p.bn = pl.bn;
+    p.stages = pl.stages;
+    p.m_tiles = (int)((M + pl.bn - 1) / pl.bn);
+    p.tiles = (int)pl.tiles;
+    p.seg_blocks = (int)((red + 63) / 64);
+    p.segs = segs;
+    p.dp_tiles = (int)pl.dp_tiles;
+    p.splits = pl.splits;
+    p.ws = reinterpret_cast<float*>(ws);
+    const int64_t units = pl.dp_tiles + (pl.tiles - pl.dp_tiles) * pl.splits;
+    const unsigned grid = 2u * (unsigned)std::min<int64_t>(units, di.num_sms / 2);
+    const size_t smem = std::max<size_t>(1024 + (size_t)pl.stages * pair_stage_bytes(pl.bn) + 512,
+                                         (size_t)di.max_smem_optin / 2 + 1024);   // one CTA per SM (all of TMEM)
+    kern<<<grid, kPairThreads, smem, st>>>(ta[0], ta[1], tb[0], tb[1], p);
+    bq_status s = launch_status();
+    if (s != BQ_OK || pl.splits == 1) return s;
+    const int64_t split_tiles = pl.tiles - pl.dp_tiles;
+    epi_reduce_kernel<EPI><<<reduce_grid(split_tiles * pl.bn * epi_tile_rows<EPI>(256) / 4, di), 256, 0, st>>>(
+        p.ws, e, (int)M, (int)outs, pl.bn, 256, p.m_tiles, p.dp_tiles, (int)split_tiles, pl.splits);
+    return launch_status();
+}
+
+bq_status dequant_rows(WFmt fmt, const QMat* w, int count, uint16_t* out, int64_t N, int64_t K, int group_size,
+                       bool interleave, const DeviceInfo& di, cudaStream_t st)
+{
+    DequantMat m[2];
+    for (int i = 0; i < 2; ++i) {
+        const QMat& q = w[i < count ? i : 0];
+        m[i] = DequantMat{reinterpret_cast<const uint32_t*>(q.wq), reinterpret_cast<const uint16_t*>(q.scales),
+                          reinterpret_cast<const uint16_t*>(q.biases)};
+    }
+    const int chunks = (int)(K / 8), shift = group_size == 32 ? 5 : group_size == 64 ? 6 : 7;
+    const dim3 grid((unsigned)std::min<int64_t>((N * chunks + 255) / 256, (int64_t)di.num_sms * 16), (unsigned)count);
+    switch (fmt) {
+    case WFmt::Q4_0: dequant_rows_kernel<0><<<grid, 256, 0, st>>>(m[0], m[1], out, (int)N, chunks, shift, interleave); break;
+    case WFmt::AFF2: dequant_rows_kernel<2><<<grid, 256, 0, st>>>(m[0], m[1], out, (int)N, chunks, shift, interleave); break;
+    case WFmt::AFF3: dequant_rows_kernel<3><<<grid, 256, 0, st>>>(m[0], m[1], out, (int)N, chunks, shift, interleave); break;
+    case WFmt::AFF4: dequant_rows_kernel<4><<<grid, 256, 0, st>>>(m[0], m[1], out, (int)N, chunks, shift, interleave); break;
+    case WFmt::AFF6: dequant_rows_kernel<6><<<grid, 256, 0, st>>>(m[0], m[1], out, (int)N, chunks, shift, interleave); break;
+    default: dequant_rows_kernel<8><<<grid, 256, 0, st>>>(m[0], m[1], out, (int)N, chunks, shift, interleave); break;
+    }
+    return launch_status();
+}
+
+// ------------------------------------------------------------------ layouts of the workspaces
+// Forward: the bf16 weights (glu: interleaved, in whole blocks of 16 rows), then the
+// partial sums of the split tiles.  Gradient: the bf16 weights, padded copies of the
+// gradients when N is not a multiple of 8 (their rows must start on 16 bytes), the
+// biases' partial sums, the product's partial sums.
+struct EpiWs {
+    PairPlan pl;
+    int64_t rows = 0;               // D rows of the product
+    size_t off_pad = 0, off_part = 0, off_split = 0, bytes = 0;
+    int64_t pitch = 0;              // elements per row of the product's token operand
+    int row_blocks = 0, rows_per_block = 0;
+};
+
+bool plan_forward(int mats, int64_t M, int64_t N, int64_t K, int num_sms, int smem_optin, EpiWs* w)
+{
+    w->rows = mats == 2 ? 32 * ((N + 15) / 16) : N;
+    if (!plan_pair(w->rows, M, (K + 63) / 64, num_sms, smem_optin, &w->pl)) return false;
+    w->off_split = up256((size_t)w->rows * (size_t)K * 2u);
+    w->bytes = w->off_split + w->pl.ws_bytes;
+    return true;
+}
+
+bool plan_backward(int mats, int64_t M, int64_t N, int64_t K, int num_sms, int smem_optin, EpiWs* w)
+{
+    w->rows = K;
+    if (K > 0 && N > 0 && !plan_pair(K, M, mats * ((N + 63) / 64), num_sms, smem_optin, &w->pl)) return false;
+    w->pitch = (N + 7) / 8 * 8;
+    // blocks of 8 warps over rows of tokens: about 8 blocks per SM, at least 32 rows each
+    const int64_t cols = std::max<int64_t>(1, (N + 255) / 256);
+    const int64_t want = std::max<int64_t>(1, (int64_t)num_sms * 8 / cols);
+    const int64_t rpb = std::max<int64_t>(32, ((M + want - 1) / want + 7) / 8 * 8);
+    w->rows_per_block = (int)rpb;
+    w->row_blocks = (int)((M + rpb - 1) / rpb);
+    size_t off = up256((size_t)mats * (size_t)N * (size_t)K * 2u);
+    w->off_pad = off;
+    if (N % 8 != 0) off += (size_t)mats * up256((size_t)M * (size_t)w->pitch * 2u);
+    w->off_part = off;
+    off += up256((size_t)w->row_blocks * (size_t)mats * (size_t)N * 4u);
+    w->off_split = off;
+    w->bytes = off + w->pl.ws_bytes;
+    return true;
+}
+
+// The caller's workspace (BQ_ERR_WORKSPACE when it is too small) or the stream's buffer.
+bq_status epi_workspace(int dev, cudaStream_t st, void* workspace, size_t workspace_bytes, size_t need, void** out)
+{
+    if (need == 0 || workspace) {
+        *out = workspace;
+        return workspace_bytes < need ? BQ_ERR_WORKSPACE : BQ_OK;
+    }
+    try {
+        return library_workspace(dev, st, need, out);
+    } catch (...) {                      // its tables could not grow: no exception leaves a C entry
+        return BQ_ERR_CUDA;
+    }
+}
+
+bool sizes_ok(int64_t M, int64_t N, int64_t K)
+{
+    // 32-bit tile, row and column numbers in the kernels, with room for a tile's width
+    return M <= INT32_MAX - 1024 && N <= INT32_MAX / 2 - 1024 && K <= INT32_MAX - 1024;
+}
+
+// ------------------------------------------------------------------ forward
+template <int EPI>
+bq_status epi_forward(const uint16_t* x, const QMat* w, const EpiParams& e, int64_t M, int64_t N, int64_t K,
+                      int group_size, int bits, void* workspace, size_t workspace_bytes, cudaStream_t st)
+{
+    constexpr int mats = EPI == kEpiGlu ? 2 : 1;
+    if (M < 0 || N < 0 || K < 0 || !sizes_ok(M, N, K)) return BQ_ERR_SHAPE;
+    if (e.act < kActNone || e.act > kActSilu) return BQ_ERR_UNSUPPORTED;
+    if (mats == 2 && (w[0].biases == nullptr) != (w[1].biases == nullptr)) return BQ_ERR_NULL;   // one format
+    WFmt fmt;
+    bq_status s = check_format(w[0].biases, N, K, group_size, bits, &fmt);
+    if (s != BQ_OK) return s;
+    if (M == 0 || N == 0) return BQ_OK;
+    if (!e.y || (EPI == kEpiGlu && (e.pre == nullptr) != (e.pre2 == nullptr))) return BQ_ERR_NULL;
+    for (const void* q : {(const void*)e.y, (const void*)e.bias, (const void*)e.bias2, (const void*)e.res,
+                          (const void*)e.pre, (const void*)e.pre2, (const void*)workspace})
+        if (!aligned16(q)) return BQ_ERR_ALIGN;
+    if (K > 0) {
+        if (!x) return BQ_ERR_NULL;
+        if (!aligned16(x)) return BQ_ERR_ALIGN;
+        for (int i = 0; i < mats; ++i) {
+            if (!w[i].wq || !w[i].scales) return BQ_ERR_NULL;
+            if (!aligned16(w[i].wq) || !aligned16(w[i].scales) || !aligned16(w[i].biases)) return BQ_ERR_ALIGN;
+        }
+    }
+    int dev;
+    DeviceInfo di;
+    if ((s = current_device(&dev, &di)) != BQ_OK) return s;
+    if (K == 0) {
+        epi_empty_kernel<EPI><<<grid_for(M * N, 256, di), 256, 0, st>>>(e, M, (int)N);
+        return launch_status();
+    }
+    EpiWs ws;
+    if (!plan_forward(mats, M, N, K, di.num_sms, di.max_smem_optin, &ws)) return BQ_ERR_UNSUPPORTED;
+    void* buf = nullptr;
+    if ((s = epi_workspace(dev, st, workspace, workspace_bytes, ws.bytes, &buf)) != BQ_OK) return s;
+    uint16_t* wb = reinterpret_cast<uint16_t*>(buf);
+    if ((s = dequant_rows(fmt, w, mats, wb, N, K, group_size, mats == 2, di, st)) != BQ_OK) return s;
+    return launch_pair<false, EPI>(di, dev, ws.pl, &wb, &x, 1, ws.rows, N, M, K, K, e,
+                                   reinterpret_cast<uint8_t*>(buf) + ws.off_split, st);
+}
+
+// ------------------------------------------------------------------ backward
+template <bool GLU, int V>
+bq_status launch_epi_grad_v(const EpiGradParams& p, int act, int row_blocks, cudaStream_t st)
+{
+    const dim3 grid((unsigned)(((int64_t)p.N + 32 * V - 1) / (32 * V)), (unsigned)row_blocks);
+    switch (act) {
+    case kActRelu: epi_grad_kernel<GLU, kActRelu, V><<<grid, 256, 0, st>>>(p); break;
+    case kActGelu: epi_grad_kernel<GLU, kActGelu, V><<<grid, 256, 0, st>>>(p); break;
+    case kActGeluTanh: epi_grad_kernel<GLU, kActGeluTanh, V><<<grid, 256, 0, st>>>(p); break;
+    case kActSilu: epi_grad_kernel<GLU, kActSilu, V><<<grid, 256, 0, st>>>(p); break;
+    default: epi_grad_kernel<GLU, kActNone, V><<<grid, 256, 0, st>>>(p); break;
+    }
+    return launch_status();
+}
+
+// dy [M][N] and the saved z (glu: g, u) to dz (dg, du), dx and the biases' gradients.
+struct EpiBackward {
+    const uint16_t* dy;
+    const uint16_t* pre[2];
+    uint16_t* dx;
+    uint16_t* d[2];
+    uint16_t* db[2];
+};
+
+template <bool GLU>
+bq_status epi_backward(const EpiBackward& b, const QMat* w, int act, int64_t M, int64_t N, int64_t K, int group_size,
+                       int bits, void* workspace, size_t workspace_bytes, cudaStream_t st)
+{
+    constexpr int mats = GLU ? 2 : 1;
+    if (M < 0 || N < 0 || K < 0 || !sizes_ok(M, N, K)) return BQ_ERR_SHAPE;
+    if (act < kActNone || act > kActSilu) return BQ_ERR_UNSUPPORTED;
+    if (GLU && (w[0].biases == nullptr) != (w[1].biases == nullptr)) return BQ_ERR_NULL;
+    WFmt fmt;
+    bq_status s = check_format(w[0].biases, N, K, group_size, bits, &fmt);
+    if (s != BQ_OK) return s;
+    const bool none = !GLU && act == kActNone;          // dz is dy
+    const bool any_db = b.db[0] || b.db[1];
+    for (const void* q : {(const void*)b.dy, (const void*)b.pre[0], (const void*)b.pre[1], (const void*)b.dx,
+                          (const void*)b.d[0], (const void*)b.d[1], (const void*)b.db[0], (const void*)b.db[1],
+                          (const void*)workspace})
+        if (!aligned16(q)) return BQ_ERR_ALIGN;
+    if (M > 0 && K > 0 && !b.dx) return BQ_ERR_NULL;
+    if (M > 0 && N > 0) {
+        if (!b.dy || (!none && (!b.pre[0] || !b.d[0])) || (GLU && (!b.pre[1] || !b.d[1]))) return BQ_ERR_NULL;
+        for (int i = 0; K > 0 && i < mats; ++i) {
+            if (!w[i].wq || !w[i].scales) return BQ_ERR_NULL;
+            if (!aligned16(w[i].wq) || !aligned16(w[i].scales) || !aligned16(w[i].biases)) return BQ_ERR_ALIGN;
+        }
+    }
+    if ((M == 0 || K == 0) && (M == 0 || N == 0) && !(any_db && N > 0)) return BQ_OK;   // nothing to write
+    int dev;
+    DeviceInfo di;
+    if ((s = current_device(&dev, &di)) != BQ_OK) return s;
+    if (M == 0) {                                        // sums over no tokens
+        for (int i = 0; i < mats; ++i)
+            if (b.db[i] && cudaMemsetAsync(b.db[i], 0, (size_t)N * 2u, st) != cudaSuccess) return BQ_ERR_CUDA;
+        return BQ_OK;
+    }
+    if (N == 0)                                          // a sum over no outputs
+        return cudaMemsetAsync(b.dx, 0, (size_t)M * (size_t)K * 2u, st) == cudaSuccess ? BQ_OK : BQ_ERR_CUDA;
+    EpiWs ws;
+    if (!plan_backward(mats, M, N, K, di.num_sms, di.max_smem_optin, &ws)) return BQ_ERR_UNSUPPORTED;
+    if (ws.row_blocks > 65535) return BQ_ERR_SHAPE;
+    void* buf = nullptr;
+    if ((s = epi_workspace(dev, st, workspace, workspace_bytes, ws.bytes, &buf)) != BQ_OK) return s;
+    uint8_t* base = reinterpret_cast<uint8_t*>(buf);
+    const bool pad = N % 8 != 0;
+    uint16_t* padded[2] = {reinterpret_cast<uint16_t*>(base + ws.off_pad),
+                           reinterpret_cast<uint16_t*>(base + ws.off_pad + up256((size_t)M * ws.pitch * 2u))};
+    if (!none || any_db || pad) {
+        EpiGradParams p;
+        p.dy = b.dy;
+        p.z = b.pre[0];
+        p.u = b.pre[1];
+        p.dz = none ? nullptr : b.d[0];
+        p.du = b.d[1];
+        p.dz_pad = pad ? padded[0] : nullptr;
+        p.du_pad = pad && GLU ? padded[1] : nullptr;
+        p.part = any_db ? reinterpret_cast<float*>(base + ws.off_part) : nullptr;
+        p.M = M;
+        p.N = (int)N;
+        p.pitch = (int)ws.pitch;
+        p.rows_per_block = ws.rows_per_block;
+        s = pad ? launch_epi_grad_v<GLU, 1>(p, act, ws.row_blocks, st) : launch_epi_grad_v<GLU, 8>(p, act, ws.row_blocks, st);
+        if (s != BQ_OK) return s;
+        if (any_db) {
+            epi_bias_grad_kernel<<<(unsigned)((N + 255) / 256), 256, 0, st>>>(p.part, b.db[0], b.db[1], (int)N, mats,
+                                                                             ws.row_blocks);
+            if ((s = launch_status()) != BQ_OK) return s;
+        }
+    }
+    if (K == 0) return BQ_OK;
+    uint16_t* wb = reinterpret_cast<uint16_t*>(base);
+    if ((s = dequant_rows(fmt, w, mats, wb, N, K, group_size, false, di, st)) != BQ_OK) return s;
+    const uint16_t* A[2] = {wb, wb + (size_t)N * (size_t)K};
+    const uint16_t* B[2] = {pad ? padded[0] : none ? b.dy : b.d[0], pad ? padded[1] : b.d[1]};
+    EpiParams e;
+    e.y = b.dx;
+    return launch_pair<true, kEpiPlain>(di, dev, ws.pl, A, B, mats, K, K, M, N, pad ? ws.pitch : N, e,
+                                        base + ws.off_split, st);
+}
+
+}  // namespace
+}  // namespace bq

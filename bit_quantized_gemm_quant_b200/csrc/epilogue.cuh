@@ -1,0 +1,364 @@
+// epilogue.cuh -- what a product with quantized weights does with its fp32 sums
+// before they are rounded: bias, activation, residual and gate, the activations'
+// derivatives, and the elementwise half of the backward pass.
+//
+//   act:  z = sum + bias,  y = residual + act(z)
+//   glu:  g = sum_g + gate_bias,  u = sum_u + up_bias,  h = act(g) u
+//
+// All arithmetic is fp32; y, h and the saved z, g, u are each rounded once, to
+// bf16, from the unrounded values (h does not see the rounding of a saved g).
+#pragma once
+
+#include "common.cuh"
+
+namespace bq {
+
+enum : int { kActNone = 0, kActRelu = 1, kActGelu = 2, kActGeluTanh = 3, kActSilu = 4 };
+
+// What a kernel's epilogue computes: kEpiPlain stores the sums (quant_matmul),
+// kEpiAct and kEpiGlu the two forms above.
+enum : int { kEpiPlain = 0, kEpiAct = 1, kEpiGlu = 2 };
+
+// Operands of an epilogue; [M][N] arrays share the output's layout.  residual may
+// be y itself: each element is read and then written by one thread.
+struct EpiParams {
+    const uint16_t* bias = nullptr;      // act: [N] or NULL; glu: gate_bias
+    const uint16_t* bias2 = nullptr;     // glu: up_bias
+    const uint16_t* res = nullptr;       // act: [M][N] or NULL
+    uint16_t* y = nullptr;               // y or h
+    uint16_t* pre = nullptr;             // saved z or g, or NULL
+    uint16_t* pre2 = nullptr;            // glu: saved u (with pre)
+    int act = kActNone;
+};
+
+// 1 / (1 + e^-z).  The divide is exact to 2 ulp; past e^-z = 2^126 it gives 0,
+// the function's value there to within 2^-126.
+BQ_DEVINL float sigmoid_f(float z) { return __fdividef(1.0f, 1.0f + __expf(-z)); }
+
+// gelu_tanh through 0.5 (1 + tanh a) = sigmoid(2 a), a = sqrt(2/pi) (z + 0.044715 z^3).
+constexpr float kGeluTanhA = 1.5957691216057308f;        // 2 sqrt(2/pi)
+constexpr float kGeluTanhB = 0.044715f;
+constexpr float kInvSqrt2 = 0.70710678118654752f;
+constexpr float kInvSqrt2Pi = 0.39894228040143268f;
+
+template <int ACT>
+BQ_DEVINL float act_f(float z)
+{
+    if constexpr (ACT == kActRelu) return z < 0.0f ? 0.0f : z;                    // NaN stays NaN
+    if constexpr (ACT == kActGelu) return 0.5f * z * erfcf(-z * kInvSqrt2);       // no cancellation for z << 0
+    if constexpr (ACT == kActGeluTanh) return z * sigmoid_f(kGeluTanhA * z * fmaf(kGeluTanhB * z, z, 1.0f));
+    if constexpr (ACT == kActSilu) return z * sigmoid_f(z);
+    return z;
+}
+
+// The derivative; where the sigmoid is 0 or 1 (or the density 0) in fp32 the term
+// it multiplies is dropped, so that large |z| gives 0 or 1 and not inf * 0.
+template <int ACT>
+BQ_DEVINL float dact_f(float z)
+{
+    if constexpr (ACT == kActRelu) return z > 0.0f ? 1.0f : (z <= 0.0f ? 0.0f : z);
+    if constexpr (ACT == kActGelu) {
+        const float d = kInvSqrt2Pi * __expf(-0.5f * z * z);
+        return fmaf(0.5f, erfcf(-z * kInvSqrt2), d == 0.0f ? 0.0f : z * d);
+    }
+    if constexpr (ACT == kActGeluTanh) {
+        const float p = sigmoid_f(kGeluTanhA * z * fmaf(kGeluTanhB * z, z, 1.0f)), t = p * (1.0f - p);
+        return t == 0.0f ? p : fmaf(z * t, kGeluTanhA * fmaf(3.0f * kGeluTanhB * z, z, 1.0f), p);
+    }
+    if constexpr (ACT == kActSilu) {
+        const float p = sigmoid_f(z), t = p * (1.0f - p);
+        return t == 0.0f ? p : fmaf(z, t, p);
+    }
+    return 1.0f;
+}
+
+// act over an array, the choice made once for all of it.
+template <int CNT>
+BQ_DEVINL void act_n(float (&z)[CNT], int act)
+{
+    switch (act) {
+    case kActRelu:
+#pragma unroll
+        for (int i = 0; i < CNT; ++i) z[i] = act_f<kActRelu>(z[i]);
+        break;
+    case kActGelu:
+#pragma unroll
+        for (int i = 0; i < CNT; ++i) z[i] = act_f<kActGelu>(z[i]);
+        break;
+    case kActGeluTanh:
+#pragma unroll
+        for (int i = 0; i < CNT; ++i) z[i] = act_f<kActGeluTanh>(z[i]);
+        break;
+    case kActSilu:
+#pragma unroll
+        for (int i = 0; i < CNT; ++i) z[i] = act_f<kActSilu>(z[i]);
+        break;
+    default: break;
+    }
+}
+
+// One output element from its sums (glu: s and s2): the form the decode kernels
+// and the K = 0 case use.
+template <int EPI>
+BQ_DEVINL void epi_one(const EpiParams& e, float s, float s2, int64_t m, int n, int64_t N)
+{
+    const int64_t o = m * N + n;
+    float z[1] = {s + (e.bias ? bf16_bits_to_f32(e.bias[n]) : 0.0f)};
+    if constexpr (EPI == kEpiGlu) {
+        const float u = s2 + (e.bias2 ? bf16_bits_to_f32(e.bias2[n]) : 0.0f);
+        if (e.pre) {
+            e.pre[o] = (uint16_t)f32_to_bf16_bits(z[0]);
+            e.pre2[o] = (uint16_t)f32_to_bf16_bits(u);
+        }
+        act_n<1>(z, e.act);
+        e.y[o] = (uint16_t)f32_to_bf16_bits(z[0] * u);
+    } else {
+        const float r = e.res ? bf16_bits_to_f32(e.res[o]) : 0.0f;
+        if (e.pre) e.pre[o] = (uint16_t)f32_to_bf16_bits(z[0]);
+        act_n<1>(z, e.act);
+        e.y[o] = (uint16_t)f32_to_bf16_bits(e.res ? z[0] + r : z[0]);
+    }
+}
+
+// The output row (column n of y) that row `r` of a weight tile stands for.  glu
+// tiles hold 16 gate rows, then the 16 up rows of the same outputs, and so on, so
+// that both sums of an output sit in one warp's 32 tensor-memory lanes.
+template <int EPI>
+__host__ __device__ constexpr int epi_tile_rows(int rows) { return EPI == kEpiGlu ? rows / 2 : rows; }
+
+template <int EPI>
+BQ_DEVINL int epi_out_row(int r) { return EPI == kEpiGlu ? 16 * (r >> 5) + (r & 15) : r; }
+
+// Per-thread state of a tensor-core tile's epilogue: this thread's output row.
+template <int EPI>
+struct EpiRow {
+    int n;
+    bool ok;
+    float b, b2;
+};
+
+template <int EPI>
+BQ_DEVINL EpiRow<EPI> epi_row(const EpiParams& e, int n, int N)
+{
+    EpiRow<EPI> r;
+    r.n = n;
+    r.ok = n < N;
+    r.b = r.ok && e.bias ? bf16_bits_to_f32(__ldg(e.bias + n)) : 0.0f;
+    r.b2 = 0.0f;
+    if constexpr (EPI == kEpiGlu) r.b2 = r.ok && e.bias2 ? bf16_bits_to_f32(__ldg(e.bias2 + n)) : 0.0f;
+    return r;
+}
+
+// 16 tokens (mb .. mb + 15) of one tile row from a tensor-memory load.  The whole
+// warp calls it: with glu, lanes l and l + 16 hold the gate and the up sum of one
+// output and trade every second token by one shuffle, so that each lane ends with
+// both sums of 8 outputs.
+template <int EPI>
+BQ_DEVINL void epi_store16(const EpiParams& e, const EpiRow<EPI>& r, const uint32_t (&v)[16], int mb, int M, int64_t N)
+{
+    if constexpr (EPI == kEpiGlu) {
+        const int up = (threadIdx.x >> 4) & 1;
+        float g[8], u[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const uint32_t mine = up ? v[2 * j + 1] : v[2 * j];
+            const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? v[2 * j] : v[2 * j + 1], 16);
+            g[j] = __uint_as_float(up ? got : mine) + r.b;
+            u[j] = __uint_as_float(up ? mine : got) + r.b2;
+        }
+        if (!r.ok) return;
+        const int64_t o = (int64_t)(mb + up) * N + r.n;
+        if (e.pre) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (mb + up + 2 * j < M) {
+                    e.pre[o + 2 * j * N] = (uint16_t)f32_to_bf16_bits(g[j]);
+                    e.pre2[o + 2 * j * N] = (uint16_t)f32_to_bf16_bits(u[j]);
+                }
+        }
+        act_n<8>(g, e.act);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (mb + up + 2 * j < M) e.y[o + 2 * j * N] = (uint16_t)f32_to_bf16_bits(g[j] * u[j]);
+    } else {
+        if (!r.ok) return;
+        const int64_t o = (int64_t)mb * N + r.n;
+        float z[16];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) z[j] = __uint_as_float(v[j]) + r.b;
+        if constexpr (EPI == kEpiAct) {
+            if (e.pre) {
+#pragma unroll
+                for (int j = 0; j < 16; ++j)
+                    if (mb + j < M) e.pre[o + j * N] = (uint16_t)f32_to_bf16_bits(z[j]);
+            }
+            act_n<16>(z, e.act);
+            if (e.res) {
+                uint16_t q[16];
+#pragma unroll
+                for (int j = 0; j < 16; ++j) q[j] = mb + j < M ? e.res[o + j * N] : 0;
+#pragma unroll
+                for (int j = 0; j < 16; ++j) z[j] += bf16_bits_to_f32(q[j]);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+            if (mb + j < M) e.y[o + j * N] = (uint16_t)f32_to_bf16_bits(z[j]);
+    }
+}
+
+// Sums the partial tiles of a K-split product in split order and applies the
+// epilogue.  Partials: [split][split tile][token of the tile (bn)][row of the tile
+// (rows)]; one thread per 4 outputs of one token.
+template <int EPI>
+__global__ void __launch_bounds__(256)
+epi_reduce_kernel(const float* __restrict__ ws, EpiParams e, int M, int N, int bn, int rows, int m_tiles, int dp_tiles,
+                  int split_tiles, int splits)
+{
+    const int q = epi_tile_rows<EPI>(rows) / 4;                       // 4-output groups per token
+    const int64_t per_tile = (int64_t)bn * q;
+    const int64_t total = (int64_t)split_tiles * per_tile;
+    const int64_t split_stride = (int64_t)split_tiles * bn * rows;    // floats
+    for (int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; i < total; i += (int64_t)gridDim.x * blockDim.x) {
+        const int j = (int)(i / per_tile);
+        const int rem = (int)(i - (int64_t)j * per_tile);
+        const int m = rem / q, r4 = (rem - m * q) * 4;
+        const int t = dp_tiles + j;
+        const int tok = (t % m_tiles) * bn + m;
+        const int64_t n0 = (int64_t)(t / m_tiles) * epi_tile_rows<EPI>(rows) + r4;
+        if (tok >= M || n0 >= N) continue;
+        const int row = EPI == kEpiGlu ? 32 * (r4 >> 4) + (r4 & 15) : r4;
+        const float* src = ws + ((int64_t)j * bn + m) * rows + row;
+        float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
+        for (int sp = 0; sp < splits; ++sp) {
+            const float4 c = *reinterpret_cast<const float4*>(src + sp * split_stride);
+            a.x += c.x; a.y += c.y; a.z += c.z; a.w += c.w;
+            if constexpr (EPI == kEpiGlu) {
+                const float4 d = *reinterpret_cast<const float4*>(src + 16 + sp * split_stride);
+                b.x += d.x; b.y += d.y; b.z += d.z; b.w += d.w;
+            }
+        }
+        const float s[4] = {a.x, a.y, a.z, a.w}, s2[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (n0 + k < N) epi_one<EPI>(e, s[k], s2[k], tok, (int)n0 + k, N);
+    }
+}
+
+// K = 0: every sum is empty.
+template <int EPI>
+__global__ void __launch_bounds__(256) epi_empty_kernel(EpiParams e, int64_t M, int N)
+{
+    const int64_t total = M * N;
+    for (int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; i < total; i += (int64_t)gridDim.x * blockDim.x)
+        epi_one<EPI>(e, 0.0f, 0.0f, i / N, (int)(i % N), N);
+}
+
+// ------------------------------------------------------------------ backward, elementwise half
+// act:  dz = dy act'(z);   glu:  dg = dh u act'(g),  du = dh act(g)
+// with the column sums over tokens (the biases' gradients) when asked for: they are
+// sums of the unrounded fp32 values, per block of rows here and over the blocks in
+// epi_bias_grad_kernel, both in a fixed order.
+//
+// Bound by HBM: act reads 2 and writes 1 bf16 [M][N] array, glu reads 3 and writes
+// 2.  A block takes 32 x V columns; its 8 warps take every 8th row.  V = 8 (16-byte
+// loads) when every row starts on 16 bytes, else 1.
+struct EpiGradParams {
+    const uint16_t* dy;
+    const uint16_t* z;         // act: z; glu: g
+    const uint16_t* u;         // glu
+    uint16_t* dz;              // act: dz; glu: dg
+    uint16_t* du;              // glu
+    uint16_t* dz_pad;          // copies with rows of `pitch` elements for the product (N % 8 != 0), or NULL
+    uint16_t* du_pad;
+    float* part;               // [row blocks][1 or 2][N] column sums, or NULL
+    int64_t M;
+    int N, pitch, rows_per_block;
+};
+
+template <bool GLU, int ACT, int V>
+__global__ void __launch_bounds__(256) epi_grad_kernel(EpiGradParams p)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int n = (int)min((int64_t)(blockIdx.x * 32 + lane) * V, (int64_t)INT32_MAX);
+    const int64_t m_end = min(p.M, (int64_t)(blockIdx.y + 1) * p.rows_per_block);
+    float sz[V], su[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) sz[i] = su[i] = 0.0f;
+    if (n < p.N) {
+        for (int64_t m = (int64_t)blockIdx.y * p.rows_per_block + warp; m < m_end; m += 8) {
+            const int64_t o = m * p.N + n;
+            __align__(16) uint16_t vd[V], vz[V], vu[V], oz[V], ou[V];
+            if constexpr (V == 8) {
+                *reinterpret_cast<uint4*>(vd) = *reinterpret_cast<const uint4*>(p.dy + o);
+                if constexpr (ACT != kActNone || GLU) *reinterpret_cast<uint4*>(vz) = *reinterpret_cast<const uint4*>(p.z + o);
+                if constexpr (GLU) *reinterpret_cast<uint4*>(vu) = *reinterpret_cast<const uint4*>(p.u + o);
+            } else {
+                vd[0] = p.dy[o];
+                if constexpr (ACT != kActNone || GLU) vz[0] = p.z[o];
+                if constexpr (GLU) vu[0] = p.u[o];
+            }
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const float d = bf16_bits_to_f32(vd[i]);
+                float a = d;
+                if constexpr (GLU) {
+                    const float g = bf16_bits_to_f32(vz[i]), b = d * act_f<ACT>(g);
+                    a = d * bf16_bits_to_f32(vu[i]) * dact_f<ACT>(g);
+                    su[i] += b;
+                    ou[i] = (uint16_t)f32_to_bf16_bits(b);
+                } else if constexpr (ACT != kActNone) {
+                    a = d * dact_f<ACT>(bf16_bits_to_f32(vz[i]));
+                }
+                sz[i] += a;
+                oz[i] = (uint16_t)f32_to_bf16_bits(a);
+            }
+            if constexpr (V == 8) {
+                if (p.dz) *reinterpret_cast<uint4*>(p.dz + o) = *reinterpret_cast<const uint4*>(oz);
+                if constexpr (GLU) *reinterpret_cast<uint4*>(p.du + o) = *reinterpret_cast<const uint4*>(ou);
+            } else {
+                if (p.dz) p.dz[o] = oz[0];
+                if constexpr (GLU) p.du[o] = ou[0];
+                if (p.dz_pad) {
+                    p.dz_pad[m * p.pitch + n] = oz[0];
+                    if constexpr (GLU) p.du_pad[m * p.pitch + n] = ou[0];
+                }
+            }
+        }
+    }
+    if (p.part) {
+        __shared__ float red[8][32 * V];
+#pragma unroll
+        for (int k = 0; k < (GLU ? 2 : 1); ++k) {
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < V; ++i) red[warp][lane * V + i] = k ? su[i] : sz[i];
+            __syncthreads();
+            for (int c = threadIdx.x; c < 32 * V; c += 256) {
+                const int64_t col = (int64_t)blockIdx.x * 32 * V + c;
+                if (col >= p.N) break;
+                float s = 0.0f;
+#pragma unroll
+                for (int w = 0; w < 8; ++w) s += red[w][c];
+                p.part[((int64_t)blockIdx.y * (GLU ? 2 : 1) + k) * p.N + col] = s;
+            }
+        }
+    }
+}
+
+// db[k][n] = bf16(sum over row blocks of part[block][k][n]), in block order.
+__global__ void __launch_bounds__(256)
+epi_bias_grad_kernel(const float* __restrict__ part, uint16_t* __restrict__ db0, uint16_t* __restrict__ db1, int N,
+                     int kinds, int blocks)
+{
+    const int64_t n = blockIdx.x * (int64_t)256 + threadIdx.x;
+    if (n >= N) return;
+    for (int k = 0; k < kinds; ++k) {
+        float s = 0.0f;
+        for (int b = 0; b < blocks; ++b) s += part[((int64_t)b * kinds + k) * N + n];
+        uint16_t* o = k ? db1 : db0;
+        if (o) o[n] = (uint16_t)f32_to_bf16_bits(s);
+    }
+}
+
+}  // namespace bq

@@ -360,6 +360,110 @@ BQ_API int quant_matmul_select_path(int64_t M, int64_t N, int64_t K, int group_s
 BQ_API bq_status bf16_matmul(const uint16_t* x_bf16, const uint16_t* w_bf16, uint16_t* y_bf16,
                       int64_t M, int64_t N, int64_t K, bq_stream_t stream);
 
+/* Activations of the fused products below (z is the fp32 sum plus the bias). */
+typedef enum {
+    BQ_ACT_NONE = 0,           /* z */
+    BQ_ACT_RELU = 1,           /* max(z, 0); derivative 0 at 0 */
+    BQ_ACT_GELU = 2,           /* z Phi(z), Phi the normal distribution function */
+    BQ_ACT_GELU_TANH = 3,      /* z / 2 (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) */
+    BQ_ACT_SILU = 4            /* z / (1 + e^-z) */
+} bq_act;
+
+/*
+ * quant_matmul_act -- quant_matmul with its epilogue in the product's kernel:
+ *   z[m][n] = sum_k x[m][k] * dequant(W)[n][k] + out_bias[n]
+ *   y[m][n] = bf16_rne(residual[m][n] + act(z[m][n]))
+ * dequant(W) is the bf16 matrix of *_dequantize, sums and epilogue are fp32, and y
+ * is rounded once.  No page has a counterpart of the epilogue; the product is
+ * quant_matmul's (mx.quantized_matmul on the MLX issue page, Repro).
+ *   x_bf16    device u16 [M][K]
+ *   wq, scales, biases  W [N][K] as in quant_matmul with transpose = 1 (biases NULL: Q4_0)
+ *   out_bias  device bf16 [N], or NULL
+ *   residual  device bf16 [M][N], or NULL; may be y_bf16 itself (y += act(z))
+ *   act       bq_act; another value returns BQ_ERR_UNSUPPORTED
+ *   y_bf16    device u16 [M][N], written
+ *   preact    device u16 [M][N], bf16_rne(z) written for the backward pass, or NULL
+ *   workspace, workspace_bytes  scratch of at least
+ *             quant_matmul_epilogue_workspace_size(BQ_OP_ACT, ...) bytes (else
+ *             BQ_ERR_WORKSPACE, nothing launched), free again once the call's work is
+ *             done; NULL: the library's buffer of this stream, under quant_matmul's
+ *             rules (no allocating call during capture; replays of graphs that share
+ *             it must not overlap)
+ * Any M, any N; K a multiple of 32 (Q4_0) or of group_size.  K == 0: z = out_bias.
+ * Every non-NULL pointer 16-byte aligned.  Results do not depend on timing: sums over
+ * split reductions are added in a fixed order.
+ */
+BQ_API bq_status quant_matmul_act(const uint16_t* x_bf16, const void* wq, const void* scales, const void* biases,
+                                  const uint16_t* out_bias, const uint16_t* residual, int act, uint16_t* y_bf16,
+                                  uint16_t* preact, int64_t M, int64_t N, int64_t K, int group_size, int bits,
+                                  void* workspace, size_t workspace_bytes, bq_stream_t stream);
+
+/*
+ * quant_matmul_act_backward -- the gradients of quant_matmul_act for frozen weights:
+ *   dz[m][n] = bf16_rne(dy[m][n] * act'(preact[m][n]))
+ *   dx[m][k] = bf16_rne(sum_n dz[m][n] * dequant(W)[n][k])       (of dz as returned)
+ *   dbias[n] = bf16_rne(sum_m dy[m][n] * act'(preact[m][n]))     (of the unrounded products)
+ * The residual's gradient is dy.  For Q4_0 this is also the only product with W itself
+ * (quant_matmul's transpose = 0 is affine only).
+ *   dy_bf16, preact  device bf16 [M][N]; preact as saved by quant_matmul_act (not read
+ *                    and may be NULL for BQ_ACT_NONE)
+ *   dx_bf16          device u16 [M][K], written
+ *   dz_bf16          device u16 [M][N], written; for BQ_ACT_NONE dz is dy, and this
+ *                    pointer is not used
+ *   dbias_bf16       device u16 [N], written, or NULL
+ * No output may overlap an input or another output.  Workspace and errors as
+ * quant_matmul_act (BQ_OP_ACT_BACKWARD).
+ */
+BQ_API bq_status quant_matmul_act_backward(const uint16_t* dy_bf16, const uint16_t* preact, const void* wq,
+                                           const void* scales, const void* biases, int act, uint16_t* dx_bf16,
+                                           uint16_t* dz_bf16, uint16_t* dbias_bf16, int64_t M, int64_t N, int64_t K,
+                                           int group_size, int bits, void* workspace, size_t workspace_bytes,
+                                           bq_stream_t stream);
+
+/*
+ * quant_matmul_glu -- the gated feed-forward's first half in one product:
+ *   g = x . dequant(Wg)^T + gate_bias,  u = x . dequant(Wu)^T + up_bias
+ *   h[m][n] = bf16_rne(act(g[m][n]) * u[m][n])
+ * Both projections share x (and N, K, format, group size); neither g nor u is stored
+ * unless asked for.  After the SYCL page "2026-05-06 Q4 sync-after focused repro"
+ * (Important source touch points), which fuses ffn_gate + ffn_up of one token into
+ * one kernel; the activation and the product are this library's addition.
+ *   wq, scales, biases  host arrays of 2 device pointers: gate, then up (biases NULL: Q4_0)
+ *   gate_bias, up_bias  device bf16 [N], or NULL
+ *   h_bf16              device u16 [M][N], written
+ *   g_bf16, u_bf16      device u16 [M][N], bf16_rne of g and u for the backward pass, or
+ *                       both NULL
+ * Other arguments, workspace (BQ_OP_GLU) and errors as quant_matmul_act.
+ */
+BQ_API bq_status quant_matmul_glu(const uint16_t* x_bf16, const void* const* wq, const void* const* scales,
+                                  const void* const* biases, const uint16_t* gate_bias, const uint16_t* up_bias,
+                                  int act, uint16_t* h_bf16, uint16_t* g_bf16, uint16_t* u_bf16, int64_t M, int64_t N,
+                                  int64_t K, int group_size, int bits, void* workspace, size_t workspace_bytes,
+                                  bq_stream_t stream);
+
+/*
+ * quant_matmul_glu_backward -- the gradients of quant_matmul_glu for frozen weights:
+ *   dg = bf16_rne(dh * u * act'(g)),  du = bf16_rne(dh * act(g))
+ *   dx = bf16_rne(dg . dequant(Wg) + du . dequant(Wu))           (of dg and du as returned)
+ *   dgate_bias, dup_bias  column sums over tokens of the unrounded products, or NULL
+ * g and u as saved by quant_matmul_glu.  No output may overlap an input or another
+ * output.  Other arguments, workspace (BQ_OP_GLU_BACKWARD) and errors as
+ * quant_matmul_act_backward.
+ */
+BQ_API bq_status quant_matmul_glu_backward(const uint16_t* dh_bf16, const uint16_t* g_bf16, const uint16_t* u_bf16,
+                                           const void* const* wq, const void* const* scales,
+                                           const void* const* biases, int act, uint16_t* dx_bf16, uint16_t* dg_bf16,
+                                           uint16_t* du_bf16, uint16_t* dgate_bias_bf16, uint16_t* dup_bias_bf16,
+                                           int64_t M, int64_t N, int64_t K, int group_size, int bits, void* workspace,
+                                           size_t workspace_bytes, bq_stream_t stream);
+
+/* Bytes of workspace the four calls above need for a problem (planned for the current
+ * device, or for a B200 when there is none; 0 for arguments they reject and for empty
+ * problems).  Having no biases pointer, it takes any valid group_size and bits; the
+ * size is the same for Q4_0 and affine 4-bit with groups of 32. */
+typedef enum { BQ_OP_ACT = 0, BQ_OP_ACT_BACKWARD = 1, BQ_OP_GLU = 2, BQ_OP_GLU_BACKWARD = 3 } bq_epilogue_op;
+BQ_API size_t quant_matmul_epilogue_workspace_size(int op, int64_t M, int64_t N, int64_t K, int group_size, int bits);
+
 /*
  * q4_0_quantize -- fp32 w[N][K] -> Q4_0 (input preparation, mx.quantize's
  * counterpart).  Per block of 32: m = the element of largest |w| (first wins a
