@@ -358,38 +358,68 @@ def quant_matmul_epilogue_workspace_size(op: int, M: int, N: int, K: int, group_
     return lib().quant_matmul_epilogue_workspace_size(op, M, N, K, group_size, bits)
 
 
-def _operand(t: torch.Tensor | None, dtypes, shape, name: str, device: torch.device):
-    """The pointer of a contiguous tensor of exactly `shape` on `device` (None: NULL)."""
-    if t is None:
-        return None
+# One decode call runs a few microseconds on the GPU, so the checks below take their
+# fast way first: one comparison per property, addresses as plain ints, and words for an
+# error only once something is wrong.
+_EMPTY_PTR = 16          # non-NULL, 16-byte aligned, never dereferenced (empty tensor)
+
+
+def _operand_error(t, dtypes, shape, name: str, device):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a tensor, got {type(t).__name__}")
     if t.dtype not in dtypes:
         raise TypeError(f"{name}: expected one of {[str(d) for d in dtypes]}, got {t.dtype}")
-    if tuple(t.shape) != shape:
+    if t.shape != shape:
         raise ValueError(f"{name}: shape {tuple(t.shape)}, the call needs {shape}")
     if t.device != device:
         raise ValueError(f"{name}: on {t.device}, the call runs on {device}")
-    return _ptr(t)
+    raise ValueError(f"{name}: tensors must be contiguous")
+
+
+def _operand(t: torch.Tensor | None, dtypes, shape, name: str, device: torch.device):
+    """The address of a contiguous tensor of exactly `shape` on `device` (None: NULL)."""
+    if t is None:
+        return None
+    if not (isinstance(t, torch.Tensor) and t.dtype in dtypes and t.shape == shape and t.device == device
+            and t.is_contiguous()):
+        _operand_error(t, dtypes, shape, name, device)
+    return t.data_ptr() or _EMPTY_PTR
 
 
 def _matrix(w, N: int, K: int, group_size: int, bits: int, device: torch.device, name: str):
-    """Checked pointers of one (wq, scales, biases | None) with W [N][K]."""
+    """Checked addresses of one (wq, scales, biases | None) with W [N][K]."""
     wq, scales, biases = w
-    q4 = biases is None
-    groups = (N, K // (32 if q4 else max(group_size, 1)))
-    sdt = BITS16 if q4 else BF16
-    return (_operand(wq, U8 if q4 else U32, (N, K // 2 if q4 else K * bits // 32), name + ".wq", device),
-            _operand(scales, sdt, groups, name + ".scales", device),
+    if biases is None:
+        return (_operand(wq, U8, (N, K // 2), name + ".wq", device),
+                _operand(scales, BITS16, (N, K // 32), name + ".scales", device), None)
+    groups = (N, K // max(group_size, 1))
+    return (_operand(wq, U32, (N, K * bits // 32), name + ".wq", device),
+            _operand(scales, BF16, groups, name + ".scales", device),
             _operand(biases, BF16, groups, name + ".biases", device))
 
 
+class _On:
+    """Makes a device and a stream current, so that a call's outputs and workspace come
+    from that stream's memory."""
+
+    def __init__(self, device: torch.device, stream):
+        self.ctx = torch.cuda.stream(stream) if stream is not None else torch.cuda.device(device)
+
+    def __enter__(self):
+        self.ctx.__enter__()
+
+    def __exit__(self, *exc):
+        return self.ctx.__exit__(*exc)
+
+
+_HERE = contextlib.nullcontext()
+
+
 def _on(device: torch.device, stream):
-    """Makes `device` and `stream` current for the call, so that the outputs and the
-    workspace come from that stream's memory; nothing to do where they are already."""
-    if stream is not None:
-        return torch.cuda.stream(stream)
-    if device.index != torch.cuda.current_device():
-        return torch.cuda.device(device)
-    return contextlib.nullcontext()
+    """_On where something has to change, else nothing."""
+    if stream is None and device.index == torch.cuda.current_device():
+        return _HERE
+    return _On(device, stream)
 
 
 def _need_cuda(t: torch.Tensor, name: str, stream) -> torch.device:
@@ -402,12 +432,12 @@ def _need_cuda(t: torch.Tensor, name: str, stream) -> torch.device:
     return t.device
 
 
-def _new(M: int, N: int, device) -> torch.Tensor:
-    return torch.empty((M, N), dtype=torch.bfloat16, device=device)
+def _raw_stream(device: torch.device) -> int:
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
 def _scratch(op: int, M: int, N: int, K: int, group_size: int, bits: int, device):
-    """(tensor to keep until the call returned, pointer, bytes)"""
+    """(tensor to keep until the call returned, address, bytes)"""
     n = _epilogue_ws_bytes(device.index, op, M, N, K, group_size, bits)
     if n == 0:
         return None, None, 0
@@ -415,11 +445,14 @@ def _scratch(op: int, M: int, N: int, K: int, group_size: int, bits: int, device
     return t, t.data_ptr(), n
 
 
-def _out(t: torch.Tensor | None, M: int, N: int, device, name: str):
+def _out(t: torch.Tensor | None, shape, device, name: str):
     if t is None:
-        t = _new(M, N, device)
-        return t, (t.data_ptr() if t.numel() else _EMPTY_TAG)
-    return t, _operand(t, (torch.bfloat16,), (M, N), name, device)
+        t = torch.empty(shape, dtype=torch.bfloat16, device=device)
+        return t, t.data_ptr() or _EMPTY_PTR
+    return t, _operand(t, (torch.bfloat16,), shape, name, device)
+
+
+_VP2 = ctypes.c_void_p * 2
 
 
 def _pair_of(gate, up, N: int, K: int, group_size: int, bits: int, device):
@@ -428,8 +461,7 @@ def _pair_of(gate, up, N: int, K: int, group_size: int, bits: int, device):
         raise ValueError("gate and up must both be Q4_0 (biases None) or both be affine")
     a = _matrix(gate, N, K, group_size, bits, device, "gate")
     b = _matrix(up, N, K, group_size, bits, device, "up")
-    VP = ctypes.c_void_p * 2
-    return VP(a[0], b[0]), VP(a[1], b[1]), None if gate[2] is None else VP(a[2], b[2])
+    return _VP2(a[0], b[0]), _VP2(a[1], b[1]), None if gate[2] is None else _VP2(a[2], b[2])
 
 
 def quant_matmul_act(x: torch.Tensor, wq: torch.Tensor, scales: torch.Tensor, biases: torch.Tensor | None = None,
@@ -448,11 +480,11 @@ def quant_matmul_act(x: torch.Tensor, wq: torch.Tensor, scales: torch.Tensor, bi
         xp = _operand(x, BF16, (M, K), "x", dev)
         bp = _operand(out_bias, BF16, (N,), "out_bias", dev)
         rp = _operand(residual, BF16, (M, N), "residual", dev)
-        out, yp = _out(out, M, N, dev, "out")
-        z, zp = _out(None, M, N, dev, "z") if save_preact else (None, None)
+        out, yp = _out(out, (M, N), dev, "out")
+        z, zp = _out(None, (M, N), dev, "z") if save_preact else (None, None)
         keep, ws, wsb = _scratch(OP_ACT, M, N, K, group_size, bits, dev)
         _check(lib().quant_matmul_act(xp, w[0], w[1], w[2], bp, rp, code, yp, zp, M, N, K, group_size, bits, ws, wsb,
-                                      torch.cuda.current_stream().cuda_stream), "quant_matmul_act")
+                                      _raw_stream(dev)), "quant_matmul_act")
     return (out, z) if save_preact else out
 
 
@@ -473,12 +505,12 @@ def quant_matmul_act_backward(dy: torch.Tensor, wq: torch.Tensor, scales: torch.
         w = _matrix((wq, scales, biases), N, K, group_size, bits, dev, "w")
         dyp = _operand(dy, (torch.bfloat16,), (M, N), "dy", dev)
         pp = _operand(preact, BF16, (M, N), "preact", dev)
-        dx, dxp = _out(None, M, K, dev, "dx")
-        dz, dzp = _out(None, M, N, dev, "dz") if code else (dy, None)
-        db = torch.empty(N, dtype=torch.bfloat16, device=dev) if need_dbias else None
+        dx, dxp = _out(None, (M, K), dev, "dx")
+        dz, dzp = _out(None, (M, N), dev, "dz") if code else (dy, None)
+        db, dbp = _out(None, (N,), dev, "dbias") if need_dbias else (None, None)
         keep, ws, wsb = _scratch(OP_ACT_BACKWARD, M, N, K, group_size, bits, dev)
-        _check(lib().quant_matmul_act_backward(dyp, pp, w[0], w[1], w[2], code, dxp, dzp, _ptr(db), M, N, K, group_size,
-                                               bits, ws, wsb, torch.cuda.current_stream().cuda_stream),
+        _check(lib().quant_matmul_act_backward(dyp, pp, w[0], w[1], w[2], code, dxp, dzp, dbp, M, N, K, group_size,
+                                               bits, ws, wsb, _raw_stream(dev)),
                "quant_matmul_act_backward")
     return (dx, dz, db) if need_dbias else (dx, dz)
 
@@ -499,12 +531,12 @@ def quant_matmul_glu(x: torch.Tensor, gate, up, gate_bias: torch.Tensor | None =
         xp = _operand(x, BF16, (M, K), "x", dev)
         gbp = _operand(gate_bias, BF16, (N,), "gate_bias", dev)
         ubp = _operand(up_bias, BF16, (N,), "up_bias", dev)
-        out, hp = _out(out, M, N, dev, "out")
-        g, gp = _out(None, M, N, dev, "g") if save_preact else (None, None)
-        u, up_ = _out(None, M, N, dev, "u") if save_preact else (None, None)
+        out, hp = _out(out, (M, N), dev, "out")
+        g, gp = _out(None, (M, N), dev, "g") if save_preact else (None, None)
+        u, up_ = _out(None, (M, N), dev, "u") if save_preact else (None, None)
         keep, ws, wsb = _scratch(OP_GLU, M, N, K, group_size, bits, dev)
         _check(lib().quant_matmul_glu(xp, w[0], w[1], w[2], gbp, ubp, code, hp, gp, up_, M, N, K, group_size, bits, ws,
-                                      wsb, torch.cuda.current_stream().cuda_stream), "quant_matmul_glu")
+                                      wsb, _raw_stream(dev)), "quant_matmul_glu")
     return (out, g, u) if save_preact else out
 
 
@@ -522,14 +554,15 @@ def quant_matmul_glu_backward(dh: torch.Tensor, g: torch.Tensor, u: torch.Tensor
         dhp = _operand(dh, BF16, (M, N), "dh", dev)
         gp = _operand(g, BF16, (M, N), "g", dev)
         up_ = _operand(u, BF16, (M, N), "u", dev)
-        dx, dxp = _out(None, M, K, dev, "dx")
-        dg, dgp = _out(None, M, N, dev, "dg")
-        du, dup = _out(None, M, N, dev, "du")
-        dgb, dub = (torch.empty(N, dtype=torch.bfloat16, device=dev) for _ in range(2)) if need_dbias else (None, None)
+        dx, dxp = _out(None, (M, K), dev, "dx")
+        dg, dgp = _out(None, (M, N), dev, "dg")
+        du, dup = _out(None, (M, N), dev, "du")
+        dgb, dgbp = _out(None, (N,), dev, "dgate_bias") if need_dbias else (None, None)
+        dub, dubp = _out(None, (N,), dev, "dup_bias") if need_dbias else (None, None)
         keep, ws, wsb = _scratch(OP_GLU_BACKWARD, M, N, K, group_size, bits, dev)
-        _check(lib().quant_matmul_glu_backward(dhp, gp, up_, w[0], w[1], w[2], code, dxp, dgp, dup, _ptr(dgb), _ptr(dub),
+        _check(lib().quant_matmul_glu_backward(dhp, gp, up_, w[0], w[1], w[2], code, dxp, dgp, dup, dgbp, dubp,
                                                M, N, K, group_size, bits, ws, wsb,
-                                               torch.cuda.current_stream().cuda_stream), "quant_matmul_glu_backward")
+                                               _raw_stream(dev)), "quant_matmul_glu_backward")
     return (dx, dg, du, dgb, dub) if need_dbias else (dx, dg, du)
 
 

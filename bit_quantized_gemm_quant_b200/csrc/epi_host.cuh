@@ -164,6 +164,89 @@ bq_status dequant_rows(WFmt fmt, const QMat* w, int count, uint16_t* out, int64_
     return launch_status();
 }
 
+// ------------------------------------------------------------------ decode sizes
+constexpr int64_t kRingMaxM = 16;
+
+// The ring kernel moves rows by tensor copies, so rows of codes must be 16-byte
+// multiples (always so for 4 and 8 bits).
+bool ring_applies(WFmt fmt, int64_t M, int64_t K) { return M <= kRingMaxM && K * bits_of(fmt) % 128 == 0; }
+
+template <int BITS, int NT, int XS, int EPI>
+bq_status launch_ring_cfg(const RingMaps& maps, RingParams& p, const DeviceInfo& di, int dev, cudaStream_t st)
+{
+    auto kern = gemv_ring_kernel<BITS, NT, XS, EPI>;
+    constexpr int kStatic = 2 * kRingWarps * 16 * (8 * NT + 1) * 4 + 2 * kRingMaxStages * 8 + 64;
+    const int room = di.max_smem_optin - kStatic - 1024;
+    static bool attr_done[kMaxDevices] = {};
+    if (!attr_done[dev]) {
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, room) != cudaSuccess) {
+            cudaGetLastError();
+            return BQ_ERR_CUDA;
+        }
+        attr_done[dev] = true;
+    }
+    p.stages = std::min(kRingMaxStages, room / ring_stage_bytes(BITS));
+    return launch_pdl(kern, std::min(p.tiles, di.num_sms), kRingThreads, (size_t)p.stages * ring_stage_bytes(BITS), st, maps,
+                      p);
+}
+
+// Activations in registers for up to 4 chunks of 2048 columns and 8 tokens (2 chunks
+// and 16 tokens): 64 registers.
+template <int BITS, int EPI>
+bq_status launch_ring_bits(const QMat* w, RingParams& p, const DeviceInfo& di, int dev, cudaStream_t st)
+{
+    constexpr int mats = EPI == kEpiGlu ? 2 : 1, rows = 16 / mats, bits = ring_bits(BITS);
+    RingMaps maps;
+    for (int i = 0; i < 2; ++i) {
+        const QMat& q = w[i < mats ? i : 0];
+        bool ok = make_map(&maps.codes[i], CU_TENSOR_MAP_DATA_TYPE_UINT64, 8, q.wq, p.N, (int64_t)p.K * bits / 64, rows,
+                           ring_code_pitch(bits) / 8, CU_TENSOR_MAP_SWIZZLE_NONE);
+        if (p.scale_bulk)
+            ok = ok && make_map(&maps.scales[i], CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, q.scales, p.N, p.K >> p.gs_shift, rows,
+                                ring_scale_pitch(p.gs_shift) / 2, CU_TENSOR_MAP_SWIZZLE_NONE) &&
+                 (BITS == 0 || make_map(&maps.biases[i], CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, q.biases, p.N,
+                                        p.K >> p.gs_shift, rows, ring_scale_pitch(p.gs_shift) / 2,
+                                        CU_TENSOR_MAP_SWIZZLE_NONE));
+        if (!ok) return BQ_ERR_CUDA;
+    }
+    if constexpr (BITS == 0 || BITS == 4 || BITS == 8) {
+        if (p.M <= 8 && p.nchunks <= 2) return launch_ring_cfg<BITS, 1, 2, EPI>(maps, p, di, dev, st);
+        if (p.M <= 8 && p.nchunks <= 4) return launch_ring_cfg<BITS, 1, 4, EPI>(maps, p, di, dev, st);
+        if (p.M > 8 && p.nchunks <= 2) return launch_ring_cfg<BITS, 2, 2, EPI>(maps, p, di, dev, st);
+    }
+    if (p.M <= 8) return launch_ring_cfg<BITS, 1, 0, EPI>(maps, p, di, dev, st);
+    return launch_ring_cfg<BITS, 2, 0, EPI>(maps, p, di, dev, st);
+}
+
+template <int EPI>
+bq_status launch_ring(WFmt fmt, const uint16_t* x, const QMat* w, const EpiParams& e, int64_t M, int64_t N, int64_t K,
+                      int group_size, const DeviceInfo& di, int dev, cudaStream_t st)
+{
+    RingParams p;
+    for (int i = 0; i < 2; ++i) {
+        const QMat& q = w[EPI == kEpiGlu ? i : 0];
+        p.w[i] = RingMat{reinterpret_cast<const uint16_t*>(q.scales), reinterpret_cast<const uint16_t*>(q.biases)};
+    }
+    p.x = x;
+    p.e = e;
+    p.M = (int)M;
+    p.N = (int)N;
+    p.K = (int)K;
+    p.gs_shift = group_size == 32 ? 5 : group_size == 64 ? 6 : 7;
+    p.nchunks = (int)((K + kRingCols - 1) / kRingCols);
+    p.scale_bulk = (K >> p.gs_shift) % 8 == 0;
+    const int64_t outs = EPI == kEpiGlu ? 8 : 16;
+    p.tiles = (int)((N + outs - 1) / outs);
+    switch (fmt) {
+    case WFmt::Q4_0: return launch_ring_bits<0, EPI>(w, p, di, dev, st);
+    case WFmt::AFF2: return launch_ring_bits<2, EPI>(w, p, di, dev, st);
+    case WFmt::AFF3: return launch_ring_bits<3, EPI>(w, p, di, dev, st);
+    case WFmt::AFF4: return launch_ring_bits<4, EPI>(w, p, di, dev, st);
+    case WFmt::AFF6: return launch_ring_bits<6, EPI>(w, p, di, dev, st);
+    default: return launch_ring_bits<8, EPI>(w, p, di, dev, st);
+    }
+}
+
 // ------------------------------------------------------------------ layouts of the workspaces
 // Forward: the bf16 weights (glu: interleaved, in whole blocks of 16 rows), then the
 // partial sums of the split tiles.  Gradient: the bf16 weights, padded copies of the
@@ -259,6 +342,7 @@ bq_status epi_forward(const uint16_t* x, const QMat* w, const EpiParams& e, int6
         epi_empty_kernel<EPI><<<grid_for(M * N, 256, di), 256, 0, st>>>(e, M, (int)N);
         return launch_status();
     }
+    if (ring_applies(fmt, M, K)) return launch_ring<EPI>(fmt, x, w, e, M, N, K, group_size, di, dev, st);
     EpiWs ws;
     if (!plan_forward(mats, M, N, K, di.num_sms, di.max_smem_optin, &ws)) return BQ_ERR_UNSUPPORTED;
     void* buf = nullptr;

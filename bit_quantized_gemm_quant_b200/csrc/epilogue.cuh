@@ -97,15 +97,29 @@ BQ_DEVINL void act_n(float (&z)[CNT], int act)
     }
 }
 
-// One output element from its sums (glu: s and s2): the form the decode kernels
-// and the K = 0 case use.
+// One output element: its operands, which can be loaded ahead of the sums, and the
+// result from the sums (glu: s and s2).
+struct EpiOperands {
+    float b, b2, r;
+};
+
 template <int EPI>
-BQ_DEVINL void epi_one(const EpiParams& e, float s, float s2, int64_t m, int n, int64_t N)
+BQ_DEVINL EpiOperands epi_operands(const EpiParams& e, int64_t m, int n, int64_t N)
+{
+    EpiOperands p;
+    p.b = e.bias ? bf16_bits_to_f32(e.bias[n]) : 0.0f;
+    p.b2 = EPI == kEpiGlu && e.bias2 ? bf16_bits_to_f32(e.bias2[n]) : 0.0f;
+    p.r = EPI == kEpiAct && e.res ? bf16_bits_to_f32(e.res[m * N + n]) : 0.0f;
+    return p;
+}
+
+template <int EPI>
+BQ_DEVINL void epi_finish(const EpiParams& e, const EpiOperands& p, float s, float s2, int64_t m, int n, int64_t N)
 {
     const int64_t o = m * N + n;
-    float z[1] = {s + (e.bias ? bf16_bits_to_f32(e.bias[n]) : 0.0f)};
+    float z[1] = {s + p.b};
     if constexpr (EPI == kEpiGlu) {
-        const float u = s2 + (e.bias2 ? bf16_bits_to_f32(e.bias2[n]) : 0.0f);
+        const float u = s2 + p.b2;
         if (e.pre) {
             e.pre[o] = (uint16_t)f32_to_bf16_bits(z[0]);
             e.pre2[o] = (uint16_t)f32_to_bf16_bits(u);
@@ -113,11 +127,16 @@ BQ_DEVINL void epi_one(const EpiParams& e, float s, float s2, int64_t m, int n, 
         act_n<1>(z, e.act);
         e.y[o] = (uint16_t)f32_to_bf16_bits(z[0] * u);
     } else {
-        const float r = e.res ? bf16_bits_to_f32(e.res[o]) : 0.0f;
         if (e.pre) e.pre[o] = (uint16_t)f32_to_bf16_bits(z[0]);
         act_n<1>(z, e.act);
-        e.y[o] = (uint16_t)f32_to_bf16_bits(e.res ? z[0] + r : z[0]);
+        e.y[o] = (uint16_t)f32_to_bf16_bits(e.res ? z[0] + p.r : z[0]);
     }
+}
+
+template <int EPI>
+BQ_DEVINL void epi_one(const EpiParams& e, float s, float s2, int64_t m, int n, int64_t N)
+{
+    epi_finish<EPI>(e, epi_operands<EPI>(e, m, n, N), s, s2, m, n, N);
 }
 
 // The output row (column n of y) that row `r` of a weight tile stands for.  glu
