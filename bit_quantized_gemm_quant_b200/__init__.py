@@ -445,9 +445,10 @@ def _scratch(op: int, M: int, N: int, K: int, group_size: int, bits: int, device
     return t, t.data_ptr(), n
 
 
-def _out(t: torch.Tensor | None, shape, device, name: str):
+def _out(t: torch.Tensor | None, shape, device, name: str, like: torch.Tensor):
+    """(output, address): the given tensor, checked, or a new one (beside `like`)."""
     if t is None:
-        t = torch.empty(shape, dtype=torch.bfloat16, device=device)
+        t = like.new_empty(shape) if like.dtype is torch.bfloat16 else torch.empty(shape, dtype=torch.bfloat16, device=device)
         return t, t.data_ptr() or _EMPTY_PTR
     return t, _operand(t, (torch.bfloat16,), shape, name, device)
 
@@ -480,8 +481,8 @@ def quant_matmul_act(x: torch.Tensor, wq: torch.Tensor, scales: torch.Tensor, bi
         xp = _operand(x, BF16, (M, K), "x", dev)
         bp = _operand(out_bias, BF16, (N,), "out_bias", dev)
         rp = _operand(residual, BF16, (M, N), "residual", dev)
-        out, yp = _out(out, (M, N), dev, "out")
-        z, zp = _out(None, (M, N), dev, "z") if save_preact else (None, None)
+        out, yp = _out(out, (M, N), dev, "out", x)
+        z, zp = _out(None, (M, N), dev, "z", x) if save_preact else (None, None)
         keep, ws, wsb = _scratch(OP_ACT, M, N, K, group_size, bits, dev)
         _check(lib().quant_matmul_act(xp, w[0], w[1], w[2], bp, rp, code, yp, zp, M, N, K, group_size, bits, ws, wsb,
                                       _raw_stream(dev)), "quant_matmul_act")
@@ -505,9 +506,9 @@ def quant_matmul_act_backward(dy: torch.Tensor, wq: torch.Tensor, scales: torch.
         w = _matrix((wq, scales, biases), N, K, group_size, bits, dev, "w")
         dyp = _operand(dy, (torch.bfloat16,), (M, N), "dy", dev)
         pp = _operand(preact, BF16, (M, N), "preact", dev)
-        dx, dxp = _out(None, (M, K), dev, "dx")
-        dz, dzp = _out(None, (M, N), dev, "dz") if code else (dy, None)
-        db, dbp = _out(None, (N,), dev, "dbias") if need_dbias else (None, None)
+        dx, dxp = _out(None, (M, K), dev, "dx", dy)
+        dz, dzp = _out(None, (M, N), dev, "dz", dy) if code else (dy, None)
+        db, dbp = _out(None, (N,), dev, "dbias", dy) if need_dbias else (None, None)
         keep, ws, wsb = _scratch(OP_ACT_BACKWARD, M, N, K, group_size, bits, dev)
         _check(lib().quant_matmul_act_backward(dyp, pp, w[0], w[1], w[2], code, dxp, dzp, dbp, M, N, K, group_size,
                                                bits, ws, wsb, _raw_stream(dev)),
@@ -531,9 +532,9 @@ def quant_matmul_glu(x: torch.Tensor, gate, up, gate_bias: torch.Tensor | None =
         xp = _operand(x, BF16, (M, K), "x", dev)
         gbp = _operand(gate_bias, BF16, (N,), "gate_bias", dev)
         ubp = _operand(up_bias, BF16, (N,), "up_bias", dev)
-        out, hp = _out(out, (M, N), dev, "out")
-        g, gp = _out(None, (M, N), dev, "g") if save_preact else (None, None)
-        u, up_ = _out(None, (M, N), dev, "u") if save_preact else (None, None)
+        out, hp = _out(out, (M, N), dev, "out", x)
+        g, gp = _out(None, (M, N), dev, "g", x) if save_preact else (None, None)
+        u, up_ = _out(None, (M, N), dev, "u", x) if save_preact else (None, None)
         keep, ws, wsb = _scratch(OP_GLU, M, N, K, group_size, bits, dev)
         _check(lib().quant_matmul_glu(xp, w[0], w[1], w[2], gbp, ubp, code, hp, gp, up_, M, N, K, group_size, bits, ws,
                                       wsb, _raw_stream(dev)), "quant_matmul_glu")
@@ -554,11 +555,11 @@ def quant_matmul_glu_backward(dh: torch.Tensor, g: torch.Tensor, u: torch.Tensor
         dhp = _operand(dh, BF16, (M, N), "dh", dev)
         gp = _operand(g, BF16, (M, N), "g", dev)
         up_ = _operand(u, BF16, (M, N), "u", dev)
-        dx, dxp = _out(None, (M, K), dev, "dx")
-        dg, dgp = _out(None, (M, N), dev, "dg")
-        du, dup = _out(None, (M, N), dev, "du")
-        dgb, dgbp = _out(None, (N,), dev, "dgate_bias") if need_dbias else (None, None)
-        dub, dubp = _out(None, (N,), dev, "dup_bias") if need_dbias else (None, None)
+        dx, dxp = _out(None, (M, K), dev, "dx", dh)
+        dg, dgp = _out(None, (M, N), dev, "dg", dh)
+        du, dup = _out(None, (M, N), dev, "du", dh)
+        dgb, dgbp = _out(None, (N,), dev, "dgate_bias", dh) if need_dbias else (None, None)
+        dub, dubp = _out(None, (N,), dev, "dup_bias", dh) if need_dbias else (None, None)
         keep, ws, wsb = _scratch(OP_GLU_BACKWARD, M, N, K, group_size, bits, dev)
         _check(lib().quant_matmul_glu_backward(dhp, gp, up_, w[0], w[1], w[2], code, dxp, dgp, dup, dgbp, dubp,
                                                M, N, K, group_size, bits, ws, wsb,

@@ -21,6 +21,7 @@
 #include "gemv_stream.cuh"
 #include "tc_gemm.cuh"
 #include "tc_pair.cuh"
+#include "tc_fused_pair.cuh"
 #include "gemv_ring.cuh"
 
 namespace bq {
@@ -1657,8 +1658,8 @@ size_t quant_matmul_epilogue_workspace_size(int op, int64_t M, int64_t N, int64_
     EpiWs ws;
     const int mats = op == BQ_OP_GLU || op == BQ_OP_GLU_BACKWARD ? 2 : 1;
     if ((op == BQ_OP_ACT || op == BQ_OP_GLU) && ring_applies(fmt, M, K)) return 0;
-    if (op == BQ_OP_ACT || op == BQ_OP_GLU) return K > 0 && plan_forward(mats, M, N, K, num_sms, smem_optin, &ws) ? ws.bytes : 0;
-    return plan_backward(mats, M, N, K, num_sms, smem_optin, &ws) ? ws.bytes : 0;
+    if (op == BQ_OP_ACT || op == BQ_OP_GLU) return K > 0 && plan_forward(fmt, mats, M, N, K, num_sms, smem_optin, &ws) ? ws.bytes : 0;
+    return plan_backward(fmt, mats, M, N, K, num_sms, smem_optin, &ws) ? ws.bytes : 0;
 }
 
 bq_status q4_0_quantize(const float* w, uint8_t* wq, uint16_t* scales_f16, int64_t N, int64_t K, bq_stream_t stream)

@@ -48,17 +48,19 @@ struct PairPlan {
 };
 
 // Token tile and reduction splits for `rows` D rows, M tokens and nk 64-element
-// blocks of the reduction.  Cost model in SM clocks, per unit of work: a block costs
-// the larger of the MMA's 2 bn and of the loads' (a 16 KB weight half-tile and bn / 2
-// tokens per SM through L2), plus a fixed start and the drain of the last tile.
-bool plan_pair(int64_t rows, int64_t M, int64_t nk, int num_sms, int smem_optin, PairPlan* pl)
+// blocks of the reduction; fixed_bytes of shared memory and per stage a_bytes of weights.  Cost model in SM clocks,
+// per unit of work: a block costs the larger of the MMA's 2 bn and of bringing it in,
+// min_block + bn / 2 (the weight tile through L2, or dequantizing it), plus a fixed
+// start and the drain of the last tile.
+bool plan_pair(int64_t rows, int64_t M, int64_t nk, int num_sms, int smem_optin, int fixed_bytes, int a_bytes,
+               double min_block, PairPlan* pl)
 {
     const int64_t pairs = std::max(num_sms / 2, 1), rtiles = (rows + 255) / 256;
     const int64_t maxb = std::min<int64_t>(256, (M + 31) / 32 * 32);
     double best = 1e300;
     for (int b = 32; b <= maxb; b += 32) {
         const int64_t tiles = ((M + b - 1) / b) * rtiles;
-        const double kb = std::max(2.0 * b, 300.0 + 0.5 * b);
+        const double kb = std::max(2.0 * b, min_block + 0.5 * b);
         auto consider = [&](double c, int sp, int64_t dp) {
             if (c < best) {
                 best = c;
@@ -81,7 +83,7 @@ bool plan_pair(int64_t rows, int64_t M, int64_t nk, int num_sms, int smem_optin,
         }
     }
     pl->tiles = ((M + pl->bn - 1) / pl->bn) * rtiles;
-    pl->stages = std::min<int>(8, (smem_optin - 1024 - 512) / (int)pair_stage_bytes(pl->bn));
+    pl->stages = std::min<int>(kFpMaxTok, (smem_optin - 1024 - 512 - fixed_bytes) / (a_bytes + pl->bn * 64));
     pl->ws_bytes = pl->splits > 1
                        ? (size_t)pl->splits * (size_t)(pl->tiles - pl->dp_tiles) * (size_t)pl->bn * 256u * 4u : 0u;
     return pl->stages >= 3 && pl->tiles <= INT32_MAX / 64;
@@ -247,32 +249,183 @@ bq_status launch_ring(WFmt fmt, const uint16_t* x, const QMat* w, const EpiParam
     }
 }
 
+// ------------------------------------------------------------------ codes dequantized inside the pair product
+// Shape of the packed scales: whole 256-row tiles and 64-column blocks forward, whole
+// 64-row blocks and 256-column tiles for the gradient.
+struct ScalePack {
+    int64_t rows, cols, mat;        // rows per column block, padded columns, words per matrix (gradient)
+    size_t bytes;
+};
+
+ScalePack scale_pack(bool mn, int mats, int64_t N, int64_t K)
+{
+    ScalePack s;
+    if (mn) {
+        s.rows = (N + 63) / 64 * 64;
+        s.cols = (K + 255) / 256 * 256;
+        s.mat = s.rows * (s.cols / 32);
+        s.bytes = up256((size_t)mats * (size_t)s.mat * 4u);
+    } else {
+        s.rows = ((mats == 2 ? 32 * ((N + 15) / 16) : N) + 255) / 256 * 256;
+        s.cols = (K + 63) / 64 * 64;
+        s.mat = 0;
+        s.bytes = up256((size_t)s.rows * (size_t)(s.cols / 32) * 4u);
+    }
+    return s;
+}
+
+// launch_pdl with a 3-D grid.
+template <typename KernelT, typename... Args>
+bq_status launch_pdl_dim(KernelT kern, dim3 grid, int threads, size_t smem, cudaStream_t st, const Args&... args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, kern, args...) != cudaSuccess) {
+        cudaGetLastError();
+        return BQ_ERR_CUDA;
+    }
+    return launch_status();
+}
+
+int fp_mode(WFmt f) { return f == WFmt::Q4_0 ? kModeQ4_0 : f == WFmt::AFF4 ? kModeAff4 : kModeAff8; }
+
+// The product of launch_pair with the codes of w (1 or 2 matrices [N][K]) in place of
+// bf16 weights.  Forward: B[0] = x, red = K; gradient (MN): B[i] = dz of matrix i,
+// red = N.
+template <int MODE, bool MN, int EPI>
+bq_status launch_fused_pair(const DeviceInfo& di, int dev, const PairPlan& pl, const QMat* w, int mats,
+                            const uint16_t* const* B, int64_t N, int64_t K, int64_t M, int64_t b_pitch, int group_size,
+                            const EpiParams& e, void* packed, void* ws, cudaStream_t st)
+{
+    auto kern = tc_fused_pair_kernel<MODE, MN, EPI>;
+    static bool attr_done[kMaxDevices] = {};
+    if (!attr_done[dev]) {
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, di.max_smem_optin) != cudaSuccess) {
+            cudaGetLastError();
+            return BQ_ERR_CUDA;
+        }
+        attr_done[dev] = true;
+    }
+    constexpr int bits = MODE == kModeAff8 ? 8 : 4, row_bytes = (MN ? 128 : 64) * bits / 8;
+    constexpr CUtensorMapSwizzle sw = row_bytes == 32   ? CU_TENSOR_MAP_SWIZZLE_32B
+                                      : row_bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B;
+    const int64_t red = MN ? N : K, outs = MN ? K : N;
+    CUtensorMap ta[2], tb[2];
+    FpParams p;
+    for (int i = 0; i < 2; ++i) {
+        const QMat& q = w[i < mats ? i : 0];
+        if (!make_map(&ta[i], CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, q.wq, N, K * bits / 8, MN ? 64 : epi_tile_rows<EPI>(128),
+                      row_bytes, sw) ||
+            !make_map_pitch(&tb[i], B[MN && i < mats ? i : 0], M, red, b_pitch, pl.bn / 2, 64))
+            return BQ_ERR_CUDA;
+    }
+    // the scales, by block
+    const ScalePack sp = scale_pack(MN, EPI == kEpiGlu ? 2 : mats, N, K);
+    ScalePackParams pp;
+    for (int i = 0; i < 2; ++i) {
+        const QMat& q = w[i < mats ? i : 0];
+        pp.scales[i] = reinterpret_cast<const uint16_t*>(q.scales);
+        pp.biases[i] = reinterpret_cast<const uint16_t*>(q.biases);
+    }
+    pp.out = reinterpret_cast<uint32_t*>(packed);
+    pp.N = (int)N;
+    pp.K = (int)K;
+    pp.gs_shift = group_size == 32 ? 5 : group_size == 64 ? 6 : 7;
+    pp.interleave = EPI == kEpiGlu;
+    pp.cols = (int)sp.cols;
+    pp.pack_rows = sp.rows;
+    pp.pack_mat = sp.mat;
+    const dim3 pgrid((unsigned)((sp.rows / (EPI == kEpiGlu ? 2 : 1) + 31) / 32), (unsigned)((sp.cols + 2047) / 2048),
+                     (unsigned)mats);
+    bq_status s = launch_pdl_dim(scale_pack_kernel<MODE == kModeQ4_0, MN>, pgrid, 256, 0, st, pp);
+    if (s != BQ_OK) return s;
+    p.scales = pp.out;
+    p.pack_rows = sp.rows;
+    p.pack_mat = sp.mat;
+    p.q.e = e;
+    p.q.M = (int)M;
+    p.q.N = (int)outs;
+    p.q.bn = pl.bn;
+    p.q.stages = pl.stages;
+    p.q.m_tiles = (int)((M + pl.bn - 1) / pl.bn);
+    p.q.tiles = (int)pl.tiles;
+    p.q.seg_blocks = (int)((red + 63) / 64);
+    p.q.segs = MN ? mats : 1;
+    p.q.dp_tiles = (int)pl.dp_tiles;
+    p.q.splits = pl.splits;
+    p.q.ws = reinterpret_cast<float*>(ws);
+    const int64_t units = pl.dp_tiles + (pl.tiles - pl.dp_tiles) * pl.splits;
+    const unsigned grid = 2u * (unsigned)std::min<int64_t>(units, di.num_sms / 2);
+    const size_t smem = std::max<size_t>(1024 + fp_fixed_bytes(MODE) + (size_t)pl.stages * (size_t)pl.bn * 64u + 512,
+                                         (size_t)di.max_smem_optin / 2 + 1024);   // one CTA per SM (all of TMEM)
+    s = launch_pdl_dim(kern, dim3(grid), kFpThreads, smem, st, ta[0], ta[1], tb[0], tb[1], p);
+    if (s != BQ_OK || pl.splits == 1) return s;
+    const int64_t split_tiles = pl.tiles - pl.dp_tiles;
+    epi_reduce_kernel<EPI><<<reduce_grid(split_tiles * pl.bn * epi_tile_rows<EPI>(256) / 4, di), 256, 0, st>>>(
+        p.q.ws, e, (int)M, (int)outs, pl.bn, 256, p.q.m_tiles, p.q.dp_tiles, (int)split_tiles, pl.splits);
+    return launch_status();
+}
+
+template <bool MN, int EPI>
+bq_status launch_fused_pair_fmt(WFmt fmt, const DeviceInfo& di, int dev, const PairPlan& pl, const QMat* w, int mats,
+                                const uint16_t* const* B, int64_t N, int64_t K, int64_t M, int64_t b_pitch,
+                                int group_size, const EpiParams& e, void* packed, void* ws, cudaStream_t st)
+{
+    if (fmt == WFmt::Q4_0)
+        return launch_fused_pair<kModeQ4_0, MN, EPI>(di, dev, pl, w, mats, B, N, K, M, b_pitch, group_size, e, packed,
+                                                         ws, st);
+    if (fmt == WFmt::AFF4)
+        return launch_fused_pair<kModeAff4, MN, EPI>(di, dev, pl, w, mats, B, N, K, M, b_pitch, group_size, e, packed,
+                                                         ws, st);
+    return launch_fused_pair<kModeAff8, MN, EPI>(di, dev, pl, w, mats, B, N, K, M, b_pitch, group_size, e, packed,
+                                                         ws, st);
+}
+
 // ------------------------------------------------------------------ layouts of the workspaces
-// Forward: the bf16 weights (glu: interleaved, in whole blocks of 16 rows), then the
-// partial sums of the split tiles.  Gradient: the bf16 weights, padded copies of the
+// Forward: the packed scales or the bf16 weights (glu: interleaved, in whole blocks of
+// 16 rows), then the partial sums of the split tiles.  Gradient: the same, then padded copies of the
 // gradients when N is not a multiple of 8 (their rows must start on 16 bytes), the
 // biases' partial sums, the product's partial sums.
 struct EpiWs {
+    bool fused = false;             // codes dequantized inside the product: no bf16 weights
     PairPlan pl;
     int64_t rows = 0;               // D rows of the product
-    size_t off_pad = 0, off_part = 0, off_split = 0, bytes = 0;
+    size_t off_pad = 0, off_part = 0, off_split = 0, bytes = 0;   // the bf16 weights or packed scales are at 0
     int64_t pitch = 0;              // elements per row of the product's token operand
     int row_blocks = 0, rows_per_block = 0;
 };
 
-bool plan_forward(int mats, int64_t M, int64_t N, int64_t K, int num_sms, int smem_optin, EpiWs* w)
+// Q4_0 and affine 4- and 8-bit codes are dequantized inside the product; the others
+// (whose rows of a stage are not 16-byte multiples) through a bf16 copy.
+bool plan_epi_product(WFmt fmt, int64_t rows, int64_t M, int64_t nk, int num_sms, int smem_optin, EpiWs* w)
 {
-    w->rows = mats == 2 ? 32 * ((N + 15) / 16) : N;
-    if (!plan_pair(w->rows, M, (K + 63) / 64, num_sms, smem_optin, &w->pl)) return false;
-    w->off_split = up256((size_t)w->rows * (size_t)K * 2u);
+    w->rows = rows;
+    w->fused = has_fast_paths(fmt);
+    return w->fused ? plan_pair(rows, M, nk, num_sms, smem_optin, (int)fp_fixed_bytes(fp_mode(fmt)), 0, 450.0,
+                                &w->pl)
+                    : plan_pair(rows, M, nk, num_sms, smem_optin, 0, (int)kPairABytes, 300.0, &w->pl);
+}
+
+bool plan_forward(WFmt fmt, int mats, int64_t M, int64_t N, int64_t K, int num_sms, int smem_optin, EpiWs* w)
+{
+    // glu: tiles of 32 rows per 16 outputs
+    if (!plan_epi_product(fmt, mats == 2 ? 32 * ((N + 15) / 16) : N, M, (K + 63) / 64, num_sms, smem_optin, w)) return false;
+    w->off_split = w->fused ? scale_pack(false, mats, N, K).bytes : up256((size_t)w->rows * (size_t)K * 2u);
     w->bytes = w->off_split + w->pl.ws_bytes;
     return true;
 }
 
-bool plan_backward(int mats, int64_t M, int64_t N, int64_t K, int num_sms, int smem_optin, EpiWs* w)
+bool plan_backward(WFmt fmt, int mats, int64_t M, int64_t N, int64_t K, int num_sms, int smem_optin, EpiWs* w)
 {
-    w->rows = K;
-    if (K > 0 && N > 0 && !plan_pair(K, M, mats * ((N + 63) / 64), num_sms, smem_optin, &w->pl)) return false;
+    if (K > 0 && !plan_epi_product(fmt, K, M, mats * ((N + 63) / 64), num_sms, smem_optin, w)) return false;
     w->pitch = (N + 7) / 8 * 8;
     // blocks of 8 warps over rows of tokens: about 8 blocks per SM, at least 32 rows each
     const int64_t cols = std::max<int64_t>(1, (N + 255) / 256);
@@ -280,7 +433,7 @@ bool plan_backward(int mats, int64_t M, int64_t N, int64_t K, int num_sms, int s
     const int64_t rpb = std::max<int64_t>(32, ((M + want - 1) / want + 7) / 8 * 8);
     w->rows_per_block = (int)rpb;
     w->row_blocks = (int)((M + rpb - 1) / rpb);
-    size_t off = up256((size_t)mats * (size_t)N * (size_t)K * 2u);
+    size_t off = w->fused ? scale_pack(true, mats, N, K).bytes : up256((size_t)mats * (size_t)N * (size_t)K * 2u);
     w->off_pad = off;
     if (N % 8 != 0) off += (size_t)mats * up256((size_t)M * (size_t)w->pitch * 2u);
     w->off_part = off;
@@ -344,9 +497,12 @@ bq_status epi_forward(const uint16_t* x, const QMat* w, const EpiParams& e, int6
     }
     if (ring_applies(fmt, M, K)) return launch_ring<EPI>(fmt, x, w, e, M, N, K, group_size, di, dev, st);
     EpiWs ws;
-    if (!plan_forward(mats, M, N, K, di.num_sms, di.max_smem_optin, &ws)) return BQ_ERR_UNSUPPORTED;
+    if (!plan_forward(fmt, mats, M, N, K, di.num_sms, di.max_smem_optin, &ws)) return BQ_ERR_UNSUPPORTED;
     void* buf = nullptr;
     if ((s = epi_workspace(dev, st, workspace, workspace_bytes, ws.bytes, &buf)) != BQ_OK) return s;
+    if (ws.fused)
+        return launch_fused_pair_fmt<false, EPI>(fmt, di, dev, ws.pl, w, mats, &x, N, K, M, K, group_size, e, buf,
+                                                 reinterpret_cast<uint8_t*>(buf) + ws.off_split, st);
     uint16_t* wb = reinterpret_cast<uint16_t*>(buf);
     if ((s = dequant_rows(fmt, w, mats, wb, N, K, group_size, mats == 2, di, st)) != BQ_OK) return s;
     return launch_pair<false, EPI>(di, dev, ws.pl, &wb, &x, 1, ws.rows, N, M, K, K, e,
@@ -414,7 +570,7 @@ bq_status epi_backward(const EpiBackward& b, const QMat* w, int act, int64_t M, 
     if (N == 0)                                          // a sum over no outputs
         return cudaMemsetAsync(b.dx, 0, (size_t)M * (size_t)K * 2u, st) == cudaSuccess ? BQ_OK : BQ_ERR_CUDA;
     EpiWs ws;
-    if (!plan_backward(mats, M, N, K, di.num_sms, di.max_smem_optin, &ws)) return BQ_ERR_UNSUPPORTED;
+    if (!plan_backward(fmt, mats, M, N, K, di.num_sms, di.max_smem_optin, &ws)) return BQ_ERR_UNSUPPORTED;
     if (ws.row_blocks > 65535) return BQ_ERR_SHAPE;
     void* buf = nullptr;
     if ((s = epi_workspace(dev, st, workspace, workspace_bytes, ws.bytes, &buf)) != BQ_OK) return s;
@@ -445,12 +601,15 @@ bq_status epi_backward(const EpiBackward& b, const QMat* w, int act, int64_t M, 
         }
     }
     if (K == 0) return BQ_OK;
-    uint16_t* wb = reinterpret_cast<uint16_t*>(base);
-    if ((s = dequant_rows(fmt, w, mats, wb, N, K, group_size, false, di, st)) != BQ_OK) return s;
-    const uint16_t* A[2] = {wb, wb + (size_t)N * (size_t)K};
     const uint16_t* B[2] = {pad ? padded[0] : none ? b.dy : b.d[0], pad ? padded[1] : b.d[1]};
     EpiParams e;
     e.y = b.dx;
+    if (ws.fused)
+        return launch_fused_pair_fmt<true, kEpiPlain>(fmt, di, dev, ws.pl, w, mats, B, N, K, M, pad ? ws.pitch : N,
+                                                      group_size, e, base, base + ws.off_split, st);
+    uint16_t* wb = reinterpret_cast<uint16_t*>(base);
+    if ((s = dequant_rows(fmt, w, mats, wb, N, K, group_size, false, di, st)) != BQ_OK) return s;
+    const uint16_t* A[2] = {wb, wb + (size_t)N * (size_t)K};
     return launch_pair<true, kEpiPlain>(di, dev, ws.pl, A, B, mats, K, K, M, N, pad ? ws.pitch : N, e,
                                         base + ws.off_split, st);
 }

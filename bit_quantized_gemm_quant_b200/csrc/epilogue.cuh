@@ -168,62 +168,75 @@ BQ_DEVINL EpiRow<EPI> epi_row(const EpiParams& e, int n, int N)
     return r;
 }
 
-// 16 tokens (mb .. mb + 15) of one tile row from a tensor-memory load.  The whole
-// warp calls it: with glu, lanes l and l + 16 hold the gate and the up sum of one
-// output and trade every second token by one shuffle, so that each lane ends with
-// both sums of 8 outputs.
-template <int EPI>
-BQ_DEVINL void epi_store16(const EpiParams& e, const EpiRow<EPI>& r, const uint32_t (&v)[16], int mb, int M, int64_t N)
+// 8 tokens (mb .. mb + 7) of one tile row from a tensor-memory load, v[O .. O + 7].  The
+// whole warp calls it: with glu, lanes l and l + 16 hold the gate and the up sum of one
+// output and trade every second token by one shuffle, so that each lane ends with both
+// sums of 4 outputs.
+template <int EPI, int O>
+BQ_DEVINL void epi_store8(const EpiParams& e, const EpiRow<EPI>& r, const uint32_t (&v)[16], int mb, int M, int64_t N)
 {
     if constexpr (EPI == kEpiGlu) {
         const int up = (threadIdx.x >> 4) & 1;
-        float g[8], u[8];
+        float g[4], u[4];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const uint32_t mine = up ? v[2 * j + 1] : v[2 * j];
-            const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? v[2 * j] : v[2 * j + 1], 16);
+        for (int j = 0; j < 4; ++j) {
+            const uint32_t mine = up ? v[O + 2 * j + 1] : v[O + 2 * j];
+            const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? v[O + 2 * j] : v[O + 2 * j + 1], 16);
             g[j] = __uint_as_float(up ? got : mine) + r.b;
             u[j] = __uint_as_float(up ? mine : got) + r.b2;
         }
         if (!r.ok) return;
-        const int64_t o = (int64_t)(mb + up) * N + r.n;
+        const int m = mb + up;
+        int64_t o = (int64_t)m * N + r.n;
         if (e.pre) {
+            int64_t q = o;
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (mb + up + 2 * j < M) {
-                    e.pre[o + 2 * j * N] = (uint16_t)f32_to_bf16_bits(g[j]);
-                    e.pre2[o + 2 * j * N] = (uint16_t)f32_to_bf16_bits(u[j]);
+            for (int j = 0; j < 4; ++j, q += 2 * N)
+                if (m + 2 * j < M) {
+                    e.pre[q] = (uint16_t)f32_to_bf16_bits(g[j]);
+                    e.pre2[q] = (uint16_t)f32_to_bf16_bits(u[j]);
                 }
         }
-        act_n<8>(g, e.act);
+        act_n<4>(g, e.act);
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            if (mb + up + 2 * j < M) e.y[o + 2 * j * N] = (uint16_t)f32_to_bf16_bits(g[j] * u[j]);
+        for (int j = 0; j < 4; ++j, o += 2 * N)
+            if (m + 2 * j < M) e.y[o] = (uint16_t)f32_to_bf16_bits(g[j] * u[j]);
     } else {
         if (!r.ok) return;
-        const int64_t o = (int64_t)mb * N + r.n;
-        float z[16];
+        int64_t o = (int64_t)mb * N + r.n;
+        float z[8];
 #pragma unroll
-        for (int j = 0; j < 16; ++j) z[j] = __uint_as_float(v[j]) + r.b;
+        for (int j = 0; j < 8; ++j) z[j] = __uint_as_float(v[O + j]) + r.b;
         if constexpr (EPI == kEpiAct) {
-            if (e.pre) {
-#pragma unroll
-                for (int j = 0; j < 16; ++j)
-                    if (mb + j < M) e.pre[o + j * N] = (uint16_t)f32_to_bf16_bits(z[j]);
-            }
-            act_n<16>(z, e.act);
+            uint32_t q[8];
             if (e.res) {
-                uint16_t q[16];
+                int64_t i = o;
 #pragma unroll
-                for (int j = 0; j < 16; ++j) q[j] = mb + j < M ? e.res[o + j * N] : 0;
+                for (int j = 0; j < 8; ++j, i += N) q[j] = mb + j < M ? e.res[i] : 0u;
+            }
+            if (e.pre) {
+                int64_t i = o;
 #pragma unroll
-                for (int j = 0; j < 16; ++j) z[j] += bf16_bits_to_f32(q[j]);
+                for (int j = 0; j < 8; ++j, i += N)
+                    if (mb + j < M) e.pre[i] = (uint16_t)f32_to_bf16_bits(z[j]);
+            }
+            act_n<8>(z, e.act);
+            if (e.res) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) z[j] += bf16_bits_to_f32(q[j]);
             }
         }
 #pragma unroll
-        for (int j = 0; j < 16; ++j)
-            if (mb + j < M) e.y[o + j * N] = (uint16_t)f32_to_bf16_bits(z[j]);
+        for (int j = 0; j < 8; ++j, o += N)
+            if (mb + j < M) e.y[o] = (uint16_t)f32_to_bf16_bits(z[j]);
     }
+}
+
+template <int EPI>
+BQ_DEVINL void epi_store16(const EpiParams& e, const EpiRow<EPI>& r, const uint32_t (&v)[16], int mb, int M, int64_t N)
+{
+    epi_store8<EPI, 0>(e, r, v, mb, M, N);
+    epi_store8<EPI, 8>(e, r, v, mb + 8, M, N);
 }
 
 // Sums the partial tiles of a K-split product in split order and applies the

@@ -1,0 +1,407 @@
+// tc_fused_pair.cuh -- prompt and training sizes of the products with an epilogue: the
+// packed weights are dequantized inside the tensor-core product, on pairs of SMs.
+//
+//   forward:   D[n][m] = sum_k W[n][k] x[m][k]       (weight tile K-major)
+//   gradient:  D[k][m] = sum_n W[n][k] dz[m][n]      (weight tile MN-major; up to two
+//              matrices summed, for the gated form)
+//
+// Tiles, pairs, accumulators and units of work are tc_pair.cuh's: 256 D rows x bn
+// tokens per pair (cta_group::2), two accumulators of 256 columns.  Here the weight
+// tile of a stage arrives as codes: 128 x 64 weights per CTA are 4 KB (8-bit: 8 KB)
+// where their bf16 form is 16 KB, so a stage moves 20 KB per SM through L2 instead of
+// 32, and no bf16 copy of W is written to or read from memory.  16 dequant warps, four
+// groups of four that take blocks in turn, expand them to bf16 in a shared-memory tile
+// in the layout that the MMA reads: 64 weights of one row per thread, either 64
+// consecutive k of an output row (forward) or 64 consecutive outputs of a reduction row
+// (gradient).  The codes land swizzled, so that both the code reads
+// and the tile writes of a warp cover all banks evenly.
+//
+// Three rings run at their own depth: codes (small, freed as soon as a dequant group has
+// read them), token tiles, and expanded weight tiles.  With codes, tokens and tile in
+// one stage a block took 1350 clocks, with codes and tokens in one stage and four tiles
+// 1130: a tile slot or stage was then held through a copy's round trip, the wait for a
+// group and the product, longer than the ring covers at the MMA's 512 clocks a block.
+// Barriers: cfull / cempty (codes, each CTA's own), bfull (tokens of both CTAs, the
+// leader's), ready (a tile, the leader's; 4 dequant warps of each CTA arrive), consumed
+// (one per block, each CTA's own; the MMA's commit arrives on both and thereby frees the
+// block's token tile and weight tile).
+//
+// Scales: a thread needs two of one row, and rows are far apart in memory; loaded by the
+// threads themselves they took longer than the rest of the dequantization (every load
+// touches 32 lines: 318 us without the MMA, 198 without the loads, gated gradient of
+// 12288 x 4096 at 2048 tokens).  So scale_pack_kernel first lays them out by block, the 1
+// KB of a block contiguous (32 weights: one word of two 16-bit values, a scale and a bias
+// or Q4_0's d split in two), and they come with the codes.
+#pragma once
+
+#include "tc_gemm.cuh"
+#include "tc_pair.cuh"
+
+namespace bq {
+
+constexpr int kFpDeqWarps = 16;                 // four groups of 4
+constexpr int kFpEpiWarp0 = kFpDeqWarps;        // 4 warps: lane quarter = warp % 4
+constexpr int kFpTokWarp = kFpEpiWarp0 + 4;     // producer of token tiles
+constexpr int kFpCodeWarp = kFpTokWarp + 1;     // producer of codes
+constexpr int kFpMmaWarp = kFpCodeWarp + 1;
+constexpr int kFpThreads = 32 * (kFpMmaWarp + 1);
+constexpr uint32_t kFpScaleBytes = 1024;        // packed scales of a stage
+constexpr int kFpTiles = 6;                     // bf16 weight tiles
+constexpr int kFpMaxCodes = 8;
+constexpr int kFpConsumed = 16;                 // consumed barriers, at least the depth of each ring
+constexpr int kFpMaxTok = 8;                    // token tiles
+
+__host__ __device__ constexpr uint32_t fp_code_bytes(int mode) { return mode == kModeAff8 ? 8192u : 4096u; }
+__host__ __device__ constexpr int fp_codes(int mode) { return mode == kModeAff8 ? 6 : 8; }   // code stages
+// Shared memory beside the token tiles
+__host__ __device__ constexpr uint32_t fp_fixed_bytes(int mode)
+{
+    return kFpTiles * kPairABytes + (uint32_t)fp_codes(mode) * (fp_code_bytes(mode) + kFpScaleBytes);
+}
+
+struct FpParams {
+    PairParams q;
+    const uint32_t* scales;        // packed (scale_pack_kernel)
+    int64_t pack_rows;             // its rows per column block
+    int64_t pack_mat;              // gradient: its words per matrix
+};
+
+// Packed scales: words of 32 weights, forward [column block of 64][tile row][2] with tile
+// rows as the product numbers them (glu: interleaved, see epi_out_row), gradient [matrix]
+// [column block of 128][row][4]; rows and columns are padded to whole tiles with weights
+// of 0.  A word holds scale and bias (bf16), or Q4_0's d as d_hi + d_lo (see gemv.cuh).
+// A block takes 32 rows x 2048 columns through shared memory: reads run along the rows
+// of the scales, writes along the rows of the result.
+struct ScalePackParams {
+    const uint16_t* scales[2];
+    const uint16_t* biases[2];
+    uint32_t* out;
+    int N, K, gs_shift, interleave;
+    int cols;                      // padded columns
+    int64_t pack_rows, pack_mat;
+};
+
+template <bool Q4, bool MN>
+__global__ void __launch_bounds__(256) scale_pack_kernel(const __grid_constant__ ScalePackParams p)
+{
+    __shared__ uint32_t sm[32][65];
+    grid_dependency_wait();
+    grid_dependents_launch();
+    const int mat = blockIdx.z, n0 = blockIdx.x * 32, k0 = blockIdx.y * 2048;
+    const int per_row = p.K >> p.gs_shift;
+    const uint16_t* sc = mat ? p.scales[1] : p.scales[0];
+    const uint16_t* bi = mat ? p.biases[1] : p.biases[0];
+    for (int i = threadIdx.x; i < 32 * 64; i += 256) {
+        const int r = i >> 6, h = i & 63, n = n0 + r, k = k0 + 32 * h;
+        uint32_t v = 0u;
+        if (n < p.N && k < p.K) {
+            const int64_t g = (int64_t)n * per_row + (k >> p.gs_shift);
+            if constexpr (Q4) {
+                const float d = f16_bits_to_f32(__ldg(sc + g));
+                const uint32_t hi = f32_to_bf16_bits(d);
+                v = hi | f32_to_bf16_bits(__fsub_rn(d, bf16_bits_to_f32(hi))) << 16;
+            } else {
+                v = (uint32_t)__ldg(sc + g) | (uint32_t)__ldg(bi + g) << 16;
+            }
+        }
+        sm[r][h] = v;
+    }
+    __syncthreads();
+    constexpr int W = MN ? 4 : 2;                       // words per output row
+    for (int i = threadIdx.x; i < 32 * (64 / W); i += 256) {
+        const int r = i & 31, c = i >> 5, n = n0 + r;
+        const int64_t blk = k0 / (32 * W) + c;
+        if (blk * (32 * W) >= p.cols) continue;
+        const int64_t row = p.interleave ? 32 * (int64_t)(n >> 4) + (n & 15) + 16 * mat : n;
+        if (row >= p.pack_rows) continue;
+        uint32_t* o = p.out + (MN ? mat * p.pack_mat : 0) + (blk * p.pack_rows + row) * W;
+        if constexpr (MN)
+            *reinterpret_cast<uint4*>(o) = make_uint4(sm[r][4 * c], sm[r][4 * c + 1], sm[r][4 * c + 2], sm[r][4 * c + 3]);
+        else
+            *reinterpret_cast<uint2*>(o) = make_uint2(sm[r][2 * c], sm[r][2 * c + 1]);
+    }
+}
+
+// tm_a0, tm_a1: codes of matrix 0 and 1 as bytes.  Forward: boxes of one stage's 64
+// columns x 128 rows (glu: 64 rows of gate and of up); gradient: 128 columns x 64 rows.
+// tm_b0, tm_b1: tokens, boxes of 64 elements x bn / 2 tokens.
+template <int MODE, bool MN, int EPI>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFpThreads, 1)
+tc_fused_pair_kernel(const __grid_constant__ CUtensorMap tm_a0, const __grid_constant__ CUtensorMap tm_a1,
+                     const __grid_constant__ CUtensorMap tm_b0, const __grid_constant__ CUtensorMap tm_b1,
+                     const __grid_constant__ FpParams fp)
+{
+    constexpr uint32_t kCBytes = fp_code_bytes(MODE), kCStage = kCBytes + kFpScaleBytes;
+    constexpr int kFpCodes = fp_codes(MODE);
+    constexpr int kBits = MODE == kModeAff8 ? 8 : 4;
+    const PairParams& p = fp.q;
+    extern __shared__ uint8_t smem_raw[];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_ctarank();
+    const int NB = p.stages;                       // token tiles in the ring
+    const int nk = p.seg_blocks * p.segs;
+    const uint32_t b_bytes = (uint32_t)p.bn * 64u;
+    const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+    const uint32_t a_base = base, c_base = a_base + kFpTiles * kPairABytes, b_base = c_base + kFpCodes * kCStage;
+    const uint32_t bar_base = b_base + (uint32_t)NB * b_bytes;
+    auto cfull_bar = [&](int i) { return bar_base + 8u * (uint32_t)i; };
+    auto cempty_bar = [&](int i) { return bar_base + 8u * (uint32_t)(kFpCodes + i); };
+    auto ready_bar = [&](int i) { return bar_base + 8u * (uint32_t)(2 * kFpCodes + i); };
+    auto bfull_bar = [&](int i) { return bar_base + 8u * (uint32_t)(2 * kFpCodes + kFpTiles + i); };
+    auto consumed_bar = [&](int i) { return bar_base + 8u * (uint32_t)(2 * kFpCodes + kFpTiles + kFpMaxTok + i); };
+    constexpr int kBars = 2 * kFpCodes + kFpTiles + kFpMaxTok + kFpConsumed;
+    auto tfull_bar = [&](int b) { return bar_base + 8u * (uint32_t)(kBars + b); };
+    auto tempty_bar = [&](int b) { return bar_base + 8u * (uint32_t)(kBars + 2 + b); };
+    const uint32_t done_bar = bar_base + 8u * (uint32_t)(kBars + 4);
+    const uint32_t tmem_slot = done_bar + 8u;
+    static_assert(8 * (kBars + 6) <= 512, "barriers fit the space the host reserves");
+    volatile uint32_t* tmem_slot_ptr =
+        reinterpret_cast<volatile uint32_t*>(smem_raw + (base - smem_u32(smem_raw)) + (tmem_slot - base));
+    // wait until the block at position pos (>= 0) is consumed
+    auto wait_consumed = [&](int pos) {
+        return mbar_wait(consumed_bar(pos & (kFpConsumed - 1)), (uint32_t)(pos / kFpConsumed) & 1u);
+    };
+
+    const int units = p.dp_tiles + (p.tiles - p.dp_tiles) * p.splits;
+    const int first = blockIdx.x >> 1, stride = gridDim.x >> 1;
+    auto unit_tile = [&](int u) { return u < p.dp_tiles ? u : p.dp_tiles + (u - p.dp_tiles) / p.splits; };
+    auto unit_split = [&](int u) { return u < p.dp_tiles ? 0 : (u - p.dp_tiles) % p.splits; };
+    auto kb_begin = [&](int u) { return u < p.dp_tiles ? 0 : (int)((int64_t)unit_split(u) * nk / p.splits); };
+    auto kb_end = [&](int u) { return u < p.dp_tiles ? nk : (int)((int64_t)(unit_split(u) + 1) * nk / p.splits); };
+    auto tile_r0 = [&](int t) { return (t / p.m_tiles) * 256 + (int)rank * 128; };
+    auto tile_m0 = [&](int t) { return (t % p.m_tiles) * p.bn; };
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kFpCodes; ++i) {
+            mbar_init(cfull_bar(i), 1);
+            mbar_init(cempty_bar(i), 4);
+        }
+        for (int i = 0; i < kFpTiles; ++i) mbar_init(ready_bar(i), 8);
+        for (int i = 0; i < NB; ++i) mbar_init(bfull_bar(i), 1);
+        for (int i = 0; i < kFpConsumed; ++i) mbar_init(consumed_bar(i), 1);
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(tfull_bar(b), 1);
+            mbar_init(tempty_bar(b), 8);
+        }
+        mbar_init(done_bar, 1);
+        fence_barrier_init();
+        fence_proxy_async_smem();
+    }
+    if (warp == kFpMmaWarp) {
+        tmem_alloc_pair(tmem_slot, 2 * kPairAccCols);
+        tmem_relinquish_pair();
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync_all();
+    tc_fence_after();
+    const uint32_t tmem_base = *tmem_slot_ptr;
+    grid_dependency_wait();
+    grid_dependents_launch();
+
+    if (warp == kFpTokWarp) {
+        // ---------------- token tiles (each CTA: its own half) ----------------
+        if (lane == 0) {
+            int b = 0, pos = 0;
+            bool ok = true;
+            for (int u = first; u < units && ok; u += stride) {
+                const int m0 = tile_m0(unit_tile(u)) + (int)rank * (p.bn / 2);
+                const int kb1 = kb_end(u);
+                for (int it = kb_begin(u); it < kb1; ++it, ++pos) {
+                    if (pos >= NB && !wait_consumed(pos - NB)) { ok = false; break; }
+                    const bool second = it >= p.seg_blocks;
+                    if (rank == 0) mbar_arrive_expect_tx(bfull_bar(b), 2u * b_bytes);
+                    tma_load_2d_pair(b_base + (uint32_t)b * b_bytes, second ? &tm_b1 : &tm_b0, map_to_cta(bfull_bar(b), 0),
+                                     (second ? it - p.seg_blocks : it) * 64, m0);
+                    if (++b == NB) b = 0;
+                }
+            }
+            // Leave only when the last blocks are consumed: every copy of the pair has then
+            // landed and every arrival on this CTA's barriers has been made.  (After a
+            // timeout the leader still waits for the copies.)
+            for (int q = max(pos - NB, 0); q < pos; ++q) {
+                if (rank == 0 && !mbar_wait(bfull_bar(q % NB), (uint32_t)(q / NB) & 1u)) ok = false;
+                if (ok) ok = wait_consumed(q);
+            }
+        }
+        __syncwarp();
+    } else if (warp == kFpCodeWarp) {
+        // ---------------- codes (each CTA: its own rows) ----------------
+        if (lane == 0) {
+            int c = 0, issued = 0;
+            uint32_t ph = 0;
+            bool ok = true;
+            for (int u = first; u < units && ok; u += stride) {
+                const int r0 = tile_r0(unit_tile(u));
+                const int kb1 = kb_end(u);
+                for (int it = kb_begin(u); it < kb1; ++it, ++issued) {
+                    if (!mbar_wait(cempty_bar(c), ph ^ 1u)) { ok = false; break; }
+                    const uint32_t dst = c_base + (uint32_t)c * kCStage;
+                    mbar_arrive_expect_tx(cfull_bar(c), kCStage);
+                    const bool second = MN && it >= p.seg_blocks;
+                    const int kb = second ? it - p.seg_blocks : it;
+                    bulk_load(dst + kCBytes,
+                              fp.scales + (MN ? (second ? fp.pack_mat : 0) + ((int64_t)(r0 / 128) * fp.pack_rows + kb * 64) * 4
+                                              : ((int64_t)kb * fp.pack_rows + r0) * 2),
+                              kFpScaleBytes, cfull_bar(c));
+                    if constexpr (MN) {
+                        tma_load_2d(dst, second ? &tm_a1 : &tm_a0, cfull_bar(c), r0 * kBits / 8, kb * 64);
+                    } else if constexpr (EPI == kEpiGlu) {
+                        tma_load_2d(dst, &tm_a0, cfull_bar(c), it * (64 * kBits / 8), r0 / 2);
+                        tma_load_2d(dst + kCBytes / 2, &tm_a1, cfull_bar(c), it * (64 * kBits / 8), r0 / 2);
+                    } else {
+                        tma_load_2d(dst, &tm_a0, cfull_bar(c), it * (64 * kBits / 8), r0);
+                    }
+                    if (++c == kFpCodes) { c = 0; ph ^= 1u; }
+                }
+            }
+            for (int q = 0; q < kFpCodes && q < issued; ++q) {      // every copy has landed
+                if (--c < 0) { c = kFpCodes - 1; ph ^= 1u; }
+                mbar_wait(cfull_bar(c), ph);
+            }
+        }
+        __syncwarp();
+    } else if (warp == kFpMmaWarp) {
+        // ---------------- MMA issuer (one lane of the leader) ----------------
+        if (rank == 0 && lane == 0) {
+            const uint32_t idesc = umma_idesc_bf16_f32(256, p.bn) | (MN ? 1u << 15 : 0u);
+            const uint64_t bd0 = umma_desc_k_sw128(b_base);
+            const uint32_t desc_hi = (uint32_t)(bd0 >> 32);
+            const uint32_t a_lo0 = MN ? (((a_base >> 4) & 0x3FFFu) | ((kPairABytes / 2) >> 4 << 16))   // as in tc_pair.cuh
+                                      : (uint32_t)umma_desc_k_sw128(a_base);
+            const uint32_t b_lo0 = (uint32_t)bd0, b_step = b_bytes >> 4;
+            uint32_t a_lo = a_lo0, b_lo = b_lo0;
+            int a = 0, b = 0, c = 0, lt = 0;
+            uint32_t pha = 0, phb = 0;
+            bool ok = true;
+            for (int u = first; u < units && ok; u += stride, ++lt) {
+                const int acc = lt & 1;
+                const int kb0 = kb_begin(u), kb1 = kb_end(u);
+                if (!mbar_wait(tempty_bar(acc), ((uint32_t)(lt >> 1) & 1u) ^ 1u)) break;
+                tc_fence_after();
+                const uint32_t d_tmem = tmem_base + (uint32_t)(acc * kPairAccCols);
+                uint32_t accumulate = 0;
+                for (int it = kb0; it < kb1; ++it) {
+                    if (!mbar_wait(bfull_bar(b), phb) || !mbar_wait(ready_bar(a), pha)) { ok = false; break; }
+                    tc_fence_after();
+                    umma_kblock_pair<MN ? 128 : 2>(d_tmem, a_lo, b_lo, desc_hi, idesc, accumulate);
+                    accumulate = 1;
+                    umma_commit_pair(consumed_bar(c));
+                    c = (c + 1) & (kFpConsumed - 1);
+                    a_lo += kPairABytes >> 4;
+                    b_lo += b_step;
+                    if (++b == NB) { b = 0; phb ^= 1u; b_lo = b_lo0; }
+                    if (++a == kFpTiles) { a = 0; pha ^= 1u; a_lo = a_lo0; }
+                }
+                umma_commit_pair(tfull_bar(acc));
+            }
+            umma_commit_leader(done_bar);   // nothing stays in flight past this point
+            mbar_wait(done_bar, 0);
+        }
+        __syncwarp();
+    } else if (warp >= kFpEpiWarp0) {
+        // ---------------- epilogue ----------------
+        const int q4 = warp & 3;
+        const uint32_t lane_addr0 = tmem_base + ((uint32_t)(32 * q4) << 16);
+        int lt = 0;
+        for (int u = first; u < units; u += stride, ++lt) {
+            const int t = unit_tile(u), acc = lt & 1;
+            const int r = 32 * q4 + lane;
+            const int m0 = tile_m0(t);
+            const bool split = p.splits > 1 && u >= p.dp_tiles;
+            const EpiRow<EPI> row = epi_row<EPI>(p.e, epi_tile_rows<EPI>(tile_r0(t)) + epi_out_row<EPI>(r), p.N);
+            if (!mbar_wait_warp(tfull_bar(acc), (uint32_t)(lt >> 1) & 1u)) break;
+            tc_fence_after();
+            const uint32_t lane_addr = lane_addr0 + (uint32_t)(acc * kPairAccCols);
+            if (split) {
+                float* pt = p.ws + ((int64_t)unit_split(u) * (p.tiles - p.dp_tiles) + (t - p.dp_tiles)) *
+                                       ((int64_t)p.bn * 256) + (int)rank * 128 + r;
+                for (int c = 0; c < p.bn; c += 16, pt += 16 * 256) {
+                    uint32_t v[16];
+                    tmem_ld_32x32b_x16(lane_addr + (uint32_t)c, v);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) pt[j * 256] = __uint_as_float(v[j]);
+                }
+            } else {
+                for (int c = 0; c < p.bn && m0 + c < p.M; c += 16) {
+                    uint32_t v[16];
+                    tmem_ld_32x32b_x16(lane_addr + (uint32_t)c, v);
+                    tmem_wait_ld();
+                    epi_store16<EPI>(p.e, row, v, m0 + c, p.M, p.N);
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(map_to_cta(tempty_bar(acc), 0));
+        }
+    } else {
+        // ---------------- dequantization ----------------
+        // Group grp (4 warps) takes the blocks at positions grp, grp + 4, ... of this
+        // CTA's sequence.  A thread expands 64 weights: forward, row r of
+        // the tile; gradient, row r of the block, outputs 64 hk .. of the tile.
+        const int grp = warp >> 2, w4 = warp & 3;
+        const int r = MN ? 32 * (w4 & 1) + lane : 32 * w4 + lane;
+        const int hk = MN ? w4 >> 1 : 0;
+        const bool up = !MN && EPI == kEpiGlu && (lane & 16);
+        const int crow = !MN && EPI == kEpiGlu ? epi_out_row<EPI>(r) + (up ? 64 : 0) : r;      // row among the stage's codes
+        constexpr int kRowBytes = (MN ? 128 : 64) * kBits / 8;                  // of codes: 32, 64 or 128
+        constexpr int kUnits = kBits / 2;                                       // 16-byte units of codes per thread
+        // the units of a row, as the copy swizzles them
+        const int sw = kRowBytes == 32 ? (crow >> 2) & 1 : kRowBytes == 64 ? (crow >> 1) & 3 : crow & 7;
+        const uint32_t code_row = c_base + (uint32_t)(crow * kRowBytes);
+        const uint32_t tile_row = a_base + (uint32_t)(hk * (int)(kPairABytes / 2) + r * 128);
+        const uint32_t ready0 = map_to_cta(ready_bar(0), 0);
+        const uint32_t scale_row = c_base + kCBytes + (uint32_t)(MN ? r * 16 + hk * 8 : r * 8);
+        int left = 0;                                    // blocks of this CTA's sequence
+        for (int u = first; u < units; u += stride) left += kb_end(u) - kb_begin(u);
+        int c = grp, a = grp;                           // code stage and tile slot of this block
+        uint32_t ph = 0;
+        bool ok = true;
+        for (int pos = grp; pos < left; pos += 4) {
+            if (!mbar_wait_warp(cfull_bar(c), ph)) break;
+            const uint32_t codes = code_row + (uint32_t)c * kCStage;
+            const uint2 sc = ld_shared_v2(scale_row + (uint32_t)c * kCStage);
+            uint4 raw[kUnits];
+#pragma unroll
+            for (int i = 0; i < kUnits; ++i) raw[i] = ld_shared_v4(codes + (uint32_t)(((hk * kUnits + i) ^ sw) << 4));
+            __syncwarp();
+            if (lane == 0) mbar_arrive(cempty_bar(c));
+            const uint32_t tile = tile_row + (uint32_t)a * kPairABytes;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                uint32_t wv[16];
+                const uint32_t w = h ? sc.y : sc.x;
+                if constexpr (MODE == kModeQ4_0)
+                    deq_q4_0_half(raw[h], prmt(w, w, 0x1010u), prmt(w, w, 0x3232u), wv);
+                else if constexpr (MODE == kModeAff4)
+                    deq_aff4_half(raw[h], prmt(w, w, 0x1010u), prmt(w, w, 0x3232u), wv);
+                else
+                    deq_aff8_half(raw[2 * h], raw[2 * h + 1], __uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u), wv);
+                if (h == 0 && pos >= kFpTiles) {           // the slot's last block is consumed
+                    ok = wait_consumed(pos - kFpTiles);
+                    __syncwarp();
+                }
+                if (!ok) break;
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    st_shared_v4(tile + (uint32_t)(((4 * h + j) ^ (r & 7)) << 4), wv[4 * j], wv[4 * j + 1],
+                                 wv[4 * j + 2], wv[4 * j + 3]);
+            }
+            if (!ok) break;
+            fence_proxy_async_smem();                    // the MMA reads the tile through the async proxy
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(ready0 + 8u * (uint32_t)a);
+            if ((c += 4) >= kFpCodes) { c -= kFpCodes; ph ^= 1u; }
+            if ((a += 4) >= kFpTiles) a -= kFpTiles;
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync_all();
+    tc_fence_after();
+    if (warp == kFpMmaWarp) tmem_dealloc_pair(tmem_base, 2 * kPairAccCols);
+}
+
+}  // namespace bq

@@ -48,9 +48,10 @@ BQ_DEVINL uint32_t map_to_cta(uint32_t a, uint32_t rank)
     return r;
 }
 
+// Arrive on a barrier of either CTA.
 BQ_DEVINL void mbar_arrive_cluster(uint32_t bar_cluster)
 {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster) : "memory");
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster) : "memory");
 }
 
 // Tiled load into this CTA, completing on a barrier of either CTA of the pair.

@@ -84,8 +84,12 @@ def test_workspace_sizes(L):
         for bad in ((0, 64, 64, 32, 4), (4, 0, 64, 32, 4), (4, 64, 48, 32, 4), (4, 64, 64, 16, 4), (4, 64, 64, 64, 5)):
             assert size(op, *bad) == 0, (op, bad)
     assert size(-1, 4, 64, 64, 32, 4) == size(4, 4, 64, 64, 32, 4) == 0
-    # the gradient's scratch holds at least the bf16 weights
-    assert size(1, 4, 64, 128, 64, 4) >= 64 * 128 * 2 and size(3, 4, 64, 128, 64, 4) >= 2 * 64 * 128 * 2
+    # 2-, 3- and 6-bit weights go through a bf16 copy, gate and up through two
+    for bits in (2, 3, 6):
+        assert size(1, 4, 64, 128, 64, bits) >= 64 * 128 * 2 and size(3, 4, 64, 128, 64, bits) >= 2 * 64 * 128 * 2
+        assert size(0, 40, 64, 128, 64, bits) >= 64 * 128 * 2 and size(2, 40, 64, 128, 64, bits) >= 2 * 64 * 128 * 2
+    # without biases Q4_0 and affine 4-bit in groups of 32 are told apart by nothing: one size
+    assert size(0, 1, 64, 128, 32, 4) == 0
 
 
 def test_binding_refusals():
