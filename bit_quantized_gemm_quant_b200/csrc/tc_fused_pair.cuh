@@ -262,41 +262,42 @@ tc_fused_pair_kernel(const __grid_constant__ CUtensorMap tm_a0, const __grid_con
         }
         __syncwarp();
     } else if (warp == kFpMmaWarp) {
-        // ---------------- MMA issuer (one lane of the leader) ----------------
-        if (rank == 0 && lane == 0) {
+        // ---------------- MMA issuer (the leader's; one elected lane issues) ----------------
+        if (rank == 0) {                                 // the whole warp, as in tc_pair.cuh
             const uint32_t idesc = umma_idesc_bf16_f32(256, p.bn) | (MN ? 1u << 15 : 0u);
             const uint64_t bd0 = umma_desc_k_sw128(b_base);
             const uint32_t desc_hi = (uint32_t)(bd0 >> 32);
             const uint32_t a_lo0 = MN ? (((a_base >> 4) & 0x3FFFu) | ((kPairABytes / 2) >> 4 << 16))   // as in tc_pair.cuh
                                       : (uint32_t)umma_desc_k_sw128(a_base);
-            const uint32_t b_lo0 = (uint32_t)bd0, b_step = b_bytes >> 4;
-            uint32_t a_lo = a_lo0, b_lo = b_lo0;
+            const uint32_t b_lo0 = (uint32_t)bd0;
             int a = 0, b = 0, c = 0, lt = 0;
             uint32_t pha = 0, phb = 0;
             bool ok = true;
             for (int u = first; u < units && ok; u += stride, ++lt) {
                 const int acc = lt & 1;
                 const int kb0 = kb_begin(u), kb1 = kb_end(u);
-                if (!mbar_wait(tempty_bar(acc), ((uint32_t)(lt >> 1) & 1u) ^ 1u)) break;
+                if (!mbar_wait_warp(tempty_bar(acc), ((uint32_t)(lt >> 1) & 1u) ^ 1u)) break;
                 tc_fence_after();
                 const uint32_t d_tmem = tmem_base + (uint32_t)(acc * kPairAccCols);
-                uint32_t accumulate = 0;
                 for (int it = kb0; it < kb1; ++it) {
-                    if (!mbar_wait(bfull_bar(b), phb) || !mbar_wait(ready_bar(a), pha)) { ok = false; break; }
+                    if (!mbar_wait_warp(bfull_bar(b), phb) || !mbar_wait_warp(ready_bar(a), pha)) { ok = false; break; }
                     tc_fence_after();
-                    umma_kblock_pair<MN ? 128 : 2>(d_tmem, a_lo, b_lo, desc_hi, idesc, accumulate);
-                    accumulate = 1;
-                    umma_commit_pair(consumed_bar(c));
+                    if (elect_one()) {
+                        umma_kblock_pair<MN ? 128 : 2>(d_tmem, a_lo0 + (uint32_t)a * (kPairABytes >> 4),
+                                                       b_lo0 + (uint32_t)b * (b_bytes >> 4), desc_hi, idesc, it > kb0);
+                        umma_commit_pair(consumed_bar(c));
+                    }
+                    __syncwarp();
                     c = (c + 1) & (kFpConsumed - 1);
-                    a_lo += kPairABytes >> 4;
-                    b_lo += b_step;
-                    if (++b == NB) { b = 0; phb ^= 1u; b_lo = b_lo0; }
-                    if (++a == kFpTiles) { a = 0; pha ^= 1u; a_lo = a_lo0; }
+                    if (++b == NB) { b = 0; phb ^= 1u; }
+                    if (++a == kFpTiles) { a = 0; pha ^= 1u; }
                 }
-                umma_commit_pair(tfull_bar(acc));
+                if (elect_one()) umma_commit_pair(tfull_bar(acc));
+                __syncwarp();
             }
-            umma_commit_leader(done_bar);   // nothing stays in flight past this point
-            mbar_wait(done_bar, 0);
+            if (elect_one()) umma_commit_leader(done_bar);   // nothing stays in flight past this point
+            __syncwarp();
+            mbar_wait_warp(done_bar, 0);
         }
         __syncwarp();
     } else if (warp >= kFpEpiWarp0) {

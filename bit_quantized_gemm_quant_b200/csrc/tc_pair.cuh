@@ -79,6 +79,14 @@ BQ_DEVINL void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols)
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
 }
 
+// True in one lane of the (converged) warp.
+BQ_DEVINL bool elect_one()
+{
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0;
+}
+
 // Arrive on `bar` (the same offset in both CTAs) when this thread's earlier tcgen05
 // operations complete.
 BQ_DEVINL void umma_commit_pair(uint32_t bar)
@@ -236,8 +244,11 @@ tc_pair_kernel(const __grid_constant__ CUtensorMap tm_a0, const __grid_constant_
         }
         __syncwarp();
     } else if (warp == kPairEpiWarps + 1) {
-        // ---------------- MMA issuer (one lane of the leader) ----------------
-        if (rank == 0 && lane == 0) {
+        // ---------------- MMA issuer (the leader's; one elected lane issues) ----------------
+        // The whole warp runs the loop, so that descriptors and addresses stay in uniform
+        // registers: with the loop in one lane every operand of an MMA is moved there
+        // first, and a block took 630 clocks with nothing else on the SM.
+        if (rank == 0) {
             const uint32_t idesc = umma_idesc_bf16_f32(256, p.bn) | (MN ? 1u << 15 : 0u);
             const uint64_t bd0 = umma_desc_k_sw128(b_base);
             const uint32_t desc_hi = (uint32_t)(bd0 >> 32);
@@ -253,23 +264,26 @@ tc_pair_kernel(const __grid_constant__ CUtensorMap tm_a0, const __grid_constant_
             for (int u = first; u < units && ok; u += stride, ++lt) {
                 const int acc = lt & 1;
                 const int kb0 = kb_begin(u), kb1 = kb_end(u);
-                if (!mbar_wait(tempty_bar(acc), ((uint32_t)(lt >> 1) & 1u) ^ 1u)) break;
+                if (!mbar_wait_warp(tempty_bar(acc), ((uint32_t)(lt >> 1) & 1u) ^ 1u)) break;
                 tc_fence_after();
                 const uint32_t d_tmem = tmem_base + (uint32_t)(acc * kPairAccCols);
-                uint32_t accumulate = 0;
                 for (int it = kb0; it < kb1; ++it) {
-                    if (!mbar_wait(full_bar(s), ph)) { ok = false; break; }
+                    if (!mbar_wait_warp(full_bar(s), ph)) { ok = false; break; }
                     tc_fence_after();
-                    umma_kblock_pair<MN ? 128 : 2>(d_tmem, a_lo0 + (uint32_t)s * (kPairABytes >> 4),
-                                                   b_lo0 + (uint32_t)s * (b_bytes >> 4), desc_hi, idesc, accumulate);
-                    accumulate = 1;
-                    umma_commit_pair(empty_bar(s));
+                    if (elect_one()) {
+                        umma_kblock_pair<MN ? 128 : 2>(d_tmem, a_lo0 + (uint32_t)s * (kPairABytes >> 4),
+                                                       b_lo0 + (uint32_t)s * (b_bytes >> 4), desc_hi, idesc, it > kb0);
+                        umma_commit_pair(empty_bar(s));
+                    }
+                    __syncwarp();
                     if (++s == S) { s = 0; ph ^= 1u; }
                 }
-                umma_commit_pair(tfull_bar(acc));
+                if (elect_one()) umma_commit_pair(tfull_bar(acc));
+                __syncwarp();
             }
-            umma_commit_leader(done_bar);   // nothing stays in flight past this point
-            mbar_wait(done_bar, 0);
+            if (elect_one()) umma_commit_leader(done_bar);   // nothing stays in flight past this point
+            __syncwarp();
+            mbar_wait_warp(done_bar, 0);
         }
         __syncwarp();
     } else {
