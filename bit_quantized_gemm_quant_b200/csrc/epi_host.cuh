@@ -42,56 +42,88 @@ void device_or_b200(int* num_sms, int* smem_optin)
 
 // ------------------------------------------------------------------ pair product
 struct PairPlan {
-    int bn = 32, stages = 0, splits = 1;
-    int64_t tiles = 0, dp_tiles = 0;
+    int bn = 32, stages = 0, pairs = 0;
+    int64_t tiles = 0;
+    TailSplit split{};
     size_t ws_bytes = 0;
 };
 
-// Token tile and reduction splits for `rows` D rows, M tokens and nk 64-element
-// blocks of the reduction; fixed_bytes of shared memory and per stage a_bytes of weights.  Cost model in SM clocks,
-// per unit of work: a block costs the larger of the MMA's 2 bn and of bringing it in,
-// min_block + bn / 2 (the weight tile through L2, or dequantizing it), plus a fixed
-// start and the drain of the last tile.
+// Token tile and split of the last round for `rows` D rows, M tokens and nk 64-element
+// blocks of the reduction; fixed_bytes of shared memory and per stage a_bytes of weights.
+// Cost model in SM clocks: a block costs the larger of the MMA's and its issue
+// (block_mma per token of the tile) and of bringing the weights in (min_block), a unit of
+// work a fixed start, and what the last unit leaves to be drained; a split last round
+// adds the partial tiles' traffic and the kernel that sums them.
 bool plan_pair(int64_t rows, int64_t M, int64_t nk, int num_sms, int smem_optin, int fixed_bytes, int a_bytes,
-               double min_block, PairPlan* pl)
+               double min_block, double block_mma, PairPlan* pl)
 {
     const int64_t pairs = std::max(num_sms / 2, 1), rtiles = (rows + 255) / 256;
     const int64_t maxb = std::min<int64_t>(256, (M + 31) / 32 * 32);
     double best = 1e300;
     for (int b = 32; b <= maxb; b += 32) {
         const int64_t tiles = ((M + b - 1) / b) * rtiles;
-        const double kb = std::max(2.0 * b, min_block + 0.5 * b);
-        auto consider = [&](double c, int sp, int64_t dp) {
+        const double kb = std::max(block_mma * b, min_block), drain = 1000.0 + 8.0 * b;
+        auto consider = [&](double c, int64_t dp, int64_t tail_pairs) {
             if (c < best) {
                 best = c;
                 pl->bn = b;
-                pl->splits = sp;
-                pl->dp_tiles = dp;
+                pl->tiles = tiles;
+                pl->split.dp_tiles = (int)dp;
+                pl->split.tail = (int)(tiles - dp);
+                pl->split.tail_pairs = (int)tail_pairs;
             }
         };
-        auto unit = [&](int64_t blocks) { return (double)blocks * kb + 1500.0; };
-        const double drain = 8.0 * b;
-        for (int sp = 1; sp <= 32 && (sp == 1 || nk / sp >= 4); ++sp) {
-            const int64_t rounds = (tiles * sp + pairs - 1) / pairs;
-            const double red = sp > 1 ? 5000.0 + (double)sp * (double)tiles * b * 256.0 * 8.0 / 2500.0 : 0.0;
-            consider((double)rounds * unit((nk + sp - 1) / sp) + drain + red, sp, sp > 1 ? 0 : tiles);
-        }
+        auto unit = [&](double blocks) { return blocks * kb + 1500.0; };
+        consider((double)((tiles + pairs - 1) / pairs) * unit((double)nk) + drain, tiles, 0);
         const int64_t dp = tiles / pairs * pairs, tail = tiles - dp;
-        for (int sp = 2; dp > 0 && tail > 0 && tail * sp <= pairs && nk / sp >= 4; ++sp) {
-            const double red = 5000.0 + (double)sp * (double)tail * b * 256.0 * 8.0 / 2500.0;
-            consider(((double)(dp / pairs) * unit(nk) + unit((nk + sp - 1) / sp) + drain + red) * 1.02, sp, dp);
-        }
+        if (tail == 0) continue;
+        // ranges of at least 4 blocks, at least one per tile
+        const int64_t tp = std::max<int64_t>(tail, std::min<int64_t>(pairs, tail * nk / 4));
+        const double range = (double)((tail * nk + tp - 1) / tp);
+        const double traffic = (double)(tp + tail) * b * 256.0 * 8.0 / 2500.0;
+        consider((double)(dp / pairs) * unit((double)nk) + unit(range) + 1500.0 + drain + 5000.0 + traffic, dp, tp);
     }
-    pl->tiles = ((M + pl->bn - 1) / pl->bn) * rtiles;
+    pl->pairs = (int)pairs;
+    pl->split.blocks = (int)nk;
     pl->stages = std::min<int>(kFpMaxTok, (smem_optin - 1024 - 512 - fixed_bytes) / (a_bytes + pl->bn * 64));
-    pl->ws_bytes = pl->splits > 1
-                       ? (size_t)pl->splits * (size_t)(pl->tiles - pl->dp_tiles) * (size_t)pl->bn * 256u * 4u : 0u;
-    return pl->stages >= 3 && pl->tiles <= INT32_MAX / 64;
+    pl->ws_bytes = pl->split.tail ? (size_t)2 * (size_t)pl->split.tail_pairs * (size_t)pl->bn * 256u * 4u : 0u;
+    return pl->stages >= 3 && pl->tiles <= INT32_MAX / 256 && nk <= INT32_MAX / 2;
 }
 
 unsigned reduce_grid(int64_t items, const DeviceInfo& di)
 {
     return (unsigned)std::max<int64_t>(1, std::min<int64_t>((items + 255) / 256, 8 * (int64_t)di.num_sms));
+}
+
+// launch_pdl with a 3-D grid.
+template <typename KernelT, typename... Args>
+bq_status launch_pdl_dim(KernelT kern, dim3 grid, int threads, size_t smem, cudaStream_t st, const Args&... args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, kern, args...) != cudaSuccess) {
+        cudaGetLastError();
+        return BQ_ERR_CUDA;
+    }
+    return launch_status();
+}
+
+// The sums of the split last round, where the plan has one.
+template <int EPI>
+bq_status launch_reduce(const DeviceInfo& di, const PairPlan& pl, const PairParams& p, cudaStream_t st)
+{
+    if (pl.split.tail == 0) return BQ_OK;
+    return launch_pdl_dim(epi_reduce_kernel<EPI>,
+                          dim3(reduce_grid((int64_t)pl.split.tail * pl.bn * (epi_tile_rows<EPI>(256) / 4), di)), 256, 0, st,
+                          (const float*)p.ws, p.e, p.M, p.N, p.bn, p.m_tiles, p.split);
 }
 
 // D = sum over segs of A_i . B_i^T with the epilogue e.  A_i: bf16 weights, a_rows
@@ -128,20 +160,16 @@ bq_status launch_pair(const DeviceInfo& di, int dev, const PairPlan& pl, const u
     p.tiles = (int)pl.tiles;
     p.seg_blocks = (int)((red + 63) / 64);
     p.segs = segs;
-    p.dp_tiles = (int)pl.dp_tiles;
-    p.splits = pl.splits;
+    p.split = pl.split;
     p.ws = reinterpret_cast<float*>(ws);
-    const int64_t units = pl.dp_tiles + (pl.tiles - pl.dp_tiles) * pl.splits;
-    const unsigned grid = 2u * (unsigned)std::min<int64_t>(units, di.num_sms / 2);
+    // every pair when there are whole rounds before the tail: the units are dealt by pair
+    const unsigned grid = 2u * (unsigned)std::min<int64_t>(pl.split.tail && pl.split.dp_tiles ? pl.pairs
+                                                           : pl.split.tail ? pl.split.tail_pairs : pl.tiles, pl.pairs);
     const size_t smem = std::max<size_t>(1024 + (size_t)pl.stages * pair_stage_bytes(pl.bn) + 512,
                                          (size_t)di.max_smem_optin / 2 + 1024);   // one CTA per SM (all of TMEM)
     kern<<<grid, kPairThreads, smem, st>>>(ta[0], ta[1], tb[0], tb[1], p);
     bq_status s = launch_status();
-    if (s != BQ_OK || pl.splits == 1) return s;
-    const int64_t split_tiles = pl.tiles - pl.dp_tiles;
-    epi_reduce_kernel<EPI><<<reduce_grid(split_tiles * pl.bn * epi_tile_rows<EPI>(256) / 4, di), 256, 0, st>>>(
-        p.ws, e, (int)M, (int)outs, pl.bn, 256, p.m_tiles, p.dp_tiles, (int)split_tiles, pl.splits);
-    return launch_status();
+    return s != BQ_OK ? s : launch_reduce<EPI>(di, pl, p, st);
 }
 
 bq_status dequant_rows(WFmt fmt, const QMat* w, int count, uint16_t* out, int64_t N, int64_t K, int group_size,
@@ -274,27 +302,6 @@ ScalePack scale_pack(bool mn, int mats, int64_t N, int64_t K)
     return s;
 }
 
-// launch_pdl with a 3-D grid.
-template <typename KernelT, typename... Args>
-bq_status launch_pdl_dim(KernelT kern, dim3 grid, int threads, size_t smem, cudaStream_t st, const Args&... args)
-{
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3((unsigned)threads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, kern, args...) != cudaSuccess) {
-        cudaGetLastError();
-        return BQ_ERR_CUDA;
-    }
-    return launch_status();
-}
-
 int fp_mode(WFmt f) { return f == WFmt::Q4_0 ? kModeQ4_0 : f == WFmt::AFF4 ? kModeAff4 : kModeAff8; }
 
 // The product of launch_pair with the codes of w (1 or 2 matrices [N][K]) in place of
@@ -359,19 +366,15 @@ bq_status launch_fused_pair(const DeviceInfo& di, int dev, const PairPlan& pl, c
     p.q.tiles = (int)pl.tiles;
     p.q.seg_blocks = (int)((red + 63) / 64);
     p.q.segs = MN ? mats : 1;
-    p.q.dp_tiles = (int)pl.dp_tiles;
-    p.q.splits = pl.splits;
+    p.q.split = pl.split;
     p.q.ws = reinterpret_cast<float*>(ws);
-    const int64_t units = pl.dp_tiles + (pl.tiles - pl.dp_tiles) * pl.splits;
-    const unsigned grid = 2u * (unsigned)std::min<int64_t>(units, di.num_sms / 2);
+    // every pair when there are whole rounds before the tail: the units are dealt by pair
+    const unsigned grid = 2u * (unsigned)std::min<int64_t>(pl.split.tail && pl.split.dp_tiles ? pl.pairs
+                                                           : pl.split.tail ? pl.split.tail_pairs : pl.tiles, pl.pairs);
     const size_t smem = std::max<size_t>(1024 + fp_fixed_bytes(MODE) + (size_t)pl.stages * (size_t)pl.bn * 64u + 512,
                                          (size_t)di.max_smem_optin / 2 + 1024);   // one CTA per SM (all of TMEM)
     s = launch_pdl_dim(kern, dim3(grid), kFpThreads, smem, st, ta[0], ta[1], tb[0], tb[1], p);
-    if (s != BQ_OK || pl.splits == 1) return s;
-    const int64_t split_tiles = pl.tiles - pl.dp_tiles;
-    epi_reduce_kernel<EPI><<<reduce_grid(split_tiles * pl.bn * epi_tile_rows<EPI>(256) / 4, di), 256, 0, st>>>(
-        p.q.ws, e, (int)M, (int)outs, pl.bn, 256, p.q.m_tiles, p.q.dp_tiles, (int)split_tiles, pl.splits);
-    return launch_status();
+    return s != BQ_OK ? s : launch_reduce<EPI>(di, pl, p.q, st);
 }
 
 template <bool MN, int EPI>
@@ -409,9 +412,9 @@ bool plan_epi_product(WFmt fmt, int64_t rows, int64_t M, int64_t nk, int num_sms
 {
     w->rows = rows;
     w->fused = has_fast_paths(fmt);
-    return w->fused ? plan_pair(rows, M, nk, num_sms, smem_optin, (int)fp_fixed_bytes(fp_mode(fmt)), 0, 450.0,
+    return w->fused ? plan_pair(rows, M, nk, num_sms, smem_optin, (int)fp_fixed_bytes(fp_mode(fmt)), 0, 520.0, 2.5,
                                 &w->pl)
-                    : plan_pair(rows, M, nk, num_sms, smem_optin, 0, (int)kPairABytes, 300.0, &w->pl);
+                    : plan_pair(rows, M, nk, num_sms, smem_optin, 0, (int)kPairABytes, 400.0, 2.5, &w->pl);
 }
 
 bool plan_forward(WFmt fmt, int mats, int64_t M, int64_t N, int64_t K, int num_sms, int smem_optin, EpiWs* w)

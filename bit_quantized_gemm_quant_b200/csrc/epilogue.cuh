@@ -41,11 +41,30 @@ constexpr float kGeluTanhB = 0.044715f;
 constexpr float kInvSqrt2 = 0.70710678118654752f;
 constexpr float kInvSqrt2Pi = 0.39894228040143268f;
 
+// The normal distribution function through Abramowitz and Stegun 7.1.26 (erf to 1.5e-7
+// absolute): with x = |z| / sqrt(2), t = 1 / (1 + 0.3275911 x), the tail 1 - Phi(|z|) is
+// t (a1 + t (a2 + ...)) e^(-x^2) / 2.  Taking the tail itself keeps Phi(z) for z << 0 free
+// of cancellation.  `e` returns e^(-z^2 / 2), the density times sqrt(2 pi).  (erfcf in
+// this place made the epilogue of a 12288 x 4096, 512-token product take 19 us.)
+BQ_DEVINL float normal_cdf(float z, float& e)
+{
+    const float x = fabsf(z) * kInvSqrt2, t = __fdividef(1.0f, fmaf(0.3275911f, x, 1.0f));
+    e = __expf(-0.5f * z * z);
+    float q = fmaf(t, 0.5f * 1.061405429f, 0.5f * -1.453152027f);
+    q = fmaf(t, q, 0.5f * 1.421413741f);
+    q = fmaf(t, q, 0.5f * -0.284496736f);
+    q = fmaf(t, q, 0.5f * 0.254829592f) * t * e;
+    return z < 0.0f ? q : 1.0f - q;
+}
+
 template <int ACT>
 BQ_DEVINL float act_f(float z)
 {
     if constexpr (ACT == kActRelu) return z < 0.0f ? 0.0f : z;                    // NaN stays NaN
-    if constexpr (ACT == kActGelu) return 0.5f * z * erfcf(-z * kInvSqrt2);       // no cancellation for z << 0
+    if constexpr (ACT == kActGelu) {
+        float e;
+        return z * normal_cdf(z, e);
+    }
     if constexpr (ACT == kActGeluTanh) return z * sigmoid_f(kGeluTanhA * z * fmaf(kGeluTanhB * z, z, 1.0f));
     if constexpr (ACT == kActSilu) return z * sigmoid_f(z);
     return z;
@@ -58,8 +77,9 @@ BQ_DEVINL float dact_f(float z)
 {
     if constexpr (ACT == kActRelu) return z > 0.0f ? 1.0f : (z <= 0.0f ? 0.0f : z);
     if constexpr (ACT == kActGelu) {
-        const float d = kInvSqrt2Pi * __expf(-0.5f * z * z);
-        return fmaf(0.5f, erfcf(-z * kInvSqrt2), d == 0.0f ? 0.0f : z * d);
+        float e;
+        const float c = normal_cdf(z, e);
+        return e == 0.0f ? c : fmaf(kInvSqrt2Pi * z, e, c);
     }
     if constexpr (ACT == kActGeluTanh) {
         const float p = sigmoid_f(kGeluTanhA * z * fmaf(kGeluTanhB * z, z, 1.0f)), t = p * (1.0f - p);
@@ -168,20 +188,25 @@ BQ_DEVINL EpiRow<EPI> epi_row(const EpiParams& e, int n, int N)
     return r;
 }
 
-// 8 tokens (mb .. mb + 7) of one tile row from a tensor-memory load, v[O .. O + 7].  The
-// whole warp calls it: with glu, lanes l and l + 16 hold the gate and the up sum of one
-// output and trade every second token by one shuffle, so that each lane ends with both
-// sums of 4 outputs.
-template <int EPI, int O>
-BQ_DEVINL void epi_store8(const EpiParams& e, const EpiRow<EPI>& r, const uint32_t (&v)[16], int mb, int M, int64_t N)
+// Consecutive tokens (mb ...) of one tile row from a tensor-memory load: 16 with glu, else
+// 8.  The whole warp calls it: with glu, lanes l and l + 16 hold the gate and the up sum
+// of one output and trade every second token by one shuffle, so that each lane ends with
+// both sums of 8 outputs.  FULL: all the tokens exist.  (The code shares the instruction
+// cache with the dequantization: at 12288 x 4096, 512 tokens, act took 71 us with 8
+// tokens at a time, 75 with 16, 84 with 16 and a FULL copy; glu, whose activations are
+// fewer per token, was fastest with 16 and both copies.)
+template <int EPI> constexpr int kEpiTokens = EPI == kEpiGlu ? 16 : 8;
+
+template <int EPI, bool FULL, int T>
+BQ_DEVINL void epi_store_tokens(const EpiParams& e, const EpiRow<EPI>& r, const uint32_t (&v)[T], int mb, int M, int64_t N)
 {
     if constexpr (EPI == kEpiGlu) {
         const int up = (threadIdx.x >> 4) & 1;
-        float g[4], u[4];
+        float g[T / 2], u[T / 2];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const uint32_t mine = up ? v[O + 2 * j + 1] : v[O + 2 * j];
-            const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? v[O + 2 * j] : v[O + 2 * j + 1], 16);
+        for (int j = 0; j < T / 2; ++j) {
+            const uint32_t mine = up ? v[2 * j + 1] : v[2 * j];
+            const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? v[2 * j] : v[2 * j + 1], 16);
             g[j] = __uint_as_float(up ? got : mine) + r.b;
             u[j] = __uint_as_float(up ? mine : got) + r.b2;
         }
@@ -191,82 +216,100 @@ BQ_DEVINL void epi_store8(const EpiParams& e, const EpiRow<EPI>& r, const uint32
         if (e.pre) {
             int64_t q = o;
 #pragma unroll
-            for (int j = 0; j < 4; ++j, q += 2 * N)
-                if (m + 2 * j < M) {
+            for (int j = 0; j < T / 2; ++j, q += 2 * N)
+                if (FULL || m + 2 * j < M) {
                     e.pre[q] = (uint16_t)f32_to_bf16_bits(g[j]);
                     e.pre2[q] = (uint16_t)f32_to_bf16_bits(u[j]);
                 }
         }
-        act_n<4>(g, e.act);
+        act_n<T / 2>(g, e.act);
 #pragma unroll
-        for (int j = 0; j < 4; ++j, o += 2 * N)
-            if (m + 2 * j < M) e.y[o] = (uint16_t)f32_to_bf16_bits(g[j] * u[j]);
+        for (int j = 0; j < T / 2; ++j, o += 2 * N)
+            if (FULL || m + 2 * j < M) e.y[o] = (uint16_t)f32_to_bf16_bits(g[j] * u[j]);
     } else {
         if (!r.ok) return;
         int64_t o = (int64_t)mb * N + r.n;
-        float z[8];
+        float z[T];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) z[j] = __uint_as_float(v[O + j]) + r.b;
+        for (int j = 0; j < T; ++j) z[j] = __uint_as_float(v[j]) + r.b;
         if constexpr (EPI == kEpiAct) {
-            uint32_t q[8];
+            uint32_t q[T];
             if (e.res) {
                 int64_t i = o;
 #pragma unroll
-                for (int j = 0; j < 8; ++j, i += N) q[j] = mb + j < M ? e.res[i] : 0u;
+                for (int j = 0; j < T; ++j, i += N) q[j] = FULL || mb + j < M ? e.res[i] : 0u;
             }
             if (e.pre) {
                 int64_t i = o;
 #pragma unroll
-                for (int j = 0; j < 8; ++j, i += N)
-                    if (mb + j < M) e.pre[i] = (uint16_t)f32_to_bf16_bits(z[j]);
+                for (int j = 0; j < T; ++j, i += N)
+                    if (FULL || mb + j < M) e.pre[i] = (uint16_t)f32_to_bf16_bits(z[j]);
             }
-            act_n<8>(z, e.act);
+            act_n<T>(z, e.act);
             if (e.res) {
 #pragma unroll
-                for (int j = 0; j < 8; ++j) z[j] += bf16_bits_to_f32(q[j]);
+                for (int j = 0; j < T; ++j) z[j] += bf16_bits_to_f32(q[j]);
             }
         }
 #pragma unroll
-        for (int j = 0; j < 8; ++j, o += N)
-            if (mb + j < M) e.y[o] = (uint16_t)f32_to_bf16_bits(z[j]);
+        for (int j = 0; j < T; ++j, o += N)
+            if (FULL || mb + j < M) e.y[o] = (uint16_t)f32_to_bf16_bits(z[j]);
     }
 }
 
-template <int EPI>
-BQ_DEVINL void epi_store16(const EpiParams& e, const EpiRow<EPI>& r, const uint32_t (&v)[16], int mb, int M, int64_t N)
+template <int EPI, int T>
+BQ_DEVINL void epi_store(const EpiParams& e, const EpiRow<EPI>& r, const uint32_t (&v)[T], int mb, int M, int64_t N)
 {
-    epi_store8<EPI, 0>(e, r, v, mb, M, N);
-    epi_store8<EPI, 8>(e, r, v, mb + 8, M, N);
+    if (EPI == kEpiGlu && mb + T <= M)                    // warp-uniform
+        epi_store_tokens<EPI, true, T>(e, r, v, mb, M, N);
+    else
+        epi_store_tokens<EPI, false, T>(e, r, v, mb, M, N);
 }
 
-// Sums the partial tiles of a K-split product in split order and applies the
-// epilogue.  Partials: [split][split tile][token of the tile (bn)][row of the tile
-// (rows)]; one thread per 4 outputs of one token.
+// How the pair products cut their work: tiles [0, dp_tiles) whole, pair i taking tiles
+// i, i + pairs, ...; the blocks of the other `tail` tiles, in order, are dealt to the
+// first `tail_pairs` pairs in equal consecutive ranges (tail <= tail_pairs, so a range
+// touches at most two tiles).  So the last round fills all pairs whatever the number of
+// tiles: 128 tiles on 74 pairs cost 1.73 tiles' time instead of 2.  A range's part of a
+// tile is an fp32 partial tile in slot 2 i + (0 or 1).
+struct TailSplit {
+    int dp_tiles, tail, tail_pairs;
+    int blocks;                                    // 64-element blocks per tile
+    __host__ __device__ int64_t range_begin(int i) const { return (int64_t)i * tail * blocks / tail_pairs; }
+};
+
+// Sums the partial tiles of the tail in the order of their blocks and applies the
+// epilogue.  Partials: [slot][token of the tile (bn)][row of the tile (256)]; one thread
+// per 4 outputs of one token.
 template <int EPI>
 __global__ void __launch_bounds__(256)
-epi_reduce_kernel(const float* __restrict__ ws, EpiParams e, int M, int N, int bn, int rows, int m_tiles, int dp_tiles,
-                  int split_tiles, int splits)
+epi_reduce_kernel(const float* __restrict__ ws, EpiParams e, int M, int N, int bn, int m_tiles, TailSplit t)
 {
-    const int q = epi_tile_rows<EPI>(rows) / 4;                       // 4-output groups per token
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int q = epi_tile_rows<EPI>(256) / 4;                        // 4-output groups per token
     const int64_t per_tile = (int64_t)bn * q;
-    const int64_t total = (int64_t)split_tiles * per_tile;
-    const int64_t split_stride = (int64_t)split_tiles * bn * rows;    // floats
+    const int64_t total = t.tail * per_tile, slot = (int64_t)bn * 256;
+    const int64_t all = (int64_t)t.tail * t.blocks;
     for (int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; i < total; i += (int64_t)gridDim.x * blockDim.x) {
         const int j = (int)(i / per_tile);
         const int rem = (int)(i - (int64_t)j * per_tile);
         const int m = rem / q, r4 = (rem - m * q) * 4;
-        const int t = dp_tiles + j;
-        const int tok = (t % m_tiles) * bn + m;
-        const int64_t n0 = (int64_t)(t / m_tiles) * epi_tile_rows<EPI>(rows) + r4;
+        const int tok = ((t.dp_tiles + j) % m_tiles) * bn + m;
+        const int64_t n0 = (int64_t)((t.dp_tiles + j) / m_tiles) * epi_tile_rows<EPI>(256) + r4;
         if (tok >= M || n0 >= N) continue;
         const int row = EPI == kEpiGlu ? 32 * (r4 >> 4) + (r4 & 15) : r4;
-        const float* src = ws + ((int64_t)j * bn + m) * rows + row;
+        const float* src = ws + (int64_t)m * 256 + row;
+        const int64_t begin = (int64_t)j * t.blocks, end = begin + t.blocks;
         float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
-        for (int sp = 0; sp < splits; ++sp) {
-            const float4 c = *reinterpret_cast<const float4*>(src + sp * split_stride);
+        // the last range that begins at or before the tile, then on through its blocks
+        for (int p = (int)(((begin + 1) * t.tail_pairs + all - 1) / all) - 1; p < t.tail_pairs; ++p) {
+            const int64_t rb = t.range_begin(p);
+            if (rb >= end) break;
+            const float* part = src + (2 * p + (rb < begin ? 1 : 0)) * slot;
+            const float4 c = *reinterpret_cast<const float4*>(part);
             a.x += c.x; a.y += c.y; a.z += c.z; a.w += c.w;
             if constexpr (EPI == kEpiGlu) {
-                const float4 d = *reinterpret_cast<const float4*>(src + 16 + sp * split_stride);
+                const float4 d = *reinterpret_cast<const float4*>(part + 16);
                 b.x += d.x; b.y += d.y; b.z += d.z; b.w += d.w;
             }
         }

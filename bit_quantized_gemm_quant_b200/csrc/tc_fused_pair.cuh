@@ -122,6 +122,72 @@ __global__ void __launch_bounds__(256) scale_pack_kernel(const __grid_constant__
     }
 }
 
+// The dequant warps' part: group grp (4 warps) takes the blocks at positions grp, grp + 4,
+// ... of the CTA's `left` blocks.  A thread expands 64 weights: forward, row r of the tile;
+// gradient, row r of the block, outputs 64 hk .. of the tile.  (A function of its own:
+// inlined, the code that follows it for these warps slowed this loop by 13%.)
+template <int MODE, bool MN, int EPI>
+__device__ __noinline__ void fp_dequantize(int left, uint32_t a_base, uint32_t c_base, uint32_t cfull0, uint32_t cempty0,
+                                           uint32_t ready0, uint32_t consumed0)
+{
+    constexpr uint32_t kCBytes = fp_code_bytes(MODE), kCStage = kCBytes + kFpScaleBytes;
+    constexpr int kBits = MODE == kModeAff8 ? 8 : 4, kCodes = fp_codes(MODE);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int grp = warp >> 2, w4 = warp & 3;
+    const int r = MN ? 32 * (w4 & 1) + lane : 32 * w4 + lane;
+    const int hk = MN ? w4 >> 1 : 0;
+    const int crow = !MN && EPI == kEpiGlu ? epi_out_row<EPI>(r) + (lane & 16 ? 64 : 0) : r;   // row among the codes
+    constexpr int kRowBytes = (MN ? 128 : 64) * kBits / 8;                  // of codes: 32, 64 or 128
+    constexpr int kUnits = kBits / 2;                                       // 16-byte units of codes per thread
+    // the units of a row, as the copy swizzles them
+    const int sw = kRowBytes == 32 ? (crow >> 2) & 1 : kRowBytes == 64 ? (crow >> 1) & 3 : crow & 7;
+    const uint32_t code_row = c_base + (uint32_t)(crow * kRowBytes);
+    const uint32_t tile_row = a_base + (uint32_t)(hk * (int)(kPairABytes / 2) + r * 128);
+    const uint32_t scale_row = c_base + kCBytes + (uint32_t)(MN ? r * 16 + hk * 8 : r * 8);
+    int c = grp, a = grp;                           // code stage and tile slot of this block
+    uint32_t ph = 0;
+    bool ok = true;
+    for (int pos = grp; pos < left; pos += 4) {
+        ok = mbar_wait_warp(cfull0 + 8u * (uint32_t)c, ph);
+        if (!ok) break;
+        const uint32_t codes = code_row + (uint32_t)c * kCStage;
+        const uint2 sc = ld_shared_v2(scale_row + (uint32_t)c * kCStage);
+        uint4 raw[kUnits];
+#pragma unroll
+        for (int i = 0; i < kUnits; ++i) raw[i] = ld_shared_v4(codes + (uint32_t)(((hk * kUnits + i) ^ sw) << 4));
+        __syncwarp();
+        if (lane == 0) mbar_arrive(cempty0 + 8u * (uint32_t)c);
+        const uint32_t tile = tile_row + (uint32_t)a * kPairABytes;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            uint32_t wv[16];
+            const uint32_t w = h ? sc.y : sc.x;
+            if constexpr (MODE == kModeQ4_0)
+                deq_q4_0_half(raw[h], prmt(w, w, 0x1010u), prmt(w, w, 0x3232u), wv);
+            else if constexpr (MODE == kModeAff4)
+                deq_aff4_half(raw[h], prmt(w, w, 0x1010u), prmt(w, w, 0x3232u), wv);
+            else
+                deq_aff8_half(raw[2 * h], raw[2 * h + 1], __uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u), wv);
+            if (h == 0 && pos >= kFpTiles) {           // the slot's last block is consumed
+                const int q = pos - kFpTiles;
+                ok = mbar_wait(consumed0 + 8u * (uint32_t)(q & (kFpConsumed - 1)), (uint32_t)(q / kFpConsumed) & 1u);
+                __syncwarp();
+            }
+            if (!ok) break;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                st_shared_v4(tile + (uint32_t)(((4 * h + j) ^ (r & 7)) << 4), wv[4 * j], wv[4 * j + 1], wv[4 * j + 2],
+                             wv[4 * j + 3]);
+        }
+        if (!ok) break;
+        fence_proxy_async_smem();                    // the MMA reads the tile through the async proxy
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(ready0 + 8u * (uint32_t)a);
+        if ((c += 4) >= kCodes) { c -= kCodes; ph ^= 1u; }
+        if ((a += 4) >= kFpTiles) a -= kFpTiles;
+    }
+}
+
 // tm_a0, tm_a1: codes of matrix 0 and 1 as bytes.  Forward: boxes of one stage's 64
 // columns x 128 rows (glu: 64 rows of gate and of up); gradient: 128 columns x 64 rows.
 // tm_b0, tm_b1: tokens, boxes of 64 elements x bn / 2 tokens.
@@ -139,7 +205,6 @@ tc_fused_pair_kernel(const __grid_constant__ CUtensorMap tm_a0, const __grid_con
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_ctarank();
     const int NB = p.stages;                       // token tiles in the ring
-    const int nk = p.seg_blocks * p.segs;
     const uint32_t b_bytes = (uint32_t)p.bn * 64u;
     const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
     const uint32_t a_base = base, c_base = a_base + kFpTiles * kPairABytes, b_base = c_base + kFpCodes * kCStage;
@@ -162,12 +227,6 @@ tc_fused_pair_kernel(const __grid_constant__ CUtensorMap tm_a0, const __grid_con
         return mbar_wait(consumed_bar(pos & (kFpConsumed - 1)), (uint32_t)(pos / kFpConsumed) & 1u);
     };
 
-    const int units = p.dp_tiles + (p.tiles - p.dp_tiles) * p.splits;
-    const int first = blockIdx.x >> 1, stride = gridDim.x >> 1;
-    auto unit_tile = [&](int u) { return u < p.dp_tiles ? u : p.dp_tiles + (u - p.dp_tiles) / p.splits; };
-    auto unit_split = [&](int u) { return u < p.dp_tiles ? 0 : (u - p.dp_tiles) % p.splits; };
-    auto kb_begin = [&](int u) { return u < p.dp_tiles ? 0 : (int)((int64_t)unit_split(u) * nk / p.splits); };
-    auto kb_end = [&](int u) { return u < p.dp_tiles ? nk : (int)((int64_t)(unit_split(u) + 1) * nk / p.splits); };
     auto tile_r0 = [&](int t) { return (t / p.m_tiles) * 256 + (int)rank * 128; };
     auto tile_m0 = [&](int t) { return (t % p.m_tiles) * p.bn; };
 
@@ -199,15 +258,24 @@ tc_fused_pair_kernel(const __grid_constant__ CUtensorMap tm_a0, const __grid_con
     grid_dependency_wait();
     grid_dependents_launch();
 
+    // Chunks idx, idx + parts, ... of the lt-th local unit, in the lane quarter of this warp.
+    auto drain = [&](int t, int slot, int lt, int idx, int parts) {
+        const int q4 = warp & 3, r = 32 * q4 + lane;
+        tc_fence_after();
+        pair_drain<EPI>(p, tmem_base + ((uint32_t)(32 * q4) << 16) + (uint32_t)((lt & 1) * kPairAccCols), tile_m0(t),
+                        epi_tile_rows<EPI>(tile_r0(t)) + epi_out_row<EPI>(r),
+                        slot < 0 ? nullptr : p.ws + (int64_t)slot * ((int64_t)p.bn * 256) + (int)rank * 128 + r, idx, parts);
+        tc_fence_before();
+    };
+
     if (warp == kFpTokWarp) {
         // ---------------- token tiles (each CTA: its own half) ----------------
         if (lane == 0) {
             int b = 0, pos = 0;
             bool ok = true;
-            for (int u = first; u < units && ok; u += stride) {
-                const int m0 = tile_m0(unit_tile(u)) + (int)rank * (p.bn / 2);
-                const int kb1 = kb_end(u);
-                for (int it = kb_begin(u); it < kb1; ++it, ++pos) {
+            for (PairUnits u(p); ok && u.next();) {
+                const int m0 = tile_m0(u.tile) + (int)rank * (p.bn / 2);
+                for (int it = u.kb0; it < u.kb1; ++it, ++pos) {
                     if (pos >= NB && !wait_consumed(pos - NB)) { ok = false; break; }
                     const bool second = it >= p.seg_blocks;
                     if (rank == 0) mbar_arrive_expect_tx(bfull_bar(b), 2u * b_bytes);
@@ -231,10 +299,9 @@ tc_fused_pair_kernel(const __grid_constant__ CUtensorMap tm_a0, const __grid_con
             int c = 0, issued = 0;
             uint32_t ph = 0;
             bool ok = true;
-            for (int u = first; u < units && ok; u += stride) {
-                const int r0 = tile_r0(unit_tile(u));
-                const int kb1 = kb_end(u);
-                for (int it = kb_begin(u); it < kb1; ++it, ++issued) {
+            for (PairUnits u(p); ok && u.next();) {
+                const int r0 = tile_r0(u.tile);
+                for (int it = u.kb0; it < u.kb1; ++it, ++issued) {
                     if (!mbar_wait(cempty_bar(c), ph ^ 1u)) { ok = false; break; }
                     const uint32_t dst = c_base + (uint32_t)c * kCStage;
                     mbar_arrive_expect_tx(cfull_bar(c), kCStage);
@@ -273,9 +340,9 @@ tc_fused_pair_kernel(const __grid_constant__ CUtensorMap tm_a0, const __grid_con
             int a = 0, b = 0, c = 0, lt = 0;
             uint32_t pha = 0, phb = 0;
             bool ok = true;
-            for (int u = first; u < units && ok; u += stride, ++lt) {
+            for (PairUnits u(p); ok && u.next(); ++lt) {
                 const int acc = lt & 1;
-                const int kb0 = kb_begin(u), kb1 = kb_end(u);
+                const int kb0 = u.kb0, kb1 = u.kb1;
                 if (!mbar_wait_warp(tempty_bar(acc), ((uint32_t)(lt >> 1) & 1u) ^ 1u)) break;
                 tc_fence_after();
                 const uint32_t d_tmem = tmem_base + (uint32_t)(acc * kPairAccCols);
@@ -295,107 +362,41 @@ tc_fused_pair_kernel(const __grid_constant__ CUtensorMap tm_a0, const __grid_con
                 if (elect_one()) umma_commit_pair(tfull_bar(acc));
                 __syncwarp();
             }
-            if (elect_one()) umma_commit_leader(done_bar);   // nothing stays in flight past this point
+            if (elect_one()) umma_commit_pair(done_bar);     // nothing stays in flight past this point
             __syncwarp();
-            mbar_wait_warp(done_bar, 0);
         }
-        __syncwarp();
+        mbar_wait_warp(done_bar, 0);
     } else if (warp >= kFpEpiWarp0) {
-        // ---------------- epilogue ----------------
-        const int q4 = warp & 3;
-        const uint32_t lane_addr0 = tmem_base + ((uint32_t)(32 * q4) << 16);
+        // ---------------- epilogue: all units but the last ----------------
         int lt = 0;
-        for (int u = first; u < units; u += stride, ++lt) {
-            const int t = unit_tile(u), acc = lt & 1;
-            const int r = 32 * q4 + lane;
-            const int m0 = tile_m0(t);
-            const bool split = p.splits > 1 && u >= p.dp_tiles;
-            const EpiRow<EPI> row = epi_row<EPI>(p.e, epi_tile_rows<EPI>(tile_r0(t)) + epi_out_row<EPI>(r), p.N);
-            if (!mbar_wait_warp(tfull_bar(acc), (uint32_t)(lt >> 1) & 1u)) break;
-            tc_fence_after();
-            const uint32_t lane_addr = lane_addr0 + (uint32_t)(acc * kPairAccCols);
-            if (split) {
-                float* pt = p.ws + ((int64_t)unit_split(u) * (p.tiles - p.dp_tiles) + (t - p.dp_tiles)) *
-                                       ((int64_t)p.bn * 256) + (int)rank * 128 + r;
-                for (int c = 0; c < p.bn; c += 16, pt += 16 * 256) {
-                    uint32_t v[16];
-                    tmem_ld_32x32b_x16(lane_addr + (uint32_t)c, v);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) pt[j * 256] = __uint_as_float(v[j]);
-                }
-            } else {
-                for (int c = 0; c < p.bn && m0 + c < p.M; c += 16) {
-                    uint32_t v[16];
-                    tmem_ld_32x32b_x16(lane_addr + (uint32_t)c, v);
-                    tmem_wait_ld();
-                    epi_store16<EPI>(p.e, row, v, m0 + c, p.M, p.N);
-                }
-            }
-            tc_fence_before();
+        PairUnits u(p);
+        for (bool more = u.next(); more; ++lt) {
+            const int tile = u.tile, slot = u.slot;
+            more = u.next();
+            if (!more || !mbar_wait_warp(tfull_bar(lt & 1), (uint32_t)(lt >> 1) & 1u)) break;
+            drain(tile, slot, lt, 0, 1);
             __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(map_to_cta(tempty_bar(acc), 0));
+            if (lane == 0) mbar_arrive_cluster(map_to_cta(tempty_bar(lt & 1), 0));
         }
     } else {
         // ---------------- dequantization ----------------
-        // Group grp (4 warps) takes the blocks at positions grp, grp + 4, ... of this
-        // CTA's sequence.  A thread expands 64 weights: forward, row r of
-        // the tile; gradient, row r of the block, outputs 64 hk .. of the tile.
-        const int grp = warp >> 2, w4 = warp & 3;
-        const int r = MN ? 32 * (w4 & 1) + lane : 32 * w4 + lane;
-        const int hk = MN ? w4 >> 1 : 0;
-        const bool up = !MN && EPI == kEpiGlu && (lane & 16);
-        const int crow = !MN && EPI == kEpiGlu ? epi_out_row<EPI>(r) + (up ? 64 : 0) : r;      // row among the stage's codes
-        constexpr int kRowBytes = (MN ? 128 : 64) * kBits / 8;                  // of codes: 32, 64 or 128
-        constexpr int kUnits = kBits / 2;                                       // 16-byte units of codes per thread
-        // the units of a row, as the copy swizzles them
-        const int sw = kRowBytes == 32 ? (crow >> 2) & 1 : kRowBytes == 64 ? (crow >> 1) & 3 : crow & 7;
-        const uint32_t code_row = c_base + (uint32_t)(crow * kRowBytes);
-        const uint32_t tile_row = a_base + (uint32_t)(hk * (int)(kPairABytes / 2) + r * 128);
-        const uint32_t ready0 = map_to_cta(ready_bar(0), 0);
-        const uint32_t scale_row = c_base + kCBytes + (uint32_t)(MN ? r * 16 + hk * 8 : r * 8);
         int left = 0;                                    // blocks of this CTA's sequence
-        for (int u = first; u < units; u += stride) left += kb_end(u) - kb_begin(u);
-        int c = grp, a = grp;                           // code stage and tile slot of this block
-        uint32_t ph = 0;
-        bool ok = true;
-        for (int pos = grp; pos < left; pos += 4) {
-            if (!mbar_wait_warp(cfull_bar(c), ph)) break;
-            const uint32_t codes = code_row + (uint32_t)c * kCStage;
-            const uint2 sc = ld_shared_v2(scale_row + (uint32_t)c * kCStage);
-            uint4 raw[kUnits];
-#pragma unroll
-            for (int i = 0; i < kUnits; ++i) raw[i] = ld_shared_v4(codes + (uint32_t)(((hk * kUnits + i) ^ sw) << 4));
-            __syncwarp();
-            if (lane == 0) mbar_arrive(cempty_bar(c));
-            const uint32_t tile = tile_row + (uint32_t)a * kPairABytes;
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                uint32_t wv[16];
-                const uint32_t w = h ? sc.y : sc.x;
-                if constexpr (MODE == kModeQ4_0)
-                    deq_q4_0_half(raw[h], prmt(w, w, 0x1010u), prmt(w, w, 0x3232u), wv);
-                else if constexpr (MODE == kModeAff4)
-                    deq_aff4_half(raw[h], prmt(w, w, 0x1010u), prmt(w, w, 0x3232u), wv);
-                else
-                    deq_aff8_half(raw[2 * h], raw[2 * h + 1], __uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u), wv);
-                if (h == 0 && pos >= kFpTiles) {           // the slot's last block is consumed
-                    ok = wait_consumed(pos - kFpTiles);
-                    __syncwarp();
-                }
-                if (!ok) break;
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    st_shared_v4(tile + (uint32_t)(((4 * h + j) ^ (r & 7)) << 4), wv[4 * j], wv[4 * j + 1],
-                                 wv[4 * j + 2], wv[4 * j + 3]);
-            }
-            if (!ok) break;
-            fence_proxy_async_smem();                    // the MMA reads the tile through the async proxy
-            __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(ready0 + 8u * (uint32_t)a);
-            if ((c += 4) >= kFpCodes) { c -= kFpCodes; ph ^= 1u; }
-            if ((a += 4) >= kFpTiles) a -= kFpTiles;
+        for (PairUnits u(p); u.next();) left += u.kb1 - u.kb0;
+        fp_dequantize<MODE, MN, EPI>(left, a_base, c_base, cfull_bar(0), cempty_bar(0), map_to_cta(ready_bar(0), 0),
+                                     consumed_bar(0));
+    }
+    __syncwarp();
+
+    // ---------------- the last unit's epilogue: dequant and epilogue warps together ----------------
+    // No product overlaps it.  (It waits on done, which has one phase: the dequant warps
+    // have not followed tfull's.)
+    if (warp < kFpTokWarp) {
+        int lt = -1, tile = 0, slot = 0;
+        for (PairUnits u(p); u.next(); ++lt) {
+            tile = u.tile;
+            slot = u.slot;
         }
+        if (lt >= 0 && mbar_wait_warp(done_bar, 0)) drain(tile, slot, lt, warp >> 2, kFpTokWarp / 4);
     }
 
     tc_fence_before();

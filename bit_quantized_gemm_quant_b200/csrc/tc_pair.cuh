@@ -141,9 +141,69 @@ struct PairParams {
     int m_tiles, tiles;
     int seg_blocks;           // 64-element blocks of the reduction per matrix
     int segs;                 // matrices summed (1 or 2)
-    int dp_tiles, splits;     // as in tc_gemm.cuh: tiles from dp_tiles on are split over the reduction
-    float* ws;                // [split][split tile][token of the tile (bn)][row of the tile (256)]
+    TailSplit split;          // tiles from split.dp_tiles on are split over the reduction
+    float* ws;                // their partial tiles
 };
+
+// The units of work of one pair, in order: whole tiles, then its range of the tail.
+struct PairUnits {
+    const PairParams& p;
+    int pair, pairs, nk, next_tile, seg;
+    int64_t pos, end;
+    int tile, kb0, kb1, slot;                      // the current unit; slot -1: a whole tile
+
+    BQ_DEVINL explicit PairUnits(const PairParams& prm)
+        : p(prm), pair((int)blockIdx.x >> 1), pairs((int)gridDim.x >> 1), nk(prm.seg_blocks * prm.segs), next_tile(pair),
+          seg(0), pos(0), end(0)
+    {
+        if (pair < p.split.tail_pairs) {
+            pos = p.split.range_begin(pair);
+            end = p.split.range_begin(pair + 1);
+        }
+    }
+    BQ_DEVINL bool next()
+    {
+        if (next_tile < p.split.dp_tiles) {
+            tile = next_tile;
+            next_tile += pairs;
+            kb0 = 0;
+            kb1 = nk;
+            slot = -1;
+            return true;
+        }
+        if (pos >= end) return false;
+        const int j = (int)(pos / nk);
+        tile = p.split.dp_tiles + j;
+        kb0 = (int)(pos - (int64_t)j * nk);
+        kb1 = (int)(end - (int64_t)j * nk < nk ? end - (int64_t)j * nk : nk);
+        pos += kb1 - kb0;
+        slot = 2 * pair + seg++;
+        return true;
+    }
+};
+
+// Chunks idx, idx + parts, ... of a unit's tokens, of one warp's lane quarter of an
+// accumulator (lane_addr), to the outputs, or to the unit's partial tile (part: this
+// thread's row of its first token).
+template <int EPI>
+BQ_DEVINL void pair_drain(const PairParams& p, uint32_t lane_addr, int m0, int n, float* part, int idx, int parts)
+{
+    constexpr int T = kEpiTokens<EPI>;
+    const EpiRow<EPI> row = epi_row<EPI>(p.e, n, p.N);
+#pragma unroll 1
+    for (int c = T * idx; c < p.bn && m0 + c < p.M; c += T * parts) {
+        uint32_t v[T];
+        if constexpr (T == 16) tmem_ld_32x32b_x16(lane_addr + (uint32_t)c, v);
+        else tmem_ld_32x32b_x8(lane_addr + (uint32_t)c, v);
+        tmem_wait_ld();
+        if (part) {
+#pragma unroll
+            for (int j = 0; j < T; ++j) part[(int64_t)(c + j) * 256] = __uint_as_float(v[j]);
+        } else {
+            epi_store<EPI, T>(p.e, row, v, m0 + c, p.M, p.N);
+        }
+    }
+}
 
 // Tensor maps: A of matrix 0 and 1 (K-major: box 64 x 128 rows; MN-major: box 64 x
 // 64 rows, two boxes side by side per stage), B likewise (box 64 x bn / 2 tokens).
@@ -157,7 +217,6 @@ tc_pair_kernel(const __grid_constant__ CUtensorMap tm_a0, const __grid_constant_
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_ctarank();
     const int S = p.stages;
-    const int nk = p.seg_blocks * p.segs;
     const uint32_t b_bytes = (uint32_t)p.bn * 64u;             // this CTA's half of the token tile
     const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
     const uint32_t a_base = base, b_base = base + (uint32_t)S * kPairABytes;
@@ -171,12 +230,6 @@ tc_pair_kernel(const __grid_constant__ CUtensorMap tm_a0, const __grid_constant_
     volatile uint32_t* tmem_slot_ptr =
         reinterpret_cast<volatile uint32_t*>(smem_raw + (base - smem_u32(smem_raw)) + (tmem_slot - base));
 
-    const int units = p.dp_tiles + (p.tiles - p.dp_tiles) * p.splits;
-    const int first = blockIdx.x >> 1, stride = gridDim.x >> 1;
-    auto unit_tile = [&](int u) { return u < p.dp_tiles ? u : p.dp_tiles + (u - p.dp_tiles) / p.splits; };
-    auto unit_split = [&](int u) { return u < p.dp_tiles ? 0 : (u - p.dp_tiles) % p.splits; };
-    auto kb_begin = [&](int u) { return u < p.dp_tiles ? 0 : (int)((int64_t)unit_split(u) * nk / p.splits); };
-    auto kb_end = [&](int u) { return u < p.dp_tiles ? nk : (int)((int64_t)(unit_split(u) + 1) * nk / p.splits); };
     auto tile_r0 = [&](int t) { return (t / p.m_tiles) * 256 + (int)rank * 128; };   // this CTA's first D row
     auto tile_m0 = [&](int t) { return (t % p.m_tiles) * p.bn; };
 
@@ -209,11 +262,9 @@ tc_pair_kernel(const __grid_constant__ CUtensorMap tm_a0, const __grid_constant_
             int s = 0, issued = 0;
             uint32_t ph = 0;
             bool ok = true;
-            for (int u = first; u < units && ok; u += stride) {
-                const int t = unit_tile(u);
-                const int r0 = tile_r0(t), m0 = tile_m0(t) + (int)rank * (p.bn / 2);
-                const int kb1 = kb_end(u);
-                for (int it = kb_begin(u); it < kb1; ++it) {
+            for (PairUnits u(p); ok && u.next();) {
+                const int r0 = tile_r0(u.tile), m0 = tile_m0(u.tile) + (int)rank * (p.bn / 2);
+                for (int it = u.kb0; it < u.kb1; ++it) {
                     if (!mbar_wait(empty_bar(s), ph ^ 1u)) { ok = false; break; }
                     const bool second = it >= p.seg_blocks;
                     const int k0 = (second ? it - p.seg_blocks : it) * 64;
@@ -261,9 +312,9 @@ tc_pair_kernel(const __grid_constant__ CUtensorMap tm_a0, const __grid_constant_
             int s = 0, lt = 0;
             uint32_t ph = 0;
             bool ok = true;
-            for (int u = first; u < units && ok; u += stride, ++lt) {
+            for (PairUnits u(p); ok && u.next(); ++lt) {
                 const int acc = lt & 1;
-                const int kb0 = kb_begin(u), kb1 = kb_end(u);
+                const int kb0 = u.kb0, kb1 = u.kb1;
                 if (!mbar_wait_warp(tempty_bar(acc), ((uint32_t)(lt >> 1) & 1u) ^ 1u)) break;
                 tc_fence_after();
                 const uint32_t d_tmem = tmem_base + (uint32_t)(acc * kPairAccCols);
@@ -291,51 +342,15 @@ tc_pair_kernel(const __grid_constant__ CUtensorMap tm_a0, const __grid_constant_
         const int q4 = warp & 3, half = warp >> 2;
         const uint32_t lane_addr0 = tmem_base + ((uint32_t)(32 * q4) << 16);
         int lt = 0;
-        for (int u = first; u < units; u += stride, ++lt) {
-            const int t = unit_tile(u), acc = lt & 1;
+        for (PairUnits u(p); u.next(); ++lt) {
+            const int t = u.tile, acc = lt & 1;
             const int r = 32 * q4 + lane;                      // row of this CTA's half of the tile
             const int m0 = tile_m0(t);
             const int n = epi_tile_rows<EPI>(tile_r0(t)) + epi_out_row<EPI>(r);
-            const bool split = p.splits > 1 && u >= p.dp_tiles;
-            float* part = split ? p.ws + ((int64_t)unit_split(u) * (p.tiles - p.dp_tiles) + (t - p.dp_tiles)) *
-                                             ((int64_t)p.bn * 256) + (int)rank * 128 + r
-                                : nullptr;
-            const EpiRow<EPI> row = epi_row<EPI>(p.e, n, p.N);
+            float* part = u.slot < 0 ? nullptr : p.ws + (int64_t)u.slot * ((int64_t)p.bn * 256) + (int)rank * 128 + r;
             if (!mbar_wait_warp(tfull_bar(acc), (uint32_t)(lt >> 1) & 1u)) break;
             tc_fence_after();
-            const uint32_t lane_addr = lane_addr0 + (uint32_t)(acc * kPairAccCols);
-            // this warp's 16-column chunks: every second one; the next load is in flight
-            // while a chunk is converted and stored
-            auto drain = [&](auto&& take) {
-                uint32_t va[16], vb[16];
-                int c = 16 * half;
-                tmem_ld_32x32b_x16(lane_addr + (uint32_t)c, va);
-                for (;;) {
-                    tmem_wait_ld();
-                    bool more = c + 32 < p.bn;
-                    if (more) tmem_ld_32x32b_x16(lane_addr + (uint32_t)(c + 32), vb);
-                    take(va, c);
-                    if (!more) break;
-                    c += 32;
-                    tmem_wait_ld();
-                    more = c + 32 < p.bn;
-                    if (more) tmem_ld_32x32b_x16(lane_addr + (uint32_t)(c + 32), va);
-                    take(vb, c);
-                    if (!more) break;
-                    c += 32;
-                }
-                tmem_wait_ld();
-            };
-            if (split)
-                drain([&](const uint32_t (&v)[16], int c) {
-                    float* pt = part + (int64_t)c * 256;
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) pt[j * 256] = __uint_as_float(v[j]);
-                });
-            else
-                drain([&](const uint32_t (&v)[16], int c) {
-                    if (m0 + c < p.M) epi_store16<EPI>(p.e, row, v, m0 + c, p.M, p.N);
-                });
+            pair_drain<EPI>(p, lane_addr0 + (uint32_t)(acc * kPairAccCols), m0, n, part, half, 2);
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive_cluster(map_to_cta(tempty_bar(acc), 0));
