@@ -48,14 +48,14 @@ struct PairPlan {
     size_t ws_bytes = 0;
 };
 
-// Token tile and split of the last round for `rows` D rows, M tokens and nk 64-element
-// blocks of the reduction; fixed_bytes of shared memory and per stage a_bytes of weights.
+// Token tile and split of the last round for `rows` D rows, M tokens and nk blocks of the
+// reduction; shared memory: fixed_bytes, and per stage a_bytes and tok_bytes per token.
 // Cost model in SM clocks: a block costs the larger of the MMA's and its issue
 // (block_mma per token of the tile) and of bringing the weights in (min_block), a unit of
 // work a fixed start, and what the last unit leaves to be drained; a split last round
 // adds the partial tiles' traffic and the kernel that sums them.
 bool plan_pair(int64_t rows, int64_t M, int64_t nk, int num_sms, int smem_optin, int fixed_bytes, int a_bytes,
-               double min_block, double block_mma, PairPlan* pl)
+               int tok_bytes, double min_block, double block_mma, PairPlan* pl)
 {
     const int64_t pairs = std::max(num_sms / 2, 1), rtiles = (rows + 255) / 256;
     const int64_t maxb = std::min<int64_t>(256, (M + 31) / 32 * 32);
@@ -77,17 +77,17 @@ bool plan_pair(int64_t rows, int64_t M, int64_t nk, int num_sms, int smem_optin,
         consider((double)((tiles + pairs - 1) / pairs) * unit((double)nk) + drain, tiles, 0);
         const int64_t dp = tiles / pairs * pairs, tail = tiles - dp;
         if (tail == 0) continue;
-        // ranges of at least 4 blocks, at least one per tile
-        const int64_t tp = std::max<int64_t>(tail, std::min<int64_t>(pairs, tail * nk / 4));
+        // ranges of at least 2 blocks, at least one per tile
+        const int64_t tp = std::max<int64_t>(tail, std::min<int64_t>(pairs, tail * nk / 2));
         const double range = (double)((tail * nk + tp - 1) / tp);
         const double traffic = (double)(tp + tail) * b * 256.0 * 8.0 / 2500.0;
         consider((double)(dp / pairs) * unit((double)nk) + unit(range) + 1500.0 + drain + 5000.0 + traffic, dp, tp);
     }
     pl->pairs = (int)pairs;
     pl->split.blocks = (int)nk;
-    pl->stages = std::min<int>(kFpMaxTok, (smem_optin - 1024 - 512 - fixed_bytes) / (a_bytes + pl->bn * 64));
+    pl->stages = std::min<int>(kFpMaxTok, (smem_optin - 1024 - 512 - fixed_bytes) / (a_bytes + pl->bn * tok_bytes));
     pl->ws_bytes = pl->split.tail ? (size_t)2 * (size_t)pl->split.tail_pairs * (size_t)pl->bn * 256u * 4u : 0u;
-    return pl->stages >= 3 && pl->tiles <= INT32_MAX / 256 && nk <= INT32_MAX / 2;
+    return pl->stages >= 2 && pl->tiles <= INT32_MAX / 256 && nk <= INT32_MAX / 2;
 }
 
 unsigned reduce_grid(int64_t items, const DeviceInfo& di)
@@ -278,8 +278,8 @@ bq_status launch_ring(WFmt fmt, const uint16_t* x, const QMat* w, const EpiParam
 }
 
 // ------------------------------------------------------------------ codes dequantized inside the pair product
-// Shape of the packed scales: whole 256-row tiles and 64-column blocks forward, whole
-// 64-row blocks and 256-column tiles for the gradient.
+// Shape of the packed scales: whole 256-row tiles and 128-column blocks forward, whole
+// 128-row blocks and 256-column tiles for the gradient.
 struct ScalePack {
     int64_t rows, cols, mat;        // rows per column block, padded columns, words per matrix (gradient)
     size_t bytes;
@@ -289,13 +289,13 @@ ScalePack scale_pack(bool mn, int mats, int64_t N, int64_t K)
 {
     ScalePack s;
     if (mn) {
-        s.rows = (N + 63) / 64 * 64;
+        s.rows = (N + 127) / 128 * 128;
         s.cols = (K + 255) / 256 * 256;
         s.mat = s.rows * (s.cols / 32);
         s.bytes = up256((size_t)mats * (size_t)s.mat * 4u);
     } else {
         s.rows = ((mats == 2 ? 32 * ((N + 15) / 16) : N) + 255) / 256 * 256;
-        s.cols = (K + 63) / 64 * 64;
+        s.cols = (K + 127) / 128 * 128;
         s.mat = 0;
         s.bytes = up256((size_t)s.rows * (size_t)(s.cols / 32) * 4u);
     }
@@ -364,14 +364,14 @@ bq_status launch_fused_pair(const DeviceInfo& di, int dev, const PairPlan& pl, c
     p.q.stages = pl.stages;
     p.q.m_tiles = (int)((M + pl.bn - 1) / pl.bn);
     p.q.tiles = (int)pl.tiles;
-    p.q.seg_blocks = (int)((red + 63) / 64);
+    p.q.seg_blocks = (int)((red + 127) / 128);
     p.q.segs = MN ? mats : 1;
     p.q.split = pl.split;
     p.q.ws = reinterpret_cast<float*>(ws);
     // every pair when there are whole rounds before the tail: the units are dealt by pair
     const unsigned grid = 2u * (unsigned)std::min<int64_t>(pl.split.tail && pl.split.dp_tiles ? pl.pairs
                                                            : pl.split.tail ? pl.split.tail_pairs : pl.tiles, pl.pairs);
-    const size_t smem = std::max<size_t>(1024 + fp_fixed_bytes(MODE) + (size_t)pl.stages * (size_t)pl.bn * 64u + 512,
+    const size_t smem = std::max<size_t>(1024 + fp_fixed_bytes(MODE) + (size_t)pl.stages * (size_t)pl.bn * 128u + 512,
                                          (size_t)di.max_smem_optin / 2 + 1024);   // one CTA per SM (all of TMEM)
     s = launch_pdl_dim(kern, dim3(grid), kFpThreads, smem, st, ta[0], ta[1], tb[0], tb[1], p);
     return s != BQ_OK ? s : launch_reduce<EPI>(di, pl, p.q, st);
@@ -408,19 +408,20 @@ struct EpiWs {
 
 // Q4_0 and affine 4- and 8-bit codes are dequantized inside the product; the others
 // (whose rows of a stage are not 16-byte multiples) through a bf16 copy.
-bool plan_epi_product(WFmt fmt, int64_t rows, int64_t M, int64_t nk, int num_sms, int smem_optin, EpiWs* w)
+bool plan_epi_product(WFmt fmt, int64_t rows, int64_t M, int segs, int64_t red, int num_sms, int smem_optin, EpiWs* w)
 {
     w->rows = rows;
     w->fused = has_fast_paths(fmt);
-    return w->fused ? plan_pair(rows, M, nk, num_sms, smem_optin, (int)fp_fixed_bytes(fp_mode(fmt)), 0, 520.0, 2.5,
-                                &w->pl)
-                    : plan_pair(rows, M, nk, num_sms, smem_optin, 0, (int)kPairABytes, 400.0, 2.5, &w->pl);
+    if (w->fused)       // blocks of 128
+        return plan_pair(rows, M, segs * ((red + 127) / 128), num_sms, smem_optin, (int)fp_fixed_bytes(fp_mode(fmt)), 0, 128,
+                         1000.0, 4.5, &w->pl);
+    return plan_pair(rows, M, segs * ((red + 63) / 64), num_sms, smem_optin, 0, (int)kPairABytes, 64, 400.0, 2.5, &w->pl);
 }
 
 bool plan_forward(WFmt fmt, int mats, int64_t M, int64_t N, int64_t K, int num_sms, int smem_optin, EpiWs* w)
 {
     // glu: tiles of 32 rows per 16 outputs
-    if (!plan_epi_product(fmt, mats == 2 ? 32 * ((N + 15) / 16) : N, M, (K + 63) / 64, num_sms, smem_optin, w)) return false;
+    if (!plan_epi_product(fmt, mats == 2 ? 32 * ((N + 15) / 16) : N, M, 1, K, num_sms, smem_optin, w)) return false;
     w->off_split = w->fused ? scale_pack(false, mats, N, K).bytes : up256((size_t)w->rows * (size_t)K * 2u);
     w->bytes = w->off_split + w->pl.ws_bytes;
     return true;
@@ -428,7 +429,7 @@ bool plan_forward(WFmt fmt, int mats, int64_t M, int64_t N, int64_t K, int num_s
 
 bool plan_backward(WFmt fmt, int mats, int64_t M, int64_t N, int64_t K, int num_sms, int smem_optin, EpiWs* w)
 {
-    if (K > 0 && !plan_epi_product(fmt, K, M, mats * ((N + 63) / 64), num_sms, smem_optin, w)) return false;
+    if (K > 0 && !plan_epi_product(fmt, K, M, mats, N, num_sms, smem_optin, w)) return false;
     w->pitch = (N + 7) / 8 * 8;
     // blocks of 8 warps over rows of tokens: about 8 blocks per SM, at least 32 rows each
     const int64_t cols = std::max<int64_t>(1, (N + 255) / 256);

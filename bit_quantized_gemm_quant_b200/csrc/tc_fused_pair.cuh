@@ -6,7 +6,10 @@
 //              matrices summed, for the gated form)
 //
 // Tiles, pairs, accumulators and units of work are tc_pair.cuh's: 256 D rows x bn
-// tokens per pair (cta_group::2), two accumulators of 256 columns.  Here the weight
+// tokens per pair (cta_group::2), two accumulators of 256 columns; a block of the
+// reduction is 128 elements here, two halves of one swizzle atom each.  (The MMA warp
+// spends 150 clocks on each of a block's two waits beside 16 busy dequant warps: at 64
+// elements a block that, not the tensor core, set the pace, 640 clocks a block.)  Here the weight
 // tile of a stage arrives as codes: 128 x 64 weights per CTA are 4 KB (8-bit: 8 KB)
 // where their bf16 form is 16 KB, so a stage moves 20 KB per SM through L2 instead of
 // 32, and no bf16 copy of W is written to or read from memory.  16 dequant warps, four
@@ -22,7 +25,7 @@
 // 1130: a tile slot or stage was then held through a copy's round trip, the wait for a
 // group and the product, longer than the ring covers at the MMA's 512 clocks a block.
 // Barriers: cfull / cempty (codes, each CTA's own), bfull (tokens of both CTAs, the
-// leader's), ready (a tile, the leader's; 4 dequant warps of each CTA arrive), consumed
+// leader's), ready (a tile, the leader's; 8 dequant warps of each CTA arrive), consumed
 // (one per block, each CTA's own; the MMA's commit arrives on both and thereby frees the
 // block's token tile and weight tile).
 //
@@ -46,17 +49,22 @@ constexpr int kFpCodeWarp = kFpTokWarp + 1;     // producer of codes
 constexpr int kFpMmaWarp = kFpCodeWarp + 1;
 constexpr int kFpThreads = 32 * (kFpMmaWarp + 1);
 constexpr uint32_t kFpScaleBytes = 1024;        // packed scales of a stage
-constexpr int kFpTiles = 6;                     // bf16 weight tiles
-constexpr int kFpMaxCodes = 8;
+// Code stages (half a block each), a multiple of the groups, so that a stage always belongs
+// to the same group: a barrier's phases are told apart by parity alone, and a group that
+// had not waited for the stage's last fill (made for another group, and possibly landing
+// after later ones) could take the fill before it for its own.
+constexpr int kFpCodes = 4;
+static_assert(kFpCodes % 4 == 0, "a code stage serves one dequant group");
+constexpr int kFpMaxTiles = 3;
 constexpr int kFpConsumed = 16;                 // consumed barriers, at least the depth of each ring
-constexpr int kFpMaxTok = 8;                    // token tiles
+constexpr int kFpMaxTok = 8;                    // token tiles of a block
 
 __host__ __device__ constexpr uint32_t fp_code_bytes(int mode) { return mode == kModeAff8 ? 8192u : 4096u; }
-__host__ __device__ constexpr int fp_codes(int mode) { return mode == kModeAff8 ? 6 : 8; }   // code stages
+__host__ __device__ constexpr int fp_tiles(int mode) { return mode == kModeAff8 ? 2 : 3; }   // bf16 weight tiles of a block
 // Shared memory beside the token tiles
 __host__ __device__ constexpr uint32_t fp_fixed_bytes(int mode)
 {
-    return kFpTiles * kPairABytes + (uint32_t)fp_codes(mode) * (fp_code_bytes(mode) + kFpScaleBytes);
+    return (uint32_t)fp_tiles(mode) * 2u * kPairABytes + kFpCodes * (fp_code_bytes(mode) + kFpScaleBytes);
 }
 
 struct FpParams {
@@ -122,16 +130,16 @@ __global__ void __launch_bounds__(256) scale_pack_kernel(const __grid_constant__
     }
 }
 
-// The dequant warps' part: group grp (4 warps) takes the blocks at positions grp, grp + 4,
-// ... of the CTA's `left` blocks.  A thread expands 64 weights: forward, row r of the tile;
-// gradient, row r of the block, outputs 64 hk .. of the tile.  (A function of its own:
+// The dequant warps' part: group grp (4 warps) takes the half-blocks at positions grp, grp
+// + 4, ... of the CTA's `left` ones.  A thread expands 64 weights: forward, row r of the tile;
+// gradient, row r of the half-block, outputs 64 hk .. of the tile.  (A function of its own:
 // inlined, the code that follows it for these warps slowed this loop by 13%.)
 template <int MODE, bool MN, int EPI>
 __device__ __noinline__ void fp_dequantize(int left, uint32_t a_base, uint32_t c_base, uint32_t cfull0, uint32_t cempty0,
                                            uint32_t ready0, uint32_t consumed0)
 {
     constexpr uint32_t kCBytes = fp_code_bytes(MODE), kCStage = kCBytes + kFpScaleBytes;
-    constexpr int kBits = MODE == kModeAff8 ? 8 : 4, kCodes = fp_codes(MODE);
+    constexpr int kBits = MODE == kModeAff8 ? 8 : 4, kTiles = fp_tiles(MODE);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int grp = warp >> 2, w4 = warp & 3;
     const int r = MN ? 32 * (w4 & 1) + lane : 32 * w4 + lane;
@@ -142,12 +150,12 @@ __device__ __noinline__ void fp_dequantize(int left, uint32_t a_base, uint32_t c
     // the units of a row, as the copy swizzles them
     const int sw = kRowBytes == 32 ? (crow >> 2) & 1 : kRowBytes == 64 ? (crow >> 1) & 3 : crow & 7;
     const uint32_t code_row = c_base + (uint32_t)(crow * kRowBytes);
-    const uint32_t tile_row = a_base + (uint32_t)(hk * (int)(kPairABytes / 2) + r * 128);
+    const uint32_t tile_row = a_base + (uint32_t)((grp & 1) * (int)kPairABytes + hk * (int)(kPairABytes / 2) + r * 128);
     const uint32_t scale_row = c_base + kCBytes + (uint32_t)(MN ? r * 16 + hk * 8 : r * 8);
-    int c = grp, a = grp;                           // code stage and tile slot of this block
+    int c = grp, a = grp >> 1, block = grp >> 1;    // code stage, tile and block of this half
     uint32_t ph = 0;
     bool ok = true;
-    for (int pos = grp; pos < left; pos += 4) {
+    for (int pos = grp; pos < left; pos += 4, block += 2) {
         ok = mbar_wait_warp(cfull0 + 8u * (uint32_t)c, ph);
         if (!ok) break;
         const uint32_t codes = code_row + (uint32_t)c * kCStage;
@@ -157,7 +165,7 @@ __device__ __noinline__ void fp_dequantize(int left, uint32_t a_base, uint32_t c
         for (int i = 0; i < kUnits; ++i) raw[i] = ld_shared_v4(codes + (uint32_t)(((hk * kUnits + i) ^ sw) << 4));
         __syncwarp();
         if (lane == 0) mbar_arrive(cempty0 + 8u * (uint32_t)c);
-        const uint32_t tile = tile_row + (uint32_t)a * kPairABytes;
+        const uint32_t tile = tile_row + (uint32_t)a * (2u * kPairABytes);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             uint32_t wv[16];
@@ -168,8 +176,8 @@ __device__ __noinline__ void fp_dequantize(int left, uint32_t a_base, uint32_t c
                 deq_aff4_half(raw[h], prmt(w, w, 0x1010u), prmt(w, w, 0x3232u), wv);
             else
                 deq_aff8_half(raw[2 * h], raw[2 * h + 1], __uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u), wv);
-            if (h == 0 && pos >= kFpTiles) {           // the slot's last block is consumed
-                const int q = pos - kFpTiles;
+            if (h == 0 && block >= kTiles) {           // the tile's last block is consumed
+                const int q = block - kTiles;
                 ok = mbar_wait(consumed0 + 8u * (uint32_t)(q & (kFpConsumed - 1)), (uint32_t)(q / kFpConsumed) & 1u);
                 __syncwarp();
             }
@@ -183,8 +191,8 @@ __device__ __noinline__ void fp_dequantize(int left, uint32_t a_base, uint32_t c
         fence_proxy_async_smem();                    // the MMA reads the tile through the async proxy
         __syncwarp();
         if (lane == 0) mbar_arrive_cluster(ready0 + 8u * (uint32_t)a);
-        if ((c += 4) >= kCodes) { c -= kCodes; ph ^= 1u; }
-        if ((a += 4) >= kFpTiles) a -= kFpTiles;
+        if ((c += 4) >= kFpCodes) { c -= kFpCodes; ph ^= 1u; }
+        a = (a + 2) % kTiles;
     }
 }
 
@@ -198,23 +206,23 @@ tc_fused_pair_kernel(const __grid_constant__ CUtensorMap tm_a0, const __grid_con
                      const __grid_constant__ FpParams fp)
 {
     constexpr uint32_t kCBytes = fp_code_bytes(MODE), kCStage = kCBytes + kFpScaleBytes;
-    constexpr int kFpCodes = fp_codes(MODE);
+    constexpr int kTiles = fp_tiles(MODE);
     constexpr int kBits = MODE == kModeAff8 ? 8 : 4;
     const PairParams& p = fp.q;
     extern __shared__ uint8_t smem_raw[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_ctarank();
-    const int NB = p.stages;                       // token tiles in the ring
+    const int NB = p.stages;                       // token tiles (of a block) in the ring
     const uint32_t b_bytes = (uint32_t)p.bn * 64u;
     const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
-    const uint32_t a_base = base, c_base = a_base + kFpTiles * kPairABytes, b_base = c_base + kFpCodes * kCStage;
-    const uint32_t bar_base = b_base + (uint32_t)NB * b_bytes;
+    const uint32_t a_base = base, c_base = a_base + kTiles * 2u * kPairABytes, b_base = c_base + kFpCodes * kCStage;
+    const uint32_t bar_base = b_base + (uint32_t)NB * 2u * b_bytes;
     auto cfull_bar = [&](int i) { return bar_base + 8u * (uint32_t)i; };
     auto cempty_bar = [&](int i) { return bar_base + 8u * (uint32_t)(kFpCodes + i); };
     auto ready_bar = [&](int i) { return bar_base + 8u * (uint32_t)(2 * kFpCodes + i); };
-    auto bfull_bar = [&](int i) { return bar_base + 8u * (uint32_t)(2 * kFpCodes + kFpTiles + i); };
-    auto consumed_bar = [&](int i) { return bar_base + 8u * (uint32_t)(2 * kFpCodes + kFpTiles + kFpMaxTok + i); };
-    constexpr int kBars = 2 * kFpCodes + kFpTiles + kFpMaxTok + kFpConsumed;
+    auto bfull_bar = [&](int i) { return bar_base + 8u * (uint32_t)(2 * kFpCodes + kFpMaxTiles + i); };
+    auto consumed_bar = [&](int i) { return bar_base + 8u * (uint32_t)(2 * kFpCodes + kFpMaxTiles + kFpMaxTok + i); };
+    constexpr int kBars = 2 * kFpCodes + kFpMaxTiles + kFpMaxTok + kFpConsumed;
     auto tfull_bar = [&](int b) { return bar_base + 8u * (uint32_t)(kBars + b); };
     auto tempty_bar = [&](int b) { return bar_base + 8u * (uint32_t)(kBars + 2 + b); };
     const uint32_t done_bar = bar_base + 8u * (uint32_t)(kBars + 4);
@@ -222,7 +230,7 @@ tc_fused_pair_kernel(const __grid_constant__ CUtensorMap tm_a0, const __grid_con
     static_assert(8 * (kBars + 6) <= 512, "barriers fit the space the host reserves");
     volatile uint32_t* tmem_slot_ptr =
         reinterpret_cast<volatile uint32_t*>(smem_raw + (base - smem_u32(smem_raw)) + (tmem_slot - base));
-    // wait until the block at position pos (>= 0) is consumed
+    // wait until the pos-th block (>= 0) is consumed
     auto wait_consumed = [&](int pos) {
         return mbar_wait(consumed_bar(pos & (kFpConsumed - 1)), (uint32_t)(pos / kFpConsumed) & 1u);
     };
@@ -235,7 +243,7 @@ tc_fused_pair_kernel(const __grid_constant__ CUtensorMap tm_a0, const __grid_con
             mbar_init(cfull_bar(i), 1);
             mbar_init(cempty_bar(i), 4);
         }
-        for (int i = 0; i < kFpTiles; ++i) mbar_init(ready_bar(i), 8);
+        for (int i = 0; i < kTiles; ++i) mbar_init(ready_bar(i), 16);
         for (int i = 0; i < NB; ++i) mbar_init(bfull_bar(i), 1);
         for (int i = 0; i < kFpConsumed; ++i) mbar_init(consumed_bar(i), 1);
         for (int b = 0; b < 2; ++b) {
@@ -278,9 +286,11 @@ tc_fused_pair_kernel(const __grid_constant__ CUtensorMap tm_a0, const __grid_con
                 for (int it = u.kb0; it < u.kb1; ++it, ++pos) {
                     if (pos >= NB && !wait_consumed(pos - NB)) { ok = false; break; }
                     const bool second = it >= p.seg_blocks;
-                    if (rank == 0) mbar_arrive_expect_tx(bfull_bar(b), 2u * b_bytes);
-                    tma_load_2d_pair(b_base + (uint32_t)b * b_bytes, second ? &tm_b1 : &tm_b0, map_to_cta(bfull_bar(b), 0),
-                                     (second ? it - p.seg_blocks : it) * 64, m0);
+                    if (rank == 0) mbar_arrive_expect_tx(bfull_bar(b), 4u * b_bytes);
+                    const uint32_t dst = b_base + (uint32_t)b * 2u * b_bytes, bar = map_to_cta(bfull_bar(b), 0);
+                    const int k0 = (second ? it - p.seg_blocks : it) * 128;
+                    tma_load_2d_pair(dst, second ? &tm_b1 : &tm_b0, bar, k0, m0);
+                    tma_load_2d_pair(dst + b_bytes, second ? &tm_b1 : &tm_b0, bar, k0 + 64, m0);
                     if (++b == NB) b = 0;
                 }
             }
@@ -301,12 +311,12 @@ tc_fused_pair_kernel(const __grid_constant__ CUtensorMap tm_a0, const __grid_con
             bool ok = true;
             for (PairUnits u(p); ok && u.next();) {
                 const int r0 = tile_r0(u.tile);
-                for (int it = u.kb0; it < u.kb1; ++it, ++issued) {
+                for (int i2 = 2 * u.kb0; i2 < 2 * u.kb1; ++i2, ++issued) {      // half-blocks
                     if (!mbar_wait(cempty_bar(c), ph ^ 1u)) { ok = false; break; }
                     const uint32_t dst = c_base + (uint32_t)c * kCStage;
                     mbar_arrive_expect_tx(cfull_bar(c), kCStage);
-                    const bool second = MN && it >= p.seg_blocks;
-                    const int kb = second ? it - p.seg_blocks : it;
+                    const bool second = MN && i2 >= 2 * p.seg_blocks;
+                    const int kb = second ? i2 - 2 * p.seg_blocks : i2;
                     bulk_load(dst + kCBytes,
                               fp.scales + (MN ? (second ? fp.pack_mat : 0) + ((int64_t)(r0 / 128) * fp.pack_rows + kb * 64) * 4
                                               : ((int64_t)kb * fp.pack_rows + r0) * 2),
@@ -314,10 +324,10 @@ tc_fused_pair_kernel(const __grid_constant__ CUtensorMap tm_a0, const __grid_con
                     if constexpr (MN) {
                         tma_load_2d(dst, second ? &tm_a1 : &tm_a0, cfull_bar(c), r0 * kBits / 8, kb * 64);
                     } else if constexpr (EPI == kEpiGlu) {
-                        tma_load_2d(dst, &tm_a0, cfull_bar(c), it * (64 * kBits / 8), r0 / 2);
-                        tma_load_2d(dst + kCBytes / 2, &tm_a1, cfull_bar(c), it * (64 * kBits / 8), r0 / 2);
+                        tma_load_2d(dst, &tm_a0, cfull_bar(c), kb * (64 * kBits / 8), r0 / 2);
+                        tma_load_2d(dst + kCBytes / 2, &tm_a1, cfull_bar(c), kb * (64 * kBits / 8), r0 / 2);
                     } else {
-                        tma_load_2d(dst, &tm_a0, cfull_bar(c), it * (64 * kBits / 8), r0);
+                        tma_load_2d(dst, &tm_a0, cfull_bar(c), kb * (64 * kBits / 8), r0);
                     }
                     if (++c == kFpCodes) { c = 0; ph ^= 1u; }
                 }
@@ -350,14 +360,15 @@ tc_fused_pair_kernel(const __grid_constant__ CUtensorMap tm_a0, const __grid_con
                     if (!mbar_wait_warp(bfull_bar(b), phb) || !mbar_wait_warp(ready_bar(a), pha)) { ok = false; break; }
                     tc_fence_after();
                     if (elect_one()) {
-                        umma_kblock_pair<MN ? 128 : 2>(d_tmem, a_lo0 + (uint32_t)a * (kPairABytes >> 4),
-                                                       b_lo0 + (uint32_t)b * (b_bytes >> 4), desc_hi, idesc, it > kb0);
+                        const uint32_t al = a_lo0 + (uint32_t)a * (kPairABytes >> 3), bl = b_lo0 + (uint32_t)b * (b_bytes >> 3);
+                        umma_kblock_pair<MN ? 128 : 2>(d_tmem, al, bl, desc_hi, idesc, it > kb0);
+                        umma_kblock_pair<MN ? 128 : 2>(d_tmem, al + (kPairABytes >> 4), bl + (b_bytes >> 4), desc_hi, idesc, 1u);
                         umma_commit_pair(consumed_bar(c));
                     }
                     __syncwarp();
                     c = (c + 1) & (kFpConsumed - 1);
                     if (++b == NB) { b = 0; phb ^= 1u; }
-                    if (++a == kFpTiles) { a = 0; pha ^= 1u; }
+                    if (++a == kTiles) { a = 0; pha ^= 1u; }
                 }
                 if (elect_one()) umma_commit_pair(tfull_bar(acc));
                 __syncwarp();
@@ -380,8 +391,8 @@ tc_fused_pair_kernel(const __grid_constant__ CUtensorMap tm_a0, const __grid_con
         }
     } else {
         // ---------------- dequantization ----------------
-        int left = 0;                                    // blocks of this CTA's sequence
-        for (PairUnits u(p); u.next();) left += u.kb1 - u.kb0;
+        int left = 0;                                    // half-blocks of this CTA's sequence
+        for (PairUnits u(p); u.next();) left += 2 * (u.kb1 - u.kb0);
         fp_dequantize<MODE, MN, EPI>(left, a_base, c_base, cfull_bar(0), cempty_bar(0), map_to_cta(ready_bar(0), 0),
                                      consumed_bar(0));
     }
