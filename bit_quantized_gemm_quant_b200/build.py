@@ -15,7 +15,7 @@ MAIN = os.path.join(CSRC, "bqgemm.cu")
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
-    "-O3", "-lineinfo", "-std=c++17", "--split-compile", "0",
+    "-O3", "-lineinfo", "-std=c++17",
     "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
     "-shared", "--expt-relaxed-constexpr",
 ]
