@@ -90,11 +90,6 @@ bool plan_pair(int64_t rows, int64_t M, int64_t nk, int num_sms, int smem_optin,
     return pl->stages >= 2 && pl->tiles <= INT32_MAX / 256 && nk <= INT32_MAX / 2;
 }
 
-unsigned reduce_grid(int64_t items, const DeviceInfo& di)
-{
-    return (unsigned)std::max<int64_t>(1, std::min<int64_t>((items + 255) / 256, 8 * (int64_t)di.num_sms));
-}
-
 // launch_pdl with a 3-D grid.
 template <typename KernelT, typename... Args>
 bq_status launch_pdl_dim(KernelT kern, dim3 grid, int threads, size_t smem, cudaStream_t st, const Args&... args)
@@ -121,9 +116,9 @@ template <int EPI>
 bq_status launch_reduce(const DeviceInfo& di, const PairPlan& pl, const PairParams& p, cudaStream_t st)
 {
     if (pl.split.tail == 0) return BQ_OK;
-    return launch_pdl_dim(epi_reduce_kernel<EPI>,
-                          dim3(reduce_grid((int64_t)pl.split.tail * pl.bn * (epi_tile_rows<EPI>(256) / 4), di)), 256, 0, st,
-                          (const float*)p.ws, p.e, p.M, p.N, p.bn, p.m_tiles, p.split);
+    const int64_t blocks = (int64_t)pl.split.tail * ((pl.bn + kReduceTokens - 1) / kReduceTokens);
+    return launch_pdl_dim(epi_reduce_kernel<EPI>, dim3((unsigned)blocks), 256, 0, st, (const float*)p.ws, p.e, p.M, p.N, p.bn,
+                          p.m_tiles, p.split);
 }
 
 // D = sum over segs of A_i . B_i^T with the epilogue e.  A_i: bf16 weights, a_rows

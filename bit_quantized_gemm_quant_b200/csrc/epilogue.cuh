@@ -278,45 +278,106 @@ struct TailSplit {
     __host__ __device__ int64_t range_begin(int i) const { return (int64_t)i * tail * blocks / tail_pairs; }
 };
 
+// Four outputs n0 .. n0 + 3 (n0 a multiple of 4) of token m from their sums; 8-byte stores
+// where rows start on 8 bytes.
+template <int EPI>
+BQ_DEVINL void epi_four(const EpiParams& e, const float (&s)[4], const float (&s2)[4], int64_t m, int n0, int N)
+{
+    if ((N & 3) != 0) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (n0 + k < N) epi_one<EPI>(e, s[k], s2[k], m, n0 + k, N);
+        return;
+    }
+    const int64_t o = m * N + n0;
+    auto four = [](const uint16_t* q, float (&v)[4]) {
+        const uint2 w = *reinterpret_cast<const uint2*>(q);
+        v[0] = __uint_as_float(w.x << 16); v[1] = __uint_as_float(w.x & 0xFFFF0000u);
+        v[2] = __uint_as_float(w.y << 16); v[3] = __uint_as_float(w.y & 0xFFFF0000u);
+    };
+    auto put = [](uint16_t* q, const float (&v)[4]) {
+        *reinterpret_cast<uint2*>(q) = make_uint2(pack_bf16x2_rn(v[0], v[1]), pack_bf16x2_rn(v[2], v[3]));
+    };
+    float z[4] = {s[0], s[1], s[2], s[3]}, v[4];
+    if (EPI != kEpiPlain && e.bias) {
+        four(e.bias + n0, v);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) z[k] += v[k];
+    }
+    if constexpr (EPI == kEpiGlu) {
+        float u[4] = {s2[0], s2[1], s2[2], s2[3]};
+        if (e.bias2) {
+            four(e.bias2 + n0, v);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) u[k] += v[k];
+        }
+        if (e.pre) {
+            put(e.pre + o, z);
+            put(e.pre2 + o, u);
+        }
+        act_n<4>(z, e.act);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) z[k] *= u[k];
+    } else if constexpr (EPI == kEpiAct) {
+        if (e.pre) put(e.pre + o, z);
+        act_n<4>(z, e.act);
+        if (e.res) {
+            four(e.res + o, v);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) z[k] += v[k];
+        }
+    }
+    put(e.y + o, z);
+}
+
 // Sums the partial tiles of the tail in the order of their blocks and applies the
-// epilogue.  Partials: [slot][token of the tile (bn)][row of the tile (256)]; one thread
-// per 4 outputs of one token.
+// epilogue.  Partials: [slot][token of the tile (bn)][row of the tile (256)].  A block
+// takes kReduceTokens tokens of one tile, a thread 4 outputs of a token at a time; a
+// tile's partials (3 to 6 as a rule) are loaded four at a time.  Bound by L2, which still
+// holds what the product has just written.
+constexpr int kReduceTokens = 8;
+
 template <int EPI>
 __global__ void __launch_bounds__(256)
 epi_reduce_kernel(const float* __restrict__ ws, EpiParams e, int M, int N, int bn, int m_tiles, TailSplit t)
 {
+    constexpr int kGroups = epi_tile_rows<EPI>(256) / 4;              // 4-output groups per token
+    const int chunks = (bn + kReduceTokens - 1) / kReduceTokens;
+    const int j = (int)blockIdx.x / chunks, c0 = ((int)blockIdx.x - j * chunks) * kReduceTokens;
+    const int tok0 = ((t.dp_tiles + j) % m_tiles) * bn;
+    const int64_t out0 = (int64_t)((t.dp_tiles + j) / m_tiles) * epi_tile_rows<EPI>(256);
+    // the ranges that share the tile: from the last one that begins at or before it
+    const int64_t all = (int64_t)t.tail * t.blocks, begin = (int64_t)j * t.blocks, end = begin + t.blocks;
+    const int p0 = (int)(((begin + 1) * t.tail_pairs + all - 1) / all) - 1;
+    const int p1 = (int)((end * t.tail_pairs + all - 1) / all);      // ranges [p0, p1): the next begins at or past the end
+    const int64_t slot = (int64_t)bn * 256;
+    const float* first = ws + (2 * p0 + (t.range_begin(p0) < begin ? 1 : 0)) * slot;
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int q = epi_tile_rows<EPI>(256) / 4;                        // 4-output groups per token
-    const int64_t per_tile = (int64_t)bn * q;
-    const int64_t total = t.tail * per_tile, slot = (int64_t)bn * 256;
-    const int64_t all = (int64_t)t.tail * t.blocks;
-    for (int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; i < total; i += (int64_t)gridDim.x * blockDim.x) {
-        const int j = (int)(i / per_tile);
-        const int rem = (int)(i - (int64_t)j * per_tile);
-        const int m = rem / q, r4 = (rem - m * q) * 4;
-        const int tok = ((t.dp_tiles + j) % m_tiles) * bn + m;
-        const int64_t n0 = (int64_t)((t.dp_tiles + j) / m_tiles) * epi_tile_rows<EPI>(256) + r4;
-        if (tok >= M || n0 >= N) continue;
-        const int row = EPI == kEpiGlu ? 32 * (r4 >> 4) + (r4 & 15) : r4;
-        const float* src = ws + (int64_t)m * 256 + row;
-        const int64_t begin = (int64_t)j * t.blocks, end = begin + t.blocks;
-        float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
-        // the last range that begins at or before the tile, then on through its blocks
-        for (int p = (int)(((begin + 1) * t.tail_pairs + all - 1) / all) - 1; p < t.tail_pairs; ++p) {
-            const int64_t rb = t.range_begin(p);
-            if (rb >= end) break;
-            const float* part = src + (2 * p + (rb < begin ? 1 : 0)) * slot;
-            const float4 c = *reinterpret_cast<const float4*>(part);
-            a.x += c.x; a.y += c.y; a.z += c.z; a.w += c.w;
-            if constexpr (EPI == kEpiGlu) {
-                const float4 d = *reinterpret_cast<const float4*>(part + 16);
-                b.x += d.x; b.y += d.y; b.z += d.z; b.w += d.w;
+#pragma unroll 2
+    for (int i = threadIdx.x; i < kReduceTokens * kGroups; i += 256) {
+        const int m = c0 + i / kGroups, r4 = i % kGroups * 4;
+        const int64_t n0 = out0 + r4;
+        if (m >= bn || tok0 + m >= M || n0 >= N) continue;
+        const int64_t at = (int64_t)m * 256 + (EPI == kEpiGlu ? 32 * (r4 >> 4) + (r4 & 15) : r4);
+        float s[4] = {0.f, 0.f, 0.f, 0.f}, s2[4] = {0.f, 0.f, 0.f, 0.f};
+        for (int p = p0; p < p1; p += 4) {
+            float4 a[4], b[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                a[k] = b[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (p + k < p1) {
+                    const float* src = (p + k == p0 ? first : ws + 2 * (p + k) * slot) + at;
+                    a[k] = *reinterpret_cast<const float4*>(src);
+                    if constexpr (EPI == kEpiGlu) b[k] = *reinterpret_cast<const float4*>(src + 16);
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                s[0] += a[k].x; s[1] += a[k].y; s[2] += a[k].z; s[3] += a[k].w;
+                if constexpr (EPI == kEpiGlu) { s2[0] += b[k].x; s2[1] += b[k].y; s2[2] += b[k].z; s2[3] += b[k].w; }
             }
         }
-        const float s[4] = {a.x, a.y, a.z, a.w}, s2[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-            if (n0 + k < N) epi_one<EPI>(e, s[k], s2[k], tok, (int)n0 + k, N);
+        epi_four<EPI>(e, s, s2, tok0 + m, (int)n0, N);
     }
 }
 

@@ -43,8 +43,10 @@
 namespace bq {
 
 constexpr int kFpDeqWarps = 16;                 // four groups of 4
-constexpr int kFpEpiWarp0 = kFpDeqWarps;        // 4 warps: lane quarter = warp % 4
-constexpr int kFpTokWarp = kFpEpiWarp0 + 4;     // producer of token tiles
+constexpr int kFpEpiWarp0 = kFpDeqWarps;        // lane quarter = warp % 4
+constexpr int kFpEpiWarps = 8;                  // two per lane quarter (with 4, affine 8-bit 4096 x 4096, 1999 tokens,
+                                                // residual and z took 75 us against 69)
+constexpr int kFpTokWarp = kFpEpiWarp0 + kFpEpiWarps;   // producer of token tiles
 constexpr int kFpCodeWarp = kFpTokWarp + 1;     // producer of codes
 constexpr int kFpMmaWarp = kFpCodeWarp + 1;
 constexpr int kFpThreads = 32 * (kFpMmaWarp + 1);
@@ -248,7 +250,7 @@ tc_fused_pair_kernel(const __grid_constant__ CUtensorMap tm_a0, const __grid_con
         for (int i = 0; i < kFpConsumed; ++i) mbar_init(consumed_bar(i), 1);
         for (int b = 0; b < 2; ++b) {
             mbar_init(tfull_bar(b), 1);
-            mbar_init(tempty_bar(b), 8);
+            mbar_init(tempty_bar(b), 2 * kFpEpiWarps);
         }
         mbar_init(done_bar, 1);
         fence_barrier_init();
@@ -385,7 +387,7 @@ tc_fused_pair_kernel(const __grid_constant__ CUtensorMap tm_a0, const __grid_con
             const int tile = u.tile, slot = u.slot;
             more = u.next();
             if (!more || !mbar_wait_warp(tfull_bar(lt & 1), (uint32_t)(lt >> 1) & 1u)) break;
-            drain(tile, slot, lt, 0, 1);
+            drain(tile, slot, lt, (warp - kFpEpiWarp0) >> 2, kFpEpiWarps / 4);
             __syncwarp();
             if (lane == 0) mbar_arrive_cluster(map_to_cta(tempty_bar(lt & 1), 0));
         }
