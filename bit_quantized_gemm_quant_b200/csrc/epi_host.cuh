@@ -43,6 +43,7 @@ void device_or_b200(int* num_sms, int* smem_optin)
 // ------------------------------------------------------------------ pair product
 struct PairPlan {
     int bn = 32, stages = 0, pairs = 0;
+    int codes = 0;                  // fused: code stages
     int64_t tiles = 0;
     TailSplit split{};
     size_t ws_bytes = 0;
@@ -50,19 +51,22 @@ struct PairPlan {
 
 // Token tile and split of the last round for `rows` D rows, M tokens and nk blocks of the
 // reduction; shared memory: fixed_bytes, and per stage a_bytes and tok_bytes per token.
-// Cost model in SM clocks: a block costs the larger of the MMA's and its issue
-// (block_mma per token of the tile) and of bringing the weights in (min_block), a unit of
-// work a fixed start, and what the last unit leaves to be drained; a split last round
-// adds the partial tiles' traffic and the kernel that sums them.
+// Cost model in SM clocks, from B200 sweeps over tile widths (12288 x 4096 and smaller, 33
+// to 2048 tokens): a block costs block0 + block1 per token of the tile (the dequantization
+// or the copies set the first, the MMA and its contention the second: 1030 clocks at 64
+// tokens, 1450 at 256 for 128-element blocks dequantized on chip), a unit of work a fixed
+// start, and the last unit its epilogue.  A split last round adds the partial tiles'
+// traffic and the kernel that sums them, and 6%: the pairs that an unsplit last round
+// leaves idle let the others run faster.
 bool plan_pair(int64_t rows, int64_t M, int64_t nk, int num_sms, int smem_optin, int fixed_bytes, int a_bytes,
-               int tok_bytes, double min_block, double block_mma, PairPlan* pl)
+               int tok_bytes, double block0, double block1, PairPlan* pl)
 {
     const int64_t pairs = std::max(num_sms / 2, 1), rtiles = (rows + 255) / 256;
     const int64_t maxb = std::min<int64_t>(256, (M + 31) / 32 * 32);
     double best = 1e300;
     for (int b = 32; b <= maxb; b += 32) {
         const int64_t tiles = ((M + b - 1) / b) * rtiles;
-        const double kb = std::max(block_mma * b, min_block), drain = 1000.0 + 8.0 * b;
+        const double kb = block0 + block1 * b, drain = 1000.0 + 8.0 * b;
         auto consider = [&](double c, int64_t dp, int64_t tail_pairs) {
             if (c < best) {
                 best = c;
@@ -81,7 +85,7 @@ bool plan_pair(int64_t rows, int64_t M, int64_t nk, int num_sms, int smem_optin,
         const int64_t tp = std::max<int64_t>(tail, std::min<int64_t>(pairs, tail * nk / 2));
         const double range = (double)((tail * nk + tp - 1) / tp);
         const double traffic = (double)(tp + tail) * b * 256.0 * 8.0 / 2500.0;
-        consider((double)(dp / pairs) * unit((double)nk) + unit(range) + 1500.0 + drain + 5000.0 + traffic, dp, tp);
+        consider(((double)(dp / pairs) * unit((double)nk) + unit(range) + 1500.0 + drain + 5000.0 + traffic) * 1.06, dp, tp);
     }
     pl->pairs = (int)pairs;
     pl->split.blocks = (int)nk;
@@ -299,8 +303,33 @@ ScalePack scale_pack(bool mn, int mats, int64_t N, int64_t K)
 
 int fp_mode(WFmt f) { return f == WFmt::Q4_0 ? kModeQ4_0 : f == WFmt::AFF4 ? kModeAff4 : kModeAff8; }
 
-// The product of launch_pair with the codes of w (1 or 2 matrices [N][K]) in place of
-// bf16 weights.  Forward: B[0] = x, red = K; gradient (MN): B[i] = dz of matrix i,
+// The scales of w (1 or 2 matrices [N][K]), by block, to `packed`; interleave: for the glu
+// forward product.
+bq_status launch_scale_pack(WFmt fmt, bool mn, const QMat* w, int mats, bool interleave, int64_t N, int64_t K,
+                            int group_size, void* packed, cudaStream_t st)
+{
+    const ScalePack sp = scale_pack(mn, mats, N, K);
+    ScalePackParams pp;
+    for (int i = 0; i < 2; ++i) {
+        const QMat& q = w[i < mats ? i : 0];
+        pp.scales[i] = reinterpret_cast<const uint16_t*>(q.scales);
+        pp.biases[i] = reinterpret_cast<const uint16_t*>(q.biases);
+    }
+    pp.out = reinterpret_cast<uint32_t*>(packed);
+    pp.N = (int)N;
+    pp.K = (int)K;
+    pp.gs_shift = group_size == 32 ? 5 : group_size == 64 ? 6 : 7;
+    pp.interleave = interleave;
+    pp.cols = (int)sp.cols;
+    pp.pack_rows = sp.rows;
+    pp.pack_mat = sp.mat;
+    const dim3 grid((unsigned)((sp.rows / (interleave ? 2 : 1) + 31) / 32), (unsigned)((sp.cols + 2047) / 2048), (unsigned)mats);
+    return fmt == WFmt::Q4_0 ? launch_pdl_dim(scale_pack_kernel<true>, grid, 256, 0, st, pp)
+                             : launch_pdl_dim(scale_pack_kernel<false>, grid, 256, 0, st, pp);
+}
+
+// The product of launch_pair with the codes of w (1 or 2 matrices [N][K]) and their
+// packed scales in place of bf16 weights.  Forward: B[0] = x, red = K; gradient (MN): B[i] = dz of matrix i,
 // red = N.
 template <int MODE, bool MN, int EPI>
 bq_status launch_fused_pair(const DeviceInfo& di, int dev, const PairPlan& pl, const QMat* w, int mats,
@@ -316,40 +345,21 @@ bq_status launch_fused_pair(const DeviceInfo& di, int dev, const PairPlan& pl, c
         }
         attr_done[dev] = true;
     }
-    constexpr int bits = MODE == kModeAff8 ? 8 : 4, row_bytes = (MN ? 128 : 64) * bits / 8;
-    constexpr CUtensorMapSwizzle sw = row_bytes == 32   ? CU_TENSOR_MAP_SWIZZLE_32B
-                                      : row_bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B;
+    constexpr int bits = MODE == kModeAff8 ? 8 : 4, row_bytes = 128 * bits / 8;
+    constexpr CUtensorMapSwizzle sw = row_bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B;
     const int64_t red = MN ? N : K, outs = MN ? K : N;
     CUtensorMap ta[2], tb[2];
     FpParams p;
     for (int i = 0; i < 2; ++i) {
         const QMat& q = w[i < mats ? i : 0];
-        if (!make_map(&ta[i], CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, q.wq, N, K * bits / 8, MN ? 64 : epi_tile_rows<EPI>(128),
+        if (!make_map(&ta[i], CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, q.wq, N, K * bits / 8, epi_tile_rows<EPI>(128),
                       row_bytes, sw) ||
             !make_map_pitch(&tb[i], B[MN && i < mats ? i : 0], M, red, b_pitch, pl.bn / 2, 64))
             return BQ_ERR_CUDA;
     }
-    // the scales, by block
     const ScalePack sp = scale_pack(MN, EPI == kEpiGlu ? 2 : mats, N, K);
-    ScalePackParams pp;
-    for (int i = 0; i < 2; ++i) {
-        const QMat& q = w[i < mats ? i : 0];
-        pp.scales[i] = reinterpret_cast<const uint16_t*>(q.scales);
-        pp.biases[i] = reinterpret_cast<const uint16_t*>(q.biases);
-    }
-    pp.out = reinterpret_cast<uint32_t*>(packed);
-    pp.N = (int)N;
-    pp.K = (int)K;
-    pp.gs_shift = group_size == 32 ? 5 : group_size == 64 ? 6 : 7;
-    pp.interleave = EPI == kEpiGlu;
-    pp.cols = (int)sp.cols;
-    pp.pack_rows = sp.rows;
-    pp.pack_mat = sp.mat;
-    const dim3 pgrid((unsigned)((sp.rows / (EPI == kEpiGlu ? 2 : 1) + 31) / 32), (unsigned)((sp.cols + 2047) / 2048),
-                     (unsigned)mats);
-    bq_status s = launch_pdl_dim(scale_pack_kernel<MODE == kModeQ4_0, MN>, pgrid, 256, 0, st, pp);
-    if (s != BQ_OK) return s;
-    p.scales = pp.out;
+    p.codes = pl.codes;
+    p.scales = reinterpret_cast<const uint32_t*>(packed);
     p.pack_rows = sp.rows;
     p.pack_mat = sp.mat;
     p.q.e = e;
@@ -366,9 +376,9 @@ bq_status launch_fused_pair(const DeviceInfo& di, int dev, const PairPlan& pl, c
     // every pair when there are whole rounds before the tail: the units are dealt by pair
     const unsigned grid = 2u * (unsigned)std::min<int64_t>(pl.split.tail && pl.split.dp_tiles ? pl.pairs
                                                            : pl.split.tail ? pl.split.tail_pairs : pl.tiles, pl.pairs);
-    const size_t smem = std::max<size_t>(1024 + fp_fixed_bytes(MODE) + (size_t)pl.stages * (size_t)pl.bn * 128u + 512,
+    const size_t smem = std::max<size_t>(1024 + fp_fixed_bytes(MODE, pl.codes) + (size_t)pl.stages * (size_t)pl.bn * 128u + 512,
                                          (size_t)di.max_smem_optin / 2 + 1024);   // one CTA per SM (all of TMEM)
-    s = launch_pdl_dim(kern, dim3(grid), kFpThreads, smem, st, ta[0], ta[1], tb[0], tb[1], p);
+    const bq_status s = launch_pdl_dim(kern, dim3(grid), kFpThreads, smem, st, ta[0], ta[1], tb[0], tb[1], p);
     return s != BQ_OK ? s : launch_reduce<EPI>(di, pl, p.q, st);
 }
 
@@ -407,10 +417,19 @@ bool plan_epi_product(WFmt fmt, int64_t rows, int64_t M, int segs, int64_t red, 
 {
     w->rows = rows;
     w->fused = has_fast_paths(fmt);
-    if (w->fused)       // blocks of 128
-        return plan_pair(rows, M, segs * ((red + 127) / 128), num_sms, smem_optin, (int)fp_fixed_bytes(fp_mode(fmt)), 0, 128,
-                         1000.0, 4.5, &w->pl);
-    return plan_pair(rows, M, segs * ((red + 63) / 64), num_sms, smem_optin, 0, (int)kPairABytes, 64, 400.0, 2.5, &w->pl);
+    if (!w->fused)      // blocks of 64
+        return plan_pair(rows, M, segs * ((red + 63) / 64), num_sms, smem_optin, 0, (int)kPairABytes, 64, 300.0, 1.5, &w->pl);
+    const int mode = fp_mode(fmt);
+    if (!plan_pair(rows, M, segs * ((red + 127) / 128), num_sms, smem_optin, (int)fp_fixed_bytes(mode, 2), 0, 128, 900.0, 2.15,
+                   &w->pl))
+        return false;
+    // Four code stages where they leave room for three token tiles, else two: 1 to 8% apart
+    // below 256 tokens a tile, and 12% the other way at 256, where two token tiles would be
+    // left.
+    const int stages = (smem_optin - 1024 - 512 - (int)fp_fixed_bytes(mode, kFpMaxCodes)) / (w->pl.bn * 128);
+    w->pl.codes = stages >= 3 ? kFpMaxCodes : 2;
+    if (stages >= 3) w->pl.stages = std::min<int>(kFpMaxTok, stages);
+    return true;
 }
 
 bool plan_forward(WFmt fmt, int mats, int64_t M, int64_t N, int64_t K, int num_sms, int smem_optin, EpiWs* w)
@@ -499,9 +518,11 @@ bq_status epi_forward(const uint16_t* x, const QMat* w, const EpiParams& e, int6
     if (!plan_forward(fmt, mats, M, N, K, di.num_sms, di.max_smem_optin, &ws)) return BQ_ERR_UNSUPPORTED;
     void* buf = nullptr;
     if ((s = epi_workspace(dev, st, workspace, workspace_bytes, ws.bytes, &buf)) != BQ_OK) return s;
-    if (ws.fused)
+    if (ws.fused) {
+        if ((s = launch_scale_pack(fmt, false, w, mats, mats == 2, N, K, group_size, buf, st)) != BQ_OK) return s;
         return launch_fused_pair_fmt<false, EPI>(fmt, di, dev, ws.pl, w, mats, &x, N, K, M, K, group_size, e, buf,
                                                  reinterpret_cast<uint8_t*>(buf) + ws.off_split, st);
+    }
     uint16_t* wb = reinterpret_cast<uint16_t*>(buf);
     if ((s = dequant_rows(fmt, w, mats, wb, N, K, group_size, mats == 2, di, st)) != BQ_OK) return s;
     return launch_pair<false, EPI>(di, dev, ws.pl, &wb, &x, 1, ws.rows, N, M, K, K, e,
@@ -509,18 +530,23 @@ bq_status epi_forward(const uint16_t* x, const QMat* w, const EpiParams& e, int6
 }
 
 // ------------------------------------------------------------------ backward
+// beside_pack: right behind scale_pack_kernel, which it may overlap.
 template <bool GLU, int V>
-bq_status launch_epi_grad_v(const EpiGradParams& p, int act, int row_blocks, cudaStream_t st)
+bq_status launch_epi_grad_v(const EpiGradParams& p, int act, int row_blocks, bool beside_pack, cudaStream_t st)
 {
     const dim3 grid((unsigned)(((int64_t)p.N + 32 * V - 1) / (32 * V)), (unsigned)row_blocks);
+    auto go = [&](auto kern) {
+        if (beside_pack) return launch_pdl_dim(kern, grid, 256, 0, st, p);
+        kern<<<grid, 256, 0, st>>>(p);
+        return launch_status();
+    };
     switch (act) {
-    case kActRelu: epi_grad_kernel<GLU, kActRelu, V><<<grid, 256, 0, st>>>(p); break;
-    case kActGelu: epi_grad_kernel<GLU, kActGelu, V><<<grid, 256, 0, st>>>(p); break;
-    case kActGeluTanh: epi_grad_kernel<GLU, kActGeluTanh, V><<<grid, 256, 0, st>>>(p); break;
-    case kActSilu: epi_grad_kernel<GLU, kActSilu, V><<<grid, 256, 0, st>>>(p); break;
-    default: epi_grad_kernel<GLU, kActNone, V><<<grid, 256, 0, st>>>(p); break;
+    case kActRelu: return go(epi_grad_kernel<GLU, kActRelu, V>);
+    case kActGelu: return go(epi_grad_kernel<GLU, kActGelu, V>);
+    case kActGeluTanh: return go(epi_grad_kernel<GLU, kActGeluTanh, V>);
+    case kActSilu: return go(epi_grad_kernel<GLU, kActSilu, V>);
+    default: return go(epi_grad_kernel<GLU, kActNone, V>);
     }
-    return launch_status();
 }
 
 // dy [M][N] and the saved z (glu: g, u) to dz (dg, du), dx and the biases' gradients.
@@ -577,6 +603,8 @@ bq_status epi_backward(const EpiBackward& b, const QMat* w, int act, int64_t M, 
     const bool pad = N % 8 != 0;
     uint16_t* padded[2] = {reinterpret_cast<uint16_t*>(base + ws.off_pad),
                            reinterpret_cast<uint16_t*>(base + ws.off_pad + up256((size_t)M * ws.pitch * 2u))};
+    const bool fused = K > 0 && ws.fused;
+    if (fused && (s = launch_scale_pack(fmt, true, w, mats, false, N, K, group_size, base, st)) != BQ_OK) return s;
     if (!none || any_db || pad) {
         EpiGradParams p;
         p.dy = b.dy;
@@ -591,19 +619,20 @@ bq_status epi_backward(const EpiBackward& b, const QMat* w, int act, int64_t M, 
         p.N = (int)N;
         p.pitch = (int)ws.pitch;
         p.rows_per_block = ws.rows_per_block;
-        s = pad ? launch_epi_grad_v<GLU, 1>(p, act, ws.row_blocks, st) : launch_epi_grad_v<GLU, 8>(p, act, ws.row_blocks, st);
+        s = pad ? launch_epi_grad_v<GLU, 1>(p, act, ws.row_blocks, fused, st)
+                : launch_epi_grad_v<GLU, 8>(p, act, ws.row_blocks, fused, st);
         if (s != BQ_OK) return s;
         if (any_db) {
-            epi_bias_grad_kernel<<<(unsigned)((N + 255) / 256), 256, 0, st>>>(p.part, b.db[0], b.db[1], (int)N, mats,
-                                                                             ws.row_blocks);
-            if ((s = launch_status()) != BQ_OK) return s;
+            s = launch_pdl_dim(epi_bias_grad_kernel, dim3((unsigned)((N + 31) / 32), (unsigned)mats), 256, 0, st,
+                               (const float*)p.part, b.db[0], b.db[1], (int)N, mats, ws.row_blocks);
+            if (s != BQ_OK) return s;
         }
     }
     if (K == 0) return BQ_OK;
     const uint16_t* B[2] = {pad ? padded[0] : none ? b.dy : b.d[0], pad ? padded[1] : b.d[1]};
     EpiParams e;
     e.y = b.dx;
-    if (ws.fused)
+    if (fused)
         return launch_fused_pair_fmt<true, kEpiPlain>(fmt, di, dev, ws.pl, w, mats, B, N, K, M, pad ? ws.pitch : N,
                                                       group_size, e, base, base + ws.off_split, st);
     uint16_t* wb = reinterpret_cast<uint16_t*>(base);

@@ -480,20 +480,35 @@ __global__ void __launch_bounds__(256) epi_grad_kernel(EpiGradParams p)
             }
         }
     }
+    // Launched beside scale_pack_kernel (which lets it start only once everything before
+    // both is complete), it ends after it, so that waiting for this kernel covers both.
+    asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
-// db[k][n] = bf16(sum over row blocks of part[block][k][n]), in block order.
+// db[k][n] = bf16(sum over row blocks of part[block][k][n]): a block takes 32 columns, its
+// 8 warps every eighth row block; their sums are added in warp order.
 __global__ void __launch_bounds__(256)
 epi_bias_grad_kernel(const float* __restrict__ part, uint16_t* __restrict__ db0, uint16_t* __restrict__ db1, int N,
                      int kinds, int blocks)
 {
-    const int64_t n = blockIdx.x * (int64_t)256 + threadIdx.x;
-    if (n >= N) return;
-    for (int k = 0; k < kinds; ++k) {
-        float s = 0.0f;
-        for (int b = 0; b < blocks; ++b) s += part[((int64_t)b * kinds + k) * N + n];
-        uint16_t* o = k ? db1 : db0;
-        if (o) o[n] = (uint16_t)f32_to_bf16_bits(s);
+    __shared__ float red[8][32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, k = blockIdx.y;
+    const int64_t n = (int64_t)blockIdx.x * 32 + lane;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    float s = 0.0f;
+    if (n < N) {
+#pragma unroll 4
+        for (int b = warp; b < blocks; b += 8) s += part[((int64_t)b * kinds + k) * N + n];
+    }
+    red[warp][lane] = s;
+    __syncthreads();
+    uint16_t* o = k ? db1 : db0;
+    if (warp == 0 && n < N && o) {
+        float t = 0.0f;
+#pragma unroll
+        for (int w = 0; w < 8; ++w) t += red[w][lane];
+        o[n] = (uint16_t)f32_to_bf16_bits(t);
     }
 }
 

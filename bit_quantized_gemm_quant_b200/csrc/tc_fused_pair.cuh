@@ -25,7 +25,7 @@
 // 1130: a tile slot or stage was then held through a copy's round trip, the wait for a
 // group and the product, longer than the ring covers at the MMA's 512 clocks a block.
 // Barriers: cfull / cempty (codes, each CTA's own), bfull (tokens of both CTAs, the
-// leader's), ready (a tile, the leader's; 8 dequant warps of each CTA arrive), consumed
+// leader's), ready (a block's tile, the leader's; 8 dequant warps of each CTA arrive), consumed
 // (one per block, each CTA's own; the MMA's commit arrives on both and thereby frees the
 // block's token tile and weight tile).
 //
@@ -50,36 +50,37 @@ constexpr int kFpTokWarp = kFpEpiWarp0 + kFpEpiWarps;   // producer of token til
 constexpr int kFpCodeWarp = kFpTokWarp + 1;     // producer of codes
 constexpr int kFpMmaWarp = kFpCodeWarp + 1;
 constexpr int kFpThreads = 32 * (kFpMmaWarp + 1);
-constexpr uint32_t kFpScaleBytes = 1024;        // packed scales of a stage
-// Code stages (half a block each), a multiple of the groups, so that a stage always belongs
-// to the same group: a barrier's phases are told apart by parity alone, and a group that
-// had not waited for the stage's last fill (made for another group, and possibly landing
-// after later ones) could take the fill before it for its own.
-constexpr int kFpCodes = 4;
-static_assert(kFpCodes % 4 == 0, "a code stage serves one dequant group");
+constexpr uint32_t kFpScaleBytes = 2048;        // packed scales of a block
+// Code stages (a block each), an even number, so that a stage always serves the same two
+// dequant groups: a barrier's phases are told apart by parity alone, and a group that had
+// not waited for the stage's last fill (made for other groups, and possibly landing after
+// later ones) could take the fill before it for its own.
+constexpr int kFpMaxCodes = 4;
+static_assert(kFpMaxCodes % 2 == 0, "a code stage serves two dequant groups");
 constexpr int kFpMaxTiles = 3;
 constexpr int kFpConsumed = 16;                 // consumed barriers, at least the depth of each ring
 constexpr int kFpMaxTok = 8;                    // token tiles of a block
 
-__host__ __device__ constexpr uint32_t fp_code_bytes(int mode) { return mode == kModeAff8 ? 8192u : 4096u; }
+__host__ __device__ constexpr uint32_t fp_code_bytes(int mode) { return mode == kModeAff8 ? 16384u : 8192u; }   // of a block
 __host__ __device__ constexpr int fp_tiles(int mode) { return mode == kModeAff8 ? 2 : 3; }   // bf16 weight tiles of a block
 // Shared memory beside the token tiles
-__host__ __device__ constexpr uint32_t fp_fixed_bytes(int mode)
+__host__ __device__ constexpr uint32_t fp_fixed_bytes(int mode, int codes)
 {
-    return (uint32_t)fp_tiles(mode) * 2u * kPairABytes + kFpCodes * (fp_code_bytes(mode) + kFpScaleBytes);
+    return (uint32_t)fp_tiles(mode) * 2u * kPairABytes + (uint32_t)codes * (fp_code_bytes(mode) + kFpScaleBytes);
 }
 
 struct FpParams {
     PairParams q;
+    int codes;                     // code stages: 2 or 4
     const uint32_t* scales;        // packed (scale_pack_kernel)
     int64_t pack_rows;             // its rows per column block
     int64_t pack_mat;              // gradient: its words per matrix
 };
 
-// Packed scales: words of 32 weights, forward [column block of 64][tile row][2] with tile
-// rows as the product numbers them (glu: interleaved, see epi_out_row), gradient [matrix]
-// [column block of 128][row][4]; rows and columns are padded to whole tiles with weights
-// of 0.  A word holds scale and bias (bf16), or Q4_0's d as d_hi + d_lo (see gemv.cuh).
+// Packed scales: words of 32 weights, [column block of 128][row][4]; forward the rows are
+// the product's tile rows (glu: interleaved, see epi_out_row), for the gradient those of
+// the matrix, one matrix after the other.  Rows and columns are padded to whole tiles with
+// weights of 0.  A word holds scale and bias (bf16), or Q4_0's d as d_hi + d_lo (see gemv.cuh).
 // A block takes 32 rows x 2048 columns through shared memory: reads run along the rows
 // of the scales, writes along the rows of the result.
 struct ScalePackParams {
@@ -91,7 +92,7 @@ struct ScalePackParams {
     int64_t pack_rows, pack_mat;
 };
 
-template <bool Q4, bool MN>
+template <bool Q4>
 __global__ void __launch_bounds__(256) scale_pack_kernel(const __grid_constant__ ScalePackParams p)
 {
     __shared__ uint32_t sm[32][65];
@@ -101,6 +102,7 @@ __global__ void __launch_bounds__(256) scale_pack_kernel(const __grid_constant__
     const int per_row = p.K >> p.gs_shift;
     const uint16_t* sc = mat ? p.scales[1] : p.scales[0];
     const uint16_t* bi = mat ? p.biases[1] : p.biases[0];
+#pragma unroll
     for (int i = threadIdx.x; i < 32 * 64; i += 256) {
         const int r = i >> 6, h = i & 63, n = n0 + r, k = k0 + 32 * h;
         uint32_t v = 0u;
@@ -117,54 +119,53 @@ __global__ void __launch_bounds__(256) scale_pack_kernel(const __grid_constant__
         sm[r][h] = v;
     }
     __syncthreads();
-    constexpr int W = MN ? 4 : 2;                       // words per output row
-    for (int i = threadIdx.x; i < 32 * (64 / W); i += 256) {
+    for (int i = threadIdx.x; i < 32 * 16; i += 256) {
         const int r = i & 31, c = i >> 5, n = n0 + r;
-        const int64_t blk = k0 / (32 * W) + c;
-        if (blk * (32 * W) >= p.cols) continue;
+        const int64_t blk = k0 / 128 + c;
+        if (blk * 128 >= p.cols) continue;
         const int64_t row = p.interleave ? 32 * (int64_t)(n >> 4) + (n & 15) + 16 * mat : n;
         if (row >= p.pack_rows) continue;
-        uint32_t* o = p.out + (MN ? mat * p.pack_mat : 0) + (blk * p.pack_rows + row) * W;
-        if constexpr (MN)
-            *reinterpret_cast<uint4*>(o) = make_uint4(sm[r][4 * c], sm[r][4 * c + 1], sm[r][4 * c + 2], sm[r][4 * c + 3]);
-        else
-            *reinterpret_cast<uint2*>(o) = make_uint2(sm[r][2 * c], sm[r][2 * c + 1]);
+        *reinterpret_cast<uint4*>(p.out + mat * p.pack_mat + (blk * p.pack_rows + row) * 4) =
+            make_uint4(sm[r][4 * c], sm[r][4 * c + 1], sm[r][4 * c + 2], sm[r][4 * c + 3]);
     }
 }
 
-// The dequant warps' part: group grp (4 warps) takes the half-blocks at positions grp, grp
-// + 4, ... of the CTA's `left` ones.  A thread expands 64 weights: forward, row r of the tile;
+// The dequant warps' part: group grp (4 warps) takes half (grp & 1) of the blocks grp >> 1,
+// grp >> 1 + 2, ... of the CTA's `left` ones.  A thread expands 64 weights: forward, row r of the tile;
 // gradient, row r of the half-block, outputs 64 hk .. of the tile.  (A function of its own:
 // inlined, the code that follows it for these warps slowed this loop by 13%.)
 template <int MODE, bool MN, int EPI>
-__device__ __noinline__ void fp_dequantize(int left, uint32_t a_base, uint32_t c_base, uint32_t cfull0, uint32_t cempty0,
+__device__ __noinline__ void fp_dequantize(int left, int codes_ring, uint32_t a_base, uint32_t c_base, uint32_t cfull0, uint32_t cempty0,
                                            uint32_t ready0, uint32_t consumed0)
 {
     constexpr uint32_t kCBytes = fp_code_bytes(MODE), kCStage = kCBytes + kFpScaleBytes;
     constexpr int kBits = MODE == kModeAff8 ? 8 : 4, kTiles = fp_tiles(MODE);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int grp = warp >> 2, w4 = warp & 3;
+    const int half = grp & 1;                       // of the block, always the same for a group
     const int r = MN ? 32 * (w4 & 1) + lane : 32 * w4 + lane;
     const int hk = MN ? w4 >> 1 : 0;
-    const int crow = !MN && EPI == kEpiGlu ? epi_out_row<EPI>(r) + (lane & 16 ? 64 : 0) : r;   // row among the codes
-    constexpr int kRowBytes = (MN ? 128 : 64) * kBits / 8;                  // of codes: 32, 64 or 128
-    constexpr int kUnits = kBits / 2;                                       // 16-byte units of codes per thread
-    // the units of a row, as the copy swizzles them
-    const int sw = kRowBytes == 32 ? (crow >> 2) & 1 : kRowBytes == 64 ? (crow >> 1) & 3 : crow & 7;
+    // row among the block's codes: forward 128 rows (glu: 64 of gate, 64 of up) of 128
+    // columns, of which this group takes 64; gradient 128 rows, of which it takes 64
+    const int crow = MN ? 64 * half + r : EPI == kEpiGlu ? epi_out_row<EPI>(r) + (lane & 16 ? 64 : 0) : r;
+    constexpr int kRowBytes = 128 * kBits / 8;      // 64 or 128
+    constexpr int kUnits = kBits / 2;               // 16-byte units of codes per thread
+    const int unit0 = (MN ? hk : half) * kUnits;
+    const int sw = kRowBytes == 64 ? (crow >> 1) & 3 : crow & 7;     // the units of a row, as the copy swizzles them
     const uint32_t code_row = c_base + (uint32_t)(crow * kRowBytes);
-    const uint32_t tile_row = a_base + (uint32_t)((grp & 1) * (int)kPairABytes + hk * (int)(kPairABytes / 2) + r * 128);
-    const uint32_t scale_row = c_base + kCBytes + (uint32_t)(MN ? r * 16 + hk * 8 : r * 8);
-    int c = grp, a = grp >> 1, block = grp >> 1;    // code stage, tile and block of this half
+    const uint32_t tile_row = a_base + (uint32_t)(half * (int)kPairABytes + hk * (int)(kPairABytes / 2) + r * 128);
+    const uint32_t scale_row = c_base + kCBytes + (uint32_t)(MN ? crow * 16 + hk * 8 : r * 16 + half * 8);
+    int a = grp >> 1, c = grp >> 1, block = grp >> 1;   // tile, code stage and block
     uint32_t ph = 0;
     bool ok = true;
-    for (int pos = grp; pos < left; pos += 4, block += 2) {
+    for (; block < left; block += 2) {
         ok = mbar_wait_warp(cfull0 + 8u * (uint32_t)c, ph);
         if (!ok) break;
         const uint32_t codes = code_row + (uint32_t)c * kCStage;
         const uint2 sc = ld_shared_v2(scale_row + (uint32_t)c * kCStage);
         uint4 raw[kUnits];
 #pragma unroll
-        for (int i = 0; i < kUnits; ++i) raw[i] = ld_shared_v4(codes + (uint32_t)(((hk * kUnits + i) ^ sw) << 4));
+        for (int i = 0; i < kUnits; ++i) raw[i] = ld_shared_v4(codes + (uint32_t)(((unit0 + i) ^ sw) << 4));
         __syncwarp();
         if (lane == 0) mbar_arrive(cempty0 + 8u * (uint32_t)c);
         const uint32_t tile = tile_row + (uint32_t)a * (2u * kPairABytes);
@@ -193,13 +194,13 @@ __device__ __noinline__ void fp_dequantize(int left, uint32_t a_base, uint32_t c
         fence_proxy_async_smem();                    // the MMA reads the tile through the async proxy
         __syncwarp();
         if (lane == 0) mbar_arrive_cluster(ready0 + 8u * (uint32_t)a);
-        if ((c += 4) >= kFpCodes) { c -= kFpCodes; ph ^= 1u; }
+        if ((c += 2) >= codes_ring) { c -= codes_ring; ph ^= 1u; }
         a = (a + 2) % kTiles;
     }
 }
 
-// tm_a0, tm_a1: codes of matrix 0 and 1 as bytes.  Forward: boxes of one stage's 64
-// columns x 128 rows (glu: 64 rows of gate and of up); gradient: 128 columns x 64 rows.
+// tm_a0, tm_a1: codes of matrix 0 and 1 as bytes, boxes of 128 columns x 128 rows (glu
+// forward: 64 rows of gate and of up).
 // tm_b0, tm_b1: tokens, boxes of 64 elements x bn / 2 tokens.
 template <int MODE, bool MN, int EPI>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFpThreads, 1)
@@ -214,17 +215,18 @@ tc_fused_pair_kernel(const __grid_constant__ CUtensorMap tm_a0, const __grid_con
     extern __shared__ uint8_t smem_raw[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_ctarank();
+    const int NC = fp.codes;
     const int NB = p.stages;                       // token tiles (of a block) in the ring
     const uint32_t b_bytes = (uint32_t)p.bn * 64u;
     const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
-    const uint32_t a_base = base, c_base = a_base + kTiles * 2u * kPairABytes, b_base = c_base + kFpCodes * kCStage;
+    const uint32_t a_base = base, c_base = a_base + kTiles * 2u * kPairABytes, b_base = c_base + (uint32_t)NC * kCStage;
     const uint32_t bar_base = b_base + (uint32_t)NB * 2u * b_bytes;
     auto cfull_bar = [&](int i) { return bar_base + 8u * (uint32_t)i; };
-    auto cempty_bar = [&](int i) { return bar_base + 8u * (uint32_t)(kFpCodes + i); };
-    auto ready_bar = [&](int i) { return bar_base + 8u * (uint32_t)(2 * kFpCodes + i); };
-    auto bfull_bar = [&](int i) { return bar_base + 8u * (uint32_t)(2 * kFpCodes + kFpMaxTiles + i); };
-    auto consumed_bar = [&](int i) { return bar_base + 8u * (uint32_t)(2 * kFpCodes + kFpMaxTiles + kFpMaxTok + i); };
-    constexpr int kBars = 2 * kFpCodes + kFpMaxTiles + kFpMaxTok + kFpConsumed;
+    auto cempty_bar = [&](int i) { return bar_base + 8u * (uint32_t)(kFpMaxCodes + i); };
+    auto ready_bar = [&](int i) { return bar_base + 8u * (uint32_t)(2 * kFpMaxCodes + i); };
+    auto bfull_bar = [&](int i) { return bar_base + 8u * (uint32_t)(2 * kFpMaxCodes + kFpMaxTiles + i); };
+    auto consumed_bar = [&](int i) { return bar_base + 8u * (uint32_t)(2 * kFpMaxCodes + kFpMaxTiles + kFpMaxTok + i); };
+    constexpr int kBars = 2 * kFpMaxCodes + kFpMaxTiles + kFpMaxTok + kFpConsumed;
     auto tfull_bar = [&](int b) { return bar_base + 8u * (uint32_t)(kBars + b); };
     auto tempty_bar = [&](int b) { return bar_base + 8u * (uint32_t)(kBars + 2 + b); };
     const uint32_t done_bar = bar_base + 8u * (uint32_t)(kBars + 4);
@@ -241,9 +243,9 @@ tc_fused_pair_kernel(const __grid_constant__ CUtensorMap tm_a0, const __grid_con
     auto tile_m0 = [&](int t) { return (t % p.m_tiles) * p.bn; };
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < kFpCodes; ++i) {
+        for (int i = 0; i < NC; ++i) {
             mbar_init(cfull_bar(i), 1);
-            mbar_init(cempty_bar(i), 4);
+            mbar_init(cempty_bar(i), 8);
         }
         for (int i = 0; i < kTiles; ++i) mbar_init(ready_bar(i), 16);
         for (int i = 0; i < NB; ++i) mbar_init(bfull_bar(i), 1);
@@ -280,64 +282,73 @@ tc_fused_pair_kernel(const __grid_constant__ CUtensorMap tm_a0, const __grid_con
 
     if (warp == kFpTokWarp) {
         // ---------------- token tiles (each CTA: its own half) ----------------
-        if (lane == 0) {
-            int b = 0, pos = 0;
-            bool ok = true;
-            for (PairUnits u(p); ok && u.next();) {
-                const int m0 = tile_m0(u.tile) + (int)rank * (p.bn / 2);
-                for (int it = u.kb0; it < u.kb1; ++it, ++pos) {
-                    if (pos >= NB && !wait_consumed(pos - NB)) { ok = false; break; }
-                    const bool second = it >= p.seg_blocks;
-                    if (rank == 0) mbar_arrive_expect_tx(bfull_bar(b), 4u * b_bytes);
-                    const uint32_t dst = b_base + (uint32_t)b * 2u * b_bytes, bar = map_to_cta(bfull_bar(b), 0);
-                    const int k0 = (second ? it - p.seg_blocks : it) * 128;
-                    tma_load_2d_pair(dst, second ? &tm_b1 : &tm_b0, bar, k0, m0);
-                    tma_load_2d_pair(dst + b_bytes, second ? &tm_b1 : &tm_b0, bar, k0 + 64, m0);
-                    if (++b == NB) b = 0;
+        // (whole warp, one elected lane issues: see the MMA warp)
+        int b = 0, pos = 0;
+        bool ok = true;
+        for (PairUnits u(p); ok && u.next();) {
+            const int m0 = tile_m0(u.tile) + (int)rank * (p.bn / 2);
+            for (int it = u.kb0; it < u.kb1; ++it, ++pos) {
+                if (pos >= NB) {
+                    ok = wait_consumed(pos - NB);
+                    __syncwarp();
+                    if (!ok) break;
                 }
+                const bool second = it >= p.seg_blocks;
+                const CUtensorMap* map = second ? &tm_b1 : &tm_b0;
+                const uint32_t dst = b_base + (uint32_t)b * 2u * b_bytes, bar = map_to_cta(bfull_bar(b), 0);
+                const int k0 = (second ? it - p.seg_blocks : it) * 128;
+                if (elect_one()) {
+                    if (rank == 0) mbar_arrive_expect_tx(bfull_bar(b), 4u * b_bytes);
+                    tma_load_2d_pair(dst, map, bar, k0, m0);
+                    tma_load_2d_pair(dst + b_bytes, map, bar, k0 + 64, m0);
+                }
+                __syncwarp();
+                if (++b == NB) b = 0;
             }
-            // Leave only when the last blocks are consumed: every copy of the pair has then
-            // landed and every arrival on this CTA's barriers has been made.  (After a
-            // timeout the leader still waits for the copies.)
-            for (int q = max(pos - NB, 0); q < pos; ++q) {
-                if (rank == 0 && !mbar_wait(bfull_bar(q % NB), (uint32_t)(q / NB) & 1u)) ok = false;
-                if (ok) ok = wait_consumed(q);
-            }
+        }
+        // Leave only when the last blocks are consumed: every copy of the pair has then
+        // landed and every arrival on this CTA's barriers has been made.  (After a timeout
+        // the leader still waits for the copies.)
+        for (int q = max(pos - NB, 0); q < pos; ++q) {
+            if (rank == 0 && !mbar_wait_warp(bfull_bar(q % NB), (uint32_t)(q / NB) & 1u)) ok = false;
+            if (ok) ok = wait_consumed(q);
         }
         __syncwarp();
     } else if (warp == kFpCodeWarp) {
-        // ---------------- codes (each CTA: its own rows) ----------------
-        if (lane == 0) {
-            int c = 0, issued = 0;
-            uint32_t ph = 0;
-            bool ok = true;
-            for (PairUnits u(p); ok && u.next();) {
-                const int r0 = tile_r0(u.tile);
-                for (int i2 = 2 * u.kb0; i2 < 2 * u.kb1; ++i2, ++issued) {      // half-blocks
-                    if (!mbar_wait(cempty_bar(c), ph ^ 1u)) { ok = false; break; }
-                    const uint32_t dst = c_base + (uint32_t)c * kCStage;
-                    mbar_arrive_expect_tx(cfull_bar(c), kCStage);
-                    const bool second = MN && i2 >= 2 * p.seg_blocks;
-                    const int kb = second ? i2 - 2 * p.seg_blocks : i2;
-                    bulk_load(dst + kCBytes,
-                              fp.scales + (MN ? (second ? fp.pack_mat : 0) + ((int64_t)(r0 / 128) * fp.pack_rows + kb * 64) * 4
-                                              : ((int64_t)kb * fp.pack_rows + r0) * 2),
-                              kFpScaleBytes, cfull_bar(c));
+        // ---------------- codes and scales (each CTA: its own rows) ----------------
+        int c = 0, issued = 0;
+        uint32_t ph = 0;
+        bool ok = true;
+        for (PairUnits u(p); ok && u.next();) {
+            const int r0 = tile_r0(u.tile);
+            for (int it = u.kb0; it < u.kb1; ++it, ++issued) {
+                if (!mbar_wait_warp(cempty_bar(c), ph ^ 1u)) { ok = false; break; }
+                const uint32_t dst = c_base + (uint32_t)c * kCStage, bar = cfull_bar(c);
+                const bool second = MN && it >= p.seg_blocks;
+                const int kb = second ? it - p.seg_blocks : it;
+                // forward: column block kb, rows r0 ..; gradient: column block r0 / 128, rows 128 kb ..
+                const uint32_t* sc = fp.scales + (second ? fp.pack_mat : 0) +
+                                     (MN ? (int64_t)(r0 / 128) * fp.pack_rows + kb * 128
+                                         : (int64_t)kb * fp.pack_rows + r0) * 4;
+                if (elect_one()) {
+                    mbar_arrive_expect_tx(bar, kCStage);
+                    bulk_load(dst + kCBytes, sc, kFpScaleBytes, bar);
                     if constexpr (MN) {
-                        tma_load_2d(dst, second ? &tm_a1 : &tm_a0, cfull_bar(c), r0 * kBits / 8, kb * 64);
+                        tma_load_2d(dst, second ? &tm_a1 : &tm_a0, bar, r0 * kBits / 8, kb * 128);
                     } else if constexpr (EPI == kEpiGlu) {
-                        tma_load_2d(dst, &tm_a0, cfull_bar(c), kb * (64 * kBits / 8), r0 / 2);
-                        tma_load_2d(dst + kCBytes / 2, &tm_a1, cfull_bar(c), kb * (64 * kBits / 8), r0 / 2);
+                        tma_load_2d(dst, &tm_a0, bar, kb * (128 * kBits / 8), r0 / 2);
+                        tma_load_2d(dst + kCBytes / 2, &tm_a1, bar, kb * (128 * kBits / 8), r0 / 2);
                     } else {
-                        tma_load_2d(dst, &tm_a0, cfull_bar(c), kb * (64 * kBits / 8), r0);
+                        tma_load_2d(dst, &tm_a0, bar, kb * (128 * kBits / 8), r0);
                     }
-                    if (++c == kFpCodes) { c = 0; ph ^= 1u; }
                 }
+                __syncwarp();
+                if (++c == NC) { c = 0; ph ^= 1u; }
             }
-            for (int q = 0; q < kFpCodes && q < issued; ++q) {      // every copy has landed
-                if (--c < 0) { c = kFpCodes - 1; ph ^= 1u; }
-                mbar_wait(cfull_bar(c), ph);
-            }
+        }
+        for (int q = 0; q < NC && q < issued; ++q) {            // every copy has landed
+            if (--c < 0) { c = NC - 1; ph ^= 1u; }
+            mbar_wait_warp(cfull_bar(c), ph);
         }
         __syncwarp();
     } else if (warp == kFpMmaWarp) {
@@ -393,9 +404,9 @@ tc_fused_pair_kernel(const __grid_constant__ CUtensorMap tm_a0, const __grid_con
         }
     } else {
         // ---------------- dequantization ----------------
-        int left = 0;                                    // half-blocks of this CTA's sequence
-        for (PairUnits u(p); u.next();) left += 2 * (u.kb1 - u.kb0);
-        fp_dequantize<MODE, MN, EPI>(left, a_base, c_base, cfull_bar(0), cempty_bar(0), map_to_cta(ready_bar(0), 0),
+        int left = 0;                                    // blocks of this CTA's sequence
+        for (PairUnits u(p); u.next();) left += u.kb1 - u.kb0;
+        fp_dequantize<MODE, MN, EPI>(left, NC, a_base, c_base, cfull_bar(0), cempty_bar(0), map_to_cta(ready_bar(0), 0),
                                      consumed_bar(0));
     }
     __syncwarp();
