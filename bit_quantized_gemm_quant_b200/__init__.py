@@ -14,7 +14,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
-import functools
+import importlib
 import os
 
 import torch
@@ -348,121 +348,40 @@ def _act_code(act: str) -> int:
     return ACTS[act]
 
 
-@functools.lru_cache(maxsize=4096)
-def _epilogue_ws_bytes(device_index: int, op: int, M: int, N: int, K: int, group_size: int, bits: int) -> int:
-    return lib().quant_matmul_epilogue_workspace_size(op, M, N, K, group_size, bits)
+_marshal = None
 
 
-def quant_matmul_epilogue_workspace_size(op: int, M: int, N: int, K: int, group_size: int, bits: int) -> int:
-    """Bytes of workspace of OP_ACT, OP_ACT_BACKWARD, OP_GLU or OP_GLU_BACKWARD."""
-    return lib().quant_matmul_epilogue_workspace_size(op, M, N, K, group_size, bits)
-
-
-# One decode call runs a few microseconds on the GPU, so the checks below take their
-# fast way first: one comparison per property, addresses as plain ints, and words for an
-# error only once something is wrong.
-_EMPTY_PTR = 16          # non-NULL, 16-byte aligned, never dereferenced (empty tensor)
-
-
-def _operand_error(t, dtypes, shape, name: str, device):
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name}: expected a tensor, got {type(t).__name__}")
-    if t.dtype not in dtypes:
-        raise TypeError(f"{name}: expected one of {[str(d) for d in dtypes]}, got {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, the call needs {shape}")
-    if t.device != device:
-        raise ValueError(f"{name}: on {t.device}, the call runs on {device}")
-    raise ValueError(f"{name}: tensors must be contiguous")
-
-
-def _operand(t: torch.Tensor | None, dtypes, shape, name: str, device: torch.device):
-    """The address of a contiguous tensor of exactly `shape` on `device` (None: NULL)."""
-    if t is None:
-        return None
-    if not (isinstance(t, torch.Tensor) and t.dtype in dtypes and t.shape == shape and t.device == device
-            and t.is_contiguous()):
-        _operand_error(t, dtypes, shape, name, device)
-    return t.data_ptr() or _EMPTY_PTR
-
-
-def _matrix(w, N: int, K: int, group_size: int, bits: int, device: torch.device, name: str):
-    """Checked addresses of one (wq, scales, biases | None) with W [N][K]."""
-    wq, scales, biases = w
-    if biases is None:
-        return (_operand(wq, U8, (N, K // 2), name + ".wq", device),
-                _operand(scales, BITS16, (N, K // 32), name + ".scales", device), None)
-    groups = (N, K // max(group_size, 1))
-    return (_operand(wq, U32, (N, K * bits // 32), name + ".wq", device),
-            _operand(scales, BF16, groups, name + ".scales", device),
-            _operand(biases, BF16, groups, name + ".biases", device))
-
-
-class _On:
-    """Makes a device and a stream current, so that a call's outputs and workspace come
-    from that stream's memory."""
-
-    def __init__(self, device: torch.device, stream):
-        self.ctx = torch.cuda.stream(stream) if stream is not None else torch.cuda.device(device)
-
-    def __enter__(self):
-        self.ctx.__enter__()
-
-    def __exit__(self, *exc):
-        return self.ctx.__exit__(*exc)
+def _calls():
+    """The compiled marshalling of these calls (loaded on first use; raises if not built)."""
+    global _marshal
+    if _marshal is None:
+        lib()
+        try:
+            m = importlib.import_module(__name__ + "._binding")
+        except ImportError as e:
+            raise RuntimeError(f"_binding.so could not be loaded from {_PKG}; build it with "
+                               "`python -c 'import __graft_entry__ as g; g.build()'`") from e
+        m.set_error(BqError)
+        _marshal = m
+    return _marshal
 
 
 _HERE = contextlib.nullcontext()
 
 
-def _on(device: torch.device, stream):
-    """_On where something has to change, else nothing."""
-    if stream is None and device.index == torch.cuda.current_device():
+def _on(stream, t: torch.Tensor, name: str):
+    """Makes the caller's stream current, so that the call runs on it and its outputs and
+    workspace come from its memory; the current stream otherwise."""
+    if stream is None:
         return _HERE
-    return _On(device, stream)
-
-
-def _need_cuda(t: torch.Tensor, name: str, stream) -> torch.device:
-    if not t.is_cuda:
-        raise ValueError("tensors must live on a CUDA device")
-    if t.dim() != 2:
-        raise ValueError(f"{name}: expected a matrix, got {t.dim()} dimensions")
-    if stream is not None and stream.device != t.device:
+    if t.is_cuda and stream.device != t.device:
         raise ValueError(f"stream: on {stream.device}, {name} is on {t.device}")
-    return t.device
+    return torch.cuda.stream(stream)
 
 
-def _raw_stream(device: torch.device) -> int:
-    return torch._C._cuda_getCurrentRawStream(device.index)
-
-
-def _scratch(op: int, M: int, N: int, K: int, group_size: int, bits: int, device):
-    """(tensor to keep until the call returned, address, bytes)"""
-    n = _epilogue_ws_bytes(device.index, op, M, N, K, group_size, bits)
-    if n == 0:
-        return None, None, 0
-    t = torch.empty(n, dtype=torch.uint8, device=device)
-    return t, t.data_ptr(), n
-
-
-def _out(t: torch.Tensor | None, shape, device, name: str, like: torch.Tensor):
-    """(output, address): the given tensor, checked, or a new one (beside `like`)."""
-    if t is None:
-        t = like.new_empty(shape) if like.dtype is torch.bfloat16 else torch.empty(shape, dtype=torch.bfloat16, device=device)
-        return t, t.data_ptr() or _EMPTY_PTR
-    return t, _operand(t, (torch.bfloat16,), shape, name, device)
-
-
-_VP2 = ctypes.c_void_p * 2
-
-
-def _pair_of(gate, up, N: int, K: int, group_size: int, bits: int, device):
-    """The host arrays (wq, scales, biases | None) of a gate and an up matrix of one format."""
-    if (gate[2] is None) != (up[2] is None):
-        raise ValueError("gate and up must both be Q4_0 (biases None) or both be affine")
-    a = _matrix(gate, N, K, group_size, bits, device, "gate")
-    b = _matrix(up, N, K, group_size, bits, device, "up")
-    return _VP2(a[0], b[0]), _VP2(a[1], b[1]), None if gate[2] is None else _VP2(a[2], b[2])
+def quant_matmul_epilogue_workspace_size(op: int, M: int, N: int, K: int, group_size: int, bits: int) -> int:
+    """Bytes of workspace of OP_ACT, OP_ACT_BACKWARD, OP_GLU or OP_GLU_BACKWARD."""
+    return lib().quant_matmul_epilogue_workspace_size(op, M, N, K, group_size, bits)
 
 
 def quant_matmul_act(x: torch.Tensor, wq: torch.Tensor, scales: torch.Tensor, biases: torch.Tensor | None = None,
@@ -472,21 +391,9 @@ def quant_matmul_act(x: torch.Tensor, wq: torch.Tensor, scales: torch.Tensor, bi
     """y = residual + act(x . dequant(W)[N][K]^T + out_bias), bf16 [M][N], in the
     product's own epilogue; act is a key of ACTS.  out may be residual itself.  With
     save_preact: (y, z), z the bf16 argument of act, for quant_matmul_act_backward."""
-    dev = _need_cuda(x, "x", stream)
-    M, K = x.shape
-    N = wq.shape[0]
     code = _act_code(act)
-    with _on(dev, stream):
-        w = _matrix((wq, scales, biases), N, K, group_size, bits, dev, "w")
-        xp = _operand(x, BF16, (M, K), "x", dev)
-        bp = _operand(out_bias, BF16, (N,), "out_bias", dev)
-        rp = _operand(residual, BF16, (M, N), "residual", dev)
-        out, yp = _out(out, (M, N), dev, "out", x)
-        z, zp = _out(None, (M, N), dev, "z", x) if save_preact else (None, None)
-        keep, ws, wsb = _scratch(OP_ACT, M, N, K, group_size, bits, dev)
-        _check(lib().quant_matmul_act(xp, w[0], w[1], w[2], bp, rp, code, yp, zp, M, N, K, group_size, bits, ws, wsb,
-                                      _raw_stream(dev)), "quant_matmul_act")
-    return (out, z) if save_preact else out
+    with _on(stream, x, "x"):
+        return _calls().act(x, wq, scales, biases, out_bias, code, residual, group_size, bits, save_preact, out)
 
 
 def quant_matmul_act_backward(dy: torch.Tensor, wq: torch.Tensor, scales: torch.Tensor,
@@ -496,24 +403,11 @@ def quant_matmul_act_backward(dy: torch.Tensor, wq: torch.Tensor, scales: torch.
     """The gradients of quant_matmul_act for frozen weights, from dy [M][N] and the
     saved z: (dx [M][K], dz [M][N]) and with need_dbias also dbias [N], all bf16.
     For act "none" dz is dy itself and preact is not needed; the residual's gradient is dy."""
-    dev = _need_cuda(dy, "dy", stream)
-    M, N = dy.shape
-    K = _k_of(wq, biases, bits)
     code = _act_code(act)
     if code and preact is None:
         raise ValueError(f"preact: act {act!r} needs the saved z")
-    with _on(dev, stream):
-        w = _matrix((wq, scales, biases), N, K, group_size, bits, dev, "w")
-        dyp = _operand(dy, (torch.bfloat16,), (M, N), "dy", dev)
-        pp = _operand(preact, BF16, (M, N), "preact", dev)
-        dx, dxp = _out(None, (M, K), dev, "dx", dy)
-        dz, dzp = _out(None, (M, N), dev, "dz", dy) if code else (dy, None)
-        db, dbp = _out(None, (N,), dev, "dbias", dy) if need_dbias else (None, None)
-        keep, ws, wsb = _scratch(OP_ACT_BACKWARD, M, N, K, group_size, bits, dev)
-        _check(lib().quant_matmul_act_backward(dyp, pp, w[0], w[1], w[2], code, dxp, dzp, dbp, M, N, K, group_size,
-                                               bits, ws, wsb, _raw_stream(dev)),
-               "quant_matmul_act_backward")
-    return (dx, dz, db) if need_dbias else (dx, dz)
+    with _on(stream, dy, "dy"):
+        return _calls().act_backward(dy, wq, scales, biases, preact, code, group_size, bits, need_dbias)
 
 
 def quant_matmul_glu(x: torch.Tensor, gate, up, gate_bias: torch.Tensor | None = None,
@@ -523,22 +417,9 @@ def quant_matmul_glu(x: torch.Tensor, gate, up, gate_bias: torch.Tensor | None =
     [M][N], both projections in one product.  gate and up are (wq, scales, biases | None)
     of one format.  With save_preact: (h, g, u), the bf16 factors before the activation,
     for quant_matmul_glu_backward."""
-    dev = _need_cuda(x, "x", stream)
-    M, K = x.shape
-    N = gate[0].shape[0]
     code = _act_code(act)
-    with _on(dev, stream):
-        w = _pair_of(gate, up, N, K, group_size, bits, dev)
-        xp = _operand(x, BF16, (M, K), "x", dev)
-        gbp = _operand(gate_bias, BF16, (N,), "gate_bias", dev)
-        ubp = _operand(up_bias, BF16, (N,), "up_bias", dev)
-        out, hp = _out(out, (M, N), dev, "out", x)
-        g, gp = _out(None, (M, N), dev, "g", x) if save_preact else (None, None)
-        u, up_ = _out(None, (M, N), dev, "u", x) if save_preact else (None, None)
-        keep, ws, wsb = _scratch(OP_GLU, M, N, K, group_size, bits, dev)
-        _check(lib().quant_matmul_glu(xp, w[0], w[1], w[2], gbp, ubp, code, hp, gp, up_, M, N, K, group_size, bits, ws,
-                                      wsb, _raw_stream(dev)), "quant_matmul_glu")
-    return (out, g, u) if save_preact else out
+    with _on(stream, x, "x"):
+        return _calls().glu(x, gate, up, gate_bias, up_bias, code, group_size, bits, save_preact, out)
 
 
 def quant_matmul_glu_backward(dh: torch.Tensor, g: torch.Tensor, u: torch.Tensor, gate, up, act: str = "silu",
@@ -546,25 +427,9 @@ def quant_matmul_glu_backward(dh: torch.Tensor, g: torch.Tensor, u: torch.Tensor
     """The gradients of quant_matmul_glu for frozen weights, from dh [M][N] and the
     saved g and u: (dx [M][K], dg [M][N], du [M][N]) and with need_dbias also
     (dgate_bias [N], dup_bias [N]), all bf16."""
-    dev = _need_cuda(dh, "dh", stream)
-    M, N = dh.shape
-    K = _k_of(gate[0], gate[2], bits)
     code = _act_code(act)
-    with _on(dev, stream):
-        w = _pair_of(gate, up, N, K, group_size, bits, dev)
-        dhp = _operand(dh, BF16, (M, N), "dh", dev)
-        gp = _operand(g, BF16, (M, N), "g", dev)
-        up_ = _operand(u, BF16, (M, N), "u", dev)
-        dx, dxp = _out(None, (M, K), dev, "dx", dh)
-        dg, dgp = _out(None, (M, N), dev, "dg", dh)
-        du, dup = _out(None, (M, N), dev, "du", dh)
-        dgb, dgbp = _out(None, (N,), dev, "dgate_bias", dh) if need_dbias else (None, None)
-        dub, dubp = _out(None, (N,), dev, "dup_bias", dh) if need_dbias else (None, None)
-        keep, ws, wsb = _scratch(OP_GLU_BACKWARD, M, N, K, group_size, bits, dev)
-        _check(lib().quant_matmul_glu_backward(dhp, gp, up_, w[0], w[1], w[2], code, dxp, dgp, dup, dgbp, dubp,
-                                               M, N, K, group_size, bits, ws, wsb,
-                                               _raw_stream(dev)), "quant_matmul_glu_backward")
-    return (dx, dg, du, dgb, dub) if need_dbias else (dx, dg, du)
+    with _on(stream, dh, "dh"):
+        return _calls().glu_backward(dh, g, u, gate, up, code, group_size, bits, need_dbias)
 
 
 # ------------------------------------------------------------------- quantize
