@@ -1759,6 +1759,6 @@ const char* bq_status_string(int status)
     }
 }
 
-int bq_version(void) { return 100; }
+int bq_version(void) { return 101; }
 
 }  // extern "C"

@@ -477,8 +477,9 @@ bq_status epi_workspace(int dev, cudaStream_t st, void* workspace, size_t worksp
 
 bool sizes_ok(int64_t M, int64_t N, int64_t K)
 {
-    // 32-bit tile, row and column numbers in the kernels, with room for a tile's width
-    return M <= INT32_MAX - 1024 && N <= INT32_MAX / 2 - 1024 && K <= INT32_MAX - 1024;
+    // 32-bit tile, row and column numbers in the kernels, with room for a tile's width; K
+    // also within scale_pack_kernel's grid (65535 blocks of 2048 columns)
+    return M <= INT32_MAX - 1024 && N <= INT32_MAX / 2 - 1024 && K <= 65535 * 2048;
 }
 
 // ------------------------------------------------------------------ forward
@@ -515,7 +516,7 @@ bq_status epi_forward(const uint16_t* x, const QMat* w, const EpiParams& e, int6
     }
     if (ring_applies(fmt, M, K)) return launch_ring<EPI>(fmt, x, w, e, M, N, K, group_size, di, dev, st);
     EpiWs ws;
-    if (!plan_forward(fmt, mats, M, N, K, di.num_sms, di.max_smem_optin, &ws)) return BQ_ERR_UNSUPPORTED;
+    if (!plan_forward(fmt, mats, M, N, K, di.num_sms, di.max_smem_optin, &ws)) return BQ_ERR_SHAPE;   // too many tiles
     void* buf = nullptr;
     if ((s = epi_workspace(dev, st, workspace, workspace_bytes, ws.bytes, &buf)) != BQ_OK) return s;
     if (ws.fused) {
@@ -595,8 +596,7 @@ bq_status epi_backward(const EpiBackward& b, const QMat* w, int act, int64_t M, 
     if (N == 0)                                          // a sum over no outputs
         return cudaMemsetAsync(b.dx, 0, (size_t)M * (size_t)K * 2u, st) == cudaSuccess ? BQ_OK : BQ_ERR_CUDA;
     EpiWs ws;
-    if (!plan_backward(fmt, mats, M, N, K, di.num_sms, di.max_smem_optin, &ws)) return BQ_ERR_UNSUPPORTED;
-    if (ws.row_blocks > 65535) return BQ_ERR_SHAPE;
+    if (!plan_backward(fmt, mats, M, N, K, di.num_sms, di.max_smem_optin, &ws)) return BQ_ERR_SHAPE;
     void* buf = nullptr;
     if ((s = epi_workspace(dev, st, workspace, workspace_bytes, ws.bytes, &buf)) != BQ_OK) return s;
     uint8_t* base = reinterpret_cast<uint8_t*>(buf);

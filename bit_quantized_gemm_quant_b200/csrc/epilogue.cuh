@@ -31,9 +31,25 @@ struct EpiParams {
     int act = kActNone;
 };
 
-// 1 / (1 + e^-z).  The divide is exact to 2 ulp; past e^-z = 2^126 it gives 0,
-// the function's value there to within 2^-126.
-BQ_DEVINL float sigmoid_f(float z) { return __fdividef(1.0f, 1.0f + __expf(-z)); }
+// e^x and 1 / x by the hardware's approximations (2^-22 relative; results below the normal
+// range become 0): one multiply and one special-function instruction, without the range
+// scaling of the library functions.  The gelu gradient of 2048 x 12288 is bound by issue.
+BQ_DEVINL float exp_approx(float x)
+{
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x * 1.4426950408889634f));
+    return r;
+}
+
+BQ_DEVINL float rcp_approx(float x)
+{
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+// 1 / (1 + e^-z); 0 where e^-z overflows.
+BQ_DEVINL float sigmoid_f(float z) { return rcp_approx(1.0f + exp_approx(-z)); }
 
 // gelu_tanh through 0.5 (1 + tanh a) = sigmoid(2 a), a = sqrt(2/pi) (z + 0.044715 z^3).
 constexpr float kGeluTanhA = 1.5957691216057308f;        // 2 sqrt(2/pi)
@@ -48,8 +64,8 @@ constexpr float kInvSqrt2Pi = 0.39894228040143268f;
 // this place made the epilogue of a 12288 x 4096, 512-token product take 19 us.)
 BQ_DEVINL float normal_cdf(float z, float& e)
 {
-    const float x = fabsf(z) * kInvSqrt2, t = __fdividef(1.0f, fmaf(0.3275911f, x, 1.0f));
-    e = __expf(-0.5f * z * z);
+    const float t = rcp_approx(fmaf(0.3275911f * kInvSqrt2, fabsf(z), 1.0f));
+    e = exp_approx(-0.5f * z * z);
     float q = fmaf(t, 0.5f * 1.061405429f, 0.5f * -1.453152027f);
     q = fmaf(t, q, 0.5f * 1.421413741f);
     q = fmaf(t, q, 0.5f * -0.284496736f);
@@ -397,7 +413,7 @@ __global__ void __launch_bounds__(256) epi_empty_kernel(EpiParams e, int64_t M, 
 // epi_bias_grad_kernel, both in a fixed order.
 //
 // Bound by HBM: act reads 2 and writes 1 bf16 [M][N] array, glu reads 3 and writes
-// 2.  A block takes 32 x V columns; its 8 warps take every 8th row.  V = 8 (16-byte
+// 2.  A block takes 32 x V columns; its 8 warps take every 8th row, R of them at a time.  V = 8 (16-byte
 // loads) when every row starts on 16 bytes, else 1.
 struct EpiGradParams {
     const uint16_t* dy;
@@ -421,43 +437,58 @@ __global__ void __launch_bounds__(256) epi_grad_kernel(EpiGradParams p)
     float sz[V], su[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) sz[i] = su[i] = 0.0f;
+    // R rows at a time, all of their loads in flight before the first is used
+    constexpr int R = V == 8 ? 2 : 4;
+    const uint16_t* __restrict__ dy = p.dy;
+    const uint16_t* __restrict__ z = p.z;
+    const uint16_t* __restrict__ u = p.u;
     if (n < p.N) {
-        for (int64_t m = (int64_t)blockIdx.y * p.rows_per_block + warp; m < m_end; m += 8) {
-            const int64_t o = m * p.N + n;
-            __align__(16) uint16_t vd[V], vz[V], vu[V], oz[V], ou[V];
-            if constexpr (V == 8) {
-                *reinterpret_cast<uint4*>(vd) = *reinterpret_cast<const uint4*>(p.dy + o);
-                if constexpr (ACT != kActNone || GLU) *reinterpret_cast<uint4*>(vz) = *reinterpret_cast<const uint4*>(p.z + o);
-                if constexpr (GLU) *reinterpret_cast<uint4*>(vu) = *reinterpret_cast<const uint4*>(p.u + o);
-            } else {
-                vd[0] = p.dy[o];
-                if constexpr (ACT != kActNone || GLU) vz[0] = p.z[o];
-                if constexpr (GLU) vu[0] = p.u[o];
+        for (int64_t m0 = (int64_t)blockIdx.y * p.rows_per_block + warp; m0 < m_end; m0 += 8 * R) {
+            __align__(16) uint16_t vd[R][V], vz[R][V], vu[R][V];
+#pragma unroll
+            for (int q = 0; q < R; ++q) {
+                const int64_t o = min(m0 + 8 * q, m_end - 1) * p.N + n;
+                if constexpr (V == 8) {
+                    *reinterpret_cast<uint4*>(vd[q]) = *reinterpret_cast<const uint4*>(dy + o);
+                    if constexpr (ACT != kActNone || GLU) *reinterpret_cast<uint4*>(vz[q]) = *reinterpret_cast<const uint4*>(z + o);
+                    if constexpr (GLU) *reinterpret_cast<uint4*>(vu[q]) = *reinterpret_cast<const uint4*>(u + o);
+                } else {
+                    vd[q][0] = dy[o];
+                    if constexpr (ACT != kActNone || GLU) vz[q][0] = z[o];
+                    if constexpr (GLU) vu[q][0] = u[o];
+                }
             }
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const float d = bf16_bits_to_f32(vd[i]);
-                float a = d;
-                if constexpr (GLU) {
-                    const float g = bf16_bits_to_f32(vz[i]), b = d * act_f<ACT>(g);
-                    a = d * bf16_bits_to_f32(vu[i]) * dact_f<ACT>(g);
-                    su[i] += b;
-                    ou[i] = (uint16_t)f32_to_bf16_bits(b);
-                } else if constexpr (ACT != kActNone) {
-                    a = d * dact_f<ACT>(bf16_bits_to_f32(vz[i]));
+            for (int q = 0; q < R; ++q) {
+                const int64_t m = m0 + 8 * q;
+                if (m >= m_end) break;
+                const int64_t o = m * p.N + n;
+                __align__(16) uint16_t oz[V], ou[V];
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    const float d = bf16_bits_to_f32(vd[q][i]);
+                    float a = d;
+                    if constexpr (GLU) {
+                        const float g = bf16_bits_to_f32(vz[q][i]), b = d * act_f<ACT>(g);
+                        a = d * bf16_bits_to_f32(vu[q][i]) * dact_f<ACT>(g);
+                        su[i] += b;
+                        ou[i] = (uint16_t)f32_to_bf16_bits(b);
+                    } else if constexpr (ACT != kActNone) {
+                        a = d * dact_f<ACT>(bf16_bits_to_f32(vz[q][i]));
+                    }
+                    sz[i] += a;
+                    oz[i] = (uint16_t)f32_to_bf16_bits(a);
                 }
-                sz[i] += a;
-                oz[i] = (uint16_t)f32_to_bf16_bits(a);
-            }
-            if constexpr (V == 8) {
-                if (p.dz) *reinterpret_cast<uint4*>(p.dz + o) = *reinterpret_cast<const uint4*>(oz);
-                if constexpr (GLU) *reinterpret_cast<uint4*>(p.du + o) = *reinterpret_cast<const uint4*>(ou);
-            } else {
-                if (p.dz) p.dz[o] = oz[0];
-                if constexpr (GLU) p.du[o] = ou[0];
-                if (p.dz_pad) {
-                    p.dz_pad[m * p.pitch + n] = oz[0];
-                    if constexpr (GLU) p.du_pad[m * p.pitch + n] = ou[0];
+                if constexpr (V == 8) {
+                    if (p.dz) *reinterpret_cast<uint4*>(p.dz + o) = *reinterpret_cast<const uint4*>(oz);
+                    if constexpr (GLU) *reinterpret_cast<uint4*>(p.du + o) = *reinterpret_cast<const uint4*>(ou);
+                } else {
+                    if (p.dz) p.dz[o] = oz[0];
+                    if constexpr (GLU) p.du[o] = ou[0];
+                    if (p.dz_pad) {
+                        p.dz_pad[m * p.pitch + n] = oz[0];
+                        if constexpr (GLU) p.du_pad[m * p.pitch + n] = ou[0];
+                    }
                 }
             }
         }

@@ -10,8 +10,10 @@
 // reduction columns come in chunks of 2048 (one ring stage: 16 rows of codes, scales
 // and biases, each one tensor copy; copies of single rows were limited by their
 // number: glu, 8 tokens, 12288 x 4096 affine 4-bit took 48 us with them).  8 compute
-// warps split a chunk, two steps of 128 columns each: the four threads of a quad take
-// 32 consecutive columns each of rows g and g + 8.  So every warp sees the same columns
+// warps split a chunk, two steps of 128 columns each (16 warps with one step each spend
+// more on waits: 22.6 against 20.3 us; fetching the next chunk ahead into registers costs
+// more issue slots than it hides, 22.4): the four threads of a quad take 32 consecutive
+// columns each of rows g and g + 8.  So every warp sees the same columns
 // of every tile, and its activations (the MMA's B fragments, 16 registers per 8 tokens
 // and step) are loaded once and stay in registers for K up to 8192.
 //
@@ -232,6 +234,13 @@ gemv_ring_kernel(const __grid_constant__ RingMaps maps, const __grid_constant__ 
         fence_barrier_init();
         fence_proxy_async_smem();
     }
+    if (threadIdx.x == 32 * kRingWarps) {
+        for (int i = 0; i < (EPI == kEpiGlu ? 2 : 1); ++i) {
+            tma_prefetch_desc(&maps.codes[i]);
+            if (p.scale_bulk) tma_prefetch_desc(&maps.scales[i]);
+            if (p.scale_bulk && kAffine) tma_prefetch_desc(&maps.biases[i]);
+        }
+    }
     __syncthreads();
     grid_dependency_wait();
     grid_dependents_launch();      // a following kernel's set-up may overlap this one (it waits before its reads)
@@ -252,7 +261,6 @@ gemv_ring_kernel(const __grid_constant__ RingMaps maps, const __grid_constant__ 
                                       : (kind == 1 ? kScaleOff : kBiasOff) + mat * kRows * sp;
         const int x0 = kind == 0 ? panel * (kPanelCols * B / 64) : 0;
         const int xj = kind == 0 ? kRingCols * B / 64 : kRingCols >> p.gs_shift;
-        if (mine) tma_prefetch_desc(map);
         int s = 0, issued = 0;
         uint32_t ph = 0;
         bool ok = true;

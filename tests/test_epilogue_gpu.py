@@ -167,6 +167,39 @@ def test_forms_over_formats_and_tokens(fmt, N, K):
     assert bq.bq_device_status() == 0
 
 
+@pytest.mark.parametrize("fmt,K", [("q4_0", 32), ("q4_0", 96), ("q4_0", 160), ("affine4", 64), ("affine8", 192), ("affine8_g32", 32),
+                                   ("affine2_g32", 32), ("affine3_g32", 32), ("affine6_g32", 96), ("affine4_g32", 224)])
+def test_shortest_and_odd_reductions(fmt, K):
+    """One block or group of columns and counts that fill no stage, chunk or 16-byte row of scales."""
+    for i, M in enumerate((1, 16, 17, 70)):
+        for N in (3, 136):
+            check_act(Case(fmt, N, K, M, 1, seed=i), ACTS[i + 1], save=True)
+            check_glu(Case(fmt, N, K, M, 2, seed=i), "silu", bias=True, save=True)
+            check_act_bwd(Case(fmt, N, K, M, 1, seed=i), ACTS[i])
+            check_glu_bwd(Case(fmt, N, K, M, 2, seed=i), ACTS[i + 1])
+    assert bq.bq_device_status() == 0
+
+
+def test_outputs_past_32_bit_offsets():
+    """70000 x 32768 outputs (2.3e9 elements): the last rows and columns against the formula."""
+    M, N, K = 70000, 32768, 64
+    g = torch.Generator(device="cuda")
+    g.manual_seed(3)
+    wq = torch.randint(0, 256, (N, K // 2), generator=g, device="cuda", dtype=torch.int32).to(torch.uint8)
+    s = (torch.rand(N, K // 32, generator=g, device="cuda") * 0.02 + 0.01).to(torch.float16)
+    W = bq.q4_0_dequantize(wq, s).double()
+    x = torch.randn(M, K, generator=g, device="cuda").to(torch.bfloat16)
+    y = bq.quant_matmul_act(x, wq, s, act="silu")
+    rows = torch.tensor([0, 1, 65535, 65536, M - 2, M - 1], device="cuda")
+    z, t = sums(x[rows], W, None)
+    near(y[rows], f("silu", z), (1.13 * t + EVAL * (1 + z.abs())) * (1 + HALF), "y")
+    dx, dz = bq.quant_matmul_act_backward(y, wq, s, preact=y, act="relu")
+    assert torch.equal(dz[rows], torch.where(y[rows] > 0, y[rows], torch.zeros_like(y[rows])))
+    want, t = product_bound([dz[rows]], [W])
+    near(dx[rows], want, t, "dx")
+    assert bq.bq_device_status() == 0
+
+
 @pytest.mark.parametrize("act", ACTS)
 def test_every_activation_each_way(act):
     for M in (3, 40):
