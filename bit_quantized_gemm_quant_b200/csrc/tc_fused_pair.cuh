@@ -7,34 +7,38 @@
 //
 // Tiles, pairs, accumulators and units of work are tc_pair.cuh's: 256 D rows x bn
 // tokens per pair (cta_group::2), two accumulators of 256 columns; a block of the
-// reduction is 128 elements here, two halves of one swizzle atom each.  (The MMA warp
-// spends 150 clocks on each of a block's two waits beside 16 busy dequant warps: at 64
-// elements a block that, not the tensor core, set the pace, 640 clocks a block.)  Here the weight
-// tile of a stage arrives as codes: 128 x 64 weights per CTA are 4 KB (8-bit: 8 KB)
-// where their bf16 form is 16 KB, so a stage moves 20 KB per SM through L2 instead of
-// 32, and no bf16 copy of W is written to or read from memory.  16 dequant warps, four
-// groups of four that take blocks in turn, expand them to bf16 in a shared-memory tile
-// in the layout that the MMA reads: 64 weights of one row per thread, either 64
-// consecutive k of an output row (forward) or 64 consecutive outputs of a reduction row
-// (gradient).  The codes land swizzled, so that both the code reads
-// and the tile writes of a warp cover all banks evenly.
+// reduction is 128 elements here, two halves of one swizzle atom each.  The weight tile
+// arrives as codes: a block's 128 x 128 weights per CTA are 8 KB (8-bit: 16 KB) and 2 KB of
+// scales where their bf16 form is 32 KB, so at 256 tokens a block moves 42 KB per SM
+// through L2 instead of 64, and no bf16 copy of W is written to or read from memory.  16
+// dequant warps, in four groups of four, two groups per block, expand the codes to bf16 in
+// shared memory in the layout that the MMA reads: 64 weights of one row per thread, either
+// 64 consecutive k of an output row (forward) or 64 consecutive outputs of a reduction row
+// (gradient).  The codes land swizzled, so that the code reads and the tile writes of a
+// warp cover all banks evenly.
 //
-// Three rings run at their own depth: codes (small, freed as soon as a dequant group has
-// read them), token tiles, and expanded weight tiles.  With codes, tokens and tile in
-// one stage a block took 1350 clocks, with codes and tokens in one stage and four tiles
-// 1130: a tile slot or stage was then held through a copy's round trip, the wait for a
-// group and the product, longer than the ring covers at the MMA's 512 clocks a block.
+// What set the pace on the way (gated 12288 x 4096 affine 4-bit, 2048 tokens, us):
+//  - scales: a thread needs two of one row, and rows are far apart in memory, so every load
+//    of a warp touches 32 lines; with the loads the dequantization alone took 318, without
+//    198.  scale_pack_kernel now lays them out by block first (32 weights: one word of two
+//    16-bit values, scale and bias, or Q4_0's d split in two), and they come with the codes;
+//  - one ring for codes, tokens and tiles held each through a copy's round trip, the wait
+//    for a group and the product: now three rings, each at its own depth;
+//  - the MMA warp and the producers beside 16 busy dequant warps: 150 clocks for each wait
+//    on a barrier, and an operand move for everything that is not in a uniform register.
+//    So blocks are 128 elements (two waits and one commit each), and these warps run their
+//    loops whole with one elected lane issuing (forward: 355 with one lane and blocks of
+//    64, 277 now);
+//  - the epilogue: eight warps, and for the last unit, which no product overlaps, the
+//    dequant warps as well.
+// Large products are now bound by the tensor cores and the power they may draw (1.49
+// PFLOP/s in isolation, cuBLAS bf16 reaches 1.64); below 192 tokens a tile the 1050 clocks
+// that a block's dequantization takes exceed the MMA's.
+//
 // Barriers: cfull / cempty (codes, each CTA's own), bfull (tokens of both CTAs, the
-// leader's), ready (a block's tile, the leader's; 8 dequant warps of each CTA arrive), consumed
-// (one per block, each CTA's own; the MMA's commit arrives on both and thereby frees the
-// block's token tile and weight tile).
-//
-// Scales: a thread needs two of one row, and rows are far apart in memory; loaded by the
-// threads themselves they took longer than the rest of the dequantization (every load
-// touches 32 lines: 318 us without the MMA, 198 without the loads, gated gradient of
-// 12288 x 4096 at 2048 tokens).  So scale_pack_kernel first lays them out by block, the 1
-// KB of a block contiguous (32 weights: one word of two 16-bit values, a scale and a bias
-// or Q4_0's d split in two), and they come with the codes.
+// leader's), ready (a block's tile, the leader's; 8 dequant warps of each CTA arrive),
+// consumed (one per block, each CTA's own; the MMA's commit arrives on both and thereby
+// frees the block's token tile and weight tile).
 #pragma once
 
 #include "tc_gemm.cuh"
