@@ -303,29 +303,37 @@ ScalePack scale_pack(bool mn, int mats, int64_t N, int64_t K)
 
 int fp_mode(WFmt f) { return f == WFmt::Q4_0 ? kModeQ4_0 : f == WFmt::AFF4 ? kModeAff4 : kModeAff8; }
 
-// The scales of w (1 or 2 matrices [N][K]), by block, to `packed`; interleave: for the glu
-// forward product.
-bq_status launch_scale_pack(WFmt fmt, bool mn, const QMat* w, int mats, bool interleave, int64_t N, int64_t K,
-                            int group_size, void* packed, cudaStream_t st)
+// The work of laying out the scales of w (1 or 2 matrices [N][K]) at `packed`, and its
+// number of blocks (0: too many); interleave: for the glu forward product.
+int64_t scale_pack_params(bool mn, const QMat* w, int mats, bool interleave, int64_t N, int64_t K, int group_size,
+                          void* packed, ScalePackParams* pp)
 {
     const ScalePack sp = scale_pack(mn, mats, N, K);
-    ScalePackParams pp;
     for (int i = 0; i < 2; ++i) {
         const QMat& q = w[i < mats ? i : 0];
-        pp.scales[i] = reinterpret_cast<const uint16_t*>(q.scales);
-        pp.biases[i] = reinterpret_cast<const uint16_t*>(q.biases);
+        pp->scales[i] = reinterpret_cast<const uint16_t*>(q.scales);
+        pp->biases[i] = reinterpret_cast<const uint16_t*>(q.biases);
     }
-    pp.out = reinterpret_cast<uint32_t*>(packed);
-    pp.N = (int)N;
-    pp.K = (int)K;
-    pp.gs_shift = group_size == 32 ? 5 : group_size == 64 ? 6 : 7;
-    pp.interleave = interleave;
-    pp.cols = (int)sp.cols;
-    pp.pack_rows = sp.rows;
-    pp.pack_mat = sp.mat;
-    const dim3 grid((unsigned)((sp.rows / (interleave ? 2 : 1) + 31) / 32), (unsigned)((sp.cols + 2047) / 2048), (unsigned)mats);
-    return fmt == WFmt::Q4_0 ? launch_pdl_dim(scale_pack_kernel<true>, grid, 256, 0, st, pp)
-                             : launch_pdl_dim(scale_pack_kernel<false>, grid, 256, 0, st, pp);
+    pp->out = reinterpret_cast<uint32_t*>(packed);
+    pp->N = (int)N;
+    pp->K = (int)K;
+    pp->gs_shift = group_size == 32 ? 5 : group_size == 64 ? 6 : 7;
+    pp->interleave = interleave;
+    pp->cols = (int)sp.cols;
+    pp->pack_rows = sp.rows;
+    pp->pack_mat = sp.mat;
+    pp->row_chunks = (int)((sp.rows / (interleave ? 2 : 1) + 31) / 32);
+    pp->col_chunks = (int)((sp.cols + 2047) / 2048);
+    const int64_t blocks = (int64_t)pp->row_chunks * pp->col_chunks * mats;
+    return blocks <= INT32_MAX / 2 ? blocks : 0;
+}
+
+bq_status launch_scale_pack(bool mn, const QMat* w, int mats, bool interleave, int64_t N, int64_t K, int group_size,
+                            void* packed, cudaStream_t st)
+{
+    ScalePackParams pp;
+    const int64_t blocks = scale_pack_params(mn, w, mats, interleave, N, K, group_size, packed, &pp);
+    return blocks ? launch_pdl_dim(scale_pack_kernel, dim3((unsigned)blocks), 256, 0, st, pp) : BQ_ERR_SHAPE;
 }
 
 // The product of launch_pair with the codes of w (1 or 2 matrices [N][K]) and their
@@ -477,8 +485,7 @@ bq_status epi_workspace(int dev, cudaStream_t st, void* workspace, size_t worksp
 
 bool sizes_ok(int64_t M, int64_t N, int64_t K)
 {
-    // 32-bit tile, row and column numbers in the kernels, with room for a tile's width; K
-    // also within scale_pack_kernel's grid (65535 blocks of 2048 columns)
+    // 32-bit tile, row and column numbers in the kernels, with room for a tile's width
     return M <= INT32_MAX - 1024 && N <= INT32_MAX / 2 - 1024 && K <= 65535 * 2048;
 }
 
@@ -520,7 +527,7 @@ bq_status epi_forward(const uint16_t* x, const QMat* w, const EpiParams& e, int6
     void* buf = nullptr;
     if ((s = epi_workspace(dev, st, workspace, workspace_bytes, ws.bytes, &buf)) != BQ_OK) return s;
     if (ws.fused) {
-        if ((s = launch_scale_pack(fmt, false, w, mats, mats == 2, N, K, group_size, buf, st)) != BQ_OK) return s;
+        if ((s = launch_scale_pack(false, w, mats, mats == 2, N, K, group_size, buf, st)) != BQ_OK) return s;
         return launch_fused_pair_fmt<false, EPI>(fmt, di, dev, ws.pl, w, mats, &x, N, K, M, K, group_size, e, buf,
                                                  reinterpret_cast<uint8_t*>(buf) + ws.off_split, st);
     }
@@ -531,16 +538,13 @@ bq_status epi_forward(const uint16_t* x, const QMat* w, const EpiParams& e, int6
 }
 
 // ------------------------------------------------------------------ backward
-// beside_pack: right behind scale_pack_kernel, which it may overlap.
 template <bool GLU, int V>
-bq_status launch_epi_grad_v(const EpiGradParams& p, int act, int row_blocks, bool beside_pack, cudaStream_t st)
+bq_status launch_epi_grad_v(EpiGradParams& p, int act, int row_blocks, cudaStream_t st)
 {
-    const dim3 grid((unsigned)(((int64_t)p.N + 32 * V - 1) / (32 * V)), (unsigned)row_blocks);
-    auto go = [&](auto kern) {
-        if (beside_pack) return launch_pdl_dim(kern, grid, 256, 0, st, p);
-        kern<<<grid, 256, 0, st>>>(p);
-        return launch_status();
-    };
+    p.col_blocks = (int)(((int64_t)p.N + 32 * V - 1) / (32 * V));
+    const int64_t blocks = p.pack_blocks + (int64_t)p.col_blocks * row_blocks;
+    if (blocks > INT32_MAX) return BQ_ERR_SHAPE;
+    auto go = [&](auto kern) { return launch_pdl_dim(kern, dim3((unsigned)blocks), 256, 0, st, p); };
     switch (act) {
     case kActRelu: return go(epi_grad_kernel<GLU, kActRelu, V>);
     case kActGelu: return go(epi_grad_kernel<GLU, kActGelu, V>);
@@ -604,9 +608,13 @@ bq_status epi_backward(const EpiBackward& b, const QMat* w, int act, int64_t M, 
     uint16_t* padded[2] = {reinterpret_cast<uint16_t*>(base + ws.off_pad),
                            reinterpret_cast<uint16_t*>(base + ws.off_pad + up256((size_t)M * ws.pitch * 2u))};
     const bool fused = K > 0 && ws.fused;
-    if (fused && (s = launch_scale_pack(fmt, true, w, mats, false, N, K, group_size, base, st)) != BQ_OK) return s;
-    if (!none || any_db || pad) {
+    if (fused && none && !any_db && !pad) {
+        if ((s = launch_scale_pack(true, w, mats, false, N, K, group_size, base, st)) != BQ_OK) return s;
+    } else if (!none || any_db || pad) {
         EpiGradParams p;
+        p.pack_blocks = 0;
+        if (fused && (p.pack_blocks = (int)scale_pack_params(true, w, mats, false, N, K, group_size, base, &p.pack)) == 0)
+            return BQ_ERR_SHAPE;
         p.dy = b.dy;
         p.z = b.pre[0];
         p.u = b.pre[1];
@@ -619,8 +627,7 @@ bq_status epi_backward(const EpiBackward& b, const QMat* w, int act, int64_t M, 
         p.N = (int)N;
         p.pitch = (int)ws.pitch;
         p.rows_per_block = ws.rows_per_block;
-        s = pad ? launch_epi_grad_v<GLU, 1>(p, act, ws.row_blocks, fused, st)
-                : launch_epi_grad_v<GLU, 8>(p, act, ws.row_blocks, fused, st);
+        s = pad ? launch_epi_grad_v<GLU, 1>(p, act, ws.row_blocks, st) : launch_epi_grad_v<GLU, 8>(p, act, ws.row_blocks, st);
         if (s != BQ_OK) return s;
         if (any_db) {
             s = launch_pdl_dim(epi_bias_grad_kernel, dim3((unsigned)((N + 31) / 32), (unsigned)mats), 256, 0, st,

@@ -10,6 +10,7 @@
 #pragma once
 
 #include "common.cuh"
+#include "scale_pack.cuh"
 
 namespace bq {
 
@@ -369,6 +370,7 @@ epi_reduce_kernel(const float* __restrict__ ws, EpiParams e, int M, int N, int b
     const int64_t slot = (int64_t)bn * 256;
     const float* first = ws + (2 * p0 + (t.range_begin(p0) < begin ? 1 : 0)) * slot;
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 #pragma unroll 2
     for (int i = threadIdx.x; i < kReduceTokens * kGroups; i += 256) {
         const int m = c0 + i / kGroups, r4 = i % kGroups * 4;
@@ -413,8 +415,10 @@ __global__ void __launch_bounds__(256) epi_empty_kernel(EpiParams e, int64_t M, 
 // epi_bias_grad_kernel, both in a fixed order.
 //
 // Bound by HBM: act reads 2 and writes 1 bf16 [M][N] array, glu reads 3 and writes
-// 2.  A block takes 32 x V columns; its 8 warps take every 8th row, R of them at a time.  V = 8 (16-byte
-// loads) when every row starts on 16 bytes, else 1.
+// 2.  A block takes 32 x V columns; its 8 warps take every 8th row, R of them at a time.
+// V = 8 (16-byte loads) when every row starts on 16 bytes, else 1.  The first `pack_blocks`
+// blocks lay out the weights' scales for the product that follows (scale_pack.cuh), which
+// would otherwise be a kernel and its start-up latency ahead of this one.
 struct EpiGradParams {
     const uint16_t* dy;
     const uint16_t* z;         // act: z; glu: g
@@ -426,14 +430,24 @@ struct EpiGradParams {
     float* part;               // [row blocks][1 or 2][N] column sums, or NULL
     int64_t M;
     int N, pitch, rows_per_block;
+    int col_blocks, pack_blocks;
+    ScalePackParams pack;
 };
 
 template <bool GLU, int ACT, int V>
-__global__ void __launch_bounds__(256) epi_grad_kernel(EpiGradParams p)
+__global__ void __launch_bounds__(256) epi_grad_kernel(const __grid_constant__ EpiGradParams p)
 {
+    __shared__ uint32_t smem[kScalePackWords > 256 * V ? kScalePackWords : 256 * V];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if ((int)blockIdx.x < p.pack_blocks) {
+        scale_pack_block(p.pack, smem, blockIdx.x);
+        return;
+    }
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int n = (int)min((int64_t)(blockIdx.x * 32 + lane) * V, (int64_t)INT32_MAX);
-    const int64_t m_end = min(p.M, (int64_t)(blockIdx.y + 1) * p.rows_per_block);
+    const int cb = ((int)blockIdx.x - p.pack_blocks) % p.col_blocks, rb = ((int)blockIdx.x - p.pack_blocks) / p.col_blocks;
+    const int n = (cb * 32 + lane) * V;                // N is below 2^30
+    const int64_t m_end = min(p.M, (int64_t)(rb + 1) * p.rows_per_block);
     float sz[V], su[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) sz[i] = su[i] = 0.0f;
@@ -443,7 +457,7 @@ __global__ void __launch_bounds__(256) epi_grad_kernel(EpiGradParams p)
     const uint16_t* __restrict__ z = p.z;
     const uint16_t* __restrict__ u = p.u;
     if (n < p.N) {
-        for (int64_t m0 = (int64_t)blockIdx.y * p.rows_per_block + warp; m0 < m_end; m0 += 8 * R) {
+        for (int64_t m0 = (int64_t)rb * p.rows_per_block + warp; m0 < m_end; m0 += 8 * R) {
             __align__(16) uint16_t vd[R][V], vz[R][V], vu[R][V];
 #pragma unroll
             for (int q = 0; q < R; ++q) {
@@ -494,7 +508,7 @@ __global__ void __launch_bounds__(256) epi_grad_kernel(EpiGradParams p)
         }
     }
     if (p.part) {
-        __shared__ float red[8][32 * V];
+        float(*red)[32 * V] = reinterpret_cast<float(*)[32 * V]>(smem);
 #pragma unroll
         for (int k = 0; k < (GLU ? 2 : 1); ++k) {
             __syncthreads();
@@ -502,18 +516,15 @@ __global__ void __launch_bounds__(256) epi_grad_kernel(EpiGradParams p)
             for (int i = 0; i < V; ++i) red[warp][lane * V + i] = k ? su[i] : sz[i];
             __syncthreads();
             for (int c = threadIdx.x; c < 32 * V; c += 256) {
-                const int64_t col = (int64_t)blockIdx.x * 32 * V + c;
+                const int64_t col = (int64_t)cb * 32 * V + c;
                 if (col >= p.N) break;
                 float s = 0.0f;
 #pragma unroll
                 for (int w = 0; w < 8; ++w) s += red[w][c];
-                p.part[((int64_t)blockIdx.y * (GLU ? 2 : 1) + k) * p.N + col] = s;
+                p.part[((int64_t)rb * (GLU ? 2 : 1) + k) * p.N + col] = s;
             }
         }
     }
-    // Launched beside scale_pack_kernel (which lets it start only once everything before
-    // both is complete), it ends after it, so that waiting for this kernel covers both.
-    asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 // db[k][n] = bf16(sum over row blocks of part[block][k][n]): a block takes 32 columns, its

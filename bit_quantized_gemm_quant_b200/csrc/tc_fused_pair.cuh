@@ -41,6 +41,7 @@
 // frees the block's token tile and weight tile).
 #pragma once
 
+#include "scale_pack.cuh"
 #include "tc_gemm.cuh"
 #include "tc_pair.cuh"
 
@@ -80,59 +81,6 @@ struct FpParams {
     int64_t pack_rows;             // its rows per column block
     int64_t pack_mat;              // gradient: its words per matrix
 };
-
-// Packed scales: words of 32 weights, [column block of 128][row][4]; forward the rows are
-// the product's tile rows (glu: interleaved, see epi_out_row), for the gradient those of
-// the matrix, one matrix after the other.  Rows and columns are padded to whole tiles with
-// weights of 0.  A word holds scale and bias (bf16), or Q4_0's d as d_hi + d_lo (see gemv.cuh).
-// A block takes 32 rows x 2048 columns through shared memory: reads run along the rows
-// of the scales, writes along the rows of the result.
-struct ScalePackParams {
-    const uint16_t* scales[2];
-    const uint16_t* biases[2];
-    uint32_t* out;
-    int N, K, gs_shift, interleave;
-    int cols;                      // padded columns
-    int64_t pack_rows, pack_mat;
-};
-
-template <bool Q4>
-__global__ void __launch_bounds__(256) scale_pack_kernel(const __grid_constant__ ScalePackParams p)
-{
-    __shared__ uint32_t sm[32][65];
-    grid_dependency_wait();
-    grid_dependents_launch();
-    const int mat = blockIdx.z, n0 = blockIdx.x * 32, k0 = blockIdx.y * 2048;
-    const int per_row = p.K >> p.gs_shift;
-    const uint16_t* sc = mat ? p.scales[1] : p.scales[0];
-    const uint16_t* bi = mat ? p.biases[1] : p.biases[0];
-#pragma unroll
-    for (int i = threadIdx.x; i < 32 * 64; i += 256) {
-        const int r = i >> 6, h = i & 63, n = n0 + r, k = k0 + 32 * h;
-        uint32_t v = 0u;
-        if (n < p.N && k < p.K) {
-            const int64_t g = (int64_t)n * per_row + (k >> p.gs_shift);
-            if constexpr (Q4) {
-                const float d = f16_bits_to_f32(__ldg(sc + g));
-                const uint32_t hi = f32_to_bf16_bits(d);
-                v = hi | f32_to_bf16_bits(__fsub_rn(d, bf16_bits_to_f32(hi))) << 16;
-            } else {
-                v = (uint32_t)__ldg(sc + g) | (uint32_t)__ldg(bi + g) << 16;
-            }
-        }
-        sm[r][h] = v;
-    }
-    __syncthreads();
-    for (int i = threadIdx.x; i < 32 * 16; i += 256) {
-        const int r = i & 31, c = i >> 5, n = n0 + r;
-        const int64_t blk = k0 / 128 + c;
-        if (blk * 128 >= p.cols) continue;
-        const int64_t row = p.interleave ? 32 * (int64_t)(n >> 4) + (n & 15) + 16 * mat : n;
-        if (row >= p.pack_rows) continue;
-        *reinterpret_cast<uint4*>(p.out + mat * p.pack_mat + (blk * p.pack_rows + row) * 4) =
-            make_uint4(sm[r][4 * c], sm[r][4 * c + 1], sm[r][4 * c + 2], sm[r][4 * c + 3]);
-    }
-}
 
 // The dequant warps' part: group grp (4 warps) takes half (grp & 1) of the blocks grp >> 1,
 // grp >> 1 + 2, ... of the CTA's `left` ones.  A thread expands 64 weights: forward, row r of the tile;
