@@ -479,31 +479,35 @@ __global__ void __launch_bounds__(256) epi_grad_kernel(const __grid_constant__ E
                 const int64_t m = m0 + 8 * q;
                 if (m >= m_end) break;
                 const int64_t o = m * p.N + n;
-                __align__(16) uint16_t oz[V], ou[V];
+                float oz[V], ou[V];
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
                     const float d = bf16_bits_to_f32(vd[q][i]);
-                    float a = d;
+                    oz[i] = d;
                     if constexpr (GLU) {
-                        const float g = bf16_bits_to_f32(vz[q][i]), b = d * act_f<ACT>(g);
-                        a = d * bf16_bits_to_f32(vu[q][i]) * dact_f<ACT>(g);
-                        su[i] += b;
-                        ou[i] = (uint16_t)f32_to_bf16_bits(b);
+                        const float g = bf16_bits_to_f32(vz[q][i]);
+                        oz[i] = d * bf16_bits_to_f32(vu[q][i]) * dact_f<ACT>(g);
+                        su[i] += ou[i] = d * act_f<ACT>(g);
                     } else if constexpr (ACT != kActNone) {
-                        a = d * dact_f<ACT>(bf16_bits_to_f32(vz[q][i]));
+                        oz[i] = d * dact_f<ACT>(bf16_bits_to_f32(vz[q][i]));
                     }
-                    sz[i] += a;
-                    oz[i] = (uint16_t)f32_to_bf16_bits(a);
+                    sz[i] += oz[i];
                 }
                 if constexpr (V == 8) {
-                    if (p.dz) *reinterpret_cast<uint4*>(p.dz + o) = *reinterpret_cast<const uint4*>(oz);
-                    if constexpr (GLU) *reinterpret_cast<uint4*>(p.du + o) = *reinterpret_cast<const uint4*>(ou);
+                    auto put = [](uint16_t* to, const float (&v)[V]) {
+                        *reinterpret_cast<uint4*>(to) = make_uint4(pack_bf16x2_rn(v[0], v[1]), pack_bf16x2_rn(v[2], v[3]),
+                                                                   pack_bf16x2_rn(v[4], v[5]), pack_bf16x2_rn(v[6], v[7]));
+                    };
+                    if (p.dz) put(p.dz + o, oz);
+                    if constexpr (GLU) put(p.du + o, ou);
                 } else {
-                    if (p.dz) p.dz[o] = oz[0];
-                    if constexpr (GLU) p.du[o] = ou[0];
-                    if (p.dz_pad) {
-                        p.dz_pad[m * p.pitch + n] = oz[0];
-                        if constexpr (GLU) p.du_pad[m * p.pitch + n] = ou[0];
+                    const uint16_t zb = (uint16_t)f32_to_bf16_bits(oz[0]);
+                    if (p.dz) p.dz[o] = zb;
+                    if (p.dz_pad) p.dz_pad[m * p.pitch + n] = zb;
+                    if constexpr (GLU) {
+                        const uint16_t ub = (uint16_t)f32_to_bf16_bits(ou[0]);
+                        p.du[o] = ub;
+                        if (p.du_pad) p.du_pad[m * p.pitch + n] = ub;
                     }
                 }
             }
