@@ -44,6 +44,7 @@ void device_or_b200(int* num_sms, int* smem_optin)
 struct PairPlan {
     int bn = 32, stages = 0, pairs = 0;
     int codes = 0;                  // fused: code stages
+    int halves = 1;                 // token tiles of bn per unit (fused: 1 or 2)
     int64_t tiles = 0;
     TailSplit split{};
     size_t ws_bytes = 0;
@@ -57,40 +58,47 @@ struct PairPlan {
 // tokens, 1450 at 256 for 128-element blocks dequantized on chip), a unit of work a fixed
 // start, and the last unit its epilogue.  A split last round adds the partial tiles'
 // traffic and the kernel that sums them, and 6%: the pairs that an unsplit last round
-// leaves idle let the others run faster.
+// leaves idle let the others run faster.  Up to max_halves token tiles per unit: a block is
+// then dequantized once for two (1400 clocks up to 230 tokens, 2600 at 512), but their
+// epilogue overlaps no product.
 bool plan_pair(int64_t rows, int64_t M, int64_t nk, int num_sms, int smem_optin, int fixed_bytes, int a_bytes,
-               int tok_bytes, double block0, double block1, PairPlan* pl)
+               int tok_bytes, double block0, double block1, int max_halves, PairPlan* pl)
 {
     const int64_t pairs = std::max(num_sms / 2, 1), rtiles = (rows + 255) / 256;
     const int64_t maxb = std::min<int64_t>(256, (M + 31) / 32 * 32);
     double best = 1e300;
-    for (int b = 32; b <= maxb; b += 32) {
-        const int64_t tiles = ((M + b - 1) / b) * rtiles;
-        const double kb = block0 + block1 * b, drain = 1000.0 + 8.0 * b;
-        auto consider = [&](double c, int64_t dp, int64_t tail_pairs) {
-            if (c < best) {
-                best = c;
-                pl->bn = b;
-                pl->tiles = tiles;
-                pl->split.dp_tiles = (int)dp;
-                pl->split.tail = (int)(tiles - dp);
-                pl->split.tail_pairs = (int)tail_pairs;
-            }
-        };
-        auto unit = [&](double blocks) { return blocks * kb + 1500.0; };
-        consider((double)((tiles + pairs - 1) / pairs) * unit((double)nk) + drain, tiles, 0);
-        const int64_t dp = tiles / pairs * pairs, tail = tiles - dp;
-        if (tail == 0) continue;
-        // ranges of at least 2 blocks, at least one per tile
-        const int64_t tp = std::max<int64_t>(tail, std::min<int64_t>(pairs, tail * nk / 2));
-        const double range = (double)((tail * nk + tp - 1) / tp);
-        const double traffic = (double)(tp + tail) * b * 256.0 * 8.0 / 2500.0;
-        consider(((double)(dp / pairs) * unit((double)nk) + unit(range) + 1500.0 + drain + 5000.0 + traffic) * 1.06, dp, tp);
+    for (int halves = 1; halves <= max_halves; ++halves) {
+        for (int b = 32; b <= maxb; b += 32) {
+            if (halves == 2 && M <= b) break;
+            const int64_t tok = (int64_t)halves * b, tiles = ((M + tok - 1) / tok) * rtiles;
+            const double kb = halves == 2 ? std::max(1400.0, 500.0 + 3.9 * (double)tok) : block0 + block1 * b;
+            const double drain = 1000.0 + 8.0 * (double)tok, start = halves == 2 ? 1500.0 + 12.0 * b : 1500.0;
+            auto consider = [&](double c, int64_t dp, int64_t tail_pairs) {
+                if (c < best) {
+                    best = c;
+                    pl->bn = b;
+                    pl->halves = halves;
+                    pl->tiles = tiles;
+                    pl->split.dp_tiles = (int)dp;
+                    pl->split.tail = (int)(tiles - dp);
+                    pl->split.tail_pairs = (int)tail_pairs;
+                }
+            };
+            auto unit = [&](double blocks) { return blocks * kb + start; };
+            consider((double)((tiles + pairs - 1) / pairs) * unit((double)nk) + drain, tiles, 0);
+            const int64_t dp = tiles / pairs * pairs, tail = tiles - dp;
+            if (tail == 0) continue;
+            // ranges of at least 2 blocks, at least one per tile
+            const int64_t tp = std::max<int64_t>(tail, std::min<int64_t>(pairs, tail * nk / 2));
+            const double range = (double)((tail * nk + tp - 1) / tp);
+            const double traffic = (double)(tp + tail) * (double)tok * 256.0 * 8.0 / 2500.0;
+            consider(((double)(dp / pairs) * unit((double)nk) + unit(range) + start + drain + 5000.0 + traffic) * 1.06, dp, tp);
+        }
     }
     pl->pairs = (int)pairs;
     pl->split.blocks = (int)nk;
     pl->stages = std::min<int>(kFpMaxTok, (smem_optin - 1024 - 512 - fixed_bytes) / (a_bytes + pl->bn * tok_bytes));
-    pl->ws_bytes = pl->split.tail ? (size_t)2 * (size_t)pl->split.tail_pairs * (size_t)pl->bn * 256u * 4u : 0u;
+    pl->ws_bytes = pl->split.tail ? (size_t)2 * (size_t)pl->split.tail_pairs * (size_t)(pl->halves * pl->bn) * 256u * 4u : 0u;
     return pl->stages >= 2 && pl->tiles <= INT32_MAX / 256 && nk <= INT32_MAX / 2;
 }
 
@@ -120,8 +128,9 @@ template <int EPI>
 bq_status launch_reduce(const DeviceInfo& di, const PairPlan& pl, const PairParams& p, cudaStream_t st)
 {
     if (pl.split.tail == 0) return BQ_OK;
-    const int64_t blocks = (int64_t)pl.split.tail * ((pl.bn + kReduceTokens - 1) / kReduceTokens);
-    return launch_pdl_dim(epi_reduce_kernel<EPI>, dim3((unsigned)blocks), 256, 0, st, (const float*)p.ws, p.e, p.M, p.N, p.bn,
+    const int tok = pl.halves * pl.bn;
+    const int64_t blocks = (int64_t)pl.split.tail * ((tok + kReduceTokens - 1) / kReduceTokens);
+    return launch_pdl_dim(epi_reduce_kernel<EPI>, dim3((unsigned)blocks), 256, 0, st, (const float*)p.ws, p.e, p.M, p.N, tok,
                           p.m_tiles, p.split);
 }
 
@@ -339,12 +348,12 @@ bq_status launch_scale_pack(bool mn, const QMat* w, int mats, bool interleave, i
 // The product of launch_pair with the codes of w (1 or 2 matrices [N][K]) and their
 // packed scales in place of bf16 weights.  Forward: B[0] = x, red = K; gradient (MN): B[i] = dz of matrix i,
 // red = N.
-template <int MODE, bool MN, int EPI>
+template <int MODE, bool MN, int EPI, int H>
 bq_status launch_fused_pair(const DeviceInfo& di, int dev, const PairPlan& pl, const QMat* w, int mats,
                             const uint16_t* const* B, int64_t N, int64_t K, int64_t M, int64_t b_pitch, int group_size,
                             const EpiParams& e, void* packed, void* ws, cudaStream_t st)
 {
-    auto kern = tc_fused_pair_kernel<MODE, MN, EPI>;
+    auto kern = tc_fused_pair_kernel<MODE, MN, EPI, H>;
     static bool attr_done[kMaxDevices] = {};
     if (!attr_done[dev]) {
         if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, di.max_smem_optin) != cudaSuccess) {
@@ -375,7 +384,7 @@ bq_status launch_fused_pair(const DeviceInfo& di, int dev, const PairPlan& pl, c
     p.q.N = (int)outs;
     p.q.bn = pl.bn;
     p.q.stages = pl.stages;
-    p.q.m_tiles = (int)((M + pl.bn - 1) / pl.bn);
+    p.q.m_tiles = (int)((M + H * pl.bn - 1) / (H * pl.bn));
     p.q.tiles = (int)pl.tiles;
     p.q.seg_blocks = (int)((red + 127) / 128);
     p.q.segs = MN ? mats : 1;
@@ -395,14 +404,16 @@ bq_status launch_fused_pair_fmt(WFmt fmt, const DeviceInfo& di, int dev, const P
                                 const uint16_t* const* B, int64_t N, int64_t K, int64_t M, int64_t b_pitch,
                                 int group_size, const EpiParams& e, void* packed, void* ws, cudaStream_t st)
 {
-    if (fmt == WFmt::Q4_0)
-        return launch_fused_pair<kModeQ4_0, MN, EPI>(di, dev, pl, w, mats, B, N, K, M, b_pitch, group_size, e, packed,
-                                                         ws, st);
-    if (fmt == WFmt::AFF4)
-        return launch_fused_pair<kModeAff4, MN, EPI>(di, dev, pl, w, mats, B, N, K, M, b_pitch, group_size, e, packed,
-                                                         ws, st);
-    return launch_fused_pair<kModeAff8, MN, EPI>(di, dev, pl, w, mats, B, N, K, M, b_pitch, group_size, e, packed,
-                                                         ws, st);
+    auto go = [&](auto mode) {
+        constexpr int m = decltype(mode)::value;
+        if constexpr (MN)
+            if (pl.halves == 2)
+                return launch_fused_pair<m, MN, EPI, 2>(di, dev, pl, w, mats, B, N, K, M, b_pitch, group_size, e, packed, ws, st);
+        return launch_fused_pair<m, MN, EPI, 1>(di, dev, pl, w, mats, B, N, K, M, b_pitch, group_size, e, packed, ws, st);
+    };
+    if (fmt == WFmt::Q4_0) return go(std::integral_constant<int, kModeQ4_0>{});
+    if (fmt == WFmt::AFF4) return go(std::integral_constant<int, kModeAff4>{});
+    return go(std::integral_constant<int, kModeAff8>{});
 }
 
 // ------------------------------------------------------------------ layouts of the workspaces
@@ -421,15 +432,20 @@ struct EpiWs {
 
 // Q4_0 and affine 4- and 8-bit codes are dequantized inside the product; the others
 // (whose rows of a stage are not 16-byte multiples) through a bf16 copy.
-bool plan_epi_product(WFmt fmt, int64_t rows, int64_t M, int segs, int64_t red, int num_sms, int smem_optin, EpiWs* w)
+// Two token tiles per unit only for gradients: their epilogue is a plain store and their
+// reductions are long (12288 x 4096, 2048 tokens: 8-bit with gelu and bias 193 us with one,
+// 170 with two; gated affine 4-bit 317 and 309).  Forward the exposed epilogue costs as much
+// as the dequantization saved (12288 x 4096 affine 4-bit with gelu, 512 tokens: 51 and 60;
+// 8-bit, 400 tokens, no activation: 54 and 52).
+bool plan_epi_product(WFmt fmt, bool gradient, int64_t rows, int64_t M, int segs, int64_t red, int num_sms, int smem_optin, EpiWs* w)
 {
     w->rows = rows;
     w->fused = has_fast_paths(fmt);
     if (!w->fused)      // blocks of 64
-        return plan_pair(rows, M, segs * ((red + 63) / 64), num_sms, smem_optin, 0, (int)kPairABytes, 64, 300.0, 1.5, &w->pl);
+        return plan_pair(rows, M, segs * ((red + 63) / 64), num_sms, smem_optin, 0, (int)kPairABytes, 64, 300.0, 1.5, 1, &w->pl);
     const int mode = fp_mode(fmt);
     if (!plan_pair(rows, M, segs * ((red + 127) / 128), num_sms, smem_optin, (int)fp_fixed_bytes(mode, 2), 0, 128, 900.0, 2.15,
-                   &w->pl))
+                   gradient ? 2 : 1, &w->pl))
         return false;
     // Four code stages where they leave room for three token tiles, else two: 1 to 8% apart
     // below 256 tokens a tile, and 12% the other way at 256, where two token tiles would be
@@ -443,7 +459,7 @@ bool plan_epi_product(WFmt fmt, int64_t rows, int64_t M, int segs, int64_t red, 
 bool plan_forward(WFmt fmt, int mats, int64_t M, int64_t N, int64_t K, int num_sms, int smem_optin, EpiWs* w)
 {
     // glu: tiles of 32 rows per 16 outputs
-    if (!plan_epi_product(fmt, mats == 2 ? 32 * ((N + 15) / 16) : N, M, 1, K, num_sms, smem_optin, w)) return false;
+    if (!plan_epi_product(fmt, false, mats == 2 ? 32 * ((N + 15) / 16) : N, M, 1, K, num_sms, smem_optin, w)) return false;
     w->off_split = w->fused ? scale_pack(false, mats, N, K).bytes : up256((size_t)w->rows * (size_t)K * 2u);
     w->bytes = w->off_split + w->pl.ws_bytes;
     return true;
@@ -451,7 +467,7 @@ bool plan_forward(WFmt fmt, int mats, int64_t M, int64_t N, int64_t K, int num_s
 
 bool plan_backward(WFmt fmt, int mats, int64_t M, int64_t N, int64_t K, int num_sms, int smem_optin, EpiWs* w)
 {
-    if (K > 0 && !plan_epi_product(fmt, K, M, mats, N, num_sms, smem_optin, w)) return false;
+    if (K > 0 && !plan_epi_product(fmt, true, K, M, mats, N, num_sms, smem_optin, w)) return false;
     w->pitch = (N + 7) / 8 * 8;
     // blocks of 8 warps over rows of tokens: about 8 blocks per SM, at least 32 rows each
     const int64_t cols = std::max<int64_t>(1, (N + 255) / 256);

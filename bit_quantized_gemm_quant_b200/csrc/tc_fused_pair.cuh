@@ -31,14 +31,18 @@
 //    64, 277 now);
 //  - the epilogue: eight warps, and for the last unit, which no product overlaps, the
 //    dequant warps as well.
-// Large products are now bound by the tensor cores and the power they may draw (1.49
+// Forward, large products are bound by the tensor cores and the power they may draw (1.49
 // PFLOP/s in isolation, cuBLAS bf16 reaches 1.64); below 192 tokens a tile the 1050 clocks
-// that a block's dequantization takes exceed the MMA's.
+// that a block's dequantization takes exceed the MMA's.  Gradients, whose epilogue is a
+// plain store and whose reductions are long, may take two token tiles per unit (H = 2): both
+// accumulators work on one weight tile, so that a block's dequantization serves up to 512
+// tokens (8-bit 12288 x 4096, 2048 tokens, gelu and bias: 199 us with one tile, 172 with
+// two).  The price is that the next unit's first products wait for the epilogue.
 //
 // Barriers: cfull / cempty (codes, each CTA's own), bfull (tokens of both CTAs, the
 // leader's), ready (a block's tile, the leader's; 8 dequant warps of each CTA arrive),
-// consumed (one per block, each CTA's own; the MMA's commit arrives on both and thereby
-// frees the block's token tile and weight tile).
+// consumed (one per product of a block and a token tile, each CTA's own; the MMA's commit
+// arrives on both and thereby frees the token tile and, the last of a block, the weight tile).
 #pragma once
 
 #include "scale_pack.cuh"
@@ -86,7 +90,7 @@ struct FpParams {
 // grp >> 1 + 2, ... of the CTA's `left` ones.  A thread expands 64 weights: forward, row r of the tile;
 // gradient, row r of the half-block, outputs 64 hk .. of the tile.  (A function of its own:
 // inlined, the code that follows it for these warps slowed this loop by 13%.)
-template <int MODE, bool MN, int EPI>
+template <int MODE, bool MN, int EPI, int H>
 __device__ __noinline__ void fp_dequantize(int left, int codes_ring, uint32_t a_base, uint32_t c_base, uint32_t cfull0, uint32_t cempty0,
                                            uint32_t ready0, uint32_t consumed0)
 {
@@ -132,7 +136,7 @@ __device__ __noinline__ void fp_dequantize(int left, int codes_ring, uint32_t a_
             else
                 deq_aff8_half(raw[2 * h], raw[2 * h + 1], __uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u), wv);
             if (h == 0 && block >= kTiles) {           // the tile's last block is consumed
-                const int q = block - kTiles;
+                const int q = (block - kTiles + 1) * H - 1;
                 ok = mbar_wait(consumed0 + 8u * (uint32_t)(q & (kFpConsumed - 1)), (uint32_t)(q / kFpConsumed) & 1u);
                 __syncwarp();
             }
@@ -154,7 +158,9 @@ __device__ __noinline__ void fp_dequantize(int left, int codes_ring, uint32_t a_
 // tm_a0, tm_a1: codes of matrix 0 and 1 as bytes, boxes of 128 columns x 128 rows (glu
 // forward: 64 rows of gate and of up).
 // tm_b0, tm_b1: tokens, boxes of 64 elements x bn / 2 tokens.
-template <int MODE, bool MN, int EPI>
+// H: token tiles per unit, 1 (the two accumulators take units in turn) or 2 (both work on
+// one unit, which reads each weight tile twice).
+template <int MODE, bool MN, int EPI, int H>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFpThreads, 1)
 tc_fused_pair_kernel(const __grid_constant__ CUtensorMap tm_a0, const __grid_constant__ CUtensorMap tm_a1,
                      const __grid_constant__ CUtensorMap tm_b0, const __grid_constant__ CUtensorMap tm_b1,
@@ -186,13 +192,13 @@ tc_fused_pair_kernel(const __grid_constant__ CUtensorMap tm_a0, const __grid_con
     static_assert(8 * (kBars + 6) <= 512, "barriers fit the space the host reserves");
     volatile uint32_t* tmem_slot_ptr =
         reinterpret_cast<volatile uint32_t*>(smem_raw + (base - smem_u32(smem_raw)) + (tmem_slot - base));
-    // wait until the pos-th block (>= 0) is consumed
+    // wait until the pos-th product (of a block and a token tile, >= 0) is done
     auto wait_consumed = [&](int pos) {
         return mbar_wait(consumed_bar(pos & (kFpConsumed - 1)), (uint32_t)(pos / kFpConsumed) & 1u);
     };
 
     auto tile_r0 = [&](int t) { return (t / p.m_tiles) * 256 + (int)rank * 128; };
-    auto tile_m0 = [&](int t) { return (t % p.m_tiles) * p.bn; };
+    auto tile_m0 = [&](int t) { return (t % p.m_tiles) * (p.bn * H); };
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < NC; ++i) {
@@ -222,13 +228,15 @@ tc_fused_pair_kernel(const __grid_constant__ CUtensorMap tm_a0, const __grid_con
     grid_dependency_wait();
     grid_dependents_launch();
 
-    // Chunks idx, idx + parts, ... of the lt-th local unit, in the lane quarter of this warp.
-    auto drain = [&](int t, int slot, int lt, int idx, int parts) {
+    // Chunks idx, idx + parts, ... of the h-th token tile of a unit, in accumulator acc, in
+    // the lane quarter of this warp.
+    auto drain = [&](int t, int slot, int acc, int h, int idx, int parts) {
         const int q4 = warp & 3, r = 32 * q4 + lane;
         tc_fence_after();
-        pair_drain<EPI>(p, tmem_base + ((uint32_t)(32 * q4) << 16) + (uint32_t)((lt & 1) * kPairAccCols), tile_m0(t),
+        pair_drain<EPI>(p, tmem_base + ((uint32_t)(32 * q4) << 16) + (uint32_t)(acc * kPairAccCols), tile_m0(t) + h * p.bn,
                         epi_tile_rows<EPI>(tile_r0(t)) + epi_out_row<EPI>(r),
-                        slot < 0 ? nullptr : p.ws + (int64_t)slot * ((int64_t)p.bn * 256) + (int)rank * 128 + r, idx, parts);
+                        slot < 0 ? nullptr : p.ws + ((int64_t)slot * H + h) * ((int64_t)p.bn * 256) + (int)rank * 128 + r, idx,
+                        parts);
         tc_fence_before();
     };
 
@@ -239,26 +247,29 @@ tc_fused_pair_kernel(const __grid_constant__ CUtensorMap tm_a0, const __grid_con
         bool ok = true;
         for (PairUnits u(p); ok && u.next();) {
             const int m0 = tile_m0(u.tile) + (int)rank * (p.bn / 2);
-            for (int it = u.kb0; it < u.kb1; ++it, ++pos) {
-                if (pos >= NB) {
-                    ok = wait_consumed(pos - NB);
-                    __syncwarp();
-                    if (!ok) break;
-                }
+            for (int it = u.kb0; ok && it < u.kb1; ++it) {
                 const bool second = it >= p.seg_blocks;
                 const CUtensorMap* map = second ? &tm_b1 : &tm_b0;
-                const uint32_t dst = b_base + (uint32_t)b * 2u * b_bytes, bar = map_to_cta(bfull_bar(b), 0);
                 const int k0 = (second ? it - p.seg_blocks : it) * 128;
-                if (elect_one()) {
-                    if (rank == 0) mbar_arrive_expect_tx(bfull_bar(b), 4u * b_bytes);
-                    tma_load_2d_pair(dst, map, bar, k0, m0);
-                    tma_load_2d_pair(dst + b_bytes, map, bar, k0 + 64, m0);
+#pragma unroll
+                for (int h = 0; h < H; ++h, ++pos) {
+                    if (pos >= NB) {
+                        ok = wait_consumed(pos - NB);
+                        __syncwarp();
+                        if (!ok) break;
+                    }
+                    const uint32_t dst = b_base + (uint32_t)b * 2u * b_bytes, bar = map_to_cta(bfull_bar(b), 0);
+                    if (elect_one()) {
+                        if (rank == 0) mbar_arrive_expect_tx(bfull_bar(b), 4u * b_bytes);
+                        tma_load_2d_pair(dst, map, bar, k0, m0 + h * p.bn);
+                        tma_load_2d_pair(dst + b_bytes, map, bar, k0 + 64, m0 + h * p.bn);
+                    }
+                    __syncwarp();
+                    if (++b == NB) b = 0;
                 }
-                __syncwarp();
-                if (++b == NB) b = 0;
             }
         }
-        // Leave only when the last blocks are consumed: every copy of the pair has then
+        // Leave only when the last products are done: every copy of the pair has then
         // landed and every arrival on this CTA's barriers has been made.  (After a timeout
         // the leader still waits for the copies.)
         for (int q = max(pos - NB, 0); q < pos; ++q) {
@@ -316,26 +327,38 @@ tc_fused_pair_kernel(const __grid_constant__ CUtensorMap tm_a0, const __grid_con
             uint32_t pha = 0, phb = 0;
             bool ok = true;
             for (PairUnits u(p); ok && u.next(); ++lt) {
-                const int acc = lt & 1;
                 const int kb0 = u.kb0, kb1 = u.kb1;
-                if (!mbar_wait_warp(tempty_bar(acc), ((uint32_t)(lt >> 1) & 1u) ^ 1u)) break;
+                const int acc = H == 1 ? lt & 1 : 0;             // the unit's first accumulator, and its uses before
+                const uint32_t use = H == 1 ? (uint32_t)(lt >> 1) : (uint32_t)lt;
+                if (!mbar_wait_warp(tempty_bar(acc), (use & 1u) ^ 1u)) break;
                 tc_fence_after();
                 const uint32_t d_tmem = tmem_base + (uint32_t)(acc * kPairAccCols);
-                for (int it = kb0; it < kb1; ++it) {
-                    if (!mbar_wait_warp(bfull_bar(b), phb) || !mbar_wait_warp(ready_bar(a), pha)) { ok = false; break; }
-                    tc_fence_after();
-                    if (elect_one()) {
-                        const uint32_t al = a_lo0 + (uint32_t)a * (kPairABytes >> 3), bl = b_lo0 + (uint32_t)b * (b_bytes >> 3);
-                        umma_kblock_pair<MN ? 128 : 2>(d_tmem, al, bl, desc_hi, idesc, it > kb0);
-                        umma_kblock_pair<MN ? 128 : 2>(d_tmem, al + (kPairABytes >> 4), bl + (b_bytes >> 4), desc_hi, idesc, 1u);
-                        umma_commit_pair(consumed_bar(c));
+                for (int it = kb0; ok && it < kb1; ++it) {
+#pragma unroll
+                    for (int h = 0; h < H; ++h) {
+                        if (!mbar_wait_warp(bfull_bar(b), phb) || (h == 0 && !mbar_wait_warp(ready_bar(a), pha)) ||
+                            (h > 0 && it == kb0 && !mbar_wait_warp(tempty_bar(h), (use & 1u) ^ 1u))) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                        if (elect_one()) {
+                            const uint32_t al = a_lo0 + (uint32_t)a * (kPairABytes >> 3), bl = b_lo0 + (uint32_t)b * (b_bytes >> 3);
+                            const uint32_t d = d_tmem + (uint32_t)(h * kPairAccCols);
+                            umma_kblock_pair<MN ? 128 : 2>(d, al, bl, desc_hi, idesc, it > kb0);
+                            umma_kblock_pair<MN ? 128 : 2>(d, al + (kPairABytes >> 4), bl + (b_bytes >> 4), desc_hi, idesc, 1u);
+                            umma_commit_pair(consumed_bar(c));
+                        }
+                        __syncwarp();
+                        c = (c + 1) & (kFpConsumed - 1);
+                        if (++b == NB) { b = 0; phb ^= 1u; }
                     }
-                    __syncwarp();
-                    c = (c + 1) & (kFpConsumed - 1);
-                    if (++b == NB) { b = 0; phb ^= 1u; }
                     if (++a == kTiles) { a = 0; pha ^= 1u; }
                 }
-                if (elect_one()) umma_commit_pair(tfull_bar(acc));
+                if (elect_one()) {
+#pragma unroll
+                    for (int h = 0; h < H; ++h) umma_commit_pair(tfull_bar(acc + h));
+                }
                 __syncwarp();
             }
             if (elect_one()) umma_commit_pair(done_bar);     // nothing stays in flight past this point
@@ -349,16 +372,21 @@ tc_fused_pair_kernel(const __grid_constant__ CUtensorMap tm_a0, const __grid_con
         for (bool more = u.next(); more; ++lt) {
             const int tile = u.tile, slot = u.slot;
             more = u.next();
-            if (!more || !mbar_wait_warp(tfull_bar(lt & 1), (uint32_t)(lt >> 1) & 1u)) break;
-            drain(tile, slot, lt, (warp - kFpEpiWarp0) >> 2, kFpEpiWarps / 4);
-            __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(map_to_cta(tempty_bar(lt & 1), 0));
+            if (!more) break;
+            for (int h = 0; h < H; ++h) {
+                const int acc = H == 1 ? lt & 1 : h, use = H == 1 ? lt >> 1 : lt;
+                more = more && mbar_wait_warp(tfull_bar(acc), (uint32_t)use & 1u);
+                if (!more) break;
+                drain(tile, slot, acc, h, (warp - kFpEpiWarp0) >> 2, kFpEpiWarps / 4);
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(map_to_cta(tempty_bar(acc), 0));
+            }
         }
     } else {
         // ---------------- dequantization ----------------
         int left = 0;                                    // blocks of this CTA's sequence
         for (PairUnits u(p); u.next();) left += u.kb1 - u.kb0;
-        fp_dequantize<MODE, MN, EPI>(left, NC, a_base, c_base, cfull_bar(0), cempty_bar(0), map_to_cta(ready_bar(0), 0),
+        fp_dequantize<MODE, MN, EPI, H>(left, NC, a_base, c_base, cfull_bar(0), cempty_bar(0), map_to_cta(ready_bar(0), 0),
                                      consumed_bar(0));
     }
     __syncwarp();
@@ -372,7 +400,8 @@ tc_fused_pair_kernel(const __grid_constant__ CUtensorMap tm_a0, const __grid_con
             tile = u.tile;
             slot = u.slot;
         }
-        if (lt >= 0 && mbar_wait_warp(done_bar, 0)) drain(tile, slot, lt, warp >> 2, kFpTokWarp / 4);
+        if (lt >= 0 && mbar_wait_warp(done_bar, 0))
+            for (int h = 0; h < H; ++h) drain(tile, slot, H == 1 ? lt & 1 : h, h, warp >> 2, kFpTokWarp / 4);
     }
 
     tc_fence_before();

@@ -221,6 +221,16 @@ def test_larger_products(fmt, N, K, M):
     assert bq.bq_device_status() == 0
 
 
+@pytest.mark.parametrize("fmt", ["q4_0", "affine4", "affine8", "affine8_g32"])
+@pytest.mark.parametrize("N,K,M", [(777, 4096, 1100), (640, 4096, 1025), (840, 6144, 2600)])
+def test_gradients_with_two_token_tiles_per_unit(fmt, N, K, M):
+    """Sizes whose gradient takes both accumulators for one weight tile: a single unit per
+    pair of SMs and several, a second tile cut short, rows of dz with and without padding."""
+    check_act_bwd(Case(fmt, N, K, M, 1), "silu")
+    check_glu_bwd(Case(fmt, N, K, M, 2), "gelu", db=False)
+    assert bq.bq_device_status() == 0
+
+
 @pytest.mark.parametrize("M", [4, 70])
 def test_residual_added_in_place(M):
     c = Case("affine4", 200, 256, M, 1)
