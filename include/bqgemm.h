@@ -383,6 +383,7 @@ typedef enum {
  *   act       bq_act; another value returns BQ_ERR_UNSUPPORTED
  *   y_bf16    device u16 [M][N], written
  *   preact    device u16 [M][N], bf16_rne(z) written for the backward pass, or NULL
+ *   (no output may overlap an input, y = residual excepted, or another output)
  *   workspace, workspace_bytes  scratch of at least
  *             quant_matmul_epilogue_workspace_size(BQ_OP_ACT, ...) bytes (else
  *             BQ_ERR_WORKSPACE, nothing launched), free again once the call's work is
@@ -433,7 +434,8 @@ BQ_API bq_status quant_matmul_act_backward(const uint16_t* dy_bf16, const uint16
  *   h_bf16              device u16 [M][N], written
  *   g_bf16, u_bf16      device u16 [M][N], bf16_rne of g and u for the backward pass, or
  *                       both NULL
- * Other arguments, workspace (BQ_OP_GLU) and errors as quant_matmul_act.
+ * No output may overlap an input or another output.  Other arguments, workspace
+ * (BQ_OP_GLU) and errors as quant_matmul_act.
  */
 BQ_API bq_status quant_matmul_glu(const uint16_t* x_bf16, const void* const* wq, const void* const* scales,
                                   const void* const* biases, const uint16_t* gate_bias, const uint16_t* up_bias,
