@@ -50,29 +50,39 @@ struct PairPlan {
     size_t ws_bytes = 0;
 };
 
+// What a block of the reduction costs a pair in SM clocks: block0, plus per token of the
+// tile, plus as much as `crowd` when all pairs are busy.
+struct PairCost {
+    double block0, per_token, crowd;
+    int max_halves;                 // token tiles per unit: with 2, max(1480, 555 + 4.67 per token)
+};
+
 // Token tile and split of the last round for `rows` D rows, M tokens and nk blocks of the
-// reduction; shared memory: fixed_bytes, and per stage a_bytes and tok_bytes per token.
-// Cost model in SM clocks, from B200 sweeps over tile widths (12288 x 4096 and smaller, 33
-// to 2048 tokens): a block costs block0 + block1 per token of the tile (the dequantization
-// or the copies set the first, the MMA and its contention the second: 1030 clocks at 64
-// tokens, 1450 at 256 for 128-element blocks dequantized on chip), a unit of work a fixed
-// start, and the last unit its epilogue.  A split last round adds the partial tiles'
-// traffic and the kernel that sums them, and 6%: the pairs that an unsplit last round
-// leaves idle let the others run faster.  Up to max_halves token tiles per unit: a block is
-// then dequantized once for two (1400 clocks up to 230 tokens, 2600 at 512), but their
-// epilogue overlaps no product.
+// reduction; shared memory: fixed_bytes, and per stage tok_bytes per token beside a_bytes.
+// The least cost of a model in SM clocks: blocks as above, a fixed start per unit of work,
+// the last unit's epilogue, and for a split last round the partial tiles' traffic and the
+// kernel that sums them.  Its numbers are fitted to a B200 sweep over every tile width,
+// one or two token tiles and every split below, for 72 problems of the fused kernel (2048
+// x 8192 to 12288 x 4096, 24 to 2048 tokens, forward and gradient): the plan it picks is
+// 1% slower than the problem's best on average, 6% at worst.
 bool plan_pair(int64_t rows, int64_t M, int64_t nk, int num_sms, int smem_optin, int fixed_bytes, int a_bytes,
-               int tok_bytes, double block0, double block1, int max_halves, PairPlan* pl)
+               int tok_bytes, const PairCost& pc, PairPlan* pl)
 {
     const int64_t pairs = std::max(num_sms / 2, 1), rtiles = (rows + 255) / 256;
     const int64_t maxb = std::min<int64_t>(256, (M + 31) / 32 * 32);
     double best = 1e300;
-    for (int halves = 1; halves <= max_halves; ++halves) {
+    for (int halves = 1; halves <= pc.max_halves; ++halves) {
         for (int b = 32; b <= maxb; b += 32) {
             if (halves == 2 && M <= b) break;
             const int64_t tok = (int64_t)halves * b, tiles = ((M + tok - 1) / tok) * rtiles;
-            const double kb = halves == 2 ? std::max(1400.0, 500.0 + 3.9 * (double)tok) : block0 + block1 * b;
-            const double drain = 1000.0 + 8.0 * (double)tok, start = halves == 2 ? 1500.0 + 12.0 * b : 1500.0;
+            const double start = halves == 2 ? 1500.0 + 12.0 * b : 1500.0, drain = 1000.0 + 8.0 * (double)tok;
+            // a unit of n blocks with `busy` pairs at work
+            auto unit = [&](int64_t n, int64_t busy) {
+                const double block = halves == 2 ? std::max(1480.0, 555.0 + 4.67 * (double)tok)
+                                                 : pc.block0 + pc.per_token * b +
+                                                       pc.crowd * (double)std::min(busy, pairs) / (double)pairs;
+                return (double)n * block + start;
+            };
             auto consider = [&](double c, int64_t dp, int64_t tail_pairs) {
                 if (c < best) {
                     best = c;
@@ -84,15 +94,20 @@ bool plan_pair(int64_t rows, int64_t M, int64_t nk, int num_sms, int smem_optin,
                     pl->split.tail_pairs = (int)tail_pairs;
                 }
             };
-            auto unit = [&](double blocks) { return blocks * kb + start; };
-            consider((double)((tiles + pairs - 1) / pairs) * unit((double)nk) + drain, tiles, 0);
+            consider((double)((tiles + pairs - 1) / pairs) * unit(nk, tiles) + drain, tiles, 0);
             const int64_t dp = tiles / pairs * pairs, tail = tiles - dp;
             if (tail == 0) continue;
-            // ranges of at least 2 blocks, at least one per tile
-            const int64_t tp = std::max<int64_t>(tail, std::min<int64_t>(pairs, tail * nk / 2));
-            const double range = (double)((tail * nk + tp - 1) / tp);
-            const double traffic = (double)(tp + tail) * (double)tok * 256.0 * 8.0 / 2500.0;
-            consider(((double)(dp / pairs) * unit((double)nk) + unit(range) + start + drain + 5000.0 + traffic) * 1.06, dp, tp);
+            // ranges of at least 2 blocks, at least one per tile: as many as there are pairs, or
+            // a whole number per tile, so that none touches two tiles (4096 x 4096 affine
+            // 4-bit, 128 tokens: 16.2 us with 4 per tile, 17.5 with 74 over 16 tiles)
+            auto split = [&](int64_t tp) {
+                const bool whole = tp % tail == 0;
+                const double traffic = (double)(whole ? tp : tp + tail) * (double)tok * 256.0 * 8.0 / 2225.0;
+                consider((double)(dp / pairs) * unit(nk, pairs) + unit((tail * nk + tp - 1) / tp, tp) + (whole ? 0.0 : start) +
+                             drain + 4800.0 + traffic, dp, tp);
+            };
+            split(std::max<int64_t>(tail, std::min<int64_t>(pairs, tail * nk / 2)));
+            for (int64_t s = 2; s * tail <= pairs && 2 * s <= nk; ++s) split(s * tail);
         }
     }
     pl->pairs = (int)pairs;
@@ -442,10 +457,11 @@ bool plan_epi_product(WFmt fmt, bool gradient, int64_t rows, int64_t M, int segs
     w->rows = rows;
     w->fused = has_fast_paths(fmt);
     if (!w->fused)      // blocks of 64
-        return plan_pair(rows, M, segs * ((red + 63) / 64), num_sms, smem_optin, 0, (int)kPairABytes, 64, 300.0, 1.5, 1, &w->pl);
+        return plan_pair(rows, M, segs * ((red + 63) / 64), num_sms, smem_optin, 0, (int)kPairABytes, 64,
+                         PairCost{300.0, 1.5, 0.0, 1}, &w->pl);
     const int mode = fp_mode(fmt);
-    if (!plan_pair(rows, M, segs * ((red + 127) / 128), num_sms, smem_optin, (int)fp_fixed_bytes(mode, 2), 0, 128, 900.0, 2.15,
-                   gradient ? 2 : 1, &w->pl))
+    if (!plan_pair(rows, M, segs * ((red + 127) / 128), num_sms, smem_optin, (int)fp_fixed_bytes(mode, 2), 0, 128,
+                   PairCost{980.0, 1.3, 300.0, gradient ? 2 : 1}, &w->pl))
         return false;
     // Four code stages where they leave room for three token tiles, else two: 1 to 8% apart
     // below 256 tokens a tile, and 12% the other way at 256, where two token tiles would be
