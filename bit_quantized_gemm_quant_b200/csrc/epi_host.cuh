@@ -44,6 +44,7 @@ void device_or_b200(int* num_sms, int* smem_optin)
 struct PairPlan {
     int bn = 32, stages = 0, pairs = 0;
     int codes = 0;                  // fused: code stages
+    int wtiles = 3;                 // fused: bf16 weight tiles
     int halves = 1;                 // token tiles of bn per unit (fused: 1 or 2)
     int64_t tiles = 0;
     TailSplit split{};
@@ -363,12 +364,12 @@ bq_status launch_scale_pack(bool mn, const QMat* w, int mats, bool interleave, i
 // The product of launch_pair with the codes of w (1 or 2 matrices [N][K]) and their
 // packed scales in place of bf16 weights.  Forward: B[0] = x, red = K; gradient (MN): B[i] = dz of matrix i,
 // red = N.
-template <int MODE, bool MN, int EPI, int H>
+template <int MODE, bool MN, int EPI, int H, int T>
 bq_status launch_fused_pair(const DeviceInfo& di, int dev, const PairPlan& pl, const QMat* w, int mats,
                             const uint16_t* const* B, int64_t N, int64_t K, int64_t M, int64_t b_pitch, int group_size,
                             const EpiParams& e, void* packed, void* ws, cudaStream_t st)
 {
-    auto kern = tc_fused_pair_kernel<MODE, MN, EPI, H>;
+    auto kern = tc_fused_pair_kernel<MODE, MN, EPI, H, T>;
     static bool attr_done[kMaxDevices] = {};
     if (!attr_done[dev]) {
         if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, di.max_smem_optin) != cudaSuccess) {
@@ -408,7 +409,7 @@ bq_status launch_fused_pair(const DeviceInfo& di, int dev, const PairPlan& pl, c
     // every pair when there are whole rounds before the tail: the units are dealt by pair
     const unsigned grid = 2u * (unsigned)std::min<int64_t>(pl.split.tail && pl.split.dp_tiles ? pl.pairs
                                                            : pl.split.tail ? pl.split.tail_pairs : pl.tiles, pl.pairs);
-    const size_t smem = std::max<size_t>(1024 + fp_fixed_bytes(MODE, pl.codes) + (size_t)pl.stages * (size_t)pl.bn * 128u + 512,
+    const size_t smem = std::max<size_t>(1024 + fp_fixed_bytes(MODE, T, pl.codes) + (size_t)pl.stages * (size_t)pl.bn * 128u + 512,
                                          (size_t)di.max_smem_optin / 2 + 1024);   // one CTA per SM (all of TMEM)
     const bq_status s = launch_pdl_dim(kern, dim3(grid), kFpThreads, smem, st, ta[0], ta[1], tb[0], tb[1], p);
     return s != BQ_OK ? s : launch_reduce<EPI>(di, pl, p.q, st);
@@ -421,10 +422,21 @@ bq_status launch_fused_pair_fmt(WFmt fmt, const DeviceInfo& di, int dev, const P
 {
     auto go = [&](auto mode) {
         constexpr int m = decltype(mode)::value;
-        if constexpr (MN)
-            if (pl.halves == 2)
-                return launch_fused_pair<m, MN, EPI, 2>(di, dev, pl, w, mats, B, N, K, M, b_pitch, group_size, e, packed, ws, st);
-        return launch_fused_pair<m, MN, EPI, 1>(di, dev, pl, w, mats, B, N, K, M, b_pitch, group_size, e, packed, ws, st);
+        auto launch = [&](auto halves, auto wtiles) {
+            return launch_fused_pair<m, MN, EPI, decltype(halves)::value, decltype(wtiles)::value>(
+                di, dev, pl, w, mats, B, N, K, M, b_pitch, group_size, e, packed, ws, st);
+        };
+        using One = std::integral_constant<int, 1>;
+        using Two = std::integral_constant<int, 2>;
+        using Three = std::integral_constant<int, 3>;
+        if constexpr (MN && m == kModeAff8)
+            return pl.halves == 2 ? launch(Two{}, Two{}) : launch(One{}, Two{});
+        else if constexpr (MN)
+            return pl.halves == 2 ? launch(Two{}, Three{}) : launch(One{}, Three{});
+        else if constexpr (m == kModeAff8)
+            return pl.wtiles == 2 ? launch(One{}, Two{}) : launch(One{}, Three{});
+        else
+            return launch(One{}, Three{});
     };
     if (fmt == WFmt::Q4_0) return go(std::integral_constant<int, kModeQ4_0>{});
     if (fmt == WFmt::AFF4) return go(std::integral_constant<int, kModeAff4>{});
@@ -452,7 +464,8 @@ struct EpiWs {
 // 170 with two; gated affine 4-bit 317 and 309).  Forward the exposed epilogue costs as much
 // as the dequantization saved (12288 x 4096 affine 4-bit with gelu, 512 tokens: 51 and 60;
 // 8-bit, 400 tokens, no activation: 54 and 52).
-bool plan_epi_product(WFmt fmt, bool gradient, int64_t rows, int64_t M, int segs, int64_t red, int num_sms, int smem_optin, EpiWs* w)
+bool plan_epi_product(WFmt fmt, bool gradient, int64_t rows, int64_t M, int segs, int64_t red, int num_sms,
+                      int smem_optin, EpiWs* w)
 {
     w->rows = rows;
     w->fused = has_fast_paths(fmt);
@@ -460,15 +473,23 @@ bool plan_epi_product(WFmt fmt, bool gradient, int64_t rows, int64_t M, int segs
         return plan_pair(rows, M, segs * ((red + 63) / 64), num_sms, smem_optin, 0, (int)kPairABytes, 64,
                          PairCost{300.0, 1.5, 0.0, 1}, &w->pl);
     const int mode = fp_mode(fmt);
-    if (!plan_pair(rows, M, segs * ((red + 127) / 128), num_sms, smem_optin, (int)fp_fixed_bytes(mode, 2), 0, 128,
+    int wtiles = mode == kModeAff8 ? 2 : 3;      // bf16 weight tiles: 8-bit codes leave room for two of them
+    if (!plan_pair(rows, M, segs * ((red + 127) / 128), num_sms, smem_optin, (int)fp_fixed_bytes(mode, wtiles, 2), 0, 128,
                    PairCost{980.0, 1.3, 300.0, gradient ? 2 : 1}, &w->pl))
         return false;
+    auto token_tiles = [&](int wt, int codes) {
+        return (smem_optin - 1024 - 512 - (int)fp_fixed_bytes(mode, wt, codes)) / (w->pl.bn * 128);
+    };
+    // 8-bit forward: three weight tiles where they leave room for three token tiles (4096 x
+    // 4096, 1999 tokens in tiles of 224: 67 us with two weight tiles, 64.5 with three; 12288 x
+    // 4096, 4096 tokens in tiles of 256, where two token tiles would be left: 316 and 346).
+    if (mode == kModeAff8 && !gradient && token_tiles(3, 2) >= 3) wtiles = 3;
     // Four code stages where they leave room for three token tiles, else two: 1 to 8% apart
     // below 256 tokens a tile, and 12% the other way at 256, where two token tiles would be
     // left.
-    const int stages = (smem_optin - 1024 - 512 - (int)fp_fixed_bytes(mode, kFpMaxCodes)) / (w->pl.bn * 128);
-    w->pl.codes = stages >= 3 ? kFpMaxCodes : 2;
-    if (stages >= 3) w->pl.stages = std::min<int>(kFpMaxTok, stages);
+    w->pl.wtiles = wtiles;
+    w->pl.codes = token_tiles(wtiles, kFpMaxCodes) >= 3 ? kFpMaxCodes : 2;
+    w->pl.stages = std::min<int>(kFpMaxTok, token_tiles(wtiles, w->pl.codes));
     return true;
 }
 

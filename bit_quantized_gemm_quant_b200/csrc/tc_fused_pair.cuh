@@ -71,11 +71,10 @@ constexpr int kFpConsumed = 16;                 // consumed barriers, at least t
 constexpr int kFpMaxTok = 8;                    // token tiles of a block
 
 __host__ __device__ constexpr uint32_t fp_code_bytes(int mode) { return mode == kModeAff8 ? 16384u : 8192u; }   // of a block
-__host__ __device__ constexpr int fp_tiles(int mode) { return mode == kModeAff8 ? 2 : 3; }   // bf16 weight tiles of a block
-// Shared memory beside the token tiles
-__host__ __device__ constexpr uint32_t fp_fixed_bytes(int mode, int codes)
+// Shared memory beside the token tiles: `tiles` bf16 weight tiles of a block and the codes
+__host__ __device__ constexpr uint32_t fp_fixed_bytes(int mode, int tiles, int codes)
 {
-    return (uint32_t)fp_tiles(mode) * 2u * kPairABytes + (uint32_t)codes * (fp_code_bytes(mode) + kFpScaleBytes);
+    return (uint32_t)tiles * 2u * kPairABytes + (uint32_t)codes * (fp_code_bytes(mode) + kFpScaleBytes);
 }
 
 struct FpParams {
@@ -90,12 +89,12 @@ struct FpParams {
 // grp >> 1 + 2, ... of the CTA's `left` ones.  A thread expands 64 weights: forward, row r of the tile;
 // gradient, row r of the half-block, outputs 64 hk .. of the tile.  (A function of its own:
 // inlined, the code that follows it for these warps slowed this loop by 13%.)
-template <int MODE, bool MN, int EPI, int H>
+template <int MODE, bool MN, int EPI, int H, int kTiles>
 __device__ __noinline__ void fp_dequantize(int left, int codes_ring, uint32_t a_base, uint32_t c_base, uint32_t cfull0, uint32_t cempty0,
                                            uint32_t ready0, uint32_t consumed0)
 {
     constexpr uint32_t kCBytes = fp_code_bytes(MODE), kCStage = kCBytes + kFpScaleBytes;
-    constexpr int kBits = MODE == kModeAff8 ? 8 : 4, kTiles = fp_tiles(MODE);
+    constexpr int kBits = MODE == kModeAff8 ? 8 : 4;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int grp = warp >> 2, w4 = warp & 3;
     const int half = grp & 1;                       // of the block, always the same for a group
@@ -159,15 +158,14 @@ __device__ __noinline__ void fp_dequantize(int left, int codes_ring, uint32_t a_
 // forward: 64 rows of gate and of up).
 // tm_b0, tm_b1: tokens, boxes of 64 elements x bn / 2 tokens.
 // H: token tiles per unit, 1 (the two accumulators take units in turn) or 2 (both work on
-// one unit, which reads each weight tile twice).
-template <int MODE, bool MN, int EPI, int H>
+// one unit, which reads each weight tile twice).  kTiles: weight tiles, 2 or 3.
+template <int MODE, bool MN, int EPI, int H, int kTiles>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFpThreads, 1)
 tc_fused_pair_kernel(const __grid_constant__ CUtensorMap tm_a0, const __grid_constant__ CUtensorMap tm_a1,
                      const __grid_constant__ CUtensorMap tm_b0, const __grid_constant__ CUtensorMap tm_b1,
                      const __grid_constant__ FpParams fp)
 {
     constexpr uint32_t kCBytes = fp_code_bytes(MODE), kCStage = kCBytes + kFpScaleBytes;
-    constexpr int kTiles = fp_tiles(MODE);
     constexpr int kBits = MODE == kModeAff8 ? 8 : 4;
     const PairParams& p = fp.q;
     extern __shared__ uint8_t smem_raw[];
@@ -386,7 +384,7 @@ tc_fused_pair_kernel(const __grid_constant__ CUtensorMap tm_a0, const __grid_con
         // ---------------- dequantization ----------------
         int left = 0;                                    // blocks of this CTA's sequence
         for (PairUnits u(p); u.next();) left += u.kb1 - u.kb0;
-        fp_dequantize<MODE, MN, EPI, H>(left, NC, a_base, c_base, cfull_bar(0), cempty_bar(0), map_to_cta(ready_bar(0), 0),
+        fp_dequantize<MODE, MN, EPI, H, kTiles>(left, NC, a_base, c_base, cfull_bar(0), cempty_bar(0), map_to_cta(ready_bar(0), 0),
                                      consumed_bar(0));
     }
     __syncwarp();
