@@ -5,7 +5,7 @@ import pytest
 import torch
 
 import bit_quantized_gemm_quant_b200 as bq
-from test_epilogue_gpu import EVAL, HALF, Case, df, f, near
+from test_epilogue_gpu import EVAL, HALF, Case, check_act, check_glu, df, f, near
 
 pytestmark = pytest.mark.gpu
 
@@ -38,4 +38,23 @@ def test_bias_gradients_over_many_row_blocks(fmt, N, K, M):
         got = bq.quant_matmul_glu_backward(dy, z, u, two.mats[0], two.mats[1], act, two.gs, two.bits, True)
         check_column_sums(got[3], D * U * df(act, Z), (err + 2.0 ** -22 * D.abs()) * U.abs(), f"dgate_bias {act}")
         check_column_sums(got[4], D * f(act, Z), err + 2.0 ** -22 * D.abs() * Z.abs(), f"dup_bias {act}")
+    assert bq.bq_device_status() == 0
+
+
+# What each covers of the kernel up to 16 tokens (2048 columns a chunk, 16 rows of W a tile):
+# 8-bit codes past 1024 columns are a stage's second panel; K > 2048 with 2, 3 and 6 bits, K > 8192
+# and 9 to 16 tokens with K > 4096 load the activations again for every chunk; N = 2500 gives a CTA
+# two tiles of 16 rows (three of 8 + 8); K with a number of groups that is not a multiple of 8
+# loads the scales past the ring.
+RING = ([("affine8", 2500, 2048, M) for M in (1, 8, 16)] + [("affine8", 2500, 4224, M) for M in (1, 8, 16)] +
+        [(fmt, 2500, 4224, 16) for fmt in ("affine8_g32", "affine8_g128")] + [("affine8_g32", 2500, 4192, 9)] +
+        [(fmt, 2500, K, M) for fmt in ("affine2", "affine3", "affine6") for K, M in ((4480, 5), (4480, 16), (4608, 13))] +
+        [("q4_0", 2500, 8480, 3), ("q4_0", 2500, 4384, 13), ("q4_0", 2501, 8704, 16), ("affine4", 2500, 10304, 2),
+         ("affine4_g128", 2500, 14336, 1), ("affine4", 4900, 192, 11)])
+
+
+@pytest.mark.parametrize("fmt,N,K,M", RING)
+def test_decode_sizes_over_panels_chunks_and_tiles(fmt, N, K, M):
+    check_act(Case(fmt, N, K, M, 1), "silu", bias=True, res=True, save=True)
+    check_glu(Case(fmt, N, K, M, 2), "gelu_tanh", bias=True, save=True)
     assert bq.bq_device_status() == 0
