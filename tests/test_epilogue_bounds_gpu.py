@@ -1,6 +1,8 @@
 """Tighter checks of quant_matmul_act, quant_matmul_glu and their gradients, beside
 test_epilogue_gpu.py, whose formulas and cases they share.
 """
+import ctypes
+
 import pytest
 import torch
 
@@ -57,4 +59,61 @@ RING = ([("affine8", 2500, 2048, M) for M in (1, 8, 16)] + [("affine8", 2500, 42
 def test_decode_sizes_over_panels_chunks_and_tiles(fmt, N, K, M):
     check_act(Case(fmt, N, K, M, 1), "silu", bias=True, res=True, save=True)
     check_glu(Case(fmt, N, K, M, 2), "gelu_tanh", bias=True, save=True)
+    assert bq.bq_device_status() == 0
+
+
+FORMS = ["act", "act_backward", "glu", "glu_backward"]
+
+
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("fmt,N,K", [("q4_0", 520, 1024), ("affine4", 777, 640), ("affine8", 203, 4160), ("affine3", 777, 640),
+                                     ("affine6", 264, 384)])
+def test_nothing_of_the_workspace_is_read_before_it_is_written(form, fmt, N, K):
+    """A workspace of exactly the reported size, filled with NaN patterns (0xFF bytes: NaN as
+    bf16 and as fp32), gives the bits of a call with its own, and the bytes behind it stay."""
+    P = ctypes.c_void_p
+    L = bq.lib()
+    for M in (17, 40, 300, 1100):
+        c = Case(fmt, N, K, M, 2)
+        (wq, s, b), (wq2, s2, b2) = c.mats
+        kw = dict(group_size=c.gs, bits=c.bits)
+        need = bq.quant_matmul_epilogue_workspace_size(FORMS.index(form), M, N, K, c.gs, c.bits)
+        assert need > 0
+        ws = torch.full((need + 4096,), 0xFF, dtype=torch.uint8, device="cuda")
+        tail = (M, N, K, c.gs, c.bits, ws.data_ptr(), need, torch.cuda.current_stream().cuda_stream)
+
+        def ptr(t):
+            return None if t is None else t.data_ptr()
+
+        def pair(x, y):
+            return None if x is None else (P * 2)(x.data_ptr(), y.data_ptr())
+
+        def out(*shape):
+            return torch.full(shape, float("nan"), dtype=torch.bfloat16, device="cuda")
+
+        if form == "act":
+            x, r = c.rand(M, K), c.rand(M, N)
+            want = bq.quant_matmul_act(x, wq, s, b, act="gelu", residual=r, save_preact=True, **kw)
+            got = out(M, N), out(M, N)
+            st = L.quant_matmul_act(ptr(x), ptr(wq), ptr(s), ptr(b), None, ptr(r), 2, ptr(got[0]), ptr(got[1]), *tail)
+        elif form == "act_backward":
+            dy, z = c.rand(M, N), c.rand(M, N)
+            want = bq.quant_matmul_act_backward(dy, wq, s, b, z, "silu", need_dbias=True, **kw)
+            got = out(M, K), out(M, N), out(N)
+            st = L.quant_matmul_act_backward(ptr(dy), ptr(z), ptr(wq), ptr(s), ptr(b), 4, *map(ptr, got), *tail)
+        elif form == "glu":
+            x = c.rand(M, K)
+            want = bq.quant_matmul_glu(x, *c.mats, act="silu", save_preact=True, **kw)
+            got = out(M, N), out(M, N), out(M, N)
+            st = L.quant_matmul_glu(ptr(x), pair(wq, wq2), pair(s, s2), pair(b, b2), None, None, 4, *map(ptr, got), *tail)
+        else:
+            dh, g, u = c.rand(M, N), c.rand(M, N), c.rand(M, N)
+            want = bq.quant_matmul_glu_backward(dh, g, u, *c.mats, act="relu", need_dbias=True, **kw)
+            got = out(M, K), out(M, N), out(M, N), out(N), out(N)
+            st = L.quant_matmul_glu_backward(ptr(dh), ptr(g), ptr(u), pair(wq, wq2), pair(s, s2), pair(b, b2), 1,
+                                             *map(ptr, got), *tail)
+        assert st == 0
+        for a, w in zip(got, want):
+            assert torch.isfinite(w).all() and torch.equal(a, w), (form, M)
+        assert (ws[need:] == 0xFF).all()
     assert bq.bq_device_status() == 0
