@@ -2,6 +2,7 @@
 test_epilogue_gpu.py, whose formulas and cases they share.
 """
 import ctypes
+import math
 
 import pytest
 import torch
@@ -117,3 +118,53 @@ def test_nothing_of_the_workspace_is_read_before_it_is_written(form, fmt, N, K):
             assert torch.isfinite(w).all() and torch.equal(a, w), (form, M)
         assert (ws[need:] == 0xFF).all()
     assert bq.bq_device_status() == 0
+
+
+# act and act' far left of 0, without the cancellation of 1 + tanh and 1 + erf: the factor p that
+# multiplies z, the two terms of the derivative, and the argument a of p's exponential.
+def tail_terms(act, z):
+    if act == "silu":
+        p = torch.sigmoid(z)
+        return p, z * p * torch.sigmoid(-z), z.abs()
+    if act == "gelu":
+        return 0.5 * torch.erfc(-z / math.sqrt(2)), z * torch.exp(-z * z / 2) / math.sqrt(2 * math.pi), z * z / 2
+    c = 2 * math.sqrt(2 / math.pi)
+    a = c * (z + 0.044715 * z ** 3)
+    p = torch.sigmoid(a)
+    return p, z * p * torch.sigmoid(-a) * c * (1 + 3 * 0.044715 * z * z), a.abs()
+
+
+@pytest.mark.parametrize("act,left", [("gelu", -12.9), ("gelu_tanh", -9.9), ("silu", -85.0)])
+def test_tails_of_the_activations(act, left):
+    """act(z) and act'(z) for z from -3 to `left`, where both vanish (1e-35), relative to themselves.
+
+    W is 0, so that z is the bias.  e^-a in fp32 is within (a + 4) 2^-23 of itself; the
+    roundings of a itself add 2 a 2^-24 (gelu: half of z z and its product with log2 e),
+    or 6 (gelu_tanh, with those of its constants); gelu's polynomial may be as far off as
+    its exponential; the reciprocal and the products are a few steps of 2^-24."""
+    N, K = 264, 64
+    z = torch.linspace(-3, left, N, device="cuda").to(torch.bfloat16)
+    Z = z.double()
+    p, q, a = tail_terms(act, Z)
+    rel = ({"silu": 1, "gelu": 3, "gelu_tanh": 4}[act] * a + 16) * 2.0 ** -23
+
+    def hold(got, want, terms, what):
+        off = (got.double() - want).abs() - HALF * want.abs() - rel * terms
+        i = int(off.max(0).values.argmax())
+        assert (off <= 0).all(), f"{what}: z = {float(Z[i])}, {got[0, i].item()} for {float(want[i])}"
+
+    one = torch.ones_like(z)
+    for fmt in ("q4_0", "affine4", "affine3"):
+        for M in (2, 40):
+            c = Case(fmt, N, K, M, 1)
+            wq, s, b = c.mats[0]
+            w = (wq, torch.zeros_like(s), None if b is None else torch.zeros_like(b))
+            x, kw = c.rand(M, K), dict(group_size=c.gs, bits=c.bits)
+            hold(bq.quant_matmul_act(x, *w, out_bias=z, act=act, **kw), Z * p, (Z * p).abs(), "act")
+            hold(bq.quant_matmul_glu(x, w, w, z, one, act, **kw), Z * p, (Z * p).abs(), "glu")
+            rows, ones = z.expand(M, N).contiguous(), one.expand(M, N).contiguous()
+            dz = bq.quant_matmul_act_backward(ones, *w, preact=rows, act=act, **kw)[1]
+            hold(dz, p + q, p + q.abs(), "dz")
+            _, dg, du = bq.quant_matmul_glu_backward(ones, rows, ones, w, w, act, **kw)
+            hold(dg, p + q, p + q.abs(), "dg")
+            hold(du, Z * p, (Z * p).abs(), "du")
