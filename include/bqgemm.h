@@ -360,7 +360,9 @@ BQ_API int quant_matmul_select_path(int64_t M, int64_t N, int64_t K, int group_s
 BQ_API bq_status bf16_matmul(const uint16_t* x_bf16, const uint16_t* w_bf16, uint16_t* y_bf16,
                       int64_t M, int64_t N, int64_t K, bq_stream_t stream);
 
-/* Activations of the fused products below (z is the fp32 sum plus the bias). */
+/* Activations of the fused products below (z is the fp32 sum plus the bias), evaluated in
+ * fp32: act(z) is within 2^-14 of itself, and 0 where its exponential leaves the normal range
+ * (z below -87 for silu, -13 for gelu, -10 for gelu_tanh). */
 typedef enum {
     BQ_ACT_NONE = 0,           /* z */
     BQ_ACT_RELU = 1,           /* max(z, 0); derivative 0 at 0 */
