@@ -359,8 +359,8 @@ def _calls():
         try:
             m = importlib.import_module(__name__ + "._binding")
         except ImportError as e:
-            raise RuntimeError(f"_binding.so could not be loaded from {_PKG}; build it with "
-                               "`python -c 'import __graft_entry__ as g; g.build()'`") from e
+            raise RuntimeError(f"_binding.so could not be loaded from {_PKG} ({e}); build it with "
+                               "`python -m bit_quantized_gemm_quant_b200.build`") from e
         m.set_error(BqError)
         _marshal = m
     return _marshal

@@ -44,9 +44,21 @@ def up_to_date() -> bool:
     return all(os.path.getmtime(s) <= t for s in _sources())
 
 
+def _binding_key() -> str:
+    """What the binding is compiled against: a change of PyTorch or Python needs a new one."""
+    import torch
+    return f"torch {torch.__version__} {sysconfig.get_config_var('SOABI')}"
+
+
 def _build_binding(force: bool, verbose: bool) -> None:
     deps = [BINDING_SRC, *glob.glob(os.path.join(INCLUDE, "*.h"))]
-    if not force and os.path.exists(BINDING) and all(os.path.getmtime(s) <= os.path.getmtime(BINDING) for s in deps):
+    stamp = os.path.join(os.path.dirname(BINDING), "_build", "binding.txt")      # the key of the built one
+    key, built = _binding_key(), ""
+    if os.path.exists(stamp):
+        with open(stamp) as f:
+            built = f.read()
+    if (not force and built == key and os.path.exists(BINDING)
+            and all(os.path.getmtime(s) <= os.path.getmtime(BINDING) for s in deps)):
         return
     import torch
     torch_root = os.path.dirname(torch.__file__)
@@ -63,6 +75,9 @@ def _build_binding(force: bool, verbose: bool) -> None:
         print(" ".join(cmd))
     subprocess.check_call(cmd)
     os.replace(tmp, BINDING)
+    os.makedirs(os.path.dirname(stamp), exist_ok=True)
+    with open(stamp, "w") as f:
+        f.write(key)
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | None = None) -> str:
