@@ -4,8 +4,8 @@
 //
 // A decode call runs 4 to 10 microseconds on the GPU; marshalled through ctypes it took 13
 // on the host (a gradient 25), most of it in Python attribute reads, argument conversion
-// and tensor creation.  Errors are those of the Python layer: TypeError, ValueError, and
-// BqError with the library's status.
+// and tensor creation.  Errors are those of the Python layer: TypeError, ValueError,
+// BqError with the library's status, and PyTorch's own (OutOfMemoryError) as PyTorch raises them.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
@@ -13,6 +13,7 @@
 #include <ATen/ops/empty.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <exception>
@@ -196,8 +197,8 @@ PyObject* guarded(Py_ssize_t got, Py_ssize_t want, F&& f)
         return f();
     } catch (const Raised&) {
         return nullptr;
-    } catch (const std::exception& e) {
-        PyErr_SetString(PyExc_RuntimeError, e.what());
+    } catch (const std::exception&) {
+        torch::translate_exception_to_python(std::current_exception());
     } catch (...) {
         PyErr_SetString(PyExc_RuntimeError, "unknown error");
     }

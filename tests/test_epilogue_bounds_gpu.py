@@ -168,3 +168,14 @@ def test_tails_of_the_activations(act, left):
             _, dg, du = bq.quant_matmul_glu_backward(ones, rows, ones, w, w, act, **kw)
             hold(dg, p + q, p + q.abs(), "dg")
             hold(du, Z * p, (Z * p).abs(), "du")
+
+
+def test_out_of_memory_is_pytorchs_error():
+    """An output of 2 TB: the error type that quant_matmul's own allocation gives, and the next call runs."""
+    n = 1 << 20
+    x = torch.zeros(n, 32, dtype=torch.bfloat16, device="cuda")
+    wq, s = torch.zeros(n, 16, dtype=torch.uint8, device="cuda"), torch.zeros(n, 1, dtype=torch.float16, device="cuda")
+    for call in (bq.quant_matmul, bq.quant_matmul_act, lambda x, wq, s: bq.quant_matmul_glu(x, (wq, s, None), (wq, s, None))):
+        with pytest.raises(torch.OutOfMemoryError):
+            call(x, wq, s)
+    assert not bq.quant_matmul_act(x[:4], wq[:8], s[:8]).any()
