@@ -389,8 +389,9 @@ def quant_matmul_act(x: torch.Tensor, wq: torch.Tensor, scales: torch.Tensor, bi
                      group_size: int = 32, bits: int = 4, save_preact: bool = False, out: torch.Tensor | None = None,
                      stream=None):
     """y = residual + act(x . dequant(W)[N][K]^T + out_bias), bf16 [M][N], in the
-    product's own epilogue; act is a key of ACTS.  out may be residual itself.  With
-    save_preact: (y, z), z the bf16 argument of act, for quant_matmul_act_backward."""
+    product's own epilogue; act is a key of ACTS.  out may be residual itself, else it
+    shares no memory with an input.  With save_preact: (y, z), z the bf16 argument of act,
+    for quant_matmul_act_backward."""
     code = _act_code(act)
     with _on(stream, x, "x"):
         return _calls().act(x, wq, scales, biases, out_bias, code, residual, group_size, bits, save_preact, out)
@@ -415,8 +416,8 @@ def quant_matmul_glu(x: torch.Tensor, gate, up, gate_bias: torch.Tensor | None =
                      save_preact: bool = False, out: torch.Tensor | None = None, stream=None):
     """h = act(x . dequant(gate)^T + gate_bias) * (x . dequant(up)^T + up_bias), bf16
     [M][N], both projections in one product.  gate and up are (wq, scales, biases | None)
-    of one format.  With save_preact: (h, g, u), the bf16 factors before the activation,
-    for quant_matmul_glu_backward."""
+    of one format; out shares no memory with an input.  With save_preact: (h, g, u), the
+    bf16 factors before the activation, for quant_matmul_glu_backward."""
     code = _act_code(act)
     with _on(stream, x, "x"):
         return _calls().glu(x, gate, up, gate_bias, up_bias, code, group_size, bits, save_preact, out)

@@ -101,6 +101,15 @@ struct Call {
     bq_stream_t stream() const { return c10::cuda::getCurrentCUDAStream(dev.index()).stream(); }
 };
 
+// `out` given by the caller and one of the call's inputs: shared memory would be written while
+// other CTAs still read it.
+void apart(const at::Tensor* out, const at::Tensor* in, const char* name)
+{
+    if (!out || !in || out->nbytes() == 0 || in->nbytes() == 0) return;
+    const char *o = static_cast<const char*>(out->data_ptr()), *i = static_cast<const char*>(in->data_ptr());
+    if (o < i + in->nbytes() && i < o + out->nbytes()) raise(PyExc_ValueError, "out: shares memory with %s%s", name);
+}
+
 Call on(const at::Tensor& t, const char* name)
 {
     if (!t.is_cuda()) raise(PyExc_ValueError, "%s: tensors must live on a CUDA device%s", name);
@@ -222,6 +231,12 @@ PyObject* py_act(PyObject*, PyObject* const* a, Py_ssize_t n)
         const uint16_t* bp = c.operand(ob, kBf16Bits, {N}, "out_bias");
         const uint16_t* rp = c.operand(res, kBf16Bits, {M, N}, "residual");
         uint16_t* gp = c.operand(given, kBf16, {M, N}, "out");
+        apart(given, &x, "x");
+        apart(given, &wq, "w.wq");
+        apart(given, &sc, "w.scales");
+        apart(given, bi, "w.biases");
+        apart(given, ob, "out_bias");
+        if (rp != gp) apart(given, res, "residual");          // the residual itself: each element is read, then written
         const at::Tensor y = given ? *given : c.make({M, N}), z = save ? c.make({M, N}) : at::Tensor();
         const Scratch s(c, BQ_OP_ACT, M, N, K, gs, bits);
         check(quant_matmul_act(xp, w.wq, w.scales, w.biases, bp, rp, act, given ? gp : address<uint16_t>(y),
@@ -313,6 +328,11 @@ PyObject* py_glu(PyObject*, PyObject* const* a, Py_ssize_t n)
         const uint16_t* gbp = c.operand(gb, kBf16Bits, {N}, "gate_bias");
         const uint16_t* ubp = c.operand(ub, kBf16Bits, {N}, "up_bias");
         uint16_t* op = c.operand(given, kBf16, {M, N}, "out");
+        apart(given, &x, "x");
+        for (const Triple* t : {&gt, &ut})
+            for (int i = 0; i < 3; ++i) apart(given, tensor(t->at(i), ""), t == &gt ? "gate" : "up");
+        apart(given, gb, "gate_bias");
+        apart(given, ub, "up_bias");
         const at::Tensor h = given ? *given : c.make({M, N}), g = save ? c.make({M, N}) : at::Tensor(),
                          u = save ? c.make({M, N}) : at::Tensor();
         const Scratch s(c, BQ_OP_GLU, M, N, K, gs, bits);

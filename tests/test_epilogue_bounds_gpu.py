@@ -179,3 +179,40 @@ def test_out_of_memory_is_pytorchs_error():
         with pytest.raises(torch.OutOfMemoryError):
             call(x, wq, s)
     assert not bq.quant_matmul_act(x[:4], wq[:8], s[:8]).any()
+
+
+def test_out_that_shares_memory_with_an_input_is_refused():
+    """Square weights make out = x fit; a residual is taken whole or not at all."""
+    M, N = 24, 128
+    c = Case("affine4", N, N, M, 2)
+    kw = dict(group_size=c.gs, bits=c.bits)
+    wq, s, b = c.mats[0]
+    buf = torch.zeros(2 * M, N, dtype=torch.bfloat16, device="cuda")
+    x, out, bias = buf[:M].copy_(c.rand(M, N)), buf[M:], c.rand(M, N)
+    act = lambda **k: bq.quant_matmul_act(k.pop("x", x), wq, s, b, **kw, **k)
+    glu = lambda **k: bq.quant_matmul_glu(k.pop("x", x), *c.mats, **kw, **k)
+    want, want_glu = act(residual=bias).clone(), glu().clone()
+    for call in (act, glu):
+        for o in (x, buf[1:M + 1], buf[M - 1:2 * M - 1]):
+            with pytest.raises(ValueError, match="shares memory with x"):
+                call(out=o)
+    with pytest.raises(ValueError, match="residual"):
+        act(residual=buf[M - 8:2 * M - 8], x=bias, out=out)
+    with pytest.raises(ValueError, match="out_bias"):
+        act(out_bias=out[3], out=out)
+    with pytest.raises(ValueError, match="up_bias"):
+        glu(up_bias=out[M - 1], out=out)
+    words = torch.zeros(N * N // 8 + M * N // 2, dtype=torch.int32, device="cuda")     # codes, then an output's place
+    codes = words[:N * N // 8].view(N, N // 8)
+    place = words.view(torch.bfloat16)[:M * N].view(M, N)
+    with pytest.raises(ValueError, match="w.wq"):
+        bq.quant_matmul_act(x, codes, s, b, out=place, **kw)
+    with pytest.raises(ValueError, match="up"):
+        bq.quant_matmul_glu(x, c.mats[0], (codes, s, b), out=place, **kw)
+    # beside an input is apart
+    assert act(residual=bias, out=out) is out and torch.equal(out, want)
+    assert glu(out=out) is out and torch.equal(out, want_glu)
+    assert torch.equal(act(residual=out.copy_(bias), out=out), want)
+    # nothing to write: nothing shared
+    e = x[:0]
+    assert act(x=e, out=e) is e
