@@ -28,7 +28,6 @@ PyObject* g_error = nullptr;            // BqError
 struct Raised {};                       // a Python exception is set
 
 using Types = std::initializer_list<at::ScalarType>;
-const Types kBf16 = {at::kBFloat16};
 const Types kBf16Bits = {at::kBFloat16, at::kShort, at::kUInt16};
 const Types kBits16 = {at::kBFloat16, at::kHalf, at::kShort, at::kUInt16};
 const Types kBytes = {at::kByte, at::kChar};
@@ -230,7 +229,7 @@ PyObject* py_act(PyObject*, PyObject* const* a, Py_ssize_t n)
         const uint16_t* xp = c.operand(&x, kBf16Bits, {M, K}, "x");
         const uint16_t* bp = c.operand(ob, kBf16Bits, {N}, "out_bias");
         const uint16_t* rp = c.operand(res, kBf16Bits, {M, N}, "residual");
-        uint16_t* gp = c.operand(given, kBf16, {M, N}, "out");
+        uint16_t* gp = c.operand(given, kBf16Bits, {M, N}, "out");
         apart(given, &x, "x");
         apart(given, &wq, "w.wq");
         apart(given, &sc, "w.scales");
@@ -263,7 +262,7 @@ PyObject* py_act_backward(PyObject*, PyObject* const* a, Py_ssize_t n)
         const int64_t M = dy.size(0), N = dy.size(1), K = columns(wq, bi, bits, "w.wq");
         const c10::cuda::CUDAGuard guard(c.dev);
         const Matrix w = matrix(c, wq, sc, bi, N, K, gs, bits, "w.wq", "w.scales", "w.biases");
-        const uint16_t* dyp = c.operand(&dy, kBf16, {M, N}, "dy");
+        const uint16_t* dyp = c.operand(&dy, kBf16Bits, {M, N}, "dy");
         const uint16_t* pp = c.operand(pre, kBf16Bits, {M, N}, "preact");
         const at::Tensor dx = c.make({M, K}), dz = act == BQ_ACT_NONE ? dy : c.make({M, N}),
                          db = need ? c.make({N}) : at::Tensor();
@@ -327,7 +326,7 @@ PyObject* py_glu(PyObject*, PyObject* const* a, Py_ssize_t n)
         const uint16_t* xp = c.operand(&x, kBf16Bits, {M, K}, "x");
         const uint16_t* gbp = c.operand(gb, kBf16Bits, {N}, "gate_bias");
         const uint16_t* ubp = c.operand(ub, kBf16Bits, {N}, "up_bias");
-        uint16_t* op = c.operand(given, kBf16, {M, N}, "out");
+        uint16_t* op = c.operand(given, kBf16Bits, {M, N}, "out");
         apart(given, &x, "x");
         for (const Triple* t : {&gt, &ut})
             for (int i = 0; i < 3; ++i) apart(given, tensor(t->at(i), ""), t == &gt ? "gate" : "up");

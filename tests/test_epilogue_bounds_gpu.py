@@ -216,3 +216,28 @@ def test_out_that_shares_memory_with_an_input_is_refused():
     # nothing to write: nothing shared
     e = x[:0]
     assert act(x=e, out=e) is e
+
+
+@pytest.mark.parametrize("bits", [torch.int16, torch.uint16])
+def test_bit_patterns_stand_for_bf16_in_every_operand(bits):
+    """int16 and uint16 tensors, as quant_matmul takes them: the results are those of the bf16 tensors."""
+    M, N, K = 20, 72, 64
+    c = Case("affine4", N, K, M, 2)
+    kw = dict(group_size=c.gs, bits=c.bits)
+    raw = lambda t: t.view(bits)
+    mats = [(wq, raw(s), raw(b)) for wq, s, b in c.mats]
+    x, bias, r, y = c.rand(M, K), c.rand(N), c.rand(M, N), c.rand(M, N)
+    for call in (lambda t, m, o: bq.quant_matmul_act(t(x), *m[0], out_bias=t(bias), act="gelu", residual=t(r), out=o, **kw),
+                 lambda t, m, o: bq.quant_matmul_glu(t(x), *m, t(bias), t(bias), out=o, **kw)):
+        out = torch.empty(M, N, dtype=bits, device="cuda")
+        assert call(raw, mats, out) is out
+        assert torch.equal(out.view(torch.bfloat16), call(lambda t: t, c.mats, None))
+    for call in (lambda t, m: bq.quant_matmul_act_backward(t(y), *m[0], preact=t(r), act="silu", need_dbias=True, **kw),
+                 lambda t, m: bq.quant_matmul_glu_backward(t(y), t(r), t(y), *m, need_dbias=True, **kw)):
+        for a, b in zip(call(raw, mats), call(lambda t: t, c.mats)):
+            assert torch.equal(a, b)
+    dy = raw(y)
+    dx, dz = bq.quant_matmul_act_backward(dy, *mats[0], **kw)
+    assert dz is dy and torch.equal(dx, bq.quant_matmul_act_backward(y, *c.mats[0], **kw)[0])
+    with pytest.raises(TypeError, match="dy"):
+        bq.quant_matmul_act_backward(y.to(torch.float16), *mats[0], **kw)
