@@ -361,8 +361,10 @@ tc_fused_pair_kernel(const __grid_constant__ CUtensorMap tm_a0, const __grid_con
             }
             if (elect_one()) umma_commit_pair(done_bar);     // nothing stays in flight past this point
             __syncwarp();
+            mbar_wait_warp(done_bar, 0);
         }
-        mbar_wait_warp(done_bar, 0);
+        // (the other CTA's MMA warp has nothing to wait for: the pair leaves together, after
+        // the leader; its wait here would last as long as the kernel, past any limit)
     } else if (warp >= kFpEpiWarp0) {
         // ---------------- epilogue: all units but the last ----------------
         int lt = 0;

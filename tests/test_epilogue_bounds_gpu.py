@@ -8,7 +8,7 @@ import pytest
 import torch
 
 import bit_quantized_gemm_quant_b200 as bq
-from test_epilogue_gpu import EVAL, HALF, Case, check_act, check_glu, df, f, near
+from test_epilogue_gpu import EVAL, HALF, Case, check_act, check_glu, df, f, near, sums
 
 pytestmark = pytest.mark.gpu
 
@@ -241,3 +241,22 @@ def test_bit_patterns_stand_for_bf16_in_every_operand(bits):
     assert dz is dy and torch.equal(dx, bq.quant_matmul_act_backward(y, *c.mats[0], **kw)[0])
     with pytest.raises(TypeError, match="dy"):
         bq.quant_matmul_act_backward(y.to(torch.float16), *mats[0], **kw)
+
+
+def test_a_product_of_seconds_is_no_timeout():
+    """2.5 s of tensor-core work in one kernel (2 x 81920 x 81920, 131072 tokens): every wait in it
+    is short, so the limit on waits (2e9 clocks, 1 to 1.5 s) is not met."""
+    M, N = 131072, 81920
+    g = torch.Generator(device="cuda")
+    g.manual_seed(5)
+    wq = torch.randint(0, 256, (N, N // 2), generator=g, device="cuda", dtype=torch.uint8)
+    s = torch.rand(N, N // 32, generator=g, device="cuda", dtype=torch.float16) * 0.002 + 0.001
+    x = torch.empty(M, N, dtype=torch.bfloat16, device="cuda").normal_(generator=g)
+    assert bq.bq_device_status() == 0
+    h = bq.quant_matmul_glu(x, (wq, s, None), (wq, s, None))
+    assert bq.bq_device_status() == 0
+    rows = torch.tensor([0, 1, 77777, M - 1], device="cuda")
+    for cols in (slice(0, 48), slice(N - 48, N)):
+        z, t = sums(x[rows], bq.q4_0_dequantize(wq[cols].contiguous(), s[cols].contiguous()).double(), None)
+        a = f("silu", z)
+        near(h[rows, cols], a * z, ((1.13 * t + EVAL * (1 + z.abs())) * (z.abs() + t) + a.abs() * t) * (1 + HALF), "h")
