@@ -244,8 +244,8 @@ bq_status launch_ring_cfg(const RingMaps& maps, RingParams& p, const DeviceInfo&
                       p);
 }
 
-// Activations in registers for up to 4 chunks of 2048 columns and 8 tokens (2 chunks
-// and 16 tokens): 64 registers.
+// Activations loaded once for up to 4 chunks of 2048 columns and 8 tokens (2 chunks and 16
+// tokens): 64 registers, in part spilled (see gemv_ring.cuh).
 template <int BITS, int EPI>
 bq_status launch_ring_bits(const QMat* w, RingParams& p, const DeviceInfo& di, int dev, cudaStream_t st)
 {
@@ -457,8 +457,11 @@ struct EpiWs {
     int row_blocks = 0, rows_per_block = 0;
 };
 
-// Q4_0 and affine 4- and 8-bit codes are dequantized inside the product; the others
-// (whose rows of a stage are not 16-byte multiples) through a bf16 copy.
+// Q4_0 and affine 4- and 8-bit codes are dequantized inside the product, which has row widths
+// and conversions for these two only; the others go through a bf16 copy of W, written and read back
+// (12288 x 4096, 64 tokens: 56 to 59 us where 4 bits take 25; 2048 tokens: 165 to 169 and 142).
+// A block's rows of 2, 3 and 6 bits, 32, 48 and 96 bytes, could be copied as well wherever K
+// times the bits is a multiple of 128.  The costs of that form's blocks are estimates, not fitted.
 // Two token tiles per unit only for gradients: their epilogue is a plain store and their
 // reductions are long (12288 x 4096, 2048 tokens: 8-bit with gelu and bias 193 us with one,
 // 170 with two; gated affine 4-bit 317 and 309).  Forward the exposed epilogue costs as much
@@ -481,8 +484,9 @@ bool plan_epi_product(WFmt fmt, bool gradient, int64_t rows, int64_t M, int segs
         return (smem_optin - 1024 - 512 - (int)fp_fixed_bytes(mode, wt, codes)) / (w->pl.bn * 128);
     };
     // 8-bit forward: three weight tiles where they leave room for three token tiles (4096 x
-    // 4096, 1999 tokens in tiles of 224: 67 us with two weight tiles, 64.5 with three; 12288 x
-    // 4096, 4096 tokens in tiles of 256, where two token tiles would be left: 316 and 346).
+    // 4096, 1999 tokens in tiles of 224, with residual and z: 67 us with two weight tiles, 64.5
+    // with three; 12288 x 4096, 4096 tokens in tiles of 256, where two token tiles would be left:
+    // 322 and 333).
     if (mode == kModeAff8 && !gradient && token_tiles(3, 2) >= 3) wtiles = 3;
     // Four code stages where they leave room for three token tiles, else two: 1 to 8% apart
     // below 256 tokens a tile, and 12% the other way at 256, where two token tiles would be

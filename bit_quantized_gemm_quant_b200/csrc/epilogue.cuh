@@ -359,8 +359,8 @@ BQ_DEVINL void epi_four(const EpiParams& e, const float (&s)[4], const float (&s
 
 // Sums the partial tiles of the tail in the order of their blocks and applies the
 // epilogue.  Partials: [slot][token of the tile (bn)][row of the tile (256)].  A block
-// takes kReduceTokens tokens of one tile, a thread 4 outputs of a token at a time; a
-// tile's partials (3 to 6 as a rule) are loaded four at a time.  Bound by L2, which still
+// takes kReduceTokens tokens of one tile, a thread 4 outputs of a token, one round of its loop
+// (glu, whose tiles hold half as many outputs: half of the threads); a tile's partials (3 to 6 as a rule) are loaded four at a time.  Bound by L2, which still
 // holds what the product has just written.  (Gated gradient of 2 x 8192 x 2048, 512 tokens:
 // 46.1 us with 8 tokens a block, 44.8 with 4, 45.7 with 2; of 2 x 12288 x 4096, 2048 tokens:
 // 326, 327, 331.)

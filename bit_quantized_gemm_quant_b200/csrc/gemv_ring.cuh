@@ -1,7 +1,7 @@
 // gemv_ring.cuh -- decode sizes (up to 16 tokens) of the products with an epilogue:
 // packed weights stream once through a shared-memory ring, are dequantized in
-// registers to the bf16 weights of the library's dequantizers and multiplied by warp
-// MMAs with fp32 accumulators; bias, activation, residual or gate follow in the same
+// registers to bf16 (Q4_0 and 8 bits: the dequantizers' bits; the others round scale q + bias
+// once, see gemv.cuh) and multiplied by warp MMAs with fp32 accumulators; bias, activation, residual or gate follow in the same
 // kernel.
 //
 // A tile is 16 rows of the MMA's M side: 16 outputs, or with a gate 8 gate rows and
@@ -15,16 +15,23 @@
 // more issue slots than it hides, 22.4): the four threads of a quad take 32 consecutive
 // columns each of rows g and g + 8.  So every warp sees the same columns
 // of every tile, and its activations (the MMA's B fragments, 16 registers per 8 tokens
-// and step) are loaded once and stay in registers for K up to 8192.
+// and step) are loaded once for Q4_0, 4 and 8 bits: up to K = 8192 with 8 tokens, up to 4096
+// with 9 to 16 (64 registers).  The compiler keeps part of them in local memory where all 64 are in
+// use: 40 to 96 bytes a thread for Q4_0, 88 to 128 for 4 bits, 176 to 288 for 8.  Longer
+// reductions and the other widths load them from L2 again for every tile.
 //
-// The floor is HBM (the packed weights, read once); what binds is issue: dequantizing costs
-// 2 to 2.5 instructions per weight on pipes that take half the issue rate (a loop of the
-// dequantization and MMAs alone takes 880 clocks per chunk for affine 4-bit, 1050 for
-// Q4_0, against 420 for the MMAs), and about 4 us of a call are launch, first copy and last
-// output.  The ring keeps about 150 KB per SM in flight.  Measured, graph-timed over
-// rotating weights: 8192 x 2048 Q4_0 gated, one token, 10.1 us (18.9 MB); 12288 x 4096
-// affine 4-bit gated, 8 tokens, 20.3 us (57 MB); 2048 x 8192 Q4_0, one token with residual,
-// 6.7 us (9.4 MB); 256 x 512, 16 tokens, 3.8 us.
+// The floor is HBM (the packed weights, read once), but neither it nor a pipe is what binds:
+// in the profile of glu, 8 tokens, 12288 x 4096 affine 4-bit, HBM runs at 29% and issue slots
+// are half busy while the kernel is active (39% of its time), with waits for loads and barriers
+// as the first stall.  The two compute warps of a scheduler each wait for a stage, load,
+// dequantize (2 to 2.5 instructions per weight) and multiply in order, so that one other warp
+// at most covers a wait: a chunk takes about 1500 clocks, where a loop of its dequantization
+// and MMAs alone takes 880 (Q4_0: 1050; the MMAs 420).  About 4 us of a call are launch, first
+// copy and last output.  The ring keeps about 150 KB per SM in flight.  Measured, graph-timed
+// over rotating weights: 8192 x 2048 Q4_0 gated, one token, 10.2 us (18.9 MB); 12288 x 4096
+// affine 4-bit gated, 8 tokens, 20.3 us (57 MB), one matrix 13.0; 2048 x 8192 Q4_0, one token
+// with residual, 6.7 us (9.4 MB); 256 x 512, 16 tokens, 3.8 us; 12288 x 4096 with 2, 3 and 6 bits,
+// one token, 15.5, 16.4 and 17.8 us; 4096 x 14336 affine 4-bit, one token, 17.1 us.
 //
 // Rows of a stage are padded so that the quads' loads of 8 rows fall in different
 // banks (ring_code_pitch).  The warps' partial sums of a tile meet in shared memory, two

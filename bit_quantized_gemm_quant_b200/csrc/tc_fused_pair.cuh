@@ -32,8 +32,12 @@
 //  - the epilogue: eight warps, and for the last unit, which no product overlaps, the
 //    dequant warps as well.
 // Forward, large products are bound by the tensor cores and the power they may draw (1.49
-// PFLOP/s in isolation, cuBLAS bf16 reaches 1.64); below 192 tokens a tile the 1050 clocks
-// that a block's dequantization takes exceed the MMA's.  Gradients, whose epilogue is a
+// PFLOP/s in isolation, cuBLAS bf16 reaches 1.64); below 192 tokens a tile the 1050 to 1300 clocks
+// that a block's dequantization takes exceed the MMA's.  No pipe is full then (12288 x 4096
+// affine 4-bit with gelu, 512 tokens: issue slots 53%, ALU 41%, shared-memory banks 17% + 17%):
+// by the decode kernel's loop the arithmetic is about 440 of them, and the rest is the chain
+// of a group's block, wait, load, convert, wait for the tile, store, fence and arrive, which
+// nothing of the same group overlaps.  Gradients, whose epilogue is a
 // plain store and whose reductions are long, may take two token tiles per unit (H = 2): both
 // accumulators work on one weight tile, so that a block's dequantization serves up to 512
 // tokens (8-bit 12288 x 4096, 2048 tokens, gelu and bias: 199 us with one tile, 172 with

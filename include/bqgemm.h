@@ -375,8 +375,10 @@ typedef enum {
  * quant_matmul_act -- quant_matmul with its epilogue in the product's kernel:
  *   z[m][n] = sum_k x[m][k] * dequant(W)[n][k] + out_bias[n]
  *   y[m][n] = bf16_rne(residual[m][n] + act(z[m][n]))
- * dequant(W) is the bf16 matrix of *_dequantize, sums and epilogue are fp32, and y
- * is rounded once.  No page has a counterpart of the epilogue; the product is
+ * dequant(W) is the bf16 matrix of *_dequantize (affine_dequantize rounds scale q + bias
+ * to fp32, then to bf16; 4-bit weights here, and 2-, 3- and 6-bit ones up to 16 tokens, round it
+ * once, which is one bf16 step away where the fp32 value lies halfway between two bf16
+ * values and the exact one does not), sums and epilogue are fp32, and y is rounded once.  No page has a counterpart of the epilogue; the product is
  * quant_matmul's (mx.quantized_matmul on the MLX issue page, Repro).
  *   x_bf16    device u16 [M][K]
  *   wq, scales, biases  W [N][K] as in quant_matmul with transpose = 1 (biases NULL: Q4_0)
