@@ -3,6 +3,9 @@ test_epilogue_gpu.py, whose formulas and cases they share.
 """
 import ctypes
 import math
+import os
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -260,3 +263,120 @@ def test_a_product_of_seconds_is_no_timeout():
         z, t = sums(x[rows], bq.q4_0_dequantize(wq[cols].contiguous(), s[cols].contiguous()).double(), None)
         a = f("silu", z)
         near(h[rows, cols], a * z, ((1.13 * t + EVAL * (1 + z.abs())) * (z.abs() + t) + a.abs() * t) * (1 + HALF), "h")
+
+
+def test_calls_on_two_streams_at_once_and_in_forked_captures():
+    """A gated forward and a gradient of other weights side by side: on two streams without order
+    between them, and as two branches of one captured graph that join before a third call."""
+    a, b, down = Case("affine4", 1024, 2048, 300, 2), Case("affine8", 768, 1024, 300, 2, seed=4), Case("q4_0", 2048, 1024, 300, 1, seed=8)
+    kw, kb = dict(group_size=a.gs, bits=a.bits), dict(group_size=b.gs, bits=b.bits)
+    x, dh, g, u, r = a.rand(300, 2048), b.rand(300, 768), b.rand(300, 768), b.rand(300, 768), a.rand(300, 2048)
+
+    def one():
+        return bq.quant_matmul_glu(x, *a.mats, save_preact=True, **kw)
+
+    def two():
+        return bq.quant_matmul_glu_backward(dh, g, u, *b.mats, act="gelu", need_dbias=True, **kb)
+
+    def three(h):
+        return bq.quant_matmul_act(h, *down.mats[0], residual=r, act="gelu_tanh")
+
+    want1, want2 = one(), two()
+    want3 = three(want1[0])
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(20):
+        with torch.cuda.stream(s1):
+            got.append((one(), want1))
+        with torch.cuda.stream(s2):
+            got.append((two(), want2))
+    torch.cuda.synchronize()
+    for t, w in got:
+        assert all(torch.equal(p, q) for p, q in zip(t, w))
+    del got
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        main = torch.cuda.current_stream()
+        s2.wait_stream(main)
+        with torch.cuda.stream(s2):
+            t2 = two()
+        t1 = one()
+        main.wait_stream(s2)
+        t3 = three(t1[0])
+    for _ in range(5):
+        for t in (*t1, *t2, t3):
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(p, q) for p, q in zip((*t1, *t2, t3), (*want1, *want2, want3)))
+    assert bq.bq_device_status() == 0
+
+
+FIRST = """
+import sys; sys.path.insert(0, {root!r}); sys.path.insert(0, {tests!r})
+import torch
+import bit_quantized_gemm_quant_b200 as bq
+from test_epilogue_gpu import Case, feed_forward
+torch.cuda.init()
+c, down = Case("affine4", 256, 192, {M}, 2), Case("affine4", 192, 256, {M}, 1, seed=9)
+x, h0 = c.rand({M}, 192), c.rand({M}, 192)
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    outs = feed_forward(c, down, x, h0)
+graph.replay()
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(outs, feed_forward(c, down, x, h0)))
+assert bq.bq_device_status() == 0
+"""
+
+
+@pytest.mark.parametrize("M", [3, 600])
+def test_the_first_calls_of_a_process_may_be_captured(M):
+    tests = os.path.dirname(os.path.abspath(__file__))
+    script = FIRST.format(root=os.path.dirname(tests), tests=tests, M=M)
+    r = subprocess.run([sys.executable, "-c", script], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
+
+
+@pytest.mark.parametrize("fmt,N,K", [("q4_0", 203, 96), ("affine4", 17, 192), ("affine8", 521, 320), ("affine3", 35, 128)])
+def test_nothing_is_written_beside_an_output(fmt, N, K):
+    """Every output between 4 KB of a pattern, which stays; gate and up are halves of one matrix."""
+    P = ctypes.c_void_p
+
+    def between(*shape):
+        n = math.prod(shape)
+        buf = torch.full((n + 4096,), -7.0, dtype=torch.bfloat16, device="cuda")
+        return buf[2048:2048 + n].view(shape), buf
+
+    for M in (1, 7, 16, 17, 300):
+        both = Case(fmt, 8 * N, K, M, 1)
+        wq, s, b = both.mats[0]
+        at = 7 * N // 8 * 8                                    # every eighth row starts on 16 bytes in every array
+        mats = [tuple(None if t is None else t[o:o + N] for t in (wq, s, b)) for o in (0, at)]
+        dense = [both.W[0][o:o + N] for o in (0, at)]
+        kw = dict(group_size=both.gs, bits=both.bits)
+        x, y = both.rand(M, K), both.rand(M, N)
+        outs = []
+        for call, want in ((lambda o: bq.quant_matmul_act(x, *mats[1], act="relu", out=o, **kw), None),
+                           (lambda o: bq.quant_matmul_glu(x, *mats, out=o, **kw), None)):
+            o, buf = between(M, N)
+            assert torch.equal(call(o), call(None))
+            outs.append((o, buf))
+        (g, tg), (u, tu) = (sums(x, w, None) for w in dense)
+        a = f("silu", g)
+        near(outs[1][0], a * u, ((1.13 * tg + EVAL * (1 + g.abs())) * (u.abs() + tu) + a.abs() * tu) * (1 + HALF), "h")
+        (dx, b0), (dg, b1), (du, b2), (db0, b3), (db1, b4) = (between(M, K), between(M, N), between(M, N), between(N), between(N))
+        pair = [None if p[0] is None else (P * 2)(*(t.data_ptr() for t in p)) for p in zip(*mats)]
+        need = bq.quant_matmul_epilogue_workspace_size(bq.OP_GLU_BACKWARD, M, N, K, both.gs, both.bits)
+        ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+        ptr = [t.data_ptr() for t in (dx, dg, du, db0, db1)]
+        st = bq.lib().quant_matmul_glu_backward(y.data_ptr(), y.data_ptr(), y.data_ptr(), *pair, 4, *ptr, M, N, K, both.gs, both.bits,
+                                                ws.data_ptr(), need, torch.cuda.current_stream().cuda_stream)
+        assert st == 0
+        for t, w in zip((dx, dg, du, db0, db1), bq.quant_matmul_glu_backward(y, y, y, *mats, need_dbias=True, **kw)):
+            assert torch.equal(t, w)
+        for t, buf in (*outs, (dx, b0), (dg, b1), (du, b2), (db0, b3), (db1, b4)):
+            assert (buf[:2048] == -7).all() and (buf[2048 + t.numel():] == -7).all(), (M, t.shape)
+    assert bq.bq_device_status() == 0
