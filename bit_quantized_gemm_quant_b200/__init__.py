@@ -8,7 +8,9 @@ Names follow the C ABI: q4_0_dequantize, affine_dequantize, quant_matmul,
 quant_matmul_ex, bf16_matmul, q4_0_quantize, affine_quantize,
 quant_matmul_select_path, quant_matmul_workspace_size, bq_device_status, and the
 products with an epilogue and their gradients: quant_matmul_act,
-quant_matmul_act_backward, quant_matmul_glu, quant_matmul_glu_backward.
+quant_matmul_act_backward, quant_matmul_glu, quant_matmul_glu_backward; microscaled rows and
+their product: mxfp4_quantize, mxfp4_dequantize, mxfp8_quantize, mxfp8_dequantize, mx_matmul,
+mx_matmul_backward; the norm ahead of a product: add_rms_norm, add_rms_norm_backward.
 """
 from __future__ import annotations
 
@@ -67,6 +69,17 @@ def lib() -> ctypes.CDLL:
         "quant_matmul_glu": [P, P, P, P, P, P, I, P, P, P, I64, I64, I64, I, I, P, SZ, P],
         "quant_matmul_glu_backward": [P, P, P, P, P, P, I, P, P, P, P, P, I64, I64, I64, I, I, P, SZ, P],
         "quant_matmul_epilogue_workspace_size": [I, I64, I64, I64, I, I],
+        "mxfp4_quantize": [P, I, P, P, I64, I64, P],
+        "mxfp8_quantize": [P, I, P, P, I64, I64, P],
+        "mxfp4_dequantize": [P, P, P, I64, I64, P],
+        "mxfp8_dequantize": [P, P, P, I64, I64, P],
+        "mx_matmul": [P, P, I, P, P, P, I64, I64, I64, P, SZ, P],
+        "mx_matmul_backward": [P, P, P, P, I64, I64, I64, P, SZ, P],
+        "mx_matmul_workspace_size": [I64, I64, I64, I],
+        "mx_matmul_backward_workspace_size": [I64, I64, I64],
+        "add_rms_norm": [P, P, P, ctypes.c_float, I, P, P, P, P, P, I64, I64, P],
+        "add_rms_norm_backward": [P, P, P, P, P, P, P, I64, I64, P, SZ, P],
+        "add_rms_norm_backward_workspace_size": [I64, I64],
         "q4_0_quantize": [P, P, P, I64, I64, P],
         "affine_quantize": [P, P, P, P, I64, I64, I, I, P],
         "bq_device_status": [],
@@ -80,6 +93,9 @@ def lib() -> ctypes.CDLL:
         fn.restype = I
     L.quant_matmul_workspace_size.restype = SZ
     L.quant_matmul_epilogue_workspace_size.restype = SZ
+    L.mx_matmul_workspace_size.restype = SZ
+    L.mx_matmul_backward_workspace_size.restype = SZ
+    L.add_rms_norm_backward_workspace_size.restype = SZ
     L.bq_status_string.restype = ctypes.c_char_p
     _lib = L
     return L
@@ -431,6 +447,79 @@ def quant_matmul_glu_backward(dh: torch.Tensor, g: torch.Tensor, u: torch.Tensor
     code = _act_code(act)
     with _on(stream, dh, "dh"):
         return _calls().glu_backward(dh, g, u, gate, up, code, group_size, bits, need_dbias)
+
+
+# ------------------------------------------------------------ microscaled rows
+def mxfp4_quantize(x: torch.Tensor, stream=None):
+    """bf16 or fp32 x [M][K] -> (codes u8 [M][K/2], scales float8_e8m0fnu [M][K/32]): blocks of
+    32 in E2M1, two codes per byte, the first one low."""
+    with _on(stream, x, "x"):
+        return _calls().mx_quantize(x, 4)
+
+
+def mxfp8_quantize(x: torch.Tensor, stream=None):
+    """bf16 or fp32 x [M][K] -> (codes float8_e4m3fn [M][K], scales float8_e8m0fnu [M][K/32])."""
+    with _on(stream, x, "x"):
+        return _calls().mx_quantize(x, 8)
+
+
+def mxfp4_dequantize(codes: torch.Tensor, scales: torch.Tensor, out: torch.Tensor | None = None, stream=None):
+    """codes u8 [M][K/2], scales float8_e8m0fnu (or their bytes) [M][K/32] -> bf16 [M][K]."""
+    with _on(stream, codes, "codes"):
+        return _calls().mx_dequantize(codes, scales, out, 4)
+
+
+def mxfp8_dequantize(codes: torch.Tensor, scales: torch.Tensor, out: torch.Tensor | None = None, stream=None):
+    """codes float8_e4m3fn [M][K], scales float8_e8m0fnu (or their bytes) [M][K/32] -> bf16 [M][K]."""
+    with _on(stream, codes, "codes"):
+        return _calls().mx_dequantize(codes, scales, out, 8)
+
+
+def mx_matmul(xq: torch.Tensor, x_scales: torch.Tensor, wq: torch.Tensor, w_scales: torch.Tensor,
+              out: torch.Tensor | None = None, stream=None):
+    """y[M][N] = x . W^T, bf16, for x as mxfp8_quantize (float8_e4m3fn codes) or mxfp4_quantize
+    (u8 codes) gives it and W [N][K] as mxfp4_quantize does.  out shares no memory with an input."""
+    with _on(stream, xq, "xq"):
+        return _calls().mx_matmul(xq, x_scales, wq, w_scales, out)
+
+
+def mx_matmul_backward(dy: torch.Tensor, wq: torch.Tensor, w_scales: torch.Tensor, stream=None):
+    """The gradient of mx_matmul for frozen weights (and of the activations' quantizer by the
+    straight-through estimate): dx [M][K] = dy [M][N] . W, bf16."""
+    with _on(stream, dy, "dy"):
+        return _calls().mx_matmul_backward(dy, wq, w_scales)
+
+
+def mx_matmul_workspace_size(M: int, N: int, K: int, x_bits: int) -> int:
+    """Bytes of workspace of mx_matmul (x_bits 4 or 8), which the binding allocates."""
+    return lib().mx_matmul_workspace_size(M, N, K, x_bits)
+
+
+# ------------------------------------------------------------------------ norm
+NORM_OUTS = {None: 0, "q8_1": 1, "mxfp8": 2, "mxfp4": 3}
+
+
+def add_rms_norm(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor | None = None, eps: float = 1e-5,
+                 quantize: str | None = None, save_rstd: bool = False, h_out: torch.Tensor | None = None, stream=None):
+    """h = x + residual, y = h / sqrt(mean(h^2) + eps) * weight over the rows of bf16 [M][K].
+
+    Returns (y, h), with save_rstd (y, h, rstd fp32 [M]) for add_rms_norm_backward; h is x itself
+    where there is no residual.  y is bf16, or quantized for the product that follows:
+    "q8_1" (xq, dx, qsum) for quant_matmul_q8, "mxfp8" or "mxfp4" (codes, scales) for mx_matmul.
+    h_out: a bf16 [M][K] tensor for h, which may be x or residual itself."""
+    if quantize not in NORM_OUTS:
+        raise ValueError(f"quantize: expected None, 'q8_1', 'mxfp8' or 'mxfp4', got {quantize!r}")
+    with _on(stream, x, "x"):
+        return _calls().add_rms_norm(x, weight, residual, eps, NORM_OUTS[quantize], save_rstd, h_out)
+
+
+def add_rms_norm_backward(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor, rstd: torch.Tensor,
+                          dh: torch.Tensor | None = None, need_dweight: bool = True, stream=None):
+    """The gradients of add_rms_norm from dy (y's; of a quantized y by the straight-through
+    estimate) and dh (what reaches h by another way, as the next residual addition's): (dx,
+    dweight), bf16, dx the gradient of x and of the residual alike; dweight None unless needed."""
+    with _on(stream, dy, "dy"):
+        return _calls().add_rms_norm_backward(dy, h, weight, rstd, dh, need_dweight)
 
 
 # ------------------------------------------------------------------- quantize

@@ -1,5 +1,5 @@
 // binding.cpp -- CPython marshalling of the products with an epilogue and their
-// gradients: argument checks, outputs and workspace from PyTorch's allocator, one call of
+// gradients, and of the microscaled rows, their product and the norm: argument checks, outputs and workspace from PyTorch's allocator, one call of
 // the C ABI on the current stream.
 //
 // A decode call runs 4 to 10 microseconds on the GPU; marshalled through ctypes it took 13
@@ -32,6 +32,10 @@ const Types kBf16Bits = {at::kBFloat16, at::kShort, at::kUInt16};
 const Types kBits16 = {at::kBFloat16, at::kHalf, at::kShort, at::kUInt16};
 const Types kBytes = {at::kByte, at::kChar};
 const Types kWords = {at::kInt, at::kUInt32};
+const Types kCodes8 = {at::kFloat8_e4m3fn};
+const Types kCodes4 = {at::kByte};
+const Types kPowers = {at::kFloat8_e8m0fnu, at::kByte};     // E8M0 values or their bytes
+const Types kFloats = {at::kFloat};
 
 constexpr uintptr_t kEmptyTag = 16;     // non-NULL, aligned, never dereferenced (empty tensor)
 
@@ -102,11 +106,11 @@ struct Call {
 
 // `out` given by the caller and one of the call's inputs: shared memory would be written while
 // other CTAs still read it.
-void apart(const at::Tensor* out, const at::Tensor* in, const char* name)
+void apart(const at::Tensor* out, const at::Tensor* in, const char* name, const char* which = "out")
 {
     if (!out || !in || out->nbytes() == 0 || in->nbytes() == 0) return;
     const char *o = static_cast<const char*>(out->data_ptr()), *i = static_cast<const char*>(in->data_ptr());
-    if (o < i + in->nbytes() && i < o + out->nbytes()) raise(PyExc_ValueError, "out: shares memory with %s%s", name);
+    if (o < i + in->nbytes() && i < o + out->nbytes()) raise(PyExc_ValueError, "%s: shares memory with %s", which, name);
 }
 
 Call on(const at::Tensor& t, const char* name)
@@ -143,7 +147,10 @@ struct Scratch {
     void* ptr = nullptr;
     size_t bytes = 0;
     Scratch(const Call& c, int op, int64_t M, int64_t N, int64_t K, int gs, int bits)
-        : bytes(quant_matmul_epilogue_workspace_size(op, M, N, K, gs, bits))
+        : Scratch(c, quant_matmul_epilogue_workspace_size(op, M, N, K, gs, bits))
+    {
+    }
+    Scratch(const Call& c, size_t need) : bytes(need)
     {
         if (bytes == 0) return;
         keep = c.make({(int64_t)bytes}, at::kByte);
@@ -376,6 +383,185 @@ PyObject* py_glu_backward(PyObject*, PyObject* const* a, Py_ssize_t n)
     });
 }
 
+// ------------------------------------------------------------------ microscaled rows
+PyObject* given_or(PyObject* arg, const at::Tensor* given, const at::Tensor& made)
+{
+    if (!given) return THPVariable_Wrap(made);
+    Py_INCREF(arg);
+    return arg;
+}
+
+// mx_quantize(x, bits) -> (codes, scales)
+PyObject* py_mx_quantize(PyObject*, PyObject* const* a, Py_ssize_t n)
+{
+    return guarded(n, 2, [&] {
+        const at::Tensor& x = needed(a[0], "x");
+        const int bits = integer(a[1]);
+        const Call c = on(x, "x");
+        const int64_t M = x.size(0), K = x.size(1);
+        const c10::cuda::CUDAGuard guard(c.dev);
+        const bool f32 = x.scalar_type() == at::kFloat;
+        const void* xp = c.operand<void>(&x, {at::kBFloat16, at::kFloat, at::kShort, at::kUInt16}, {M, K}, "x");
+        const at::Tensor codes = bits == 8 ? c.make({M, K}, at::kFloat8_e4m3fn) : c.make({M, K / 2}, at::kByte);
+        const at::Tensor scales = c.make({M, K / 32}, at::kFloat8_e8m0fnu);
+        check((bits == 8 ? mxfp8_quantize : mxfp4_quantize)(xp, f32 ? BQ_TYPE_F32 : BQ_TYPE_BF16, address<uint8_t>(codes),
+                                                            address<uint8_t>(scales), M, K, c.stream()),
+              bits == 8 ? "mxfp8_quantize" : "mxfp4_quantize");
+        return wrap({&codes, &scales});
+    });
+}
+
+// mx_dequantize(codes, scales, out, bits)
+PyObject* py_mx_dequantize(PyObject*, PyObject* const* a, Py_ssize_t n)
+{
+    return guarded(n, 4, [&] {
+        const at::Tensor &codes = needed(a[0], "codes"), &scales = needed(a[1], "scales");
+        const at::Tensor* given = tensor(a[2], "out");
+        const int bits = integer(a[3]);
+        const Call c = on(codes, "codes");
+        const int64_t M = codes.size(0), K = codes.size(1) * (bits == 8 ? 1 : 2);
+        const c10::cuda::CUDAGuard guard(c.dev);
+        const uint8_t* cp = c.operand<uint8_t>(&codes, bits == 8 ? kCodes8 : kCodes4, {M, codes.size(1)}, "codes");
+        const uint8_t* sp = c.operand<uint8_t>(&scales, kPowers, {M, K / 32}, "scales");
+        uint16_t* gp = c.operand(given, kBf16Bits, {M, K}, "out");
+        apart(given, &codes, "codes");
+        apart(given, &scales, "scales");
+        const at::Tensor out = given ? *given : c.make({M, K});
+        check((bits == 8 ? mxfp8_dequantize : mxfp4_dequantize)(cp, sp, given ? gp : address<uint16_t>(out), M, K, c.stream()),
+              bits == 8 ? "mxfp8_dequantize" : "mxfp4_dequantize");
+        return given_or(a[2], given, out);
+    });
+}
+
+// mx_matmul(xq, x_scales, wq, w_scales, out)
+PyObject* py_mx_matmul(PyObject*, PyObject* const* a, Py_ssize_t n)
+{
+    return guarded(n, 5, [&] {
+        const at::Tensor &xq = needed(a[0], "xq"), &xs = needed(a[1], "x_scales"), &wq = needed(a[2], "wq"),
+                         &ws = needed(a[3], "w_scales");
+        const at::Tensor* given = tensor(a[4], "out");
+        const Call c = on(xq, "xq");
+        const int x_bits = xq.scalar_type() == at::kByte ? 4 : 8;
+        const int64_t M = xq.size(0), K = xq.size(1) * (8 / x_bits), N = wq.dim() == 2 ? wq.size(0) : 0;
+        const c10::cuda::CUDAGuard guard(c.dev);
+        const void* xp = c.operand<void>(&xq, {at::kFloat8_e4m3fn, at::kByte}, {M, xq.size(1)}, "xq");
+        const uint8_t* xsp = c.operand<uint8_t>(&xs, kPowers, {M, K / 32}, "x_scales");
+        const uint8_t* wp = c.operand<uint8_t>(&wq, kCodes4, {N, K / 2}, "wq");
+        const uint8_t* wsp = c.operand<uint8_t>(&ws, kPowers, {N, K / 32}, "w_scales");
+        uint16_t* gp = c.operand(given, kBf16Bits, {M, N}, "out");
+        apart(given, &xq, "xq");
+        apart(given, &xs, "x_scales");
+        apart(given, &wq, "wq");
+        apart(given, &ws, "w_scales");
+        const at::Tensor y = given ? *given : c.make({M, N});
+        const Scratch s(c, mx_matmul_workspace_size(M, N, K, x_bits));
+        check(mx_matmul(xp, xsp, x_bits, wp, wsp, given ? gp : address<uint16_t>(y), M, N, K, s.ptr, s.bytes, c.stream()),
+              "mx_matmul");
+        return given_or(a[4], given, y);
+    });
+}
+
+// mx_matmul_backward(dy, wq, w_scales)
+PyObject* py_mx_matmul_backward(PyObject*, PyObject* const* a, Py_ssize_t n)
+{
+    return guarded(n, 3, [&] {
+        const at::Tensor &dy = needed(a[0], "dy"), &wq = needed(a[1], "wq"), &ws = needed(a[2], "w_scales");
+        const Call c = on(dy, "dy");
+        const int64_t M = dy.size(0), N = dy.size(1), K = wq.dim() == 2 ? wq.size(1) * 2 : 0;
+        const c10::cuda::CUDAGuard guard(c.dev);
+        const uint16_t* dyp = c.operand(&dy, kBf16Bits, {M, N}, "dy");
+        const uint8_t* wp = c.operand<uint8_t>(&wq, kCodes4, {N, K / 2}, "wq");
+        const uint8_t* wsp = c.operand<uint8_t>(&ws, kPowers, {N, K / 32}, "w_scales");
+        const at::Tensor dx = c.make({M, K});
+        const Scratch s(c, mx_matmul_backward_workspace_size(M, N, K));
+        check(mx_matmul_backward(dyp, wp, wsp, address<uint16_t>(dx), M, N, K, s.ptr, s.bytes, c.stream()),
+              "mx_matmul_backward");
+        return THPVariable_Wrap(dx);
+    });
+}
+
+// ------------------------------------------------------------------ norm
+// add_rms_norm(x, weight, residual, eps, out, save_rstd, h_out) -> (y, h[, rstd]), y a tuple
+// when it is quantized
+PyObject* py_add_rms_norm(PyObject*, PyObject* const* a, Py_ssize_t n)
+{
+    return guarded(n, 7, [&]() -> PyObject* {
+        const at::Tensor &x = needed(a[0], "x"), &w = needed(a[1], "weight");
+        const at::Tensor *res = tensor(a[2], "residual"), *given = tensor(a[6], "h_out");
+        const double eps = PyFloat_AsDouble(a[3]);
+        if (eps == -1.0 && PyErr_Occurred()) throw Raised{};
+        const int out = integer(a[4]);
+        const bool save = truth(a[5]);
+        const Call c = on(x, "x");
+        const int64_t M = x.size(0), K = x.size(1);
+        const c10::cuda::CUDAGuard guard(c.dev);
+        const uint16_t* xp = c.operand(&x, kBf16Bits, {M, K}, "x");
+        const uint16_t* wp = c.operand(&w, kBf16Bits, {K}, "weight");
+        const uint16_t* rp = c.operand(res, kBf16Bits, {M, K}, "residual");
+        uint16_t* hp = c.operand(given, kBf16Bits, {M, K}, "h_out");
+        if (hp != xp) apart(given, &x, "x", "h_out");          // x or residual itself: each element is read, then written
+        if (rp != hp) apart(given, res, "residual", "h_out");
+        apart(given, &w, "weight", "h_out");
+        at::Tensor y, scales, qsum;
+        if (out == BQ_NORM_BF16) {
+            y = c.make({M, K});
+        } else if (out == BQ_NORM_Q8_1) {
+            y = c.make({M, K}, at::kChar);
+            scales = c.make({M, K / 32}, at::kFloat);
+            qsum = c.make({M, K / 32}, at::kInt);
+        } else {
+            y = out == BQ_NORM_MXFP8 ? c.make({M, K}, at::kFloat8_e4m3fn) : c.make({M, K / 2}, at::kByte);
+            scales = c.make({M, K / 32}, at::kFloat8_e8m0fnu);
+        }
+        const bool new_h = res && !given;
+        const at::Tensor h = new_h ? c.make({M, K}) : at::Tensor(), rstd = save ? c.make({M}, at::kFloat) : at::Tensor();
+        check(add_rms_norm(xp, rp, wp, (float)eps, out, address(y), scales.defined() ? address(scales) : nullptr,
+                           qsum.defined() ? address<int32_t>(qsum) : nullptr,
+                           new_h ? address<uint16_t>(h) : given ? hp : nullptr, save ? address<float>(rstd) : nullptr, M, K,
+                           c.stream()),
+              "add_rms_norm");
+        PyObject* result = PyTuple_New(save ? 3 : 2);
+        if (!result) return nullptr;
+        PyObject* py = qsum.defined() ? wrap({&y, &scales, &qsum}) : scales.defined() ? wrap({&y, &scales}) : THPVariable_Wrap(y);
+        PyTuple_SET_ITEM(result, 0, py);
+        PyObject* ph = new_h ? THPVariable_Wrap(h) : given ? a[6] : a[0];
+        if (!new_h) Py_INCREF(ph);
+        PyTuple_SET_ITEM(result, 1, ph);
+        if (save) PyTuple_SET_ITEM(result, 2, THPVariable_Wrap(rstd));
+        return result;
+    });
+}
+
+// add_rms_norm_backward(dy, h, weight, rstd, dh, need_dweight) -> (dx, dweight | None)
+PyObject* py_add_rms_norm_backward(PyObject*, PyObject* const* a, Py_ssize_t n)
+{
+    return guarded(n, 6, [&]() -> PyObject* {
+        const at::Tensor &dy = needed(a[0], "dy"), &h = needed(a[1], "h"), &w = needed(a[2], "weight"),
+                         &rstd = needed(a[3], "rstd");
+        const at::Tensor* dh = tensor(a[4], "dh");
+        const bool need = truth(a[5]);
+        const Call c = on(dy, "dy");
+        const int64_t M = dy.size(0), K = dy.size(1);
+        const c10::cuda::CUDAGuard guard(c.dev);
+        const uint16_t* dyp = c.operand(&dy, kBf16Bits, {M, K}, "dy");
+        const uint16_t* hp = c.operand(&h, kBf16Bits, {M, K}, "h");
+        const uint16_t* wp = c.operand(&w, kBf16Bits, {K}, "weight");
+        const float* rp = c.operand<float>(&rstd, kFloats, {M}, "rstd");
+        const uint16_t* dhp = c.operand(dh, kBf16Bits, {M, K}, "dh");
+        const at::Tensor dx = c.make({M, K}), dw = need ? c.make({K}) : at::Tensor();
+        const Scratch s(c, need ? add_rms_norm_backward_workspace_size(M, K) : 0);
+        check(add_rms_norm_backward(dyp, hp, wp, rp, dhp, address<uint16_t>(dx), need ? address<uint16_t>(dw) : nullptr, M, K,
+                                    s.ptr, s.bytes, c.stream()),
+              "add_rms_norm_backward");
+        PyObject* result = PyTuple_New(2);
+        if (!result) return nullptr;
+        PyTuple_SET_ITEM(result, 0, THPVariable_Wrap(dx));
+        if (!need) Py_INCREF(Py_None);
+        PyTuple_SET_ITEM(result, 1, need ? THPVariable_Wrap(dw) : Py_None);
+        return result;
+    });
+}
+
 PyObject* py_set_error(PyObject*, PyObject* type)
 {
     Py_INCREF(type);
@@ -389,6 +575,12 @@ PyMethodDef kMethods[] = {
     {"act_backward", BQ_FAST(py_act_backward), METH_FASTCALL, nullptr},
     {"glu", BQ_FAST(py_glu), METH_FASTCALL, nullptr},
     {"glu_backward", BQ_FAST(py_glu_backward), METH_FASTCALL, nullptr},
+    {"mx_quantize", BQ_FAST(py_mx_quantize), METH_FASTCALL, nullptr},
+    {"mx_dequantize", BQ_FAST(py_mx_dequantize), METH_FASTCALL, nullptr},
+    {"mx_matmul", BQ_FAST(py_mx_matmul), METH_FASTCALL, nullptr},
+    {"mx_matmul_backward", BQ_FAST(py_mx_matmul_backward), METH_FASTCALL, nullptr},
+    {"add_rms_norm", BQ_FAST(py_add_rms_norm), METH_FASTCALL, nullptr},
+    {"add_rms_norm_backward", BQ_FAST(py_add_rms_norm_backward), METH_FASTCALL, nullptr},
     {"set_error", py_set_error, METH_O, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };

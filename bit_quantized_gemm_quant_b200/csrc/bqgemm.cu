@@ -8,6 +8,7 @@
 #include <type_traits>
 #include <cstdlib>
 #include <cstring>
+#include <initializer_list>
 #include <map>
 #include <mutex>
 #include <vector>
@@ -23,6 +24,8 @@
 #include "tc_pair.cuh"
 #include "tc_fused_pair.cuh"
 #include "gemv_ring.cuh"
+#include "mx.cuh"
+#include "norm.cuh"
 
 namespace bq {
 namespace {
@@ -1298,6 +1301,7 @@ bq_status noalloc_scratch(void** out)
 }  // namespace bq
 
 #include "epi_host.cuh"
+#include "mx_host.cuh"
 
 using namespace bq;
 
@@ -1662,6 +1666,133 @@ size_t quant_matmul_epilogue_workspace_size(int op, int64_t M, int64_t N, int64_
     return plan_backward(fmt, mats, M, N, K, num_sms, smem_optin, &ws) ? ws.bytes : 0;
 }
 
+bq_status mxfp4_quantize(const void* x, int x_type, uint8_t* codes, uint8_t* scales, int64_t M, int64_t K,
+                         bq_stream_t stream)
+{
+    return mx_quantize<4>(x, x_type, codes, scales, M, K, (cudaStream_t)stream);
+}
+
+bq_status mxfp8_quantize(const void* x, int x_type, uint8_t* codes, uint8_t* scales, int64_t M, int64_t K,
+                         bq_stream_t stream)
+{
+    return mx_quantize<8>(x, x_type, codes, scales, M, K, (cudaStream_t)stream);
+}
+
+bq_status mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales, uint16_t* out_bf16, int64_t M, int64_t K,
+                           bq_stream_t stream)
+{
+    return mx_dequantize<4>(codes, scales, out_bf16, M, K, (cudaStream_t)stream);
+}
+
+bq_status mxfp8_dequantize(const uint8_t* codes, const uint8_t* scales, uint16_t* out_bf16, int64_t M, int64_t K,
+                           bq_stream_t stream)
+{
+    return mx_dequantize<8>(codes, scales, out_bf16, M, K, (cudaStream_t)stream);
+}
+
+bq_status mx_matmul(const void* xq, const uint8_t* x_scales, int x_bits, const uint8_t* wq, const uint8_t* w_scales,
+                    uint16_t* y_bf16, int64_t M, int64_t N, int64_t K, void* workspace, size_t workspace_bytes,
+                    bq_stream_t stream)
+{
+    return mx_product(xq, x_scales, x_bits, wq, w_scales, y_bf16, M, N, K, workspace, workspace_bytes,
+                      (cudaStream_t)stream);
+}
+
+bq_status mx_matmul_backward(const uint16_t* dy_bf16, const uint8_t* wq, const uint8_t* w_scales, uint16_t* dx_bf16,
+                             int64_t M, int64_t N, int64_t K, void* workspace, size_t workspace_bytes,
+                             bq_stream_t stream)
+{
+    return mx_gradient(dy_bf16, wq, w_scales, dx_bf16, M, N, K, workspace, workspace_bytes, (cudaStream_t)stream);
+}
+
+size_t mx_matmul_workspace_size(int64_t M, int64_t N, int64_t K, int x_bits)
+{
+    if (M <= 0 || N <= 0 || K <= 0 || K % 32 != 0 || !sizes_ok(M, N, K) || (x_bits != 4 && x_bits != 8)) return 0;
+    int num_sms, smem;
+    device_or_b200(&num_sms, &smem);
+    MxWs w;
+    return plan_mx(M, N, K, num_sms, smem, &w) ? w.bytes : 0;
+}
+
+size_t mx_matmul_backward_workspace_size(int64_t M, int64_t N, int64_t K)
+{
+    if (M <= 0 || N <= 0 || K <= 0 || K % 32 != 0 || !sizes_ok(M, N, K)) return 0;
+    int num_sms, smem;
+    device_or_b200(&num_sms, &smem);
+    MxGradWs w;
+    return plan_mx_grad(M, N, K, num_sms, smem, &w) ? w.bytes : 0;
+}
+
+bq_status add_rms_norm(const uint16_t* x_bf16, const uint16_t* residual, const uint16_t* weight, float eps, int out,
+                       void* y, void* scales, int32_t* qsum, uint16_t* h_bf16, float* rstd, int64_t M, int64_t K,
+                       bq_stream_t stream)
+{
+    if (!norm_sizes_ok(M, K)) return BQ_ERR_SHAPE;
+    if (out < BQ_NORM_BF16 || out > BQ_NORM_MXFP4 || !(eps >= 0.0f) || eps > 3.4028234e38f) return BQ_ERR_UNSUPPORTED;
+    if (out != BQ_NORM_BF16 && K % 32 != 0) return BQ_ERR_SHAPE;
+    if (M == 0 || K == 0) return BQ_OK;
+    if (!x_bf16 || !weight || !y || (out != BQ_NORM_BF16 && !scales) || (out == BQ_NORM_Q8_1 && !qsum)) return BQ_ERR_NULL;
+    if (!all_aligned16({x_bf16, residual, weight, y, scales, qsum, h_bf16, rstd})) return BQ_ERR_ALIGN;
+    int dev;
+    DeviceInfo di;
+    bq_status s = current_device(&dev, &di);
+    if (s != BQ_OK) return s;
+    NormParams p;
+    p.x = x_bf16;
+    p.res = residual;
+    p.w = weight;
+    p.h = h_bf16;
+    p.y = y;
+    p.scales = scales;
+    p.qsum = qsum;
+    p.rstd = rstd;
+    p.inv_k = 1.0 / (double)K;
+    p.eps = eps;
+    p.M = M;
+    p.K = (int)K;
+    return norm_forward(p, out, (cudaStream_t)stream);
+}
+
+bq_status add_rms_norm_backward(const uint16_t* dy_bf16, const uint16_t* h_bf16, const uint16_t* weight,
+                                const float* rstd, const uint16_t* dh_bf16, uint16_t* dx_bf16, uint16_t* dweight_bf16,
+                                int64_t M, int64_t K, void* workspace, size_t workspace_bytes, bq_stream_t stream)
+{
+    if (!norm_sizes_ok(M, K)) return BQ_ERR_SHAPE;
+    if (K == 0 || (M == 0 && !dweight_bf16)) return BQ_OK;
+    if (!all_aligned16({dy_bf16, h_bf16, weight, rstd, dh_bf16, dx_bf16, dweight_bf16, workspace})) return BQ_ERR_ALIGN;
+    if (M > 0 && (!dy_bf16 || !h_bf16 || !weight || !rstd || !dx_bf16)) return BQ_ERR_NULL;
+    int dev;
+    DeviceInfo di;
+    bq_status s = current_device(&dev, &di);
+    if (s != BQ_OK) return s;
+    cudaStream_t st = (cudaStream_t)stream;
+    if (M == 0)                                          // a sum over no tokens
+        return cudaMemsetAsync(dweight_bf16, 0, (size_t)K * 2u, st) == cudaSuccess ? BQ_OK : BQ_ERR_CUDA;
+    const NormGradPlan pl = plan_norm_grad(M, K, di.num_sms);
+    void* buf = nullptr;
+    if (dweight_bf16 && (s = epi_workspace(dev, st, workspace, workspace_bytes, pl.bytes, &buf)) != BQ_OK) return s;
+    NormGradParams p;
+    p.dy = dy_bf16;
+    p.h = h_bf16;
+    p.w = weight;
+    p.rstd = rstd;
+    p.dh = dh_bf16;
+    p.dx = dx_bf16;
+    p.part = reinterpret_cast<float*>(buf);
+    p.inv_k = (float)(1.0 / (double)K);
+    p.M = M;
+    p.K = (int)K;
+    return norm_backward(pl, p, dweight_bf16, st);
+}
+
+size_t add_rms_norm_backward_workspace_size(int64_t M, int64_t K)
+{
+    if (M <= 0 || K <= 0 || !norm_sizes_ok(M, K)) return 0;
+    int num_sms, smem;
+    device_or_b200(&num_sms, &smem);
+    return plan_norm_grad(M, K, num_sms).bytes;
+}
+
 bq_status q4_0_quantize(const float* w, uint8_t* wq, uint16_t* scales_f16, int64_t N, int64_t K, bq_stream_t stream)
 {
     if (N < 0 || K < 0 || K % 32 != 0) return BQ_ERR_SHAPE;
@@ -1759,6 +1890,6 @@ const char* bq_status_string(int status)
     }
 }
 
-int bq_version(void) { return 101; }
+int bq_version(void) { return 102; }
 
 }  // extern "C"

@@ -1,0 +1,197 @@
+// mx.cuh -- microscaled (MX) rows: conversions, quantizers and dequantizers.
+//
+// The formats are those of the OCP Microscaling Formats specification v1.0: blocks of 32
+// consecutive elements of a row share a power of two X = 2^(byte - 127) (E8M0; byte 255 is
+// NaN), and an element stands for X times its value in a small type:
+//   MXFP8  E4M3: 1 sign, 4 exponent, 3 mantissa bits, largest value 448, no infinity
+//   MXFP4  E2M1: 0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives; two per byte, the first low
+// The quantizers follow its section 6.3: X = 2^(floor(log2(amax)) - emax) with amax the
+// block's largest magnitude and emax that of the type's largest power of two (8; 2), each
+// element rounded to nearest, ties to even, and saturated.  What the specification leaves
+// open: X is at least 2^-127 (so a block of zeros has byte 0), and a block that holds a NaN or an infinity
+// becomes NaN as a whole (byte 255, codes 0): neither type could hold it element by element.
+#pragma once
+
+#include "common.cuh"
+
+namespace bq {
+
+constexpr uint32_t kMxNan = 255;
+
+// Largest power of two of the element type, by its bits.
+template <int BITS>
+__host__ __device__ constexpr uint32_t mx_emax() { return BITS == 8 ? 8u : 2u; }
+
+// The scale's byte from the bit pattern of amax (sign off).  The exponent field of a finite
+// fp32 is floor(log2) + 127; of a subnormal one it is 0, where the floor at 2^-127 holds anyway.
+template <int BITS>
+BQ_DEVINL uint32_t mx_scale_byte(uint32_t amax_bits)
+{
+    const uint32_t e = amax_bits >> 23;
+    return e == 255u ? kMxNan : e > mx_emax<BITS>() ? e - mx_emax<BITS>() : 0u;
+}
+
+// 1 / X, 0 for a NaN scale.  Multiplying by it is exact (but for results below 2^-126, which
+// round to the type's 0 either way).
+BQ_DEVINL float mx_inverse(uint32_t byte) { return byte == kMxNan ? 0.0f : __uint_as_float((254u - byte) << 23); }
+
+// X itself, as fp32 and as bf16 bits (exact: 2^-127 is subnormal in both).
+BQ_DEVINL float mx_scale(uint32_t byte)
+{
+    return byte == kMxNan ? __uint_as_float(0x7FC00000u) : byte == 0 ? __uint_as_float(0x00400000u) : __uint_as_float(byte << 23);
+}
+BQ_DEVINL uint32_t mx_scale_bf16(uint32_t byte) { return byte == kMxNan ? 0x7FC0u : byte == 0 ? 0x0040u : byte << 7; }
+
+// Four values to E4M3 (first in the low byte), eight to E2M1 (first in the low nibble): to
+// nearest even, saturated.
+BQ_DEVINL uint32_t to_e4m3x4(float a, float b, float c, float d)
+{
+    uint32_t r;
+    asm("{\n\t.reg .b16 lo, hi;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f32 lo, %2, %1;\n\tcvt.rn.satfinite.e4m3x2.f32 hi, %4, %3;\n\t"
+        "mov.b32 %0, {lo, hi};\n\t}" : "=r"(r) : "f"(a), "f"(b), "f"(c), "f"(d));
+    return r;
+}
+
+BQ_DEVINL uint32_t to_e2m1x8(const float (&v)[8])
+{
+    uint32_t r;
+    asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\tcvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+        "mov.b32 %0, {a, b, c, d};\n\t}"
+        : "=r"(r) : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
+    return r;
+}
+
+// Eight E2M1 codes to bf16 pairs (unscaled, exact).  A magnitude's two bytes are looked up
+// by byte permutes, whose selector is the code without its sign.
+BQ_DEVINL void e2m1x8_to_bf16(uint32_t w, uint32_t (&out)[4])
+{
+    const uint32_t m = w & 0x77777777u;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const uint32_t sel = h ? m >> 16 : m;                                // four codes (the permute reads 16 bits)
+        const uint32_t lo = prmt(0xC0800000u, 0xC0804000u, sel);             // low bytes of 0 .5 1 1.5 | 2 3 4 6
+        const uint32_t hi = prmt(0x3F3F3F00u, 0x40404040u, sel);             // high bytes
+        const uint32_t s = h ? w >> 16 : w;
+        out[2 * h] = prmt(lo, hi, 0x5140u) | ((s << 12) & 0x00008000u) | ((s << 24) & 0x80000000u);
+        out[2 * h + 1] = prmt(lo, hi, 0x7362u) | ((s << 4) & 0x00008000u) | ((s << 16) & 0x80000000u);
+    }
+}
+
+// Two E4M3 codes to fp32 (exact).
+BQ_DEVINL void e4m3x2_to_f32(uint32_t w, float& a, float& b)
+{
+    uint32_t h;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)w));
+    const __half2 v = *reinterpret_cast<__half2*>(&h);
+    a = __low2float(v);
+    b = __high2float(v);
+}
+
+// The largest magnitude, as bits, of 8 values in each of 4 consecutive lanes (a block of
+// 32).  As bits, so that a NaN counts as larger than all else.
+BQ_DEVINL uint32_t block_amax_bits(const float (&v)[8])
+{
+    uint32_t a = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) a = max(a, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+    a = max(a, __shfl_xor_sync(0xFFFFFFFFu, a, 1));
+    return max(a, __shfl_xor_sync(0xFFFFFFFFu, a, 2));
+}
+
+// 8 of the values of a block, whose other 24 are in the lanes' neighbours, to codes at
+// element `at` (a multiple of 8) of the codes, and the block's scale.  `live`: this lane's values exist
+// (all lanes of the warp come here).
+template <int BITS>
+BQ_DEVINL void mx_store8(const float (&v)[8], uint8_t* __restrict__ codes, uint8_t* __restrict__ scales, int64_t at, bool live)
+{
+    const uint32_t byte = mx_scale_byte<BITS>(block_amax_bits(v));
+    const float inv = mx_inverse(byte);
+    float t[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) t[i] = byte == kMxNan ? 0.0f : __fmul_rn(v[i], inv);
+    if (!live) return;
+    if constexpr (BITS == 8)
+        *reinterpret_cast<uint2*>(codes + at) = make_uint2(to_e4m3x4(t[0], t[1], t[2], t[3]), to_e4m3x4(t[4], t[5], t[6], t[7]));
+    else
+        *reinterpret_cast<uint32_t*>(codes + at / 2) = to_e2m1x8(t);
+    if ((at & 31) == 0) scales[at >> 5] = (uint8_t)byte;
+}
+
+// 8 consecutive elements as fp32.
+template <bool F32>
+BQ_DEVINL void load8(const void* x, int64_t at, float (&v)[8])
+{
+    if constexpr (F32) {
+        const float* p = reinterpret_cast<const float*>(x) + at;
+        const uint4 a = ldg_stream(p), b = ldg_stream(p + 4);
+        v[0] = __uint_as_float(a.x); v[1] = __uint_as_float(a.y); v[2] = __uint_as_float(a.z); v[3] = __uint_as_float(a.w);
+        v[4] = __uint_as_float(b.x); v[5] = __uint_as_float(b.y); v[6] = __uint_as_float(b.z); v[7] = __uint_as_float(b.w);
+    } else {
+        const uint4 a = ldg_stream(reinterpret_cast<const uint16_t*>(x) + at);
+        const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[2 * i] = __uint_as_float(w[i] << 16);
+            v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+        }
+    }
+}
+
+// ------------------------------------------------------------------ quantize
+// A thread takes 8 elements, 4 threads a block.  Rows are whole blocks, so the matrix is one
+// run of `n` elements (a multiple of 32).  Bound by HBM.
+template <int BITS, bool F32>
+__global__ void __launch_bounds__(256)
+mx_quantize_kernel(const void* __restrict__ x, uint8_t* __restrict__ codes, uint8_t* __restrict__ scales, int64_t n)
+{
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int64_t step = (int64_t)gridDim.x * 2048;
+    for (int64_t base = (int64_t)blockIdx.x * 2048; base < n; base += step) {
+        const int64_t at = base + threadIdx.x * 8;
+        float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        if (at < n) load8<F32>(x, at, v);
+        mx_store8<BITS>(v, codes, scales, at, at < n);
+    }
+}
+
+// ------------------------------------------------------------------ dequantize
+// out = bf16_rne(X * element): exact unless it leaves bf16's range (beyond it infinity, below 2^-133 to
+// nearest even; a NaN scale gives NaN).  A thread takes 8 elements.  Bound by HBM, mostly by the writes.
+template <int BITS>
+BQ_DEVINL uint4 mx_dequant8(const uint8_t* __restrict__ codes, uint32_t byte, int64_t at)
+{
+    uint32_t o[4];
+    if constexpr (BITS == 4) {
+        const uint32_t s = mx_scale_bf16(byte) * 0x10001u;
+        e2m1x8_to_bf16(__ldg(reinterpret_cast<const uint32_t*>(codes) + (at >> 3)), o);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[i] = hmul2_bf16(o[i], s);
+    } else {
+        const uint2 w = __ldg(reinterpret_cast<const uint2*>(codes) + (at >> 3));
+        const float s = mx_scale(byte);
+        float v[8];
+        e4m3x2_to_f32(w.x, v[0], v[1]);
+        e4m3x2_to_f32(w.x >> 16, v[2], v[3]);
+        e4m3x2_to_f32(w.y, v[4], v[5]);
+        e4m3x2_to_f32(w.y >> 16, v[6], v[7]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[i] = pack_bf16x2_rn(__fmul_rn(v[2 * i], s), __fmul_rn(v[2 * i + 1], s));
+    }
+    return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+template <int BITS>
+__global__ void __launch_bounds__(256)
+mx_dequant_kernel(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales, uint16_t* __restrict__ out, int64_t n8)
+{
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    for (int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; i < n8; i += (int64_t)gridDim.x * blockDim.x)
+        reinterpret_cast<uint4*>(out)[i] = mx_dequant8<BITS>(codes, scales[i >> 2], 8 * i);
+}
+
+}  // namespace bq

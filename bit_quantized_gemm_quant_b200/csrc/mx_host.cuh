@@ -1,0 +1,247 @@
+// mx_host.cuh -- host side of the microscaled formats, their product and its gradient, and
+// of the root-mean-square norm: argument checks, plans, workspaces and launches.  Included
+// by bqgemm.cu, after the helpers it uses.
+#pragma once
+
+namespace bq {
+namespace {
+
+bool all_aligned16(std::initializer_list<const void*> ps)
+{
+    for (const void* q : ps)
+        if (!aligned16(q)) return false;
+    return true;
+}
+
+// ------------------------------------------------------------------ quantize, dequantize
+template <int BITS>
+bq_status mx_quantize(const void* x, int x_type, uint8_t* codes, uint8_t* scales, int64_t M, int64_t K, cudaStream_t st)
+{
+    if (M < 0 || K < 0 || K % 32 != 0) return BQ_ERR_SHAPE;
+    if (x_type != BQ_TYPE_BF16 && x_type != BQ_TYPE_F32) return BQ_ERR_UNSUPPORTED;
+    if (M == 0 || K == 0) return BQ_OK;
+    if (M > INT64_MAX / 8 / K) return BQ_ERR_SHAPE;
+    if (!x || !codes || !scales) return BQ_ERR_NULL;
+    if (!all_aligned16({x, codes, scales})) return BQ_ERR_ALIGN;
+    int dev;
+    DeviceInfo di;
+    bq_status s = current_device(&dev, &di);
+    if (s != BQ_OK) return s;
+    const int64_t n = M * K;
+    const int grid = grid_for(n / 8, 256, di);
+    return x_type == BQ_TYPE_F32 ? launch_pdl(mx_quantize_kernel<BITS, true>, grid, 256, 0, st, x, codes, scales, n)
+                                 : launch_pdl(mx_quantize_kernel<BITS, false>, grid, 256, 0, st, x, codes, scales, n);
+}
+
+template <int BITS>
+bq_status launch_mx_dequant(const uint8_t* codes, const uint8_t* scales, uint16_t* out, int64_t n, const DeviceInfo& di,
+                            cudaStream_t st)
+{
+    return launch_pdl(mx_dequant_kernel<BITS>, grid_for(n / 8, 256, di), 256, 0, st, codes, scales, out, n / 8);
+}
+
+template <int BITS>
+bq_status mx_dequantize(const uint8_t* codes, const uint8_t* scales, uint16_t* out, int64_t M, int64_t K, cudaStream_t st)
+{
+    if (M < 0 || K < 0 || K % 32 != 0) return BQ_ERR_SHAPE;
+    if (M == 0 || K == 0) return BQ_OK;
+    if (M > INT64_MAX / 8 / K) return BQ_ERR_SHAPE;
+    if (!codes || !scales || !out) return BQ_ERR_NULL;
+    if (!all_aligned16({codes, scales, out})) return BQ_ERR_ALIGN;
+    int dev;
+    DeviceInfo di;
+    bq_status s = current_device(&dev, &di);
+    return s != BQ_OK ? s : launch_mx_dequant<BITS>(codes, scales, out, M * K, di, st);
+}
+
+// ------------------------------------------------------------------ product
+// The bf16 pair's workspace: W, then x, then the product's partial sums.
+struct MxWs {
+    PairPlan pl;
+    size_t off_x = 0, off_split = 0, bytes = 0;
+};
+
+bool plan_mx(int64_t M, int64_t N, int64_t K, int num_sms, int smem_optin, MxWs* w)
+{
+    if (!plan_pair(N, M, (K + 63) / 64, num_sms, smem_optin, 0, (int)kPairABytes, 64, PairCost{300.0, 1.5, 0.0, 1}, &w->pl))
+        return false;
+    w->off_x = up256((size_t)N * (size_t)K * 2u);
+    w->off_split = w->off_x + up256((size_t)M * (size_t)K * 2u);
+    w->bytes = w->off_split + w->pl.ws_bytes;
+    return true;
+}
+
+bq_status mx_product(const void* xq, const uint8_t* xs, int x_bits, const uint8_t* wq, const uint8_t* ws, uint16_t* y,
+                     int64_t M, int64_t N, int64_t K, void* workspace, size_t workspace_bytes, cudaStream_t st)
+{
+    if (M < 0 || N < 0 || K < 0 || K % 32 != 0 || !sizes_ok(M, N, K)) return BQ_ERR_SHAPE;
+    if (x_bits != 4 && x_bits != 8) return BQ_ERR_UNSUPPORTED;
+    if (M == 0 || N == 0) return BQ_OK;
+    if (!y || (K > 0 && (!xq || !xs || !wq || !ws))) return BQ_ERR_NULL;
+    if (!all_aligned16({y, workspace}) || (K > 0 && !all_aligned16({xq, xs, wq, ws}))) return BQ_ERR_ALIGN;
+    int dev;
+    DeviceInfo di;
+    bq_status s = current_device(&dev, &di);
+    if (s != BQ_OK) return s;
+    if (K == 0)
+        return cudaMemsetAsync(y, 0, (size_t)M * (size_t)N * 2u, st) == cudaSuccess ? BQ_OK : BQ_ERR_CUDA;
+    MxWs w;
+    if (!plan_mx(M, N, K, di.num_sms, di.max_smem_optin, &w)) return BQ_ERR_SHAPE;
+    void* buf = nullptr;
+    if ((s = epi_workspace(dev, st, workspace, workspace_bytes, w.bytes, &buf)) != BQ_OK) return s;
+    uint8_t* base = reinterpret_cast<uint8_t*>(buf);
+    uint16_t *wb = reinterpret_cast<uint16_t*>(base), *xb = reinterpret_cast<uint16_t*>(base + w.off_x);
+    if ((s = launch_mx_dequant<4>(wq, ws, wb, N * K, di, st)) != BQ_OK) return s;
+    s = x_bits == 8 ? launch_mx_dequant<8>(reinterpret_cast<const uint8_t*>(xq), xs, xb, M * K, di, st)
+                    : launch_mx_dequant<4>(reinterpret_cast<const uint8_t*>(xq), xs, xb, M * K, di, st);
+    if (s != BQ_OK) return s;
+    EpiParams e;
+    e.y = y;
+    return launch_pair<false, kEpiPlain>(di, dev, w.pl, &wb, &xb, 1, N, N, M, K, K, e, base + w.off_split, st);
+}
+
+// ------------------------------------------------------------------ its gradient
+// Workspace: the bf16 weights, dy with rows of whole 16 bytes where N % 8 != 0, partial sums.
+struct MxGradWs {
+    PairPlan pl;
+    int64_t pitch = 0;
+    size_t off_pad = 0, off_split = 0, bytes = 0;
+};
+
+bool plan_mx_grad(int64_t M, int64_t N, int64_t K, int num_sms, int smem_optin, MxGradWs* w)
+{
+    if (!plan_pair(K, M, (N + 63) / 64, num_sms, smem_optin, 0, (int)kPairABytes, 64, PairCost{300.0, 1.5, 0.0, 1}, &w->pl))
+        return false;
+    w->pitch = (N + 7) / 8 * 8;
+    w->off_pad = up256((size_t)N * (size_t)K * 2u);
+    w->off_split = w->off_pad + (N % 8 != 0 ? up256((size_t)M * (size_t)w->pitch * 2u) : 0u);
+    w->bytes = w->off_split + w->pl.ws_bytes;
+    return true;
+}
+
+bq_status mx_gradient(const uint16_t* dy, const uint8_t* wq, const uint8_t* ws, uint16_t* dx, int64_t M, int64_t N, int64_t K,
+                      void* workspace, size_t workspace_bytes, cudaStream_t st)
+{
+    if (M < 0 || N < 0 || K < 0 || K % 32 != 0 || !sizes_ok(M, N, K)) return BQ_ERR_SHAPE;
+    if (M == 0 || K == 0) return BQ_OK;
+    if (!dx || (N > 0 && (!dy || !wq || !ws))) return BQ_ERR_NULL;
+    if (!all_aligned16({dx, workspace}) || (N > 0 && !all_aligned16({dy, wq, ws}))) return BQ_ERR_ALIGN;
+    int dev;
+    DeviceInfo di;
+    bq_status s = current_device(&dev, &di);
+    if (s != BQ_OK) return s;
+    if (N == 0)
+        return cudaMemsetAsync(dx, 0, (size_t)M * (size_t)K * 2u, st) == cudaSuccess ? BQ_OK : BQ_ERR_CUDA;
+    MxGradWs w;
+    if (!plan_mx_grad(M, N, K, di.num_sms, di.max_smem_optin, &w)) return BQ_ERR_SHAPE;
+    void* buf = nullptr;
+    if ((s = epi_workspace(dev, st, workspace, workspace_bytes, w.bytes, &buf)) != BQ_OK) return s;
+    uint8_t* base = reinterpret_cast<uint8_t*>(buf);
+    const uint16_t* B = dy;
+    if (N % 8 != 0) {
+        B = reinterpret_cast<const uint16_t*>(base + w.off_pad);
+        if (cudaMemcpy2DAsync(base + w.off_pad, (size_t)w.pitch * 2u, dy, (size_t)N * 2u, (size_t)N * 2u, (size_t)M,
+                              cudaMemcpyDeviceToDevice, st) != cudaSuccess) {
+            cudaGetLastError();
+            return BQ_ERR_CUDA;
+        }
+    }
+    uint16_t* wb = reinterpret_cast<uint16_t*>(base);
+    if ((s = launch_mx_dequant<4>(wq, ws, wb, N * K, di, st)) != BQ_OK) return s;
+    EpiParams e;
+    e.y = dx;
+    return launch_pair<true, kEpiPlain>(di, dev, w.pl, &wb, &B, 1, K, K, M, N, w.pitch, e, base + w.off_split, st);
+}
+
+// ------------------------------------------------------------------ norm
+// Warps a row and chunks a thread for rows of K elements (C = 0: the second pass reads again).
+template <typename F>
+auto norm_config(int64_t K, F&& go)
+{
+    if (K <= 256) return go(std::integral_constant<int, 1>{}, std::integral_constant<int, 1>{});
+    if (K <= 512) return go(std::integral_constant<int, 2>{}, std::integral_constant<int, 1>{});
+    if (K <= 1024) return go(std::integral_constant<int, 4>{}, std::integral_constant<int, 1>{});
+    if (K <= 2048) return go(std::integral_constant<int, 8>{}, std::integral_constant<int, 1>{});
+    if (K <= 4096) return go(std::integral_constant<int, 16>{}, std::integral_constant<int, 1>{});
+    if (K <= 8192) return go(std::integral_constant<int, 16>{}, std::integral_constant<int, 2>{});
+    return go(std::integral_constant<int, 32>{}, std::integral_constant<int, 2>{});
+}
+constexpr int64_t kNormMaxK = 16384;       // held in registers
+
+bq_status norm_forward(const NormParams& p, int out, cudaStream_t st)
+{
+    const int64_t M = p.M, K = p.K;
+    if (K % 8 != 0) {
+        return launch_pdl(rms_norm_any_kernel, (int)M, 256, 0, st, p);
+    }
+    auto by_out = [&](auto w, auto c) {
+        constexpr int W = decltype(w)::value, C = decltype(c)::value;
+        const int grid = (int)((M + norm_rows(W) - 1) / norm_rows(W));
+        switch (out) {
+        case kNormQ8_1: return launch_pdl(rms_norm_kernel<W, C, kNormQ8_1>, grid, norm_threads(W), 0, st, p);
+        case kNormMx8: return launch_pdl(rms_norm_kernel<W, C, kNormMx8>, grid, norm_threads(W), 0, st, p);
+        case kNormMx4: return launch_pdl(rms_norm_kernel<W, C, kNormMx4>, grid, norm_threads(W), 0, st, p);
+        default: return launch_pdl(rms_norm_kernel<W, C, kNormBf16>, grid, norm_threads(W), 0, st, p);
+        }
+    };
+    if (K > kNormMaxK) return by_out(std::integral_constant<int, 16>{}, std::integral_constant<int, 0>{});
+    return norm_config(K, by_out);
+}
+
+// CTAs of the gradient and rows of its partial sums.
+struct NormGradPlan {
+    bool any = false;              // element by element
+    int grid = 0;
+    int64_t parts = 0;
+    int rows = 0;                  // any: rows per partial sum
+    size_t bytes = 0;
+};
+
+NormGradPlan plan_norm_grad(int64_t M, int64_t K, int num_sms)
+{
+    NormGradPlan pl;
+    if (K % 8 != 0 || K > kNormMaxK) {
+        pl.any = true;
+        const int64_t cols = (K + 127) / 128, want = std::max<int64_t>(1, (int64_t)num_sms * 16 / cols);
+        const int64_t rows = std::max<int64_t>(16, (M + want - 1) / want);
+        pl.rows = (int)rows;
+        pl.parts = (M + rows - 1) / rows;
+    } else {
+        norm_config(K, [&](auto w, auto) {
+            constexpr int W = decltype(w)::value;
+            pl.grid = (int)std::min<int64_t>((M + norm_rows(W) - 1) / norm_rows(W),
+                                             (int64_t)num_sms * std::max(1, 1024 / norm_threads(W)));
+            pl.parts = (int64_t)pl.grid * norm_rows(W);
+            return 0;
+        });
+    }
+    pl.bytes = up256((size_t)pl.parts * (size_t)K * 4u);
+    return pl;
+}
+
+bool norm_sizes_ok(int64_t M, int64_t K)
+{
+    return M >= 0 && K >= 0 && M < (1 << 30) && K < (1 << 30);
+}
+
+bq_status norm_backward(const NormGradPlan& pl, const NormGradParams& p, uint16_t* dw, cudaStream_t st)
+{
+    bq_status s;
+    if (pl.any) {
+        s = launch_pdl(rms_norm_grad_any_kernel, (int)p.M, 256, 0, st, p);
+        if (s == BQ_OK && dw)
+            s = launch_pdl_dim(rms_norm_weight_grad_any_kernel, dim3((unsigned)((p.K + 127) / 128), (unsigned)pl.parts), 128, 0,
+                               st, p, pl.rows);
+    } else {
+        s = norm_config(p.K, [&](auto w, auto c) {
+            constexpr int W = decltype(w)::value, C = decltype(c)::value;
+            return launch_pdl(rms_norm_grad_kernel<W, C>, pl.grid, norm_threads(W), 0, st, p);
+        });
+    }
+    if (s != BQ_OK || !dw) return s;
+    return launch_pdl_dim(epi_bias_grad_kernel, dim3((unsigned)((p.K + 31) / 32), 1u), 256, 0, st, (const float*)p.part, dw,
+                          (uint16_t*)nullptr, p.K, 1, (int)pl.parts);
+}
+
+}  // namespace
+}  // namespace bq

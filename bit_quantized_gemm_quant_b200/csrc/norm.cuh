@@ -1,0 +1,407 @@
+// norm.cuh -- root-mean-square norm with the residual's addition, its result as bf16 or
+// quantized for the products that follow, and its gradient.
+//
+//   forward:   h = bf16(x + r),  s = 1 / sqrt(mean_k h^2 + eps),  y = h s w
+//   gradient:  g = dy w,  dx = dh + s (g - h s^2 mean_k(g h)),  dw = sum_m dy h s
+//
+// The norm is that of the rounded h, which the caller gets and the gradient starts from.
+// Bound by HBM: forward reads x and r once and writes h and the result, the gradient reads
+// dy, h and dh once and writes dx.  So a row stays in registers between its sum and its
+// use, 8 elements a chunk and thread, and quantizing costs the output's bytes only: a block
+// of 32 is 4 neighbouring lanes.
+//
+// Precision.  Squares of bf16 are exact in fp32; a thread adds 8 at a time in fp32, and all
+// further sums are fp64, as is s (one Newton step from the fp32 reciprocal root).  h w is
+// exact in fp32 (8 + 8 bits), and s is used as the sum of two fp32 numbers.  For the MX types
+// the product is truncated and its last bit set (round to odd: Boldo and Melquiond, "Emulation
+// of FMA and correctly rounded sums", 2008), so that the second rounding, to the small type, gives what
+// one rounding of the product would, also next to a border between two codes, and so does the
+// exponent of a block's largest value next to a power of two.
+#pragma once
+
+#include "mx.cuh"
+
+namespace bq {
+
+enum : int { kNormBf16 = 0, kNormQ8_1 = 1, kNormMx8 = 2, kNormMx4 = 3 };
+
+struct NormParams {
+    const uint16_t* x;
+    const uint16_t* res;       // or NULL
+    const uint16_t* w;
+    uint16_t* h;               // or NULL; may be x or res itself
+    void* y;                   // bf16, or codes
+    void* scales;              // q8_1: fp32 per block; mx: a byte per block
+    int32_t* qsum;             // q8_1
+    float* rstd;               // or NULL
+    double inv_k;
+    float eps;
+    int64_t M;
+    int K;
+};
+
+BQ_DEVINL double warp_sum(double v)
+{
+#pragma unroll
+    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    return v;
+}
+
+BQ_DEVINL float warp_sum(float v)
+{
+#pragma unroll
+    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    return v;
+}
+
+// 1 / sqrt(v) to about 2^-46, as hi + lo.
+BQ_DEVINL void norm_rstd(double v, float& hi, float& lo)
+{
+    const float r0 = rsqrtf((float)v);
+    const double d = (double)r0;
+    const double r = d * (1.5 - 0.5 * v * d * d);
+    // rows of zeros without eps, or past fp32's range: the fp32 root's infinity, 0 or NaN
+    const bool plain = !(r0 > 0.0f && r0 < __uint_as_float(0x7F800000u));
+    hi = plain ? r0 : (float)r;
+    lo = plain ? 0.0f : (float)(r - (double)hi);
+}
+
+BQ_DEVINL float norm_scaled(float h, float w, float hi, float lo)
+{
+    const float p = __fmul_rn(h, w);
+    return __fmaf_rn(p, hi, __fmul_rn(p, lo));
+}
+
+// Rounded to odd.  (A row whose s is an fp32 number gets no odd bit: its products may be exact.)
+BQ_DEVINL float norm_scaled_odd(float h, float w, float hi, float lo)
+{
+    const float p = __fmul_rn(h, w);
+    const float y = __fmaf_rz(p, hi, __fmul_rn(p, lo));
+    return __uint_as_float(__float_as_uint(y) | (lo != 0.0f && p != 0.0f && fabsf(y) < __uint_as_float(0x7F800000u) ? 1u : 0u));
+}
+
+BQ_DEVINL void unpack8(const uint4& q, float (&v)[8])
+{
+    const uint32_t u[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        v[2 * i] = __uint_as_float(u[i] << 16);
+        v[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
+    }
+}
+
+BQ_DEVINL uint4 pack8(const float (&v)[8])
+{
+    return make_uint4(pack_bf16x2_rn(v[0], v[1]), pack_bf16x2_rn(v[2], v[3]), pack_bf16x2_rn(v[4], v[5]),
+                      pack_bf16x2_rn(v[6], v[7]));
+}
+
+// The 8 values of one chunk to the output, `at` elements from its start.  All lanes of the
+// warp come here.
+template <int OUT>
+BQ_DEVINL void norm_store8(const NormParams& p, const float (&y)[8], int64_t at, bool live)
+{
+    if constexpr (OUT == kNormBf16) {
+        if (live) *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(p.y) + at) = pack8(y);
+    } else if constexpr (OUT == kNormQ8_1) {                 // q8_1_quantize_kernel's rule
+        float amax = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(y[i]));
+        amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
+        amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 2));
+        const float d = __fdiv_rn(amax, 127.0f);
+        const float id = d != 0.0f ? __fdiv_rn(1.0f, d) : 0.0f;
+        uint32_t word[2] = {0u, 0u};
+        int sum = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int q = (int)roundf(__fmul_rn(y[i], id));
+            sum += q;
+            word[i >> 2] |= ((uint32_t)q & 0xFFu) << (8 * (i & 3));
+        }
+        sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 1);
+        sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 2);
+        if (!live) return;
+        *reinterpret_cast<uint2*>(reinterpret_cast<uint8_t*>(p.y) + at) = make_uint2(word[0], word[1]);
+        if ((at & 31) == 0) {
+            reinterpret_cast<float*>(p.scales)[at >> 5] = d;
+            p.qsum[at >> 5] = sum;
+        }
+    } else {
+        mx_store8<OUT == kNormMx8 ? 8 : 4>(y, reinterpret_cast<uint8_t*>(p.y), reinterpret_cast<uint8_t*>(p.scales), at, live);
+    }
+}
+
+constexpr int norm_threads(int W) { return W < 8 ? 256 : 32 * W; }
+constexpr int norm_rows(int W) { return W < 8 ? 8 / W : 1; }      // rows of a CTA
+
+// W warps a row, C chunks of 8 elements a thread: K a multiple of 8, at most 256 W C.
+// C = 0: any multiple of 8; the second pass reads x and r (or h) again.
+template <int W, int C, int OUT>
+__global__ void __launch_bounds__(norm_threads(W))
+rms_norm_kernel(const __grid_constant__ NormParams p)
+{
+    constexpr int R = norm_rows(W);
+    constexpr int kHeld = C ? C : 1;
+    __shared__ double part[R][W];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, group = warp / W, wi = warp % W;
+    const int64_t row = (int64_t)blockIdx.x * R + group;
+    const bool live = row < p.M;
+    const int64_t at0 = row * p.K;
+    const int col0 = (wi * 32 + lane) * 8, step = W * 256;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+    auto load_h = [&](int col) {
+        const uint4 q = *reinterpret_cast<const uint4*>(p.x + at0 + col);
+        if (!p.res) return q;
+        const uint4 b = *reinterpret_cast<const uint4*>(p.res + at0 + col);
+        float v[8], u[8];
+        unpack8(q, v);
+        unpack8(b, u);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] += u[i];
+        return pack8(v);
+    };
+    auto squares = [&](const uint4& q) {
+        float v[8];
+        unpack8(q, v);
+        float a = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) a = __fmaf_rn(v[i], v[i], a);
+        return (double)a;
+    };
+
+    uint4 held[kHeld];
+    double ss = 0.0;
+    if constexpr (C > 0) {
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const int col = col0 + c * step;
+            held[c] = live && col < p.K ? load_h(col) : make_uint4(0u, 0u, 0u, 0u);
+        }
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const int col = col0 + c * step;
+            ss += squares(held[c]);
+            if (p.h && live && col < p.K) *reinterpret_cast<uint4*>(p.h + at0 + col) = held[c];
+        }
+    } else {
+        for (int col = col0; live && col < p.K; col += step) {
+            const uint4 q = load_h(col);
+            ss += squares(q);
+            if (p.h) *reinterpret_cast<uint4*>(p.h + at0 + col) = q;
+        }
+    }
+    ss = warp_sum(ss);
+    if constexpr (W > 1) {
+        if (lane == 0) part[group][wi] = ss;
+        __syncthreads();
+        ss = 0.0;
+#pragma unroll
+        for (int i = 0; i < W; ++i) ss += part[group][i];
+    }
+    float hi, lo;
+    norm_rstd(ss * p.inv_k + (double)p.eps, hi, lo);
+    if (p.rstd && live && wi == 0 && lane == 0) p.rstd[row] = hi;
+
+    auto emit = [&](const uint4& q, int col) {
+        const bool in = live && col < p.K;
+        float v[8], w[8];
+        unpack8(q, v);
+        unpack8(in ? ldg_cached(p.w + col) : make_uint4(0u, 0u, 0u, 0u), w);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            v[i] = !in ? 0.0f : OUT == kNormMx8 || OUT == kNormMx4 ? norm_scaled_odd(v[i], w[i], hi, lo)
+                                                                   : norm_scaled(v[i], w[i], hi, lo);
+        norm_store8<OUT>(p, v, at0 + col, in);
+    };
+    if constexpr (C > 0) {
+#pragma unroll
+        for (int c = 0; c < C; ++c) emit(held[c], col0 + c * step);
+    } else {
+        // h where it is stored (this thread wrote it, possibly over x or r)
+        for (int base = 0; base < p.K; base += step) {
+            const int col = base + col0;
+            const bool in = live && col < p.K;
+            emit(!in ? make_uint4(0u, 0u, 0u, 0u) : p.h ? *reinterpret_cast<const uint4*>(p.h + at0 + col) : load_h(col), col);
+        }
+    }
+}
+
+// Any K, element by element, bf16 result: one row a CTA.
+__global__ void __launch_bounds__(256) rms_norm_any_kernel(const __grid_constant__ NormParams p)
+{
+    __shared__ double part[8];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t row = blockIdx.x, at0 = row * p.K;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    auto load_h = [&](int k) {
+        const uint32_t a = p.x[at0 + k];
+        return p.res ? f32_to_bf16_bits(bf16_bits_to_f32(a) + bf16_bits_to_f32(p.res[at0 + k])) : a;
+    };
+    double ss = 0.0;
+    for (int k = threadIdx.x; k < p.K; k += 256) {
+        const uint32_t q = load_h(k);
+        const float v = bf16_bits_to_f32(q);
+        ss += (double)__fmul_rn(v, v);
+        if (p.h) p.h[at0 + k] = (uint16_t)q;
+    }
+    ss = warp_sum(ss);
+    if (lane == 0) part[warp] = ss;
+    __syncthreads();
+    ss = 0.0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) ss += part[i];
+    float hi, lo;
+    norm_rstd(ss * p.inv_k + (double)p.eps, hi, lo);
+    if (p.rstd && threadIdx.x == 0) p.rstd[row] = hi;
+    for (int k = threadIdx.x; k < p.K; k += 256) {
+        const float v = bf16_bits_to_f32(p.h ? p.h[at0 + k] : load_h(k));
+        reinterpret_cast<uint16_t*>(p.y)[at0 + k] =
+            (uint16_t)f32_to_bf16_bits(norm_scaled(v, bf16_bits_to_f32(p.w[k]), hi, lo));
+    }
+}
+
+// ------------------------------------------------------------------ gradient
+struct NormGradParams {
+    const uint16_t* dy;
+    const uint16_t* h;
+    const uint16_t* w;
+    const float* rstd;
+    const uint16_t* dh;        // or NULL
+    uint16_t* dx;
+    float* part;               // [CTAs x rows of a CTA][K] sums of dw, or NULL
+    float inv_k;
+    int64_t M;
+    int K;
+};
+
+// CTAs walk the rows (row groups of the grid apart); a thread keeps its columns' share of dw
+// in registers until its last row.
+template <int W, int C>
+__global__ void __launch_bounds__(norm_threads(W))
+rms_norm_grad_kernel(const __grid_constant__ NormGradParams p)
+{
+    constexpr int R = norm_rows(W);
+    __shared__ float part[2][R][W];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, group = warp / W, wi = warp % W;
+    const int col0 = (wi * 32 + lane) * 8, step = W * 256;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+    uint4 w[C];
+    float acc[C][8];
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+        w[c] = col0 + c * step < p.K ? ldg_cached(p.w + col0 + c * step) : zero;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) acc[c][i] = 0.0f;
+    }
+    int buf = 0;
+    for (int64_t row0 = (int64_t)blockIdx.x * R; row0 < p.M; row0 += (int64_t)gridDim.x * R, buf ^= 1) {
+        const int64_t row = row0 + group, at0 = row * p.K;
+        const bool live = row < p.M;
+        uint4 d[C], h[C], r[C];
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const int col = col0 + c * step;
+            const bool in = live && col < p.K;
+            d[c] = in ? ldg_stream(p.dy + at0 + col) : zero;
+            h[c] = in ? ldg_stream(p.h + at0 + col) : zero;
+            r[c] = in && p.dh ? ldg_stream(p.dh + at0 + col) : zero;
+        }
+        const float s = live ? p.rstd[row] : 0.0f;
+        float dot = 0.0f;
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            float dv[8], hv[8], wv[8];
+            unpack8(d[c], dv);
+            unpack8(h[c], hv);
+            unpack8(w[c], wv);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float t = dv[i] * hv[i];               // exact
+                dot = __fmaf_rn(t, wv[i], dot);
+                acc[c][i] = __fmaf_rn(t, s, acc[c][i]);
+            }
+        }
+        dot = warp_sum(dot);
+        if constexpr (W > 1) {
+            if (lane == 0) part[buf][group][wi] = dot;
+            __syncthreads();                                 // (the other buffer is free: every warp has passed here once more)
+            dot = 0.0f;
+#pragma unroll
+            for (int i = 0; i < W; ++i) dot += part[buf][group][i];
+        }
+        const float coef = s * s * (dot * p.inv_k);
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const int col = col0 + c * step;
+            if (!(live && col < p.K)) continue;
+            float dv[8], hv[8], wv[8], rv[8];
+            unpack8(d[c], dv);
+            unpack8(h[c], hv);
+            unpack8(w[c], wv);
+            unpack8(r[c], rv);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                dv[i] = __fmaf_rn(s, __fmaf_rn(-hv[i], coef, dv[i] * wv[i]), rv[i]);
+            *reinterpret_cast<uint4*>(p.dx + at0 + col) = pack8(dv);
+        }
+    }
+    if (!p.part) return;
+    float* out = p.part + ((int64_t)blockIdx.x * R + group) * p.K;
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+        const int col = col0 + c * step;
+        if (col >= p.K) continue;
+        *reinterpret_cast<float4*>(out + col) = make_float4(acc[c][0], acc[c][1], acc[c][2], acc[c][3]);
+        *reinterpret_cast<float4*>(out + col + 4) = make_float4(acc[c][4], acc[c][5], acc[c][6], acc[c][7]);
+    }
+}
+
+// Any K: dx, one row a CTA, element by element; dy and h are read twice.
+__global__ void __launch_bounds__(256) rms_norm_grad_any_kernel(const __grid_constant__ NormGradParams p)
+{
+    __shared__ float part[8];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t row = blockIdx.x, at0 = row * p.K;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const float s = p.rstd[row];
+    float dot = 0.0f;
+    for (int k = threadIdx.x; k < p.K; k += 256)
+        dot = __fmaf_rn(bf16_bits_to_f32(p.dy[at0 + k]) * bf16_bits_to_f32(p.h[at0 + k]), bf16_bits_to_f32(p.w[k]), dot);
+    dot = warp_sum(dot);
+    if (lane == 0) part[warp] = dot;
+    __syncthreads();
+    dot = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) dot += part[i];
+    const float coef = s * s * (dot * p.inv_k);
+    for (int k = threadIdx.x; k < p.K; k += 256) {
+        const float g = bf16_bits_to_f32(p.dy[at0 + k]) * bf16_bits_to_f32(p.w[k]);
+        const float r = p.dh ? bf16_bits_to_f32(p.dh[at0 + k]) : 0.0f;
+        p.dx[at0 + k] = (uint16_t)f32_to_bf16_bits(__fmaf_rn(s, __fmaf_rn(-bf16_bits_to_f32(p.h[at0 + k]), coef, g), r));
+    }
+}
+
+// ... and its share of dw: a thread a column, a block `rows` rows.
+__global__ void __launch_bounds__(128)
+rms_norm_weight_grad_any_kernel(const __grid_constant__ NormGradParams p, int rows)
+{
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int k = (int)blockIdx.x * 128 + threadIdx.x;
+    if (k >= p.K) return;
+    const int64_t m0 = (int64_t)blockIdx.y * rows, m1 = min(p.M, m0 + rows);
+    float acc = 0.0f;
+#pragma unroll 4
+    for (int64_t m = m0; m < m1; ++m)
+        acc = __fmaf_rn(bf16_bits_to_f32(p.dy[m * p.K + k]) * bf16_bits_to_f32(p.h[m * p.K + k]), p.rstd[m], acc);
+    p.part[(int64_t)blockIdx.y * p.K + k] = acc;
+}
+
+}  // namespace bq

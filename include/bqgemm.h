@@ -33,6 +33,10 @@
  *      scales  bf16 [N][K/group_size]
  *      biases  bf16 [N][K/group_size]
  *
+ * Microscaled (MX) weights and activations, their product on the block-scaled tensor
+ * cores, and the root-mean-square norm that writes them are declared after the
+ * quantizers (mxfp4_quantize and on).
+ *
  * Tensors are row-major and contiguous: x bf16 [M][K], y bf16 [M][N],
  * W (and its dequantized form) [N][K] -- the transpose=True convention of
  * mx.quantized_matmul, one output feature per weight row.
@@ -490,6 +494,114 @@ BQ_API bq_status q4_0_quantize(const float* w, uint8_t* wq, uint16_t* scales_f16
  */
 BQ_API bq_status affine_quantize(const float* w, uint32_t* wq, uint16_t* scales_bf16, uint16_t* biases_bf16,
                           int64_t N, int64_t K, int group_size, int bits, bq_stream_t stream);
+
+/*
+ * Microscaled rows, the OCP Microscaling Formats specification v1.0 (no page has a
+ * counterpart): blocks of 32 consecutive elements share a power of two X, and an element
+ * stands for X times its value in a small type.
+ *   scales  u8 [M][K/32]  E8M0: X = 2^(byte - 127); 255 is NaN
+ *   MXFP8   u8 [M][K]     E4M3 (sign, 4 exponent, 3 mantissa bits; largest 448)
+ *   MXFP4   u8 [M][K/2]   E2M1: codes 0..7 are 0, 0.5, 1, 1.5, 2, 3, 4, 6, bit 3 the sign;
+ *                         element 2j in the low nibble of byte j, 2j + 1 in the high one
+ *                         (not Q4_0's order)
+ *
+ * mxfp4_quantize, mxfp8_quantize -- x [M][K] to codes and scales.  Per block: amax = max |x|,
+ * X = 2^(floor(log2(amax)) - emax), emax 2 (E2M1) or 8 (E4M3), at least 2^-127 (byte 0 for a
+ * block of zeros); an element is x / X rounded to nearest, ties to even, beyond the largest
+ * value that value.  A block that holds a NaN or an infinity becomes NaN: byte 255, codes 0.
+ *   x       device bf16 or f32 [M][K], by x_type (bq_type; another returns BQ_ERR_UNSUPPORTED)
+ *   codes   device u8 [M][K/2] or [M][K], written;  scales device u8 [M][K/32], written
+ *   K % 32 == 0 (BQ_ERR_SHAPE).  Outputs may not overlap x or one another.
+ */
+typedef enum { BQ_TYPE_BF16 = 0, BQ_TYPE_F32 = 1 } bq_type;
+BQ_API bq_status mxfp4_quantize(const void* x, int x_type, uint8_t* codes, uint8_t* scales, int64_t M, int64_t K,
+                                bq_stream_t stream);
+BQ_API bq_status mxfp8_quantize(const void* x, int x_type, uint8_t* codes, uint8_t* scales, int64_t M, int64_t K,
+                                bq_stream_t stream);
+
+/*
+ * mxfp4_dequantize, mxfp8_dequantize -- codes and scales to bf16: bf16_rne(X * element), which
+ * is exact within bf16's range (beyond it infinity, below it to nearest even; a NaN scale NaN).
+ *   out_bf16  device u16 [M][K], written.  K % 32 == 0.
+ */
+BQ_API bq_status mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales, uint16_t* out_bf16, int64_t M, int64_t K,
+                                  bq_stream_t stream);
+BQ_API bq_status mxfp8_dequantize(const uint8_t* codes, const uint8_t* scales, uint16_t* out_bf16, int64_t M, int64_t K,
+                                  bq_stream_t stream);
+
+/*
+ * mx_matmul -- y[m][n] = bf16_rne(sum_k x[m][k] * W[n][k]) for microscaled x and W, fp32
+ * accumulation.
+ *   xq, x_scales  x: MXFP8 codes u8 [M][K] (x_bits 8) or MXFP4 codes u8 [M][K/2] (x_bits 4;
+ *                 another value returns BQ_ERR_UNSUPPORTED), scales u8 [M][K/32]
+ *   wq, w_scales  W: MXFP4 codes u8 [N][K/2], scales u8 [N][K/32]
+ *   y_bf16        device u16 [M][N], written; may not overlap an input
+ *   workspace, workspace_bytes  scratch of at least mx_matmul_workspace_size(...) bytes (else
+ *                 BQ_ERR_WORKSPACE, nothing launched), under quant_matmul_act's rules
+ * Any M, any N; K % 32 == 0; K == 0 writes zeros.  Products of scales and elements are exact
+ * while they stay in fp32's range.  Results do not depend on timing.
+ */
+BQ_API bq_status mx_matmul(const void* xq, const uint8_t* x_scales, int x_bits, const uint8_t* wq,
+                           const uint8_t* w_scales, uint16_t* y_bf16, int64_t M, int64_t N, int64_t K, void* workspace,
+                           size_t workspace_bytes, bq_stream_t stream);
+BQ_API size_t mx_matmul_workspace_size(int64_t M, int64_t N, int64_t K, int x_bits);
+
+/*
+ * mx_matmul_backward -- the gradient of mx_matmul for frozen weights and x as a rounding of its
+ * unquantized self (the straight-through estimate):
+ *   dx[m][k] = bf16_rne(sum_n dy[m][n] * W[n][k])
+ * Blocks run along K and the sum along N, so the product takes W's values as bf16 (exact within
+ * bf16's range).
+ *   dy_bf16  device bf16 [M][N];  wq, w_scales as mx_matmul;  dx_bf16 device u16 [M][K], written,
+ *            may not overlap an input
+ * Any M, any N (N == 0 writes zeros); K % 32 == 0.  Workspace (mx_matmul_backward_workspace_size)
+ * and errors as mx_matmul.
+ */
+BQ_API bq_status mx_matmul_backward(const uint16_t* dy_bf16, const uint8_t* wq, const uint8_t* w_scales,
+                                    uint16_t* dx_bf16, int64_t M, int64_t N, int64_t K, void* workspace,
+                                    size_t workspace_bytes, bq_stream_t stream);
+BQ_API size_t mx_matmul_backward_workspace_size(int64_t M, int64_t N, int64_t K);
+
+/*
+ * add_rms_norm -- the residual's addition and the root-mean-square norm ahead of a product:
+ *   h = bf16_rne(x + residual)   (x itself without a residual)
+ *   rstd[m] = 1 / sqrt(mean_k h[m][k]^2 + eps),  y[m][k] = h[m][k] * rstd[m] * weight[k]
+ * y is written as bf16, or quantized from its unrounded fp32 values as q8_1_quantize,
+ * mxfp8_quantize and mxfp4_quantize would (for quant_matmul_q8 and mx_matmul).  Squares are
+ * fp32 (a row whose sum of squares passes fp32's range has rstd 0), sums fp64.  (No page has
+ * a counterpart.)
+ *   x_bf16, residual  device bf16 [M][K]; residual may be NULL
+ *   weight            device bf16 [K];  eps >= 0 and finite (else BQ_ERR_UNSUPPORTED)
+ *   out               bq_norm_out (another value returns BQ_ERR_UNSUPPORTED)
+ *   y, scales, qsum   by out: bf16 [M][K], scales and qsum not used; i8 [M][K] with f32 and
+ *                     i32 [M][K/32]; u8 [M][K] or [M][K/2] with u8 [M][K/32].  Written.
+ *   h_bf16            device u16 [M][K], written, or NULL; may be x_bf16 or residual itself
+ *   rstd              device f32 [M], written for the gradient, or NULL
+ * No other overlap of an output with an input or another output.  K any (BQ_NORM_BF16) or a
+ * multiple of 32; M and K below 2^30.
+ */
+typedef enum { BQ_NORM_BF16 = 0, BQ_NORM_Q8_1 = 1, BQ_NORM_MXFP8 = 2, BQ_NORM_MXFP4 = 3 } bq_norm_out;
+BQ_API bq_status add_rms_norm(const uint16_t* x_bf16, const uint16_t* residual, const uint16_t* weight, float eps, int out,
+                              void* y, void* scales, int32_t* qsum, uint16_t* h_bf16, float* rstd, int64_t M, int64_t K,
+                              bq_stream_t stream);
+
+/*
+ * add_rms_norm_backward -- its gradient, from the saved h and rstd, with g = dy * weight:
+ *   dx = bf16_rne(dh + rstd (g - h rstd^2 mean_k(g h)))   (x's gradient, and the residual's)
+ *   dweight[k] = bf16_rne(sum_m dy[m][k] h[m][k] rstd[m])
+ * A quantized y is taken as a rounding of its unquantized self (the straight-through estimate).
+ *   dy_bf16, h_bf16  device bf16 [M][K];  rstd device f32 [M]
+ *   dh_bf16          device bf16 [M][K], the gradient that reaches h by another way, or NULL
+ *   dx_bf16          device u16 [M][K], written;  dweight_bf16 device u16 [K], written, or NULL
+ *   workspace        add_rms_norm_backward_workspace_size(M, K) bytes; not used without dweight
+ * No output may overlap an input or another output.  Any K; M and K below 2^30.  Sums are fp32, in
+ * a fixed order.  Errors as mx_matmul.
+ */
+BQ_API bq_status add_rms_norm_backward(const uint16_t* dy_bf16, const uint16_t* h_bf16, const uint16_t* weight,
+                                       const float* rstd, const uint16_t* dh_bf16, uint16_t* dx_bf16,
+                                       uint16_t* dweight_bf16, int64_t M, int64_t K, void* workspace,
+                                       size_t workspace_bytes, bq_stream_t stream);
+BQ_API size_t add_rms_norm_backward_workspace_size(int64_t M, int64_t K);
 
 /*
  * bq_selftest_wait_timeout -- exercises the failure detection of the device-side
