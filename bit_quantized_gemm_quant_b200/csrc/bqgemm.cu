@@ -25,6 +25,7 @@
 #include "tc_fused_pair.cuh"
 #include "gemv_ring.cuh"
 #include "mx.cuh"
+#include "mx_pair.cuh"
 #include "norm.cuh"
 
 namespace bq {
@@ -1711,7 +1712,7 @@ size_t mx_matmul_workspace_size(int64_t M, int64_t N, int64_t K, int x_bits)
     int num_sms, smem;
     device_or_b200(&num_sms, &smem);
     MxWs w;
-    return plan_mx(M, N, K, num_sms, smem, &w) ? w.bytes : 0;
+    return plan_mx(M, N, K, x_bits, num_sms, smem, &w) ? w.bytes : 0;
 }
 
 size_t mx_matmul_backward_workspace_size(int64_t M, int64_t N, int64_t K)

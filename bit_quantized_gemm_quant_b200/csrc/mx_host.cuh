@@ -55,20 +55,92 @@ bq_status mx_dequantize(const uint8_t* codes, const uint8_t* scales, uint16_t* o
 }
 
 // ------------------------------------------------------------------ product
-// The bf16 pair's workspace: W, then x, then the product's partial sums.
+// Packed 4-bit codes [rows][K] spread to 8-byte groups with 8-byte gaps, boxes of 128
+// elements x box_rows, 128-byte swizzle (K a multiple of 128, ptr 32-byte aligned).
+bool make_map_spread4(CUtensorMap* m, const void* ptr, int64_t rows, int64_t K, int box_rows)
+{
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    cuuint64_t gdim[2] = {(cuuint64_t)K, (cuuint64_t)rows};
+    cuuint64_t gstride[1] = {(cuuint64_t)(K / 2)};
+    cuuint32_t box[2] = {128, (cuuint32_t)box_rows};
+    cuuint32_t estride[2] = {1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B, 2, const_cast<void*>(ptr), gdim, gstride, box, estride,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Workspace of the block-scaled product: the partial sums of split tiles.  Of the bf16 pair:
+// W, then x, then the partial sums.
 struct MxWs {
     PairPlan pl;
+    bool scaled = false;            // the block-scaled product
     size_t off_x = 0, off_split = 0, bytes = 0;
 };
 
-bool plan_mx(int64_t M, int64_t N, int64_t K, int num_sms, int smem_optin, MxWs* w)
+// The block-scaled product takes any K with 4-bit activations, and rows of whole 128 elements
+// with 8-bit ones (what the copy that spreads the codes wants); the rest goes through bf16.
+bool plan_mx(int64_t M, int64_t N, int64_t K, int x_bits, int num_sms, int smem_optin, MxWs* w)
 {
+    w->scaled = x_bits == 4 || K % 128 == 0;
+    if (w->scaled) {
+        const int sk = mx_stage_k(x_bits);
+        if (!plan_pair(N, M, (K + sk - 1) / sk, num_sms, smem_optin, 0, (int)(kPairABytes + mx_scale_bytes(x_bits)), 64,
+                       PairCost{300.0, 1.5, 0.0, 1, kMxMaxBn}, &w->pl))
+            return false;
+        w->pl.stages = std::min(std::min(w->pl.stages, kMxMaxStages), (512 - 2 * w->pl.bn) / mx_scale_cols(x_bits));
+        w->bytes = w->pl.ws_bytes;
+        return true;
+    }
     if (!plan_pair(N, M, (K + 63) / 64, num_sms, smem_optin, 0, (int)kPairABytes, 64, PairCost{300.0, 1.5, 0.0, 1}, &w->pl))
         return false;
     w->off_x = up256((size_t)N * (size_t)K * 2u);
     w->off_split = w->off_x + up256((size_t)M * (size_t)K * 2u);
     w->bytes = w->off_split + w->pl.ws_bytes;
     return true;
+}
+
+template <int XB>
+bq_status launch_mx_pair(const DeviceInfo& di, int dev, const PairPlan& pl, const void* xq, const uint8_t* xs, const uint8_t* wq,
+                         const uint8_t* wsc, uint16_t* y, int64_t M, int64_t N, int64_t K, void* ws, cudaStream_t st)
+{
+    auto kern = mx_pair_kernel<XB>;
+    static bool attr_done[kMaxDevices] = {};
+    if (!attr_done[dev]) {
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, di.max_smem_optin) != cudaSuccess) {
+            cudaGetLastError();
+            return BQ_ERR_CUDA;
+        }
+        attr_done[dev] = true;
+    }
+    CUtensorMap ta, tb;
+    const bool a_ok = XB == 8 ? make_map_spread4(&ta, wq, N, K, 128)
+                              : make_map(&ta, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, wq, N, K / 2, 128, 128, CU_TENSOR_MAP_SWIZZLE_128B);
+    if (!a_ok || !make_map(&tb, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, xq, M, K * XB / 8, pl.bn / 2, 128, CU_TENSOR_MAP_SWIZZLE_128B))
+        return BQ_ERR_CUDA;
+    MxParams p;
+    p.q.e.y = y;
+    p.q.M = (int)M;
+    p.q.N = (int)N;
+    p.q.bn = pl.bn;
+    p.q.stages = pl.stages;
+    p.q.m_tiles = (int)((M + pl.bn - 1) / pl.bn);
+    p.q.tiles = (int)pl.tiles;
+    p.q.seg_blocks = pl.split.blocks;
+    p.q.segs = 1;
+    p.q.split = pl.split;
+    p.q.ws = reinterpret_cast<float*>(ws);
+    p.xs = xs;
+    p.ws = wsc;
+    p.blocks = (int)(K / 32);
+    p.vec = p.blocks % 16 == 0 ? 16 : p.blocks % 4 == 0 ? 4 : 1;
+    // every pair when there are whole rounds before the tail: the units are dealt by pair
+    const unsigned grid = 2u * (unsigned)std::min<int64_t>(pl.split.tail && pl.split.dp_tiles ? pl.pairs
+                                                           : pl.split.tail ? pl.split.tail_pairs : pl.tiles, pl.pairs);
+    const size_t smem = std::max<size_t>(1024 + (size_t)pl.stages * (pair_stage_bytes(pl.bn) + mx_scale_bytes(XB)) + 512,
+                                         (size_t)di.max_smem_optin / 2 + 1024);   // one CTA per SM (all of TMEM)
+    const bq_status s = launch_pdl_dim(kern, dim3(grid), kMxThreads, smem, st, ta, tb, p);
+    return s != BQ_OK ? s : launch_reduce<kEpiPlain>(di, pl, p.q, st);
 }
 
 bq_status mx_product(const void* xq, const uint8_t* xs, int x_bits, const uint8_t* wq, const uint8_t* ws, uint16_t* y,
@@ -79,6 +151,7 @@ bq_status mx_product(const void* xq, const uint8_t* xs, int x_bits, const uint8_
     if (M == 0 || N == 0) return BQ_OK;
     if (!y || (K > 0 && (!xq || !xs || !wq || !ws))) return BQ_ERR_NULL;
     if (!all_aligned16({y, workspace}) || (K > 0 && !all_aligned16({xq, xs, wq, ws}))) return BQ_ERR_ALIGN;
+    if (x_bits == 8 && K % 128 == 0 && (reinterpret_cast<uintptr_t>(wq) & 31u) != 0) return BQ_ERR_ALIGN;
     int dev;
     DeviceInfo di;
     bq_status s = current_device(&dev, &di);
@@ -86,9 +159,12 @@ bq_status mx_product(const void* xq, const uint8_t* xs, int x_bits, const uint8_
     if (K == 0)
         return cudaMemsetAsync(y, 0, (size_t)M * (size_t)N * 2u, st) == cudaSuccess ? BQ_OK : BQ_ERR_CUDA;
     MxWs w;
-    if (!plan_mx(M, N, K, di.num_sms, di.max_smem_optin, &w)) return BQ_ERR_SHAPE;
+    if (!plan_mx(M, N, K, x_bits, di.num_sms, di.max_smem_optin, &w)) return BQ_ERR_SHAPE;
     void* buf = nullptr;
     if ((s = epi_workspace(dev, st, workspace, workspace_bytes, w.bytes, &buf)) != BQ_OK) return s;
+    if (w.scaled)
+        return x_bits == 8 ? launch_mx_pair<8>(di, dev, w.pl, xq, xs, wq, ws, y, M, N, K, buf, st)
+                           : launch_mx_pair<4>(di, dev, w.pl, xq, xs, wq, ws, y, M, N, K, buf, st);
     uint8_t* base = reinterpret_cast<uint8_t*>(buf);
     uint16_t *wb = reinterpret_cast<uint16_t*>(base), *xb = reinterpret_cast<uint16_t*>(base + w.off_x);
     if ((s = launch_mx_dequant<4>(wq, ws, wb, N * K, di, st)) != BQ_OK) return s;

@@ -534,7 +534,8 @@ BQ_API bq_status mxfp8_dequantize(const uint8_t* codes, const uint8_t* scales, u
  * accumulation.
  *   xq, x_scales  x: MXFP8 codes u8 [M][K] (x_bits 8) or MXFP4 codes u8 [M][K/2] (x_bits 4;
  *                 another value returns BQ_ERR_UNSUPPORTED), scales u8 [M][K/32]
- *   wq, w_scales  W: MXFP4 codes u8 [N][K/2], scales u8 [N][K/32]
+ *   wq, w_scales  W: MXFP4 codes u8 [N][K/2], scales u8 [N][K/32]; for x_bits 8 and K % 128 == 0
+ *                 wq is 32-byte aligned (BQ_ERR_ALIGN)
  *   y_bf16        device u16 [M][N], written; may not overlap an input
  *   workspace, workspace_bytes  scratch of at least mx_matmul_workspace_size(...) bytes (else
  *                 BQ_ERR_WORKSPACE, nothing launched), under quant_matmul_act's rules
