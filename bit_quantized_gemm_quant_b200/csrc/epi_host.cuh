@@ -56,7 +56,6 @@ struct PairPlan {
 struct PairCost {
     double block0, per_token, crowd;
     int max_halves;                 // token tiles per unit: with 2, max(1480, 555 + 4.67 per token)
-    int max_bn = 256;
 };
 
 // Token tile and split of the last round for `rows` D rows, M tokens and nk blocks of the
@@ -71,7 +70,7 @@ bool plan_pair(int64_t rows, int64_t M, int64_t nk, int num_sms, int smem_optin,
                int tok_bytes, const PairCost& pc, PairPlan* pl)
 {
     const int64_t pairs = std::max(num_sms / 2, 1), rtiles = (rows + 255) / 256;
-    const int64_t maxb = std::min<int64_t>(pc.max_bn, (M + 31) / 32 * 32);
+    const int64_t maxb = std::min<int64_t>(256, (M + 31) / 32 * 32);
     double best = 1e300;
     for (int halves = 1; halves <= pc.max_halves; ++halves) {
         for (int b = 32; b <= maxb; b += 32) {

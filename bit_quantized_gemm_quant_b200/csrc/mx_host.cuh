@@ -70,13 +70,62 @@ bool make_map_spread4(CUtensorMap* m, const void* ptr, int64_t rows, int64_t K, 
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Workspace of the block-scaled product: the partial sums of split tiles.  Of the bf16 pair:
-// W, then x, then the partial sums.
+// Workspace of the block-scaled product: the packed scales of W and of x, the partial sums of
+// split tiles.  Of the bf16 pair: W, then x, then the partial sums.
 struct MxWs {
     PairPlan pl;
     bool scaled = false;            // the block-scaled product
+    int chunks = 0;                 // 128-element chunks of a row, whole stages
     size_t off_x = 0, off_split = 0, bytes = 0;
 };
+
+// Token tile, tiles per unit (halves) and split of the last round of the block-scaled product, by the least cost of
+// a model in SM clocks.
+bool plan_mx_pair(int64_t N, int64_t M, int64_t K, int xbits, int num_sms, int smem_optin, PairPlan* pl)
+{
+    const int64_t pairs = std::max(num_sms / 2, 1), rtiles = (N + 255) / 256;
+    const int64_t maxb = std::min<int64_t>(kMxMaxBn, (M + 31) / 32 * 32);
+    double best = 1e300;
+    for (int h = 1; h <= 2; ++h) {
+        const int64_t nk = (K + mx_stage_k(xbits, h) - 1) / mx_stage_k(xbits, h);
+        for (int b = 32; b <= maxb; b += 32) {
+            if (h == 2 && M <= b) break;
+            const int64_t tok = (int64_t)h * b, mt = (M + tok - 1) / tok, tiles = mt * rtiles;
+            const double a_bytes = (h == 1 ? 2.0 : 1.0) * (xbits == 4 ? 16384.0 : 8192.0);
+            const double l2 = (a_bytes + 128.0 * b + 512.0 * mx_scale_units(xbits, h, b)) / 68.0;
+            const double stage = std::max({4.2 * b, l2, 420.0, a_bytes / 26.0 / (double)std::min<int64_t>(mt, 4)});
+            const double start = h == 2 ? 2500.0 + 6.0 * b : 400.0, drain = 2000.0 + 8.0 * (double)tok;
+            auto unit = [&](int64_t n) { return (double)n * stage + start; };
+            auto consider = [&](double c, int64_t dp, int64_t tail_pairs) {
+                if (c >= best) return;
+                best = c;
+                pl->bn = b;
+                pl->halves = h;
+                pl->tiles = tiles;
+                pl->split.dp_tiles = (int)dp;
+                pl->split.tail = (int)(tiles - dp);
+                pl->split.tail_pairs = (int)tail_pairs;
+                pl->split.blocks = (int)nk;
+            };
+            consider((double)((tiles + pairs - 1) / pairs) * unit(nk) + drain, tiles, 0);
+            const int64_t dp = tiles / pairs * pairs, tail = tiles - dp;
+            if (tail == 0) continue;
+            // ranges of at least 2 stages, at least one per tile, as in plan_pair
+            auto split = [&](int64_t tp) {
+                const bool whole = tp % tail == 0;
+                const double traffic = (double)(whole ? tp : tp + tail) * (double)tok * 256.0 * 8.0 / 2225.0;
+                consider((double)(dp / pairs) * unit(nk) + unit((tail * nk + tp - 1) / tp) + (whole ? 0.0 : start) + drain + 4800.0 +
+                             traffic, dp, tp);
+            };
+            split(std::max<int64_t>(tail, std::min<int64_t>(pairs, tail * nk / 2)));
+            for (int64_t q = 2; q * tail <= pairs && 2 * q <= nk; ++q) split(q * tail);
+        }
+    }
+    pl->pairs = (int)pairs;
+    pl->stages = std::min<int>(kMxMaxStages, (smem_optin - 1024 - 512) / (int)mx_stage_bytes(xbits, pl->halves, pl->bn));
+    pl->ws_bytes = pl->split.tail ? (size_t)2 * (size_t)pl->split.tail_pairs * (size_t)(pl->halves * pl->bn) * 256u * 4u : 0u;
+    return pl->stages >= 2 && pl->tiles <= INT32_MAX / 256;
+}
 
 // The block-scaled product takes any K with 4-bit activations, and rows of whole 128 elements
 // with 8-bit ones (what the copy that spreads the codes wants); the rest goes through bf16.
@@ -84,12 +133,15 @@ bool plan_mx(int64_t M, int64_t N, int64_t K, int x_bits, int num_sms, int smem_
 {
     w->scaled = x_bits == 4 || K % 128 == 0;
     if (w->scaled) {
-        const int sk = mx_stage_k(x_bits);
-        if (!plan_pair(N, M, (K + sk - 1) / sk, num_sms, smem_optin, 0, (int)(kPairABytes + mx_scale_bytes(x_bits)), 64,
-                       PairCost{300.0, 1.5, 0.0, 1, kMxMaxBn}, &w->pl))
-            return false;
-        w->pl.stages = std::min(std::min(w->pl.stages, kMxMaxStages), (512 - 2 * w->pl.bn) / mx_scale_cols(x_bits));
-        w->bytes = w->pl.ws_bytes;
+        if (!plan_mx_pair(N, M, K, x_bits, num_sms, smem_optin, &w->pl)) return false;
+        const int h = w->pl.halves;
+        w->chunks = w->pl.split.blocks * mx_chunks(x_bits, h);
+        const int64_t wt = (N + 255) / 256 * 2, xt = (M + h * w->pl.bn - 1) / (h * w->pl.bn) * h;
+        // rows of 128 bytes of the packed scales are 32-bit coordinates
+        if (wt * w->chunks > INT32_MAX / 4 || xt * w->chunks * 2 > INT32_MAX / 4) return false;
+        w->off_x = (size_t)wt * (size_t)w->chunks * 512u;
+        w->off_split = w->off_x + (size_t)xt * (size_t)w->chunks * (size_t)(512 * mx_groups(w->pl.bn));
+        w->bytes = w->off_split + w->pl.ws_bytes;
         return true;
     }
     if (!plan_pair(N, M, (K + 63) / 64, num_sms, smem_optin, 0, (int)kPairABytes, 64, PairCost{300.0, 1.5, 0.0, 1}, &w->pl))
@@ -100,11 +152,28 @@ bool plan_mx(int64_t M, int64_t N, int64_t K, int x_bits, int num_sms, int smem_
     return true;
 }
 
-template <int XB>
-bq_status launch_mx_pair(const DeviceInfo& di, int dev, const PairPlan& pl, const void* xq, const uint8_t* xs, const uint8_t* wq,
-                         const uint8_t* wsc, uint16_t* y, int64_t M, int64_t N, int64_t K, void* ws, cudaStream_t st)
+// The scales of W and x into the layout of the block-scaled product's plan.
+bq_status launch_mx_pack(const MxWs& w, const uint8_t* xs, const uint8_t* wsc, uint8_t* buf, int64_t M, int64_t N, int64_t K,
+                         cudaStream_t st)
 {
-    auto kern = mx_pair_kernel<XB>;
+    MxPackParams p;
+    p.blocks = (int)(K / 32);
+    p.chunks = w.chunks;
+    p.quads = (w.chunks + 3) / 4;
+    p.vec = p.blocks % 16 == 0 ? 16 : p.blocks % 4 == 0 ? 4 : 1;
+    const int groups = mx_groups(w.pl.bn), tok = w.pl.halves * w.pl.bn;
+    p.side[0] = MxPackSide{wsc, buf, (int)N, 128, 1, (N + 255) / 256 * 2 * p.quads};
+    p.side[1] = MxPackSide{xs, buf + w.off_x, (int)M, w.pl.bn, groups, (M + tok - 1) / tok * w.pl.halves * groups * p.quads};
+    const int64_t blocks = (p.side[0].items + p.side[1].items + 7) / 8;
+    return blocks > INT32_MAX ? BQ_ERR_SHAPE : launch_pdl(mx_pack_kernel, (int)blocks, 256, 0, st, p);
+}
+
+template <int XB, int H>
+bq_status launch_mx_pair(const DeviceInfo& di, int dev, const MxWs& w, const void* xq, const uint8_t* wq, uint16_t* y, int64_t M,
+                         int64_t N, int64_t K, uint8_t* buf, cudaStream_t st)
+{
+    const PairPlan& pl = w.pl;
+    auto kern = mx_pair_kernel<XB, H>;
     static bool attr_done[kMaxDevices] = {};
     if (!attr_done[dev]) {
         if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, di.max_smem_optin) != cudaSuccess) {
@@ -113,10 +182,16 @@ bq_status launch_mx_pair(const DeviceInfo& di, int dev, const PairPlan& pl, cons
         }
         attr_done[dev] = true;
     }
-    CUtensorMap ta, tb;
+    CUtensorMap ta, tb, tsa, tsb;
+    const int groups = mx_groups(pl.bn), chunks = mx_chunks(XB, H);
+    const int64_t m_tiles = (M + H * pl.bn - 1) / (H * pl.bn);
     const bool a_ok = XB == 8 ? make_map_spread4(&ta, wq, N, K, 128)
                               : make_map(&ta, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, wq, N, K / 2, 128, 128, CU_TENSOR_MAP_SWIZZLE_128B);
-    if (!a_ok || !make_map(&tb, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, xq, M, K * XB / 8, pl.bn / 2, 128, CU_TENSOR_MAP_SWIZZLE_128B))
+    if (!a_ok || !make_map(&tb, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, xq, M, K * XB / 8, pl.bn / 2, 128, CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !make_map(&tsa, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, buf, (N + 255) / 256 * 2 * w.chunks * 4, 128, 4 * chunks, 128,
+                  CU_TENSOR_MAP_SWIZZLE_NONE) ||
+        !make_map(&tsb, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, buf + w.off_x, m_tiles * H * w.chunks * groups * 4, 128,
+                  4 * chunks * groups, 128, CU_TENSOR_MAP_SWIZZLE_NONE))
         return BQ_ERR_CUDA;
     MxParams p;
     p.q.e.y = y;
@@ -124,22 +199,20 @@ bq_status launch_mx_pair(const DeviceInfo& di, int dev, const PairPlan& pl, cons
     p.q.N = (int)N;
     p.q.bn = pl.bn;
     p.q.stages = pl.stages;
-    p.q.m_tiles = (int)((M + pl.bn - 1) / pl.bn);
+    p.q.m_tiles = (int)m_tiles;
     p.q.tiles = (int)pl.tiles;
     p.q.seg_blocks = pl.split.blocks;
     p.q.segs = 1;
     p.q.split = pl.split;
-    p.q.ws = reinterpret_cast<float*>(ws);
-    p.xs = xs;
-    p.ws = wsc;
-    p.blocks = (int)(K / 32);
-    p.vec = p.blocks % 16 == 0 ? 16 : p.blocks % 4 == 0 ? 4 : 1;
+    p.q.ws = reinterpret_cast<float*>(buf + w.off_split);
+    p.chunks = w.chunks;
+    p.slots = std::min(pl.stages, (512 - 2 * pl.bn) / mx_scale_cols(XB, H, pl.bn));
     // every pair when there are whole rounds before the tail: the units are dealt by pair
     const unsigned grid = 2u * (unsigned)std::min<int64_t>(pl.split.tail && pl.split.dp_tiles ? pl.pairs
                                                            : pl.split.tail ? pl.split.tail_pairs : pl.tiles, pl.pairs);
-    const size_t smem = std::max<size_t>(1024 + (size_t)pl.stages * (pair_stage_bytes(pl.bn) + mx_scale_bytes(XB)) + 512,
+    const size_t smem = std::max<size_t>(1024 + (size_t)pl.stages * mx_stage_bytes(XB, H, pl.bn) + 512,
                                          (size_t)di.max_smem_optin / 2 + 1024);   // one CTA per SM (all of TMEM)
-    const bq_status s = launch_pdl_dim(kern, dim3(grid), kMxThreads, smem, st, ta, tb, p);
+    const bq_status s = launch_pdl_dim(kern, dim3(grid), kMxThreads, smem, st, ta, tb, tsa, tsb, p);
     return s != BQ_OK ? s : launch_reduce<kEpiPlain>(di, pl, p.q, st);
 }
 
@@ -162,9 +235,15 @@ bq_status mx_product(const void* xq, const uint8_t* xs, int x_bits, const uint8_
     if (!plan_mx(M, N, K, x_bits, di.num_sms, di.max_smem_optin, &w)) return BQ_ERR_SHAPE;
     void* buf = nullptr;
     if ((s = epi_workspace(dev, st, workspace, workspace_bytes, w.bytes, &buf)) != BQ_OK) return s;
-    if (w.scaled)
-        return x_bits == 8 ? launch_mx_pair<8>(di, dev, w.pl, xq, xs, wq, ws, y, M, N, K, buf, st)
-                           : launch_mx_pair<4>(di, dev, w.pl, xq, xs, wq, ws, y, M, N, K, buf, st);
+    if (w.scaled) {
+        uint8_t* to = reinterpret_cast<uint8_t*>(buf);
+        if ((s = launch_mx_pack(w, xs, ws, to, M, N, K, st)) != BQ_OK) return s;
+        if (x_bits == 8)
+            return w.pl.halves == 2 ? launch_mx_pair<8, 2>(di, dev, w, xq, wq, y, M, N, K, to, st)
+                                    : launch_mx_pair<8, 1>(di, dev, w, xq, wq, y, M, N, K, to, st);
+        return w.pl.halves == 2 ? launch_mx_pair<4, 2>(di, dev, w, xq, wq, y, M, N, K, to, st)
+                                : launch_mx_pair<4, 1>(di, dev, w, xq, wq, y, M, N, K, to, st);
+    }
     uint8_t* base = reinterpret_cast<uint8_t*>(buf);
     uint16_t *wb = reinterpret_cast<uint16_t*>(base), *xb = reinterpret_cast<uint16_t*>(base + w.off_x);
     if ((s = launch_mx_dequant<4>(wq, ws, wb, N * K, di, st)) != BQ_OK) return s;

@@ -10,23 +10,31 @@
 //   x in E4M3: kind::mxf8f6f4, K = 32; its 4-bit operand lies in shared memory in 8-byte
 //     groups of 16 codes with 8-byte gaps, which the copy makes (16U4_ALIGN16B; it wants rows of whole
 //     128 codes and 32-byte aligned).
-// Either way a stage is one 128-byte swizzle atom per row: 256 elements (4 bits) or 128.
+// Either way a swizzle atom, 128 bytes a row, is 256 elements (4 bits) or 128.
 //
-// Tiles, pairs, units of work and the epilogue are tc_pair.cuh's: 256 rows of W x bn tokens
-// per pair, two accumulators (bn columns each, bn <= 192), so that 512 - 2 bn columns of
-// tensor memory are left for scales.  These live there as the instruction wants them: row r
-// of an operand in lane r % 32, column r / 32, a 32-bit word of the scales of 128
-// consecutive k (the same in all four lane quarters).  Per stage, one warp each for W's
-// 128 rows, tokens 0 .. 127 and tokens 128 .. reads 16 scale bytes of a row at a time (512
-// k), and writes a stage's words, four rows' per lane, as the 16 bytes that tcgen05.cp.32x128b.warpx4
-// takes to the four lane quarters.  Each CTA holds the scales of its own 128 rows and of all of
-// the pair's tokens.
+// Tiles, pairs, units of work and the epilogue's stores are tc_pair.cuh's: 256 rows of W x bn tokens
+// per accumulator and pair, two accumulators (bn columns each, bn <= 192), so that 512 - 2 bn
+// columns of tensor memory are left for scales.  A stage is two products of an atom's k:
+//   H = 1: two atoms along k of both operands; the two accumulators take units in turn;
+//   H = 2: one atom of W and of 2 bn tokens, an accumulator each: a weight tile costs L2 half as
+//     much per token, but the next unit's products wait until the epilogue has read the accumulators.
+// (With one product a stage the barriers set the pace: a turn of the loop from full to empty
+// and back, with no copies, scales or products in it, takes 330 to 450 clocks, the product at
+// 192 tokens 384.)
 //
-// Each pipeline stage has its own columns of scales, freed with it, so a copy never
-// overwrites scales that an earlier product may still read.
+// Scales live in tensor memory as the instruction wants them: row r of an operand in lane
+// r % 32, column r / 32, a 32-bit word of the scales of 128 consecutive k (the same in all four
+// lane quarters), which tcgen05.cp.32x128b.warpx4 takes from 512 consecutive bytes, 16 for each lane.
+// mx_pack_kernel lays both operands' scales out in such units, by tiles and stages, so that a
+// stage's arrive as one copy per operand and accumulator beside the codes.  (Warps of this kernel that gathered
+// them from their rows instead, 16 bytes a row ahead in registers, held the products up: 12288 x
+// 4096, 2048 tokens of 4 bits: 62 us.)  Each CTA holds the scales of its own 128 rows and of all of
+// the pair's tokens.  Tensor memory has room for fewer stages' scales than shared memory: before
+// its copies the MMA warp waits until the products of the stage that used the columns before
+// are done.
 //
-// Barriers of a stage: full (the leader's: both CTAs' copies, and an arrival per scale warp of
-// both), empty (each CTA's own; the MMA's commit arrives on both).
+// Barriers of a stage: full (the leader's: both CTAs' copies), empty (each CTA's own; the MMA's
+// commit arrives on both).
 #pragma once
 
 #include "mx.cuh"
@@ -34,25 +42,30 @@
 
 namespace bq {
 
-constexpr int kMxEpiWarps = 8;
-constexpr int kMxTmaWarp = kMxEpiWarps, kMxMmaWarp = kMxEpiWarps + 1, kMxScaleWarp0 = kMxEpiWarps + 2;
-constexpr int kMxThreads = 32 * (kMxScaleWarp0 + 3);
-constexpr int kMxMaxStages = 8;
+constexpr int kMxEpiWarps = 12;                  // three per lane quarter
+constexpr int kMxTmaWarp = kMxEpiWarps, kMxMmaWarp = kMxEpiWarps + 1;
+constexpr int kMxThreads = 32 * (kMxEpiWarps + 2);
+constexpr int kMxMaxStages = 6;
 constexpr int kMxMaxBn = 192;
 
-// Elements of a stage, its 128-element chunks, shared bytes and tensor-memory columns of its scales
-// (a chunk: 512 bytes and 4 columns for W, twice that for the tokens).
-__host__ __device__ constexpr int mx_stage_k(int xbits) { return xbits == 4 ? 256 : 128; }
-__host__ __device__ constexpr int mx_chunks(int xbits) { return mx_stage_k(xbits) / 128; }
-__host__ __device__ constexpr uint32_t mx_scale_bytes(int xbits) { return 1536u * (uint32_t)mx_chunks(xbits); }
-__host__ __device__ constexpr int mx_scale_cols(int xbits) { return 12 * mx_chunks(xbits); }
+// Elements of an atom, and of a stage; a stage's 128-element chunks; groups of 128 tokens of an accumulator's
+// bn; the 512-byte units of scales of a stage (W's chunks, then each accumulator's), which take
+// 4 columns of tensor memory each; its shared bytes.
+__host__ __device__ constexpr int mx_atom_k(int xbits) { return xbits == 4 ? 256 : 128; }
+__host__ __device__ constexpr int mx_stage_k(int xbits, int h) { return mx_atom_k(xbits) * (h == 1 ? 2 : 1); }
+__host__ __device__ constexpr int mx_chunks(int xbits, int h) { return mx_stage_k(xbits, h) / 128; }
+__host__ __device__ constexpr int mx_groups(int bn) { return bn > 128 ? 2 : 1; }
+__host__ __device__ constexpr int mx_scale_units(int xbits, int h, int bn) { return mx_chunks(xbits, h) * (1 + h * mx_groups(bn)); }
+__host__ __device__ constexpr int mx_scale_cols(int xbits, int h, int bn) { return 4 * mx_scale_units(xbits, h, bn); }
+__host__ __device__ constexpr uint32_t mx_stage_bytes(int xbits, int h, int bn)
+{
+    return kPairABytes * (h == 1 ? 2u : 1u) + (uint32_t)bn * 128u + 512u * (uint32_t)mx_scale_units(xbits, h, bn);
+}
 
 struct MxParams {
-    PairParams q;
-    const uint8_t* xs;         // [M][blocks]
-    const uint8_t* ws;         // [N][blocks]
-    int blocks;                // K / 32
-    int vec;                   // scale bytes of one load: 16, 4 or 1 (what rows are a multiple of)
+    PairParams q;              // m_tiles, tiles, split: of H bn tokens; seg_blocks: stages
+    int chunks;                // of a row, a multiple of a stage's
+    int slots;                 // stages whose scales tensor memory holds, at most the ring's
 };
 
 // One product of the pair, D += A B with the scales at sfa and sfb (tensor memory).
@@ -92,17 +105,16 @@ __host__ __device__ constexpr uint32_t umma_idesc_mx(int M, int N)
     return (XB == 4 ? (1u << 7) | (1u << 10) : 5u << 7) | ((uint32_t)(N >> 3) << 17) | (1u << 23) | ((uint32_t)(M >> 7) << 27);
 }
 
-// Bytes 16 g .. 16 g + 15 of a row of `blocks` scale bytes, zero past its end.
+// ------------------------------------------------------------------ layout of the scales
+// Bytes 16 g .. 16 g + 15 of a row of `blocks` scale bytes, zero past its end.  vec: what row
+// lengths are a multiple of, 16, 4 or 1.
 BQ_DEVINL uint4 load_scales16(const uint8_t* row, int g, int blocks, int vec)
 {
-    uint4 v = make_uint4(0u, 0u, 0u, 0u);
     const int b0 = 16 * g;
-    if (vec == 16) {
-        if (b0 < blocks) v = __ldg(reinterpret_cast<const uint4*>(row + b0));
-        return v;
-    }
     uint32_t w[4] = {0u, 0u, 0u, 0u};
-    if (vec == 4) {
+    if (vec == 16) {
+        return b0 < blocks ? __ldg(reinterpret_cast<const uint4*>(row + b0)) : make_uint4(0u, 0u, 0u, 0u);
+    } else if (vec == 4) {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             if (b0 + 4 * i < blocks) w[i] = __ldg(reinterpret_cast<const uint32_t*>(row + b0 + 4 * i));
@@ -114,26 +126,151 @@ BQ_DEVINL uint4 load_scales16(const uint8_t* row, int g, int blocks, int vec)
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-BQ_DEVINL uint32_t word_of(const uint4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
+// The packed scales are [128 rows of W][chunk] and [accumulator's tile of bn tokens][chunk][group] of units.
+// One operand's rows [rows][blocks] in tiles of `tile` rows, each in `groups` of 128: unit (tile,
+// chunk, group) holds at 16 i + 4 j the word of row 32 j + i of the group (zero beyond the tile and the
+// matrix, and past a row's end).  A warp makes four chunks' units, lane i reading 16 bytes of four rows.
+struct MxPackSide {
+    const uint8_t* src;
+    uint8_t* dst;
+    int rows, tile, groups;
+    int64_t items;             // warps' work: tiles x groups x chunk quadruples
+};
+struct MxPackParams {
+    MxPackSide side[2];
+    int blocks, chunks, quads, vec;
+};
 
-// tm_a: codes of W, boxes of a stage x 128 rows; tm_b: codes of the tokens, boxes of a
-// stage x bn / 2 tokens.
-template <int XB>
+__global__ void __launch_bounds__(256) mx_pack_kernel(const __grid_constant__ MxPackParams p)
+{
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    int64_t item = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+    const int lane = threadIdx.x & 31;
+    const bool second = item >= p.side[0].items;
+    const MxPackSide& q = p.side[second];
+    if (second) item -= p.side[0].items;
+    if (item >= q.items) return;
+    const int quad = (int)(item % p.quads);
+    const int64_t tg = item / p.quads;
+    const int group = (int)(tg % q.groups);
+    const int64_t tile = tg / q.groups;
+    uint4 v[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const int in_tile = 128 * group + 32 * j + lane;
+        const int64_t r = tile * q.tile + in_tile;
+        v[j] = in_tile < q.tile && r < q.rows ? load_scales16(q.src + r * p.blocks, quad, p.blocks, p.vec) : make_uint4(0u, 0u, 0u, 0u);
+    }
+    uint4* to = reinterpret_cast<uint4*>(q.dst + ((tile * p.chunks + 4 * quad) * q.groups + group) * 512) + lane;
+    const int step = 32 * q.groups;
+    to[0] = make_uint4(v[0].x, v[1].x, v[2].x, v[3].x);
+    if (4 * quad + 1 < p.chunks) to[step] = make_uint4(v[0].y, v[1].y, v[2].y, v[3].y);
+    if (4 * quad + 2 < p.chunks) to[2 * step] = make_uint4(v[0].z, v[1].z, v[2].z, v[3].z);
+    if (4 * quad + 3 < p.chunks) to[3 * step] = make_uint4(v[0].w, v[1].w, v[2].w, v[3].w);
+}
+
+// ------------------------------------------------------------------ the product
+// One warp's share of a unit's accumulators: its lane quarter and every third 16 columns, from
+// the idx-th on.  They are read whole, and freed, before anything is stored (H = 2: the next unit's
+// products wait for it), to y rounded to bf16 in registers, to a partial tile one after the other.
+// `left`: tokens of the unit that exist; n: this thread's row of W; m0: the unit's first token; part: the
+// thread's row of the partial tile's first token.  Few instructions per token are what counts: with 64-bit
+// compares and products of the row number the stores of a tile took 7000 clocks, its MMAs 6100.
+constexpr int kMxParts = kMxMaxBn / 16 / (kMxEpiWarps / 4);
+
+BQ_DEVINL void mx_free(uint32_t bar)
+{
+    tc_fence_before();
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive_cluster(bar);
+}
+
+template <int H, typename Wait>
+BQ_DEVINL bool mx_drain(const PairParams& p, uint32_t lane_addr, int acc0, int idx, uint32_t tempty0, int64_t m0, int left, int n,
+                        float* part, Wait&& wait)
+{
+    constexpr int kStep = 16 * (kMxEpiWarps / 4);
+    uint32_t two[H][kMxParts][8];
+#pragma unroll
+    for (int h = 0; h < H; ++h) {
+        const int acc = H == 1 ? acc0 : h;
+        const uint32_t addr = lane_addr + (uint32_t)(acc * p.bn), freed = tempty0 + 8u * (uint32_t)acc;
+        if (!wait(acc)) return false;
+        tc_fence_after();
+        if (part) {
+#pragma unroll 1
+            for (int c = 16 * idx; c < p.bn; c += kStep) {
+                uint32_t v[16];
+                tmem_ld_32x32b_x16(addr + (uint32_t)c, v);
+                tmem_wait_ld();
+                float* to = part + (h * p.bn + c) * 256;
+#pragma unroll
+                for (int j = 0; j < 16; ++j)
+                    if (h * p.bn + c + j < left) to[j * 256] = __uint_as_float(v[j]);
+            }
+            mx_free(freed);
+            continue;
+        }
+#pragma unroll
+        for (int i = 0; i < kMxParts; i += 2) {
+            uint32_t v[2][16];
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+                if (16 * idx + (i + q) * kStep < p.bn) tmem_ld_32x32b_x16(addr + (uint32_t)(16 * idx + (i + q) * kStep), v[q]);
+            tmem_wait_ld();
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    two[h][i + q][j] = pack_bf16x2_rn(__uint_as_float(v[q][2 * j]), __uint_as_float(v[q][2 * j + 1]));
+        }
+        mx_free(freed);
+    }
+    if (part || n >= p.N) return true;
+    const int64_t pitch = p.N;
+#pragma unroll
+    for (int h = 0; h < H; ++h) {
+#pragma unroll
+        for (int i = 0; i < kMxParts; ++i) {
+            const int c = 16 * idx + i * kStep, m = h * p.bn + c;
+            if (c >= p.bn || m >= left) break;
+            uint16_t* y = p.e.y + (m0 + m) * pitch + n;
+            const int rest = left - m;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                if (2 * j < rest) *y = (uint16_t)two[h][i][j];
+                y += pitch;
+                if (2 * j + 1 < rest) *y = (uint16_t)(two[h][i][j] >> 16);
+                y += pitch;
+            }
+        }
+    }
+    return true;
+}
+
+// tm_a: codes of W, boxes of an atom x 128 rows; tm_b: codes of the tokens, boxes of an
+// atom x bn / 2 tokens; tm_sa, tm_sb: their packed scales as rows of 128 bytes (4 a unit), boxes of a stage's
+// units of one operand or accumulator.  (Tiled copies, since only those may complete on the other CTA's barrier.)
+template <int XB, int H>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
 mx_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
+               const __grid_constant__ CUtensorMap tm_sa, const __grid_constant__ CUtensorMap tm_sb,
                const __grid_constant__ MxParams mp)
 {
-    constexpr int kChunks = mx_chunks(XB), kGroup = 4 / kChunks;       // stages of one 16-byte scale load
-    constexpr uint32_t kSfBytes = mx_scale_bytes(XB);
+    constexpr int kChunks = mx_chunks(XB, H);
+    constexpr uint32_t kAStage = kPairABytes * (H == 1 ? 2u : 1u);
     const PairParams& p = mp.q;
     extern __shared__ uint8_t smem_raw[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_ctarank();
     const int S = p.stages;
-    const uint32_t b_bytes = (uint32_t)p.bn * 64u;             // this CTA's half of the token tile
+    const uint32_t b_bytes = (uint32_t)p.bn * 64u;             // this CTA's half of an atom's token tile
     const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
-    const uint32_t a_base = base, b_base = base + (uint32_t)S * kPairABytes, sf_base = b_base + (uint32_t)S * b_bytes;
-    const uint32_t bar_base = sf_base + (uint32_t)S * kSfBytes;
+    const uint32_t a_base = base, b_base = base + (uint32_t)S * kAStage, sf_base = b_base + (uint32_t)S * 2u * b_bytes;
+    const int groups = mx_groups(p.bn);
+    const uint32_t sf_bytes = 512u * (uint32_t)mx_scale_units(XB, H, p.bn);
+    const uint32_t bar_base = sf_base + (uint32_t)S * sf_bytes;
     auto full_bar = [&](int s) { return bar_base + 8u * (uint32_t)s; };
     auto empty_bar = [&](int s) { return bar_base + 8u * (uint32_t)(S + s); };
     auto tfull_bar = [&](int b) { return bar_base + 8u * (uint32_t)(2 * S + b); };
@@ -142,14 +279,13 @@ mx_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__
     const uint32_t tmem_slot = done_bar + 8u;
     volatile uint32_t* tmem_slot_ptr =
         reinterpret_cast<volatile uint32_t*>(smem_raw + (base - smem_u32(smem_raw)) + (tmem_slot - base));
-    const int scale_warps = p.bn > 128 ? 3 : 2;
 
     auto tile_r0 = [&](int t) { return (t / p.m_tiles) * 256 + (int)rank * 128; };   // this CTA's first row of W
-    auto tile_m0 = [&](int t) { return (t % p.m_tiles) * p.bn; };
+    auto tile_m0 = [&](int t) { return (t % p.m_tiles) * (p.bn * H); };
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < S; ++s) {
-            mbar_init(full_bar(s), 1 + 2 * (uint32_t)scale_warps);
+            mbar_init(full_bar(s), 1);
             mbar_init(empty_bar(s), 1);
         }
         for (int b = 0; b < 2; ++b) {
@@ -183,10 +319,26 @@ mx_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__
                 if (!mbar_wait_warp(empty_bar(s), ph ^ 1u)) { ok = false; break; }
                 const uint32_t bar = map_to_cta(full_bar(s), 0);
                 if (elect_one()) {
+                    const uint32_t ad = a_base + (uint32_t)s * kAStage, bd = b_base + (uint32_t)s * 2u * b_bytes;
                     // 16U4_ALIGN16B copies count the packed bytes
-                    if (rank == 0) mbar_arrive_expect_tx(full_bar(s), 2u * ((XB == 4 ? kPairABytes : kPairABytes / 2) + b_bytes));
-                    tma_load_2d_pair(a_base + (uint32_t)s * kPairABytes, &tm_a, bar, it * 128, r0);
-                    tma_load_2d_pair(b_base + (uint32_t)s * b_bytes, &tm_b, bar, it * 128, m0);
+                    if (rank == 0)
+                        mbar_arrive_expect_tx(full_bar(s), 2u * ((XB == 4 ? kAStage : kAStage / 2) + 2u * b_bytes + sf_bytes));
+                    if constexpr (H == 1) {
+                        tma_load_2d_pair(ad, &tm_a, bar, it * 256, r0);
+                        tma_load_2d_pair(bd, &tm_b, bar, it * 256, m0);
+                        tma_load_2d_pair(ad + kPairABytes, &tm_a, bar, it * 256 + 128, r0);
+                        tma_load_2d_pair(bd + b_bytes, &tm_b, bar, it * 256 + 128, m0);
+                    } else {
+                        tma_load_2d_pair(ad, &tm_a, bar, it * 128, r0);
+                        tma_load_2d_pair(bd, &tm_b, bar, it * 128, m0);
+                        tma_load_2d_pair(bd + b_bytes, &tm_b, bar, it * 128, m0 + p.bn);
+                    }
+                    const uint32_t sd = sf_base + (uint32_t)s * sf_bytes, x_bytes = 512u * (uint32_t)(kChunks * groups);
+                    tma_load_2d_pair(sd, &tm_sa, bar, 0, ((r0 >> 7) * mp.chunks + it * kChunks) * 4);
+#pragma unroll
+                    for (int h = 0; h < H; ++h)
+                        tma_load_2d_pair(sd + 512u * kChunks + x_bytes * h, &tm_sb, bar, 0,
+                                         (((u.tile % p.m_tiles) * H + h) * mp.chunks + it * kChunks) * groups * 4);
                 }
                 __syncwarp();
                 ++issued;
@@ -206,111 +358,77 @@ mx_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__
             const uint64_t bd0 = umma_desc_k_sw128(b_base);
             const uint32_t desc_hi = (uint32_t)(bd0 >> 32), b_lo0 = (uint32_t)bd0, a_lo0 = (uint32_t)umma_desc_k_sw128(a_base);
             const uint32_t sf_tmem0 = tmem_base + 2u * (uint32_t)p.bn;
-            int s = 0, lt = 0;
-            uint32_t ph = 0;
+            const int T = mp.slots, sf_cols = mx_scale_cols(XB, H, p.bn);
+            const uint32_t group_cols = 4u * (uint32_t)groups;   // of a chunk of one accumulator's tokens
+            int s = 0, t = 0, lt = 0;                    // stage, slot of its scales, unit
+            int back = S - T;                            // the stage that used the slot before, once that exists
+            int issued = 0;
+            uint32_t ph = 0, ph_back = 1;
             bool ok = true;
             for (PairUnits u(p); ok && u.next(); ++lt) {
-                const int acc = lt & 1;
                 const int kb0 = u.kb0, kb1 = u.kb1;
-                if (!mbar_wait_warp(tempty_bar(acc), ((uint32_t)(lt >> 1) & 1u) ^ 1u)) break;
-                tc_fence_after();
-                const uint32_t d_tmem = tmem_base + (uint32_t)(acc * p.bn);
+                const int acc0 = H == 1 ? lt & 1 : 0;
+                const uint32_t use = H == 1 ? (uint32_t)(lt >> 1) : (uint32_t)lt;
+                if (!mbar_wait_warp(tempty_bar(acc0), (use & 1u) ^ 1u)) break;
                 for (int it = kb0; it < kb1; ++it) {
+                    if (T < S && issued >= T && !mbar_wait_warp(empty_bar(back), ph_back)) { ok = false; break; }
                     if (!mbar_wait_warp(full_bar(s), ph)) { ok = false; break; }
+                    if (H == 2 && it == kb0 && !mbar_wait_warp(tempty_bar(1), (use & 1u) ^ 1u)) { ok = false; break; }
                     tc_fence_after();
                     if (elect_one()) {
-                        const uint32_t sfa = sf_tmem0 + (uint32_t)(s * mx_scale_cols(XB)), sfb = sfa + 4u * kChunks;
-                        const uint32_t sm = sf_base + (uint32_t)s * kSfBytes;
+                        const uint32_t sfa = sf_tmem0 + (uint32_t)(t * sf_cols), sfb = sfa + 4u * kChunks;
+                        const uint32_t sm = sf_base + (uint32_t)s * sf_bytes;
 #pragma unroll
                         for (int c = 0; c < kChunks; ++c) {
                             scales_to_tmem_pair(sfa + 4u * c, sm + 512u * c);
-                            scales_to_tmem_pair(sfb + 8u * c, sm + 512u * kChunks + 1024u * c);
-                            if (p.bn > 128) scales_to_tmem_pair(sfb + 8u * c + 4u, sm + 512u * kChunks + 1024u * c + 512u);
-                        }
-                        const uint32_t al = a_lo0 + (uint32_t)s * (kPairABytes >> 4), bl = b_lo0 + (uint32_t)s * (b_bytes >> 4);
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const int c = XB == 4 ? k >> 1 : 0;
-                            const uint32_t sf = XB == 4 ? 2u * (k & 1) : (uint32_t)k;        // the first scale byte of its word
-                            umma_mx_pair<XB>(d_tmem, al + 2u * k, bl + 2u * k, desc_hi, idesc | sf << 4 | sf << 29, sfa + 4u * c,
-                                             sfb + 8u * c, it > kb0 || k > 0);
+                            for (int h = 0; h < H; ++h) {
+                                const uint32_t hc = (uint32_t)(h * kChunks + c), from = sm + 512u * kChunks + 128u * group_cols * hc;
+                                scales_to_tmem_pair(sfb + group_cols * hc, from);
+                                if (groups == 2) scales_to_tmem_pair(sfb + group_cols * hc + 4u, from + 512u);
+                            }
+                        }
+                        const uint32_t al0 = a_lo0 + (uint32_t)s * (kAStage >> 4), bl0 = b_lo0 + (uint32_t)s * (b_bytes >> 3);
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const uint32_t al = al0 + (H == 1 ? i * (kPairABytes >> 4) : 0u), bl = bl0 + i * (b_bytes >> 4);
+                            const uint32_t d = tmem_base + (uint32_t)((H == 1 ? acc0 : i) * p.bn);
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                const uint32_t c = (H == 1 ? i * (kChunks / 2) : 0) + (XB == 4 ? k >> 1 : 0);
+                                const uint32_t hc = H == 1 ? c : i * kChunks + c;
+                                const uint32_t sf = XB == 4 ? 2u * (k & 1) : (uint32_t)k;        // the first scale byte of its word
+                                umma_mx_pair<XB>(d, al + 2u * k, bl + 2u * k, desc_hi, idesc | sf << 4 | sf << 29, sfa + 4u * c,
+                                                 sfb + group_cols * hc, it > kb0 || k > 0 || (H == 1 && i > 0));
+                            }
+                            if (H == 2 && i == 0 && it + 1 == kb1) umma_commit_pair(tfull_bar(0));
                         }
                         umma_commit_pair(empty_bar(s));
+                        if (it + 1 == kb1) umma_commit_pair(tfull_bar(H == 1 ? acc0 : 1));
                     }
                     __syncwarp();
+                    ++issued;
                     if (++s == S) { s = 0; ph ^= 1u; }
+                    if (++t == T) t = 0;
+                    if (++back == S) { back = 0; ph_back ^= 1u; }
                 }
-                if (elect_one()) umma_commit_pair(tfull_bar(acc));
-                __syncwarp();
             }
             if (elect_one()) umma_commit_leader(done_bar);   // nothing stays in flight past this point
             __syncwarp();
             mbar_wait_warp(done_bar, 0);
         }
-    } else if (warp >= kMxScaleWarp0) {
-        // ---------------- scales ----------------
-        const int which = warp - kMxScaleWarp0;              // W's rows, tokens 0 .. 127, tokens 128 ..
-        if (which < scale_warps) {
-            const uint8_t* src = which == 0 ? mp.ws : mp.xs;
-            const int limit = which == 0 ? p.N : p.M;
-            const uint32_t dst0 = sf_base + (which == 0 ? 0u : 512u * kChunks + 512u * (uint32_t)(which - 1)) + 16u * (uint32_t)lane;
-            int s = 0;
-            uint32_t ph = 0;
-            bool ok = true;
-            for (PairUnits u(p); ok && u.next();) {
-                const int row0 = which == 0 ? tile_r0(u.tile) : tile_m0(u.tile) + 128 * (which - 1);
-                const uint8_t* row[4];
-                bool in[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int r = row0 + 32 * j + lane;
-                    in[j] = r < limit && (which == 0 || 128 * (which - 1) + 32 * j < p.bn);
-                    row[j] = src + (int64_t)(in[j] ? r : 0) * mp.blocks;
-                }
-                uint4 cur[4], next[4];
-                auto load = [&](uint4 (&v)[4], int g) {
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        v[j] = in[j] ? load_scales16(row[j], g, mp.blocks, mp.vec) : make_uint4(0u, 0u, 0u, 0u);
-                };
-                load(next, u.kb0 / kGroup);
-                for (int it = u.kb0; it < u.kb1; ++it) {
-                    const int sub = it & (kGroup - 1);
-                    if (it == u.kb0 || sub == 0) {
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) cur[j] = next[j];
-                        load(next, it / kGroup + 1);
-                    }
-                    if (!mbar_wait_warp(empty_bar(s), ph ^ 1u)) { ok = false; break; }
-                    const uint32_t dst = dst0 + (uint32_t)s * kSfBytes;
-#pragma unroll
-                    for (int c = 0; c < kChunks; ++c) {
-                        const int w = sub * kChunks + c;
-                        st_shared_v4(dst + (which == 0 ? 512u : 1024u) * c, word_of(cur[0], w), word_of(cur[1], w),
-                                     word_of(cur[2], w), word_of(cur[3], w));
-                    }
-                    fence_proxy_async_smem();                // the copy to tensor memory reads through the async proxy
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive_cluster(map_to_cta(full_bar(s), 0));
-                    if (++s == S) { s = 0; ph ^= 1u; }
-                }
-            }
-        }
     } else {
         // ---------------- epilogue ----------------
-        const int q4 = warp & 3, half = warp >> 2;
-        const uint32_t lane_addr0 = tmem_base + ((uint32_t)(32 * q4) << 16);
+        const int q4 = warp & 3, r = 32 * q4 + lane;         // lane quarter, row of this CTA's half of the tile
+        const uint32_t lane_addr = tmem_base + ((uint32_t)(32 * q4) << 16), tempty0 = map_to_cta(tempty_bar(0), 0);
         int lt = 0;
-        for (PairUnits u(p); u.next(); ++lt) {
-            const int t = u.tile, acc = lt & 1;
-            const int r = 32 * q4 + lane;                    // row of this CTA's half of the tile
-            float* part = u.slot < 0 ? nullptr : p.ws + (int64_t)u.slot * ((int64_t)p.bn * 256) + (int)rank * 128 + r;
-            if (!mbar_wait_warp(tfull_bar(acc), (uint32_t)(lt >> 1) & 1u)) break;
-            tc_fence_after();
-            pair_drain<kEpiPlain>(p, lane_addr0 + (uint32_t)(acc * p.bn), tile_m0(t), tile_r0(t) + r, part, half, 2);
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(map_to_cta(tempty_bar(acc), 0));
+        bool ok = true;
+        for (PairUnits u(p); ok && u.next(); ++lt) {
+            const int m0 = tile_m0(u.tile);
+            float* part = u.slot < 0 ? nullptr : p.ws + (int64_t)u.slot * H * ((int64_t)p.bn * 256) + (int)rank * 128 + r;
+            ok = mx_drain<H>(p, lane_addr, lt & 1, warp >> 2, tempty0, m0, p.M - m0, tile_r0(u.tile) + r, part, [&](int acc) {
+                return mbar_wait_warp(tfull_bar(acc), (uint32_t)(H == 1 ? lt >> 1 : lt) & 1u);
+            });
         }
     }
     __syncwarp();
