@@ -26,6 +26,7 @@
 #include "gemv_ring.cuh"
 #include "mx.cuh"
 #include "mx_pair.cuh"
+#include "mx_decode.cuh"
 #include "norm.cuh"
 
 namespace bq {

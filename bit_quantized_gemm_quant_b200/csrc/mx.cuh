@@ -194,4 +194,20 @@ mx_dequant_kernel(const uint8_t* __restrict__ codes, const uint8_t* __restrict__
         reinterpret_cast<uint4*>(out)[i] = mx_dequant8<BITS>(codes, scales[i >> 2], 8 * i);
 }
 
+// Rows of 16-byte units to longer ones, zeros behind: [rows][in] to [rows][out] units.  (Codes of W for
+// products whose copies want rows of whole 128 codes.)
+__global__ void __launch_bounds__(256)
+mx_pad_kernel(const uint4* __restrict__ from, uint4* __restrict__ to, int64_t rows, int in, int out)
+{
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int64_t n = rows * out;
+#pragma unroll 4
+    for (int64_t i = blockIdx.x * (int64_t)256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
+        const int64_t r = i / out;
+        const int c = (int)(i - r * out);
+        to[i] = c < in ? ldg_stream(from + r * in + c) : make_uint4(0u, 0u, 0u, 0u);
+    }
+}
+
 }  // namespace bq

@@ -1,0 +1,267 @@
+// mx_decode.cuh -- the product of microscaled activations and weights at decode sizes (up to 64
+// tokens), in one launch.
+//
+//   D[n][m] = sum_k W[n][k] x[m][k],  each a code times its block's power of two
+//
+// The products are mx_pair.cuh's, on single SMs: 128 rows of W x bn tokens per CTA, K dealt
+// to the C CTAs of a cluster in ranges of whole stages (a stage is one 128-byte swizzle atom
+// per row: 256 elements of 4-bit activations, 128 of 8-bit ones).  The tensor cores read the packed weights, so a
+// decode step has no unpacking to do and is bound by streaming W from HBM; what counts is that
+// enough of it is in flight (all of a CTA's range, up to the ring's depth, is asked for at the start, and two CTAs
+// share an SM), and that nothing but the stream stands between launch and result: the
+// scales go from their rows to shared memory in the layout of tcgen05.cp while the codes arrive (asked
+// for first: behind a range of codes in the memory's queues they took 3000 clocks), and the cluster's
+// CTAs write their partial products into the shared memory of the CTA that adds them, in rank order.
+//
+// Scales: thread t reads row t's bytes of the CTA's range (tokens: thread t token t).
+// Word of row r and chunk c (128 elements): 512 c + 16 (r % 32) + 4 (r / 32).
+#pragma once
+
+#include "mx_pair.cuh"
+
+namespace bq {
+
+constexpr int kMdThreads = 128;               // 4 warps: scales, then epilogue; between them warp 0 copies, warp 1 issues MMAs
+constexpr int kMdMaxM = 64;
+constexpr int kMdMaxStages = 8;
+constexpr int kMdMaxChunks = 64;              // of a CTA's range
+constexpr int kMdTmemCols = 256;              // D: 64, scales from 64: 8 per chunk
+
+__host__ __device__ constexpr int md_chunks(int xbits) { return mx_atom_k(xbits) / 128; }
+__host__ __device__ constexpr uint32_t md_stage_bytes(int bn) { return kPairABytes + (uint32_t)bn * 128u; }
+
+struct MdParams {
+    const uint8_t* xs;         // [M][blocks]
+    const uint8_t* ws;         // [N][blocks]
+    uint16_t* y;
+    int M, N;
+    int bn;                    // a multiple of 16, at least M
+    int blocks, vec;           // K / 32; scale bytes of one load (16, 4 or 1)
+    int nk, log_cluster;       // stages of K, CTAs that share them (a power of two)
+    int stages;                // of the ring
+    int range_chunks;          // chunks of the longest range
+};
+
+// One product on this SM, D += A B with the scales at sfa and sfb (tensor memory).
+template <int XB>
+BQ_DEVINL void umma_mx(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t hi, uint32_t idesc, uint32_t sfa, uint32_t sfb,
+                       uint32_t accumulate)
+{
+    if constexpr (XB == 4)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\tsetp.ne.b32 p, %7, 0;\n\t"
+            "mov.b64 da, {%1, %3};\n\tmov.b64 db, {%2, %3};\n\t"
+            "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], da, db, %4, [%5], [%6], p;\n\t}"
+            ::"r"(d), "r"(a_lo), "r"(b_lo), "r"(hi), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate) : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\tsetp.ne.b32 p, %7, 0;\n\t"
+            "mov.b64 da, {%1, %3};\n\tmov.b64 db, {%2, %3};\n\t"
+            "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], da, db, %4, [%5], [%6], p;\n\t}"
+            ::"r"(d), "r"(a_lo), "r"(b_lo), "r"(hi), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate) : "memory");
+}
+
+BQ_DEVINL void scales_to_tmem(uint32_t taddr, uint32_t smem)
+{
+    const uint64_t desc = (uint64_t)((smem >> 4) & 0x3FFFu) | (uint64_t)1u << 16 | (uint64_t)(128u >> 4) << 32 | (uint64_t)1u << 46;
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+}
+
+BQ_DEVINL void st_cluster_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d)
+{
+    asm volatile("st.shared::cluster.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+
+// A cluster's CTA makes the sums of 128 / (its size) rows of the tile, from partial sums
+// [rank][row][token] (fp32; rows of whole fours of tokens, and four more so that 16-byte accesses
+// of neighbouring rows meet other banks): their bytes.
+__host__ __device__ constexpr int md_sum_pitch(int m) { return (m + 3) / 4 * 4 + 4; }
+__host__ __device__ constexpr uint32_t md_sum_bytes(int c, int m) { return c == 1 ? 0u : 128u * (uint32_t)md_sum_pitch(m) * 4u; }
+
+// Dynamic shared memory: ring (1024-aligned), scales of W and of the tokens (512 bytes a chunk
+// each), partial sums.
+template <int XB>
+__global__ void __launch_bounds__(kMdThreads)
+mx_decode_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
+                 const __grid_constant__ MdParams p)
+{
+    constexpr int kChunks = md_chunks(XB);
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ __align__(8) uint64_t bars[2 * kMdMaxStages + 1];
+    __shared__ uint32_t tmem_slot;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+    const int S = p.stages;
+    const uint32_t b_bytes = (uint32_t)p.bn * 128u;
+    const uint32_t a_base = base, b_base = base + (uint32_t)S * kPairABytes;
+    const uint32_t sfa_base = b_base + (uint32_t)S * b_bytes, sfb_base = sfa_base + 512u * (uint32_t)p.range_chunks;
+    const uint32_t sum_base = sfb_base + 512u * (uint32_t)p.range_chunks;
+    auto full_bar = [&](int s) { return smem_u32(&bars[s]); };
+    auto empty_bar = [&](int s) { return smem_u32(&bars[kMdMaxStages + s]); };
+    const uint32_t done_bar = smem_u32(&bars[2 * kMdMaxStages]);
+
+    // (From blockIdx, not from the cluster's registers: the range, and with it the MMA warp's loop and
+    // operands, stay in uniform registers; else a stage took 640 clocks to issue.)
+    const uint32_t csize = 1u << p.log_cluster, rank = blockIdx.x & (csize - 1u);
+    const int r0 = (int)(blockIdx.x >> p.log_cluster) * 128;
+    const int kb0 = (int)((int64_t)p.nk * rank >> p.log_cluster), kb1 = (int)((int64_t)p.nk * (rank + 1) >> p.log_cluster);
+    const int n_stages = kb1 - kb0;                          // at least 1
+
+    if (tid == 0) {
+        for (int s = 0; s < S; ++s) {
+            mbar_init(full_bar(s), 1);
+            mbar_init(empty_bar(s), 1);
+        }
+        mbar_init(done_bar, 1);
+        fence_barrier_init();
+        fence_proxy_async_smem();
+    }
+    if (warp == 1) {
+        tmem_alloc(smem_u32(&tmem_slot), kMdTmemCols);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = tmem_slot;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+    if (csize > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    auto copy_stage = [&](int i, int s) {                    // stage i of the range into slot s
+        const int x = (kb0 + i) * 128;                       // bytes, or elements of the spread codes
+        mbar_arrive_expect_tx(full_bar(s), (XB == 4 ? kPairABytes : kPairABytes / 2) + b_bytes);
+        tma_load_2d(a_base + (uint32_t)s * kPairABytes, &tm_a, full_bar(s), x, r0);
+        tma_load_2d(b_base + (uint32_t)s * b_bytes, &tm_b, full_bar(s), x, 0);
+    };
+
+    {
+        // ---------------- scales ----------------
+        // chunk c of the range is chunk kb0 kChunks + c of the row; 16 bytes of a row (four
+        // chunks) at a time from a multiple of four chunks on, a batch's loads in flight together,
+        // the first one's before the codes are asked for
+        constexpr int kBatch = 4;
+        const int c0 = kb0 * kChunks, nc = n_stages * kChunks;
+        const bool live[2] = {r0 + tid < p.N, tid < p.M};
+        const uint32_t dst = 16u * (uint32_t)lane + 4u * (uint32_t)warp;
+        for (int g0 = c0 >> 2; 4 * g0 < c0 + nc; g0 += kBatch) {
+            uint4 v[2][kBatch];
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i)
+#pragma unroll
+                for (int side = 0; side < 2; ++side)
+                    v[side][i] = !live[side] || 4 * (g0 + i) >= c0 + nc ? make_uint4(0u, 0u, 0u, 0u)
+                                 : side == 0 ? load_scales16(p.ws, r0 + tid, p.N, g0 + i, p.blocks, p.vec)
+                                             : load_scales16(p.xs, tid, p.M, g0 + i, p.blocks, p.vec);
+            if (warp == 0 && g0 == c0 >> 2 && elect_one())
+                for (int i = 0; i < S && i < n_stages; ++i) copy_stage(i, i);
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int c = 4 * (g0 + i) + j - c0;
+                    if (c < 0 || c >= nc) continue;
+#pragma unroll
+                    for (int side = 0; side < 2; ++side) {
+                        const uint32_t w = j == 0 ? v[side][i].x : j == 1 ? v[side][i].y : j == 2 ? v[side][i].z : v[side][i].w;
+                        if (side == 0 || tid < p.bn)
+                            asm volatile("st.shared.u32 [%0], %1;" ::"r"((side == 0 ? sfa_base : sfb_base) + dst + 512u * (uint32_t)c), "r"(w)
+                                         : "memory");
+                    }
+                }
+        }
+        fence_proxy_async_smem();                            // the copy to tensor memory reads through the async proxy
+        __syncthreads();
+        if (warp == 0) {
+            // ---------------- the rest of the range ----------------
+            for (int i = S; i < n_stages; ++i) {
+                if (!mbar_wait_warp(empty_bar(i % S), (uint32_t)(i / S - 1) & 1u)) break;
+                if (elect_one()) copy_stage(i, i % S);
+                __syncwarp();
+            }
+        } else if (warp == 1) {
+            // ---------------- MMA issuer ----------------
+            const uint32_t idesc = umma_idesc_mx<XB>(128, p.bn);
+            const uint64_t bd0 = umma_desc_k_sw128(b_base);
+            const uint32_t desc_hi = (uint32_t)(bd0 >> 32), b_lo0 = (uint32_t)bd0, a_lo0 = (uint32_t)umma_desc_k_sw128(a_base);
+            int s = 0;
+            uint32_t ph = 0;
+            for (int i = 0; i < n_stages; ++i) {
+                if (!mbar_wait_warp(full_bar(s), ph)) break;
+                tc_fence_after();
+                if (elect_one()) {
+                    const uint32_t sf = tmem + (uint32_t)kMdMaxM + (uint32_t)(s * kChunks) * 8u;
+#pragma unroll
+                    for (int c = 0; c < kChunks; ++c) {
+                        scales_to_tmem(sf + 8u * c, sfa_base + 512u * (uint32_t)(i * kChunks + c));
+                        scales_to_tmem(sf + 8u * c + 4u, sfb_base + 512u * (uint32_t)(i * kChunks + c));
+                    }
+                    const uint32_t al = a_lo0 + (uint32_t)s * (kPairABytes >> 4), bl = b_lo0 + (uint32_t)s * (b_bytes >> 4);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const uint32_t at = sf + (XB == 4 ? 8u * (k >> 1) : 0u);
+                        const uint32_t id = XB == 4 ? 2u * (k & 1) : (uint32_t)k;
+                        umma_mx<XB>(tmem, al + 2u * k, bl + 2u * k, desc_hi, idesc | id << 4 | id << 29, at, at + 4u, i > 0 || k > 0);
+                    }
+                    umma_commit(empty_bar(s));
+                    if (i + 1 == n_stages) umma_commit(done_bar);
+                }
+                __syncwarp();
+                if (++s == S) { s = 0; ph ^= 1u; }
+            }
+        }
+    }
+    __syncwarp();
+
+    // ---------------- epilogue: row r0 + tid ----------------
+    const bool ok = mbar_wait_warp(done_bar, 0);
+    tc_fence_after();
+    if (csize > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");     // every CTA of the cluster runs
+    const int log_share = 7 - p.log_cluster, share = 1 << log_share, pitch = md_sum_pitch(p.M);
+    if (ok) {
+        const uint32_t lane_addr = tmem + ((uint32_t)(32 * warp) << 16);
+        const int n = r0 + tid, owner = tid >> log_share;
+        const uint32_t to = csize == 1 ? 0u
+                                       : map_to_cta(sum_base + (uint32_t)((((int)rank << log_share) + tid - (owner << log_share)) * pitch) * 4u,
+                                                    (uint32_t)owner);
+        for (int c = 0; c < p.M; c += 16) {
+            uint32_t v[16];
+            tmem_ld_32x32b_x16(lane_addr + (uint32_t)c, v);
+            tmem_wait_ld();
+            if (csize > 1) {
+#pragma unroll
+                for (int j = 0; j < 16; j += 4)
+                    if (c + j < p.M) st_cluster_v4(to + (uint32_t)(c + j) * 4u, v[j], v[j + 1], v[j + 2], v[j + 3]);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 16; ++j)
+                    if (n < p.N && c + j < p.M) p.y[(int64_t)(c + j) * p.N + n] = (uint16_t)f32_to_bf16_bits(__uint_as_float(v[j]));
+            }
+        }
+    }
+    __syncwarp();
+    if (csize > 1) {
+        cluster_sync_all();                                  // (after a timeout the sums are not valid)
+        for (int i = tid; i < (p.M + 3) / 4 << log_share; i += kMdThreads) {
+            const int r = i & (share - 1), m = 4 * (i >> log_share), n = r0 + ((int)rank << log_share) + r;
+            float sum[4] = {0.f, 0.f, 0.f, 0.f};
+            for (uint32_t q = 0; q < csize; ++q) {
+                const uint4 v = ld_shared_v4(sum_base + (uint32_t)(((q << log_share) + r) * pitch + m) * 4u);
+                sum[0] += __uint_as_float(v.x);
+                sum[1] += __uint_as_float(v.y);
+                sum[2] += __uint_as_float(v.z);
+                sum[3] += __uint_as_float(v.w);
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (n < p.N && m + j < p.M) p.y[(int64_t)(m + j) * p.N + n] = (uint16_t)f32_to_bf16_bits(sum[j]);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 1) tmem_dealloc(tmem, kMdTmemCols);
+}
+
+}  // namespace bq

@@ -70,13 +70,140 @@ bool make_map_spread4(CUtensorMap* m, const void* ptr, int64_t rows, int64_t K, 
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Workspace of the block-scaled product: the packed scales of W and of x, the partial sums of
-// split tiles.  Of the bf16 pair: W, then x, then the partial sums.
+// ------------------------------------------------------------------ decode sizes
+constexpr int kMdMaxSmem = 116 * 1024;
+
+struct MdPlan {
+    int log_cluster = 0, stages = 0, nk = 0, range = 0;      // range: the longest, in stages
+    size_t smem = 0;
+};
+
+// Clusters of 2^l CTAs that run at once with one CTA on an SM (what the GPCs' sizes leave; a B200's
+// where there is no device).
+int md_clusters(int l)
+{
+    static const int b200[4] = {148, 74, 33, 15};
+    static int found[kMaxDevices][4] = {};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) {
+        cudaGetLastError();
+        return b200[l];
+    }
+    std::lock_guard<std::mutex> lk(g_mu);
+    int& v = found[dev][l];
+    if (v == 0) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(256u << l);
+        cfg.blockDim = dim3(kMdThreads);
+        cfg.dynamicSmemBytes = kMdMaxSmem;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = 1u << l;
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        auto kern = mx_decode_kernel<4>;
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMdMaxSmem) != cudaSuccess ||
+            cudaOccupancyMaxActiveClusters(&v, kern, &cfg) != cudaSuccess || v < 1)
+            v = b200[l];
+        cudaGetLastError();
+    }
+    return v;
+}
+
+// The CTAs of a cluster that share a tile's K, by the rounds of clusters that the device needs, and in each
+// the stages of a CTA and of the busiest SM beside what a round costs anyhow (about ten stages' time).  Two CTAs may share an SM, and never three (each holds half of the tensor
+// memory, and a cluster that waited for a third one's could wait for itself).  12288 x 4096, one token, 4 bits: 9.9 us
+// with one CTA a tile, 8.5 with two, 13.5 with three (90 of 96 clusters fit); 2048 x 8192: 6.9 with 4, 6.0 with 8.
+bool plan_md(int64_t M, int64_t N, int64_t K, int xbits, int num_sms, int smem_optin, MdPlan* pl)
+{
+    if (M > kMdMaxM) return false;
+    const int64_t rt = (N + 127) / 128, nk = (K + mx_atom_k(xbits) - 1) / mx_atom_k(xbits);
+    const int bn = (int)((M + 15) / 16 * 16), chunks = md_chunks(xbits);
+    const int64_t room = smem_optin / 2 - 3072;                               // two CTAs on an SM
+    double best = 1e300;
+    for (int l = 0; l <= 3 && (1 << l) <= nk; ++l) {
+        const int c = 1 << l;
+        const int64_t range = (nk + c - 1) / c, fixed = range * chunks * 1024 + (int64_t)md_sum_bytes(c, (int)M);
+        const int64_t stages = std::min<int64_t>(std::min<int64_t>(kMdMaxStages, range), (room - fixed) / md_stage_bytes(bn));
+        if (range * chunks > kMdMaxChunks || room < fixed || stages < std::min<int64_t>(2, range)) continue;
+        const int64_t fit = 2 * (int64_t)md_clusters(l), rounds = (rt + fit - 1) / fit;
+        const int64_t per_sm = (std::min(rt, fit) * c + num_sms - 1) / num_sms;
+        const double cost = (double)rounds * ((double)(range * (1 + per_sm)) / 2.0 + 10.0);
+        if (cost >= best) continue;
+        best = cost;
+        pl->log_cluster = l;
+        pl->range = (int)range;
+        pl->stages = (int)stages;
+        pl->smem = std::max<size_t>((size_t)(1024 + stages * (int64_t)md_stage_bytes(bn) + fixed), 79872);
+    }
+    if (best == 1e300 || rt << pl->log_cluster > INT32_MAX) return false;
+    pl->nk = (int)nk;
+    return true;
+}
+
+template <int XB>
+bq_status launch_md(int dev, const MdPlan& pl, const void* xq, const uint8_t* xs, const uint8_t* wq, int64_t w_k,
+                    const uint8_t* wsc, uint16_t* y, int64_t M, int64_t N, int64_t K, cudaStream_t st)
+{
+    auto kern = mx_decode_kernel<XB>;
+    static bool attr_done[kMaxDevices] = {};
+    if (!attr_done[dev]) {
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMdMaxSmem) != cudaSuccess) {
+            cudaGetLastError();
+            return BQ_ERR_CUDA;
+        }
+        attr_done[dev] = true;
+    }
+    MdParams p;
+    p.bn = (int)((M + 15) / 16 * 16);
+    CUtensorMap ta, tb;
+    const bool a_ok = XB == 4 ? make_map(&ta, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, wq, N, K / 2, 128, 128, CU_TENSOR_MAP_SWIZZLE_128B)
+                              : make_map_spread4(&ta, wq, N, w_k, 128);
+    if (!a_ok || !make_map(&tb, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, xq, M, K * XB / 8, p.bn, 128, CU_TENSOR_MAP_SWIZZLE_128B))
+        return BQ_ERR_CUDA;
+    p.xs = xs;
+    p.ws = wsc;
+    p.y = y;
+    p.M = (int)M;
+    p.N = (int)N;
+    p.blocks = (int)(K / 32);
+    p.vec = p.blocks % 16 == 0 ? 16 : p.blocks % 4 == 0 ? 4 : 1;
+    p.nk = pl.nk;
+    p.log_cluster = pl.log_cluster;
+    p.stages = pl.stages;
+    p.range_chunks = pl.range * md_chunks(XB);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((N + 127) / 128) << pl.log_cluster);
+    cfg.blockDim = dim3(kMdThreads);
+    cfg.dynamicSmemBytes = pl.smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = 1u << pl.log_cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    if (cudaLaunchKernelEx(&cfg, kern, ta, tb, p) != cudaSuccess) {
+        cudaGetLastError();
+        return BQ_ERR_CUDA;
+    }
+    return launch_status();
+}
+
+// Workspace: W's codes in rows of whole 128 where the copies want them (K % 128 != 0 with 8-bit
+// activations; its rows have `k` elements then), and on pairs of SMs the packed scales of W and of
+// x and the partial sums of split tiles.
 struct MxWs {
     PairPlan pl;
-    bool scaled = false;            // the block-scaled product
+    MdPlan md;
+    bool decode = false;            // up to 64 tokens, one launch; else pairs of SMs
+    bool pad = false;
+    int64_t k = 0;
     int chunks = 0;                 // 128-element chunks of a row, whole stages
-    size_t off_x = 0, off_split = 0, bytes = 0;
+    size_t off_w = 0, off_x = 0, off_split = 0, bytes = 0;
 };
 
 // Token tile, tiles per unit (halves) and split of the last round of the block-scaled product, by the least cost of
@@ -127,27 +254,22 @@ bool plan_mx_pair(int64_t N, int64_t M, int64_t K, int xbits, int num_sms, int s
     return pl->stages >= 2 && pl->tiles <= INT32_MAX / 256;
 }
 
-// The block-scaled product takes any K with 4-bit activations, and rows of whole 128 elements
-// with 8-bit ones (what the copy that spreads the codes wants); the rest goes through bf16.
 bool plan_mx(int64_t M, int64_t N, int64_t K, int x_bits, int num_sms, int smem_optin, MxWs* w)
 {
-    w->scaled = x_bits == 4 || K % 128 == 0;
-    if (w->scaled) {
-        if (!plan_mx_pair(N, M, K, x_bits, num_sms, smem_optin, &w->pl)) return false;
-        const int h = w->pl.halves;
-        w->chunks = w->pl.split.blocks * mx_chunks(x_bits, h);
-        const int64_t wt = (N + 255) / 256 * 2, xt = (M + h * w->pl.bn - 1) / (h * w->pl.bn) * h;
-        // rows of 128 bytes of the packed scales are 32-bit coordinates
-        if (wt * w->chunks > INT32_MAX / 4 || xt * w->chunks * 2 > INT32_MAX / 4) return false;
-        w->off_x = (size_t)wt * (size_t)w->chunks * 512u;
-        w->off_split = w->off_x + (size_t)xt * (size_t)w->chunks * (size_t)(512 * mx_groups(w->pl.bn));
-        w->bytes = w->off_split + w->pl.ws_bytes;
-        return true;
-    }
-    if (!plan_pair(N, M, (K + 63) / 64, num_sms, smem_optin, 0, (int)kPairABytes, 64, PairCost{300.0, 1.5, 0.0, 1}, &w->pl))
-        return false;
-    w->off_x = up256((size_t)N * (size_t)K * 2u);
-    w->off_split = w->off_x + up256((size_t)M * (size_t)K * 2u);
+    w->pad = x_bits == 8 && K % 128 != 0;
+    w->k = w->pad ? (K + 127) / 128 * 128 : K;
+    w->off_w = w->pad ? up256((size_t)N * (size_t)w->k / 2) : 0u;
+    w->decode = plan_md(M, N, K, x_bits, num_sms, smem_optin, &w->md);
+    w->bytes = w->off_w;
+    if (w->decode) return true;
+    if (!plan_mx_pair(N, M, K, x_bits, num_sms, smem_optin, &w->pl)) return false;
+    const int h = w->pl.halves;
+    w->chunks = w->pl.split.blocks * mx_chunks(x_bits, h);
+    const int64_t wt = (N + 255) / 256 * 2, xt = (M + h * w->pl.bn - 1) / (h * w->pl.bn) * h;
+    // rows of 128 bytes of the packed scales are 32-bit coordinates
+    if (wt * w->chunks > INT32_MAX / 4 || xt * w->chunks * 2 > INT32_MAX / 4) return false;
+    w->off_x = w->off_w + (size_t)wt * (size_t)w->chunks * 512u;
+    w->off_split = w->off_x + (size_t)xt * (size_t)w->chunks * (size_t)(512 * mx_groups(w->pl.bn));
     w->bytes = w->off_split + w->pl.ws_bytes;
     return true;
 }
@@ -162,7 +284,7 @@ bq_status launch_mx_pack(const MxWs& w, const uint8_t* xs, const uint8_t* wsc, u
     p.quads = (w.chunks + 3) / 4;
     p.vec = p.blocks % 16 == 0 ? 16 : p.blocks % 4 == 0 ? 4 : 1;
     const int groups = mx_groups(w.pl.bn), tok = w.pl.halves * w.pl.bn;
-    p.side[0] = MxPackSide{wsc, buf, (int)N, 128, 1, (N + 255) / 256 * 2 * p.quads};
+    p.side[0] = MxPackSide{wsc, buf + w.off_w, (int)N, 128, 1, (N + 255) / 256 * 2 * p.quads};
     p.side[1] = MxPackSide{xs, buf + w.off_x, (int)M, w.pl.bn, groups, (M + tok - 1) / tok * w.pl.halves * groups * p.quads};
     const int64_t blocks = (p.side[0].items + p.side[1].items + 7) / 8;
     return blocks > INT32_MAX ? BQ_ERR_SHAPE : launch_pdl(mx_pack_kernel, (int)blocks, 256, 0, st, p);
@@ -185,10 +307,10 @@ bq_status launch_mx_pair(const DeviceInfo& di, int dev, const MxWs& w, const voi
     CUtensorMap ta, tb, tsa, tsb;
     const int groups = mx_groups(pl.bn), chunks = mx_chunks(XB, H);
     const int64_t m_tiles = (M + H * pl.bn - 1) / (H * pl.bn);
-    const bool a_ok = XB == 8 ? make_map_spread4(&ta, wq, N, K, 128)
+    const bool a_ok = XB == 8 ? make_map_spread4(&ta, wq, N, w.k, 128)
                               : make_map(&ta, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, wq, N, K / 2, 128, 128, CU_TENSOR_MAP_SWIZZLE_128B);
     if (!a_ok || !make_map(&tb, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, xq, M, K * XB / 8, pl.bn / 2, 128, CU_TENSOR_MAP_SWIZZLE_128B) ||
-        !make_map(&tsa, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, buf, (N + 255) / 256 * 2 * w.chunks * 4, 128, 4 * chunks, 128,
+        !make_map(&tsa, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, buf + w.off_w, (N + 255) / 256 * 2 * w.chunks * 4, 128, 4 * chunks, 128,
                   CU_TENSOR_MAP_SWIZZLE_NONE) ||
         !make_map(&tsb, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, buf + w.off_x, m_tiles * H * w.chunks * groups * 4, 128,
                   4 * chunks * groups, 128, CU_TENSOR_MAP_SWIZZLE_NONE))
@@ -235,24 +357,23 @@ bq_status mx_product(const void* xq, const uint8_t* xs, int x_bits, const uint8_
     if (!plan_mx(M, N, K, x_bits, di.num_sms, di.max_smem_optin, &w)) return BQ_ERR_SHAPE;
     void* buf = nullptr;
     if ((s = epi_workspace(dev, st, workspace, workspace_bytes, w.bytes, &buf)) != BQ_OK) return s;
-    if (w.scaled) {
-        uint8_t* to = reinterpret_cast<uint8_t*>(buf);
-        if ((s = launch_mx_pack(w, xs, ws, to, M, N, K, st)) != BQ_OK) return s;
-        if (x_bits == 8)
-            return w.pl.halves == 2 ? launch_mx_pair<8, 2>(di, dev, w, xq, wq, y, M, N, K, to, st)
-                                    : launch_mx_pair<8, 1>(di, dev, w, xq, wq, y, M, N, K, to, st);
-        return w.pl.halves == 2 ? launch_mx_pair<4, 2>(di, dev, w, xq, wq, y, M, N, K, to, st)
-                                : launch_mx_pair<4, 1>(di, dev, w, xq, wq, y, M, N, K, to, st);
+    uint8_t* to = reinterpret_cast<uint8_t*>(buf);
+    if (w.pad) {
+        const int in = (int)(K / 32), out = (int)(w.k / 32);          // 16-byte units of a row
+        s = launch_pdl(mx_pad_kernel, grid_for(N * out / 4, 256, di), 256, 0, st, reinterpret_cast<const uint4*>(wq),
+                       reinterpret_cast<uint4*>(to), N, in, out);
+        if (s != BQ_OK) return s;
+        wq = to;
     }
-    uint8_t* base = reinterpret_cast<uint8_t*>(buf);
-    uint16_t *wb = reinterpret_cast<uint16_t*>(base), *xb = reinterpret_cast<uint16_t*>(base + w.off_x);
-    if ((s = launch_mx_dequant<4>(wq, ws, wb, N * K, di, st)) != BQ_OK) return s;
-    s = x_bits == 8 ? launch_mx_dequant<8>(reinterpret_cast<const uint8_t*>(xq), xs, xb, M * K, di, st)
-                    : launch_mx_dequant<4>(reinterpret_cast<const uint8_t*>(xq), xs, xb, M * K, di, st);
-    if (s != BQ_OK) return s;
-    EpiParams e;
-    e.y = y;
-    return launch_pair<false, kEpiPlain>(di, dev, w.pl, &wb, &xb, 1, N, N, M, K, K, e, base + w.off_split, st);
+    if (w.decode)
+        return x_bits == 8 ? launch_md<8>(dev, w.md, xq, xs, wq, w.k, ws, y, M, N, K, st)
+                           : launch_md<4>(dev, w.md, xq, xs, wq, w.k, ws, y, M, N, K, st);
+    if ((s = launch_mx_pack(w, xs, ws, to, M, N, K, st)) != BQ_OK) return s;
+    if (x_bits == 8)
+        return w.pl.halves == 2 ? launch_mx_pair<8, 2>(di, dev, w, xq, wq, y, M, N, K, to, st)
+                                : launch_mx_pair<8, 1>(di, dev, w, xq, wq, y, M, N, K, to, st);
+    return w.pl.halves == 2 ? launch_mx_pair<4, 2>(di, dev, w, xq, wq, y, M, N, K, to, st)
+                            : launch_mx_pair<4, 1>(di, dev, w, xq, wq, y, M, N, K, to, st);
 }
 
 // ------------------------------------------------------------------ its gradient

@@ -106,24 +106,41 @@ __host__ __device__ constexpr uint32_t umma_idesc_mx(int M, int N)
 }
 
 // ------------------------------------------------------------------ layout of the scales
-// Bytes 16 g .. 16 g + 15 of a row of `blocks` scale bytes, zero past its end.  vec: what row
-// lengths are a multiple of, 16, 4 or 1.
-BQ_DEVINL uint4 load_scales16(const uint8_t* row, int g, int blocks, int vec)
+// Bytes 16 g .. 16 g + 15 of row r of scales [rows][blocks] (16-byte aligned), zero past the row's
+// end.  vec: what row lengths are a multiple of, 16, 4 or 1 (then by aligned words, shifted; the last
+// row's last one byte by byte, since it may pass the matrix's end).
+BQ_DEVINL uint4 load_scales16(const uint8_t* src, int64_t r, int64_t rows, int g, int blocks, int vec)
 {
-    const int b0 = 16 * g;
-    uint32_t w[4] = {0u, 0u, 0u, 0u};
-    if (vec == 16) {
-        return b0 < blocks ? __ldg(reinterpret_cast<const uint4*>(row + b0)) : make_uint4(0u, 0u, 0u, 0u);
-    } else if (vec == 4) {
+    const int b0 = 16 * g, left = blocks - b0;
+    const uint8_t* p = src + r * blocks + b0;
+    if (left <= 0) return make_uint4(0u, 0u, 0u, 0u);
+    if (vec == 16) return __ldg(reinterpret_cast<const uint4*>(p));
+    uint32_t o[4];
+    if (vec == 4) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (b0 + 4 * i < blocks) w[i] = __ldg(reinterpret_cast<const uint32_t*>(row + b0 + 4 * i));
-    } else {
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-            if (b0 + i < blocks) w[i >> 2] |= (uint32_t)__ldg(row + b0 + i) << (8 * (i & 3));
+        for (int i = 0; i < 4; ++i) o[i] = 4 * i < left ? __ldg(reinterpret_cast<const uint32_t*>(p) + i) : 0u;
+        return make_uint4(o[0], o[1], o[2], o[3]);
     }
-    return make_uint4(w[0], w[1], w[2], w[3]);
+    const int sh = (int)(reinterpret_cast<uintptr_t>(p) & 3u);
+    const uint8_t* end = src + rows * blocks;
+    uint32_t w[5];
+#pragma unroll
+    for (int i = 0; i < 5; ++i) {
+        const uint8_t* q = p - sh + 4 * i;
+        w[i] = 0u;
+        if (4 * i - sh >= left || 4 * i - sh >= 16) continue;
+        if (q + 4 <= end) {
+            w[i] = __ldg(reinterpret_cast<const uint32_t*>(q));
+        } else {
+            for (int k = 0; q + k < end; ++k) w[i] |= (uint32_t)__ldg(q + k) << (8 * k);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int bytes = left - 4 * i;                      // of this word that the row has
+        o[i] = __funnelshift_r(w[i], w[i + 1], 8 * sh) & (bytes >= 4 ? 0xFFFFFFFFu : bytes <= 0 ? 0u : (1u << (8 * bytes)) - 1u);
+    }
+    return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
 // The packed scales are [128 rows of W][chunk] and [accumulator's tile of bn tokens][chunk][group] of units.
@@ -160,7 +177,7 @@ __global__ void __launch_bounds__(256) mx_pack_kernel(const __grid_constant__ Mx
     for (int j = 0; j < 4; ++j) {
         const int in_tile = 128 * group + 32 * j + lane;
         const int64_t r = tile * q.tile + in_tile;
-        v[j] = in_tile < q.tile && r < q.rows ? load_scales16(q.src + r * p.blocks, quad, p.blocks, p.vec) : make_uint4(0u, 0u, 0u, 0u);
+        v[j] = in_tile < q.tile && r < q.rows ? load_scales16(q.src, r, q.rows, quad, p.blocks, p.vec) : make_uint4(0u, 0u, 0u, 0u);
     }
     uint4* to = reinterpret_cast<uint4*>(q.dst + ((tile * p.chunks + 4 * quad) * q.groups + group) * 512) + lane;
     const int step = 32 * q.groups;
