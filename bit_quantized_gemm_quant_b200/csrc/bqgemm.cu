@@ -1752,7 +1752,7 @@ bq_status add_rms_norm(const uint16_t* x_bf16, const uint16_t* residual, const u
     p.eps = eps;
     p.M = M;
     p.K = (int)K;
-    return norm_forward(p, out, (cudaStream_t)stream);
+    return norm_forward(p, out, di, (cudaStream_t)stream);
 }
 
 bq_status add_rms_norm_backward(const uint16_t* dy_bf16, const uint16_t* h_bf16, const uint16_t* weight,

@@ -103,6 +103,31 @@ BQ_DEVINL uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c)
     return d;
 }
 
+BQ_DEVINL uint64_t mul_f32x2(uint64_t a, uint64_t b)
+{
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
+// a b + c, truncated.
+BQ_DEVINL uint64_t fma_rz_f32x2(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t d;
+    asm("fma.rz.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+
+// Two bf16 as fp32.
+BQ_DEVINL uint64_t bf16x2_to_f32x2(uint32_t v) { return f32x2_pack(v << 16, v & 0xFFFF0000u); }
+
+BQ_DEVINL uint32_t f32x2_to_bf16x2(uint64_t v)
+{
+    float lo, hi;
+    f32x2_unpack(v, lo, hi);
+    return pack_bf16x2_rn(lo, hi);
+}
+
 // Affine 8-bit: bytes e and e+1 of a code word to bf16x2 (bf16_rne(fmaf(scale,
 // q, bias)) per lane).  Each byte becomes the fp32 2^23 + q by a byte permute;
 // subtracting 2^23 is exact.

@@ -90,15 +90,22 @@ BQ_DEVINL void e4m3x2_to_f32(uint32_t w, float& a, float& b)
     b = __high2float(v);
 }
 
-// The largest magnitude, as bits, of 8 values in each of 4 consecutive lanes (a block of
-// 32).  As bits, so that a NaN counts as larger than all else.
+// The larger magnitudes of three; NaN if there is one.
+BQ_DEVINL float amax3(float a, float b, float c)
+{
+    float d;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
+// The bits of the largest magnitude of 8 values in each of 4 consecutive lanes (a block of
+// 32); a NaN's if there is one.
 BQ_DEVINL uint32_t block_amax_bits(const float (&v)[8])
 {
-    uint32_t a = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) a = max(a, __float_as_uint(v[i]) & 0x7FFFFFFFu);
-    a = max(a, __shfl_xor_sync(0xFFFFFFFFu, a, 1));
-    return max(a, __shfl_xor_sync(0xFFFFFFFFu, a, 2));
+    float a = amax3(amax3(v[0], v[1], v[2]), amax3(v[3], v[4], v[5]), amax3(v[6], v[7], v[7]));
+    a = amax3(a, __shfl_xor_sync(0xFFFFFFFFu, a, 1), a);
+    a = amax3(a, __shfl_xor_sync(0xFFFFFFFFu, a, 2), a);
+    return __float_as_uint(a);
 }
 
 // 8 of the values of a block, whose other 24 are in the lanes' neighbours, to codes at
@@ -108,15 +115,20 @@ template <int BITS>
 BQ_DEVINL void mx_store8(const float (&v)[8], uint8_t* __restrict__ codes, uint8_t* __restrict__ scales, int64_t at, bool live)
 {
     const uint32_t byte = mx_scale_byte<BITS>(block_amax_bits(v));
-    const float inv = mx_inverse(byte);
+    const uint64_t inv = f32x2_splat(mx_inverse(byte));
+    const bool whole = byte != kMxNan;
     float t[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) t[i] = byte == kMxNan ? 0.0f : __fmul_rn(v[i], inv);
+    for (int i = 0; i < 4; ++i)
+        f32x2_unpack(mul_f32x2(f32x2_pack(__float_as_uint(v[2 * i]), __float_as_uint(v[2 * i + 1])), inv), t[2 * i], t[2 * i + 1]);
     if (!live) return;
-    if constexpr (BITS == 8)
-        *reinterpret_cast<uint2*>(codes + at) = make_uint2(to_e4m3x4(t[0], t[1], t[2], t[3]), to_e4m3x4(t[4], t[5], t[6], t[7]));
-    else
-        *reinterpret_cast<uint32_t*>(codes + at / 2) = to_e2m1x8(t);
+    if constexpr (BITS == 8) {
+        const uint32_t lo = to_e4m3x4(t[0], t[1], t[2], t[3]), hi = to_e4m3x4(t[4], t[5], t[6], t[7]);
+        *reinterpret_cast<uint2*>(codes + at) = make_uint2(whole ? lo : 0u, whole ? hi : 0u);
+    } else {
+        const uint32_t c = to_e2m1x8(t);
+        *reinterpret_cast<uint32_t*>(codes + at / 2) = whole ? c : 0u;
+    }
     if ((at & 31) == 0) scales[at >> 5] = (uint8_t)byte;
 }
 

@@ -430,26 +430,53 @@ bq_status mx_gradient(const uint16_t* dy, const uint8_t* wq, const uint8_t* ws, 
 }
 
 // ------------------------------------------------------------------ norm
-// Warps a row and chunks a thread for rows of K elements (C = 0: the second pass reads again).
+// Warps a row and chunks a thread: with few rows many warps for each (its latency counts), with many a
+// warp holds up to 8 chunks a lane (fewer warps to meet and more loads in flight).
 template <typename F>
-auto norm_config(int64_t K, F&& go)
+auto norm_config(int64_t M, int64_t K, int num_sms, F&& go)
 {
-    if (K <= 256) return go(std::integral_constant<int, 1>{}, std::integral_constant<int, 1>{});
-    if (K <= 512) return go(std::integral_constant<int, 2>{}, std::integral_constant<int, 1>{});
-    if (K <= 1024) return go(std::integral_constant<int, 4>{}, std::integral_constant<int, 1>{});
-    if (K <= 2048) return go(std::integral_constant<int, 8>{}, std::integral_constant<int, 1>{});
-    if (K <= 4096) return go(std::integral_constant<int, 16>{}, std::integral_constant<int, 1>{});
-    if (K <= 8192) return go(std::integral_constant<int, 16>{}, std::integral_constant<int, 2>{});
-    return go(std::integral_constant<int, 32>{}, std::integral_constant<int, 2>{});
+    using std::integral_constant;
+#define BQ_NORM(W, C) return go(integral_constant<int, W>{}, integral_constant<int, C>{})
+    const int64_t want = (int64_t)num_sms * 8;               // warps
+    if (M >= want && K > 256) {
+        if (K <= 512) BQ_NORM(1, 2);
+        if (K <= 1024) BQ_NORM(1, 4);
+        if (K <= 2048) BQ_NORM(1, 8);
+        if (K <= 4096) BQ_NORM(2, 8);
+        if (K <= 8192) BQ_NORM(4, 8);
+        BQ_NORM(8, 8);
+    }
+    if (K <= 256) BQ_NORM(1, 1);
+    if (K <= 512) BQ_NORM(2, 1);
+    if (K <= 1024) BQ_NORM(4, 1);
+    if (K <= 2048) BQ_NORM(8, 1);
+    if (K <= 4096) BQ_NORM(16, 1);
+    if (K <= 8192) BQ_NORM(32, 1);
+    BQ_NORM(32, 2);
+#undef BQ_NORM
 }
 constexpr int64_t kNormMaxK = 16384;       // held in registers
 
-bq_status norm_forward(const NormParams& p, int out, cudaStream_t st)
+// The gradient's: a thread keeps three rows' chunks twice and the sums of dw.
+template <typename F>
+auto norm_grad_config(int64_t K, F&& go)
+{
+    using std::integral_constant;
+#define BQ_NORM(W, C) return go(integral_constant<int, W>{}, integral_constant<int, C>{})
+    if (K <= 256) BQ_NORM(1, 1);
+    if (K <= 512) BQ_NORM(2, 1);
+    if (K <= 1024) BQ_NORM(4, 1);
+    if (K <= 2048) BQ_NORM(8, 1);
+    if (K <= 4096) BQ_NORM(8, 2);
+    if (K <= 8192) BQ_NORM(16, 2);
+    BQ_NORM(32, 2);
+#undef BQ_NORM
+}
+
+bq_status norm_forward(const NormParams& p, int out, const DeviceInfo& di, cudaStream_t st)
 {
     const int64_t M = p.M, K = p.K;
-    if (K % 8 != 0) {
-        return launch_pdl(rms_norm_any_kernel, (int)M, 256, 0, st, p);
-    }
+    if (K % 8 != 0) return launch_pdl(rms_norm_any_kernel, (int)M, 256, 0, st, p);
     auto by_out = [&](auto w, auto c) {
         constexpr int W = decltype(w)::value, C = decltype(c)::value;
         const int grid = (int)((M + norm_rows(W) - 1) / norm_rows(W));
@@ -461,7 +488,7 @@ bq_status norm_forward(const NormParams& p, int out, cudaStream_t st)
         }
     };
     if (K > kNormMaxK) return by_out(std::integral_constant<int, 16>{}, std::integral_constant<int, 0>{});
-    return norm_config(K, by_out);
+    return norm_config(M, K, di.num_sms, by_out);
 }
 
 // CTAs of the gradient and rows of its partial sums.
@@ -483,10 +510,10 @@ NormGradPlan plan_norm_grad(int64_t M, int64_t K, int num_sms)
         pl.rows = (int)rows;
         pl.parts = (M + rows - 1) / rows;
     } else {
-        norm_config(K, [&](auto w, auto) {
+        norm_grad_config(K, [&](auto w, auto) {
             constexpr int W = decltype(w)::value;
             pl.grid = (int)std::min<int64_t>((M + norm_rows(W) - 1) / norm_rows(W),
-                                             (int64_t)num_sms * std::max(1, 1024 / norm_threads(W)));
+                                             (int64_t)num_sms * (norm_threads(W) <= 256 ? 2 : 1));
             pl.parts = (int64_t)pl.grid * norm_rows(W);
             return 0;
         });
@@ -509,7 +536,7 @@ bq_status norm_backward(const NormGradPlan& pl, const NormGradParams& p, uint16_
             s = launch_pdl_dim(rms_norm_weight_grad_any_kernel, dim3((unsigned)((p.K + 127) / 128), (unsigned)pl.parts), 128, 0,
                                st, p, pl.rows);
     } else {
-        s = norm_config(p.K, [&](auto w, auto c) {
+        s = norm_grad_config(p.K, [&](auto w, auto c) {
             constexpr int W = decltype(w)::value, C = decltype(c)::value;
             return launch_pdl(rms_norm_grad_kernel<W, C>, pl.grid, norm_threads(W), 0, st, p);
         });

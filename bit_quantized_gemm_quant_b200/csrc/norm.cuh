@@ -72,12 +72,15 @@ BQ_DEVINL float norm_scaled(float h, float w, float hi, float lo)
     return __fmaf_rn(p, hi, __fmul_rn(p, lo));
 }
 
-// Rounded to odd.  (A row whose s is an fp32 number gets no odd bit: its products may be exact.)
-BQ_DEVINL float norm_scaled_odd(float h, float w, float hi, float lo)
+// Two products rounded to odd: `odd` is 1, or 0 for a row whose s is an fp32 number (its products may be
+// exact).  A zero becomes 2^-149, which is a zero in every type it goes to; an infinity becomes a NaN,
+// which as well makes its block one.
+BQ_DEVINL void norm_scaled_odd2(uint32_t h2, uint32_t w2, uint64_t hi, uint64_t lo, uint32_t odd, float& a, float& b)
 {
-    const float p = __fmul_rn(h, w);
-    const float y = __fmaf_rz(p, hi, __fmul_rn(p, lo));
-    return __uint_as_float(__float_as_uint(y) | (lo != 0.0f && p != 0.0f && fabsf(y) < __uint_as_float(0x7F800000u) ? 1u : 0u));
+    const uint64_t p = mul_f32x2(bf16x2_to_f32x2(h2), bf16x2_to_f32x2(w2));
+    f32x2_unpack(fma_rz_f32x2(p, hi, mul_f32x2(p, lo)), a, b);
+    a = __uint_as_float(__float_as_uint(a) | odd);
+    b = __uint_as_float(__float_as_uint(b) | odd);
 }
 
 BQ_DEVINL void unpack8(const uint4& q, float (&v)[8])
@@ -90,20 +93,12 @@ BQ_DEVINL void unpack8(const uint4& q, float (&v)[8])
     }
 }
 
-BQ_DEVINL uint4 pack8(const float (&v)[8])
-{
-    return make_uint4(pack_bf16x2_rn(v[0], v[1]), pack_bf16x2_rn(v[2], v[3]), pack_bf16x2_rn(v[4], v[5]),
-                      pack_bf16x2_rn(v[6], v[7]));
-}
-
 // The 8 values of one chunk to the output, `at` elements from its start.  All lanes of the
 // warp come here.
 template <int OUT>
 BQ_DEVINL void norm_store8(const NormParams& p, const float (&y)[8], int64_t at, bool live)
 {
-    if constexpr (OUT == kNormBf16) {
-        if (live) *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(p.y) + at) = pack8(y);
-    } else if constexpr (OUT == kNormQ8_1) {                 // q8_1_quantize_kernel's rule
+    if constexpr (OUT == kNormQ8_1) {                        // q8_1_quantize_kernel's rule
         float amax = 0.0f;
 #pragma unroll
         for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(y[i]));
@@ -135,6 +130,18 @@ BQ_DEVINL void norm_store8(const NormParams& p, const float (&y)[8], int64_t at,
 constexpr int norm_threads(int W) { return W < 8 ? 256 : 32 * W; }
 constexpr int norm_rows(int W) { return W < 8 ? 8 / W : 1; }      // rows of a CTA
 
+// The W warps of a row (the group-th of the CTA) meet.
+template <int W>
+BQ_DEVINL void row_sync(int group)
+{
+    if constexpr (W == 1) __syncwarp();
+    else if constexpr (W >= 8) __syncthreads();
+    else asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "n"(32 * W) : "memory");
+}
+
+// x + r, rounded.
+BQ_DEVINL uint32_t norm_add2(uint32_t a, uint32_t b) { return f32x2_to_bf16x2(add_f32x2(bf16x2_to_f32x2(a), bf16x2_to_f32x2(b))); }
+
 // W warps a row, C chunks of 8 elements a thread: K a multiple of 8, at most 256 W C.
 // C = 0: any multiple of 8; the second pass reads x and r (or h) again.
 template <int W, int C, int OUT>
@@ -146,48 +153,55 @@ rms_norm_kernel(const __grid_constant__ NormParams p)
     __shared__ double part[R][W];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, group = warp / W, wi = warp % W;
     const int64_t row = (int64_t)blockIdx.x * R + group;
-    const bool live = row < p.M;
     const int64_t at0 = row * p.K;
     const int col0 = (wi * 32 + lane) * 8, step = W * 256;
+    const int cols = row < p.M ? p.K : 0;                    // a row past the last has none
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
 
     auto load_h = [&](int col) {
-        const uint4 q = *reinterpret_cast<const uint4*>(p.x + at0 + col);
-        if (!p.res) return q;
+        const uint4 a = *reinterpret_cast<const uint4*>(p.x + at0 + col);
+        if (!p.res) return a;
         const uint4 b = *reinterpret_cast<const uint4*>(p.res + at0 + col);
-        float v[8], u[8];
-        unpack8(q, v);
-        unpack8(b, u);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] += u[i];
-        return pack8(v);
+        return make_uint4(norm_add2(a.x, b.x), norm_add2(a.y, b.y), norm_add2(a.z, b.z), norm_add2(a.w, b.w));
     };
     auto squares = [&](const uint4& q) {
-        float v[8];
-        unpack8(q, v);
-        float a = 0.0f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) a = __fmaf_rn(v[i], v[i], a);
-        return (double)a;
+        uint64_t v = bf16x2_to_f32x2(q.x), a = mul_f32x2(v, v);
+        v = bf16x2_to_f32x2(q.y), a = fma_f32x2(v, v, a);
+        v = bf16x2_to_f32x2(q.z), a = fma_f32x2(v, v, a);
+        v = bf16x2_to_f32x2(q.w), a = fma_f32x2(v, v, a);
+        return (double)f32x2_sum(a);
     };
 
     uint4 held[kHeld];
     double ss = 0.0;
     if constexpr (C > 0) {
+        if (p.res) {                                         // all loads before the first use
+            uint4 r[C];
 #pragma unroll
-        for (int c = 0; c < C; ++c) {
-            const int col = col0 + c * step;
-            held[c] = live && col < p.K ? load_h(col) : make_uint4(0u, 0u, 0u, 0u);
+            for (int c = 0; c < C; ++c) {
+                const int col = col0 + c * step;
+                held[c] = col < cols ? *reinterpret_cast<const uint4*>(p.x + at0 + col) : zero;
+                r[c] = col < cols ? *reinterpret_cast<const uint4*>(p.res + at0 + col) : zero;
+            }
+#pragma unroll
+            for (int c = 0; c < C; ++c)
+                held[c] = make_uint4(norm_add2(held[c].x, r[c].x), norm_add2(held[c].y, r[c].y), norm_add2(held[c].z, r[c].z),
+                                     norm_add2(held[c].w, r[c].w));
+        } else {
+#pragma unroll
+            for (int c = 0; c < C; ++c)
+                held[c] = col0 + c * step < cols ? *reinterpret_cast<const uint4*>(p.x + at0 + col0 + c * step) : zero;
         }
 #pragma unroll
         for (int c = 0; c < C; ++c) {
             const int col = col0 + c * step;
             ss += squares(held[c]);
-            if (p.h && live && col < p.K) *reinterpret_cast<uint4*>(p.h + at0 + col) = held[c];
+            if (p.h && col < cols) *reinterpret_cast<uint4*>(p.h + at0 + col) = held[c];
         }
     } else {
-        for (int col = col0; live && col < p.K; col += step) {
+        for (int col = col0; col < cols; col += step) {
             const uint4 q = load_h(col);
             ss += squares(q);
             if (p.h) *reinterpret_cast<uint4*>(p.h + at0 + col) = q;
@@ -196,25 +210,47 @@ rms_norm_kernel(const __grid_constant__ NormParams p)
     ss = warp_sum(ss);
     if constexpr (W > 1) {
         if (lane == 0) part[group][wi] = ss;
-        __syncthreads();
-        ss = 0.0;
+        row_sync<W>(group);
+        if constexpr (W <= 8) {
+            ss = 0.0;
 #pragma unroll
-        for (int i = 0; i < W; ++i) ss += part[group][i];
+            for (int i = 0; i < W; ++i) ss += part[group][i];
+        } else {
+            ss = warp_sum(lane < W ? part[group][lane] : 0.0);
+        }
     }
     float hi, lo;
     norm_rstd(ss * p.inv_k + (double)p.eps, hi, lo);
-    if (p.rstd && live && wi == 0 && lane == 0) p.rstd[row] = hi;
+    if (p.rstd && cols > 0 && wi == 0 && lane == 0) p.rstd[row] = hi;
+    const uint64_t hi2 = f32x2_splat(hi), lo2 = f32x2_splat(lo);
+    const uint32_t odd = lo != 0.0f ? 1u : 0u;
 
     auto emit = [&](const uint4& q, int col) {
-        const bool in = live && col < p.K;
-        float v[8], w[8];
-        unpack8(q, v);
-        unpack8(in ? ldg_cached(p.w + col) : make_uint4(0u, 0u, 0u, 0u), w);
+        const bool in = col < cols;
+        const uint4 w = in ? ldg_cached(p.w + col) : zero;
+        if constexpr (OUT == kNormBf16) {
+            auto two = [&](uint32_t a, uint32_t b) {
+                const uint64_t v = mul_f32x2(bf16x2_to_f32x2(a), bf16x2_to_f32x2(b));
+                return f32x2_to_bf16x2(fma_f32x2(v, hi2, mul_f32x2(v, lo2)));
+            };
+            if (in)
+                *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(p.y) + at0 + col) =
+                    make_uint4(two(q.x, w.x), two(q.y, w.y), two(q.z, w.z), two(q.w, w.w));
+        } else if constexpr (OUT == kNormQ8_1) {
+            float v[8], u[8];
+            unpack8(q, v);
+            unpack8(w, u);
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            v[i] = !in ? 0.0f : OUT == kNormMx8 || OUT == kNormMx4 ? norm_scaled_odd(v[i], w[i], hi, lo)
-                                                                   : norm_scaled(v[i], w[i], hi, lo);
-        norm_store8<OUT>(p, v, at0 + col, in);
+            for (int i = 0; i < 8; ++i) v[i] = in ? norm_scaled(v[i], u[i], hi, lo) : 0.0f;
+            norm_store8<OUT>(p, v, at0 + col, in);
+        } else {
+            float v[8];
+            norm_scaled_odd2(q.x, w.x, hi2, lo2, odd, v[0], v[1]);
+            norm_scaled_odd2(q.y, w.y, hi2, lo2, odd, v[2], v[3]);
+            norm_scaled_odd2(q.z, w.z, hi2, lo2, odd, v[4], v[5]);
+            norm_scaled_odd2(q.w, w.w, hi2, lo2, odd, v[6], v[7]);
+            norm_store8<OUT>(p, v, at0 + col, in);           // (whole blocks are in or out: columns are in blocks of 32)
+        }
     };
     if constexpr (C > 0) {
 #pragma unroll
@@ -223,8 +259,7 @@ rms_norm_kernel(const __grid_constant__ NormParams p)
         // h where it is stored (this thread wrote it, possibly over x or r)
         for (int base = 0; base < p.K; base += step) {
             const int col = base + col0;
-            const bool in = live && col < p.K;
-            emit(!in ? make_uint4(0u, 0u, 0u, 0u) : p.h ? *reinterpret_cast<const uint4*>(p.h + at0 + col) : load_h(col), col);
+            emit(col >= cols ? zero : p.h ? *reinterpret_cast<const uint4*>(p.h + at0 + col) : load_h(col), col);
         }
     }
 }
@@ -278,8 +313,8 @@ struct NormGradParams {
     int K;
 };
 
-// CTAs walk the rows (row groups of the grid apart); a thread keeps its columns' share of dw
-// in registers until its last row.
+// CTAs walk the rows (row groups of the grid apart), the next row's loads in flight while one is
+// worked on; a thread keeps its columns' share of dw in registers until its last row.
 template <int W, int C>
 __global__ void __launch_bounds__(norm_threads(W))
 rms_norm_grad_kernel(const __grid_constant__ NormGradParams p)
@@ -291,65 +326,79 @@ rms_norm_grad_kernel(const __grid_constant__ NormGradParams p)
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-    uint4 w[C];
-    float acc[C][8];
-#pragma unroll
-    for (int c = 0; c < C; ++c) {
-        w[c] = col0 + c * step < p.K ? ldg_cached(p.w + col0 + c * step) : zero;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) acc[c][i] = 0.0f;
-    }
-    int buf = 0;
-    for (int64_t row0 = (int64_t)blockIdx.x * R; row0 < p.M; row0 += (int64_t)gridDim.x * R, buf ^= 1) {
-        const int64_t row = row0 + group, at0 = row * p.K;
-        const bool live = row < p.M;
+    struct Row {
         uint4 d[C], h[C], r[C];
+        float s;
+    };
+    auto load = [&](Row& v, int64_t row) {
+        const bool live = row < p.M;
+        const int64_t at0 = row * p.K;
 #pragma unroll
         for (int c = 0; c < C; ++c) {
             const int col = col0 + c * step;
             const bool in = live && col < p.K;
-            d[c] = in ? ldg_stream(p.dy + at0 + col) : zero;
-            h[c] = in ? ldg_stream(p.h + at0 + col) : zero;
-            r[c] = in && p.dh ? ldg_stream(p.dh + at0 + col) : zero;
+            v.d[c] = in ? ldg_stream(p.dy + at0 + col) : zero;
+            v.h[c] = in ? ldg_stream(p.h + at0 + col) : zero;
+            v.r[c] = in && p.dh ? ldg_stream(p.dh + at0 + col) : zero;
         }
-        const float s = live ? p.rstd[row] : 0.0f;
-        float dot = 0.0f;
+        v.s = live ? p.rstd[row] : 0.0f;
+    };
+    uint4 w[C];
+    uint64_t acc[C][4];
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+        w[c] = col0 + c * step < p.K ? ldg_cached(p.w + col0 + c * step) : zero;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[c][i] = 0;
+    }
+    const int64_t stride = (int64_t)gridDim.x * R;
+    int64_t row = (int64_t)blockIdx.x * R + group;
+    Row cur, next;
+    load(cur, row);
+    int buf = 0;
+    for (int64_t row0 = (int64_t)blockIdx.x * R; row0 < p.M; row0 += stride, row += stride, buf ^= 1) {
+        load(next, row + stride);
+        const uint64_t s2 = f32x2_splat(cur.s);
+        uint64_t dot2 = 0;
 #pragma unroll
         for (int c = 0; c < C; ++c) {
-            float dv[8], hv[8], wv[8];
-            unpack8(d[c], dv);
-            unpack8(h[c], hv);
-            unpack8(w[c], wv);
+            const uint32_t dv[4] = {cur.d[c].x, cur.d[c].y, cur.d[c].z, cur.d[c].w}, hv[4] = {cur.h[c].x, cur.h[c].y, cur.h[c].z, cur.h[c].w},
+                           wv[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float t = dv[i] * hv[i];               // exact
-                dot = __fmaf_rn(t, wv[i], dot);
-                acc[c][i] = __fmaf_rn(t, s, acc[c][i]);
+            for (int i = 0; i < 4; ++i) {
+                const uint64_t t = mul_f32x2(bf16x2_to_f32x2(dv[i]), bf16x2_to_f32x2(hv[i]));      // exact
+                dot2 = fma_f32x2(t, bf16x2_to_f32x2(wv[i]), dot2);
+                acc[c][i] = fma_f32x2(t, s2, acc[c][i]);
             }
         }
-        dot = warp_sum(dot);
+        float dot = warp_sum(f32x2_sum(dot2));
         if constexpr (W > 1) {
             if (lane == 0) part[buf][group][wi] = dot;
-            __syncthreads();                                 // (the other buffer is free: every warp has passed here once more)
-            dot = 0.0f;
+            row_sync<W>(group);                              // (the other buffer is free: every warp of the row has passed here once more)
+            if constexpr (W <= 8) {
+                dot = 0.0f;
 #pragma unroll
-            for (int i = 0; i < W; ++i) dot += part[buf][group][i];
+                for (int i = 0; i < W; ++i) dot += part[buf][group][i];
+            } else {
+                dot = warp_sum(lane < W ? part[buf][group][lane] : 0.0f);
+            }
         }
-        const float coef = s * s * (dot * p.inv_k);
+        const uint64_t coef = f32x2_splat(-(cur.s * cur.s * (dot * p.inv_k)));
+        const int64_t at0 = row * p.K;
 #pragma unroll
         for (int c = 0; c < C; ++c) {
             const int col = col0 + c * step;
-            if (!(live && col < p.K)) continue;
-            float dv[8], hv[8], wv[8], rv[8];
-            unpack8(d[c], dv);
-            unpack8(h[c], hv);
-            unpack8(w[c], wv);
-            unpack8(r[c], rv);
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                dv[i] = __fmaf_rn(s, __fmaf_rn(-hv[i], coef, dv[i] * wv[i]), rv[i]);
-            *reinterpret_cast<uint4*>(p.dx + at0 + col) = pack8(dv);
+            if (!(row < p.M && col < p.K)) continue;
+            // s (g - h coef) + dh
+            auto two = [&](uint32_t d, uint32_t h, uint32_t ww, uint32_t r) {
+                const uint64_t g = mul_f32x2(bf16x2_to_f32x2(d), bf16x2_to_f32x2(ww));             // exact
+                return f32x2_to_bf16x2(fma_f32x2(s2, fma_f32x2(bf16x2_to_f32x2(h), coef, g), bf16x2_to_f32x2(r)));
+            };
+            *reinterpret_cast<uint4*>(p.dx + at0 + col) =
+                make_uint4(two(cur.d[c].x, cur.h[c].x, w[c].x, cur.r[c].x), two(cur.d[c].y, cur.h[c].y, w[c].y, cur.r[c].y),
+                           two(cur.d[c].z, cur.h[c].z, w[c].z, cur.r[c].z), two(cur.d[c].w, cur.h[c].w, w[c].w, cur.r[c].w));
         }
+        cur = next;
     }
     if (!p.part) return;
     float* out = p.part + ((int64_t)blockIdx.x * R + group) * p.K;
@@ -357,8 +406,8 @@ rms_norm_grad_kernel(const __grid_constant__ NormGradParams p)
     for (int c = 0; c < C; ++c) {
         const int col = col0 + c * step;
         if (col >= p.K) continue;
-        *reinterpret_cast<float4*>(out + col) = make_float4(acc[c][0], acc[c][1], acc[c][2], acc[c][3]);
-        *reinterpret_cast<float4*>(out + col + 4) = make_float4(acc[c][4], acc[c][5], acc[c][6], acc[c][7]);
+        *reinterpret_cast<ulonglong2*>(out + col) = make_ulonglong2(acc[c][0], acc[c][1]);
+        *reinterpret_cast<ulonglong2*>(out + col + 4) = make_ulonglong2(acc[c][2], acc[c][3]);
     }
 }
 
