@@ -70,7 +70,7 @@ def _build_binding(force: bool, verbose: bool) -> None:
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
            *[a for i in incs for a in ("-isystem", i)], "-I", INCLUDE, BINDING_SRC, "-o", tmp,
            "-L" + os.path.join(torch_root, "lib"), "-lc10", "-ltorch_cpu", "-ltorch_python",
-           "-lc10_cuda", "-L" + PKG, "-l:" + os.path.basename(LIB), "-Wl,-rpath,$ORIGIN"]
+           "-lc10_cuda", "-ltorch_cuda", "-L" + PKG, "-l:" + os.path.basename(LIB), "-Wl,-rpath,$ORIGIN"]
     if verbose:
         print(" ".join(cmd))
     subprocess.check_call(cmd)

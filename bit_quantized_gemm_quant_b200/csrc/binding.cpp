@@ -10,7 +10,7 @@
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
-#include <ATen/ops/empty.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -98,7 +98,7 @@ struct Call {
 
     at::Tensor make(at::IntArrayRef shape, at::ScalarType type = at::kBFloat16) const
     {
-        return at::empty(shape, at::TensorOptions().dtype(type).device(dev));
+        return at::detail::empty_cuda(shape, type, dev, std::nullopt);      // at::empty without its dispatch, 0.3 us less
     }
 
     bq_stream_t stream() const { return c10::cuda::getCurrentCUDAStream(dev.index()).stream(); }

@@ -74,7 +74,8 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 
 // Q4_0, affine 4- and 8-bit (every path), affine 2-, 3- and 6-bit (dequantize,
 // quantize, the decode GEMV up to kGaMaxM tokens and the unfused pair).
-enum class WFmt { Q4_0, AFF4, AFF8, AFF2, AFF3, AFF6 };
+// MX4: the gradient of mx_matmul only.
+enum class WFmt { Q4_0, AFF4, AFF8, AFF2, AFF3, AFF6, MX4 };
 
 bool has_fast_paths(WFmt f) { return f == WFmt::Q4_0 || f == WFmt::AFF4 || f == WFmt::AFF8; }
 
@@ -1721,8 +1722,8 @@ size_t mx_matmul_backward_workspace_size(int64_t M, int64_t N, int64_t K)
     if (M <= 0 || N <= 0 || K <= 0 || K % 32 != 0 || !sizes_ok(M, N, K)) return 0;
     int num_sms, smem;
     device_or_b200(&num_sms, &smem);
-    MxGradWs w;
-    return plan_mx_grad(M, N, K, num_sms, smem, &w) ? w.bytes : 0;
+    EpiWs w;
+    return plan_backward(WFmt::MX4, 1, M, N, K, num_sms, smem, &w) ? w.bytes : 0;
 }
 
 bq_status add_rms_norm(const uint16_t* x_bf16, const uint16_t* residual, const uint16_t* weight, float eps, int out,

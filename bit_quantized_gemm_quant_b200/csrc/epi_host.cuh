@@ -11,6 +11,7 @@ struct QMat {
     const void* wq;
     const void* scales;
     const void* biases;
+    bool mx = false;           // MXFP4: scales are E8M0 bytes, no biases
 };
 
 int bits_of(WFmt f)
@@ -326,7 +327,10 @@ ScalePack scale_pack(bool mn, int mats, int64_t N, int64_t K)
     return s;
 }
 
-int fp_mode(WFmt f) { return f == WFmt::Q4_0 ? kModeQ4_0 : f == WFmt::AFF4 ? kModeAff4 : kModeAff8; }
+int fp_mode(WFmt f)
+{
+    return f == WFmt::Q4_0 ? kModeQ4_0 : f == WFmt::AFF4 ? kModeAff4 : f == WFmt::MX4 ? kModeMx4 : kModeAff8;
+}
 
 // The work of laying out the scales of w (1 or 2 matrices [N][K]) at `packed`, and its
 // number of blocks (0: too many); interleave: for the glu forward product.
@@ -339,6 +343,7 @@ int64_t scale_pack_params(bool mn, const QMat* w, int mats, bool interleave, int
         pp->scales[i] = reinterpret_cast<const uint16_t*>(q.scales);
         pp->biases[i] = reinterpret_cast<const uint16_t*>(q.biases);
     }
+    pp->mx = w[0].mx;
     pp->out = reinterpret_cast<uint32_t*>(packed);
     pp->N = (int)N;
     pp->K = (int)K;
@@ -438,6 +443,8 @@ bq_status launch_fused_pair_fmt(WFmt fmt, const DeviceInfo& di, int dev, const P
         else
             return launch(One{}, Three{});
     };
+    if constexpr (MN && EPI == kEpiPlain)
+        if (fmt == WFmt::MX4) return go(std::integral_constant<int, kModeMx4>{});
     if (fmt == WFmt::Q4_0) return go(std::integral_constant<int, kModeQ4_0>{});
     if (fmt == WFmt::AFF4) return go(std::integral_constant<int, kModeAff4>{});
     return go(std::integral_constant<int, kModeAff8>{});
@@ -471,7 +478,7 @@ bool plan_epi_product(WFmt fmt, bool gradient, int64_t rows, int64_t M, int segs
                       int smem_optin, EpiWs* w)
 {
     w->rows = rows;
-    w->fused = has_fast_paths(fmt);
+    w->fused = has_fast_paths(fmt) || fmt == WFmt::MX4;
     if (!w->fused)      // blocks of 64
         return plan_pair(rows, M, segs * ((red + 63) / 64), num_sms, smem_optin, 0, (int)kPairABytes, 64,
                          PairCost{300.0, 1.5, 0.0, 1}, &w->pl);
@@ -611,7 +618,7 @@ bq_status launch_epi_grad_v(EpiGradParams& p, int act, int row_blocks, cudaStrea
     }
 }
 
-// dy [M][N] and the saved z (glu: g, u) to dz (dg, du), dx and the biases' gradients.
+// dy [M][N] and the saved z (glu: g, u) to dz (dg, du), dx and the biases' gradients.  (MXFP4: dx alone.)
 struct EpiBackward {
     const uint16_t* dy;
     const uint16_t* pre[2];
@@ -629,7 +636,13 @@ bq_status epi_backward(const EpiBackward& b, const QMat* w, int act, int64_t M, 
     if (act < kActNone || act > kActSilu) return BQ_ERR_UNSUPPORTED;
     if (GLU && (w[0].biases == nullptr) != (w[1].biases == nullptr)) return BQ_ERR_NULL;
     WFmt fmt;
-    bq_status s = check_format(w[0].biases, N, K, group_size, bits, &fmt);
+    bq_status s = BQ_OK;
+    if (w[0].mx) {
+        if (K % 32 != 0) return BQ_ERR_SHAPE;
+        fmt = WFmt::MX4;
+    } else {
+        s = check_format(w[0].biases, N, K, group_size, bits, &fmt);
+    }
     if (s != BQ_OK) return s;
     const bool none = !GLU && act == kActNone;          // dz is dy
     const bool any_db = b.db[0] || b.db[1];

@@ -80,6 +80,19 @@ BQ_DEVINL void e2m1x8_to_bf16(uint32_t w, uint32_t (&out)[4])
     }
 }
 
+// 32 of them times X (s2: two of its bf16), as the pair products' other conversions write them.
+BQ_DEVINL void deq_mx4_half(uint4 raw, uint32_t s2, uint32_t (&out)[16])
+{
+    const uint32_t words[4] = {raw.x, raw.y, raw.z, raw.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        uint32_t v[4];
+        e2m1x8_to_bf16(words[i], v);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) out[4 * i + j] = hmul2_bf16(v[j], s2);
+    }
+}
+
 // Two E4M3 codes to fp32 (exact).
 BQ_DEVINL void e4m3x2_to_f32(uint32_t w, float& a, float& b)
 {

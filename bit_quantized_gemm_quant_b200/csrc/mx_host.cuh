@@ -377,56 +377,16 @@ bq_status mx_product(const void* xq, const uint8_t* xs, int x_bits, const uint8_
 }
 
 // ------------------------------------------------------------------ its gradient
-// Workspace: the bf16 weights, dy with rows of whole 16 bytes where N % 8 != 0, partial sums.
-struct MxGradWs {
-    PairPlan pl;
-    int64_t pitch = 0;
-    size_t off_pad = 0, off_split = 0, bytes = 0;
-};
-
-bool plan_mx_grad(int64_t M, int64_t N, int64_t K, int num_sms, int smem_optin, MxGradWs* w)
-{
-    if (!plan_pair(K, M, (N + 63) / 64, num_sms, smem_optin, 0, (int)kPairABytes, 64, PairCost{300.0, 1.5, 0.0, 1}, &w->pl))
-        return false;
-    w->pitch = (N + 7) / 8 * 8;
-    w->off_pad = up256((size_t)N * (size_t)K * 2u);
-    w->off_split = w->off_pad + (N % 8 != 0 ? up256((size_t)M * (size_t)w->pitch * 2u) : 0u);
-    w->bytes = w->off_split + w->pl.ws_bytes;
-    return true;
-}
-
+// The blocks run along K and the reduction along N, so the codes are dequantized inside the bf16
+// product, as those of the products with an epilogue (tc_fused_pair.cuh).
 bq_status mx_gradient(const uint16_t* dy, const uint8_t* wq, const uint8_t* ws, uint16_t* dx, int64_t M, int64_t N, int64_t K,
                       void* workspace, size_t workspace_bytes, cudaStream_t st)
 {
     if (M < 0 || N < 0 || K < 0 || K % 32 != 0 || !sizes_ok(M, N, K)) return BQ_ERR_SHAPE;
     if (M == 0 || K == 0) return BQ_OK;
-    if (!dx || (N > 0 && (!dy || !wq || !ws))) return BQ_ERR_NULL;
-    if (!all_aligned16({dx, workspace}) || (N > 0 && !all_aligned16({dy, wq, ws}))) return BQ_ERR_ALIGN;
-    int dev;
-    DeviceInfo di;
-    bq_status s = current_device(&dev, &di);
-    if (s != BQ_OK) return s;
-    if (N == 0)
-        return cudaMemsetAsync(dx, 0, (size_t)M * (size_t)K * 2u, st) == cudaSuccess ? BQ_OK : BQ_ERR_CUDA;
-    MxGradWs w;
-    if (!plan_mx_grad(M, N, K, di.num_sms, di.max_smem_optin, &w)) return BQ_ERR_SHAPE;
-    void* buf = nullptr;
-    if ((s = epi_workspace(dev, st, workspace, workspace_bytes, w.bytes, &buf)) != BQ_OK) return s;
-    uint8_t* base = reinterpret_cast<uint8_t*>(buf);
-    const uint16_t* B = dy;
-    if (N % 8 != 0) {
-        B = reinterpret_cast<const uint16_t*>(base + w.off_pad);
-        if (cudaMemcpy2DAsync(base + w.off_pad, (size_t)w.pitch * 2u, dy, (size_t)N * 2u, (size_t)N * 2u, (size_t)M,
-                              cudaMemcpyDeviceToDevice, st) != cudaSuccess) {
-            cudaGetLastError();
-            return BQ_ERR_CUDA;
-        }
-    }
-    uint16_t* wb = reinterpret_cast<uint16_t*>(base);
-    if ((s = launch_mx_dequant<4>(wq, ws, wb, N * K, di, st)) != BQ_OK) return s;
-    EpiParams e;
-    e.y = dx;
-    return launch_pair<true, kEpiPlain>(di, dev, w.pl, &wb, &B, 1, K, K, M, N, w.pitch, e, base + w.off_split, st);
+    const QMat w{wq, ws, nullptr, true};
+    const EpiBackward b{dy, {nullptr, nullptr}, dx, {nullptr, nullptr}, {nullptr, nullptr}};
+    return epi_backward<false>(b, &w, kActNone, M, N, K, 32, 4, workspace, workspace_bytes, st);
 }
 
 // ------------------------------------------------------------------ norm

@@ -3,20 +3,21 @@
 // rows are the product's tile rows (glu: interleaved, see epi_out_row), for the gradient
 // those of the matrix, one matrix after the other.  Rows and columns are padded to whole
 // tiles with weights of 0.  A word holds scale and bias (bf16), or Q4_0's d as d_hi + d_lo
-// (see gemv.cuh).
+// (see gemv.cuh), or a microscaled block's power of two as bf16 (bias 0).
 //
 // A block takes 32 rows x 2048 columns through shared memory: reads run along the rows of
 // the scales, writes along the rows of the result.  1.6 us by itself for 704 x 1024, latency
 // throughout; 12288 x 4096 reads 3 to 6 MB and writes 6.
 #pragma once
 
-#include "common.cuh"
+#include "mx.cuh"
 
 namespace bq {
 
 struct ScalePackParams {
     const uint16_t* scales[2];
-    const uint16_t* biases[2];     // NULL: Q4_0
+    const uint16_t* biases[2];     // NULL: Q4_0, or mx
+    int mx;                        // scales are E8M0 bytes
     uint32_t* out;
     int N, K, gs_shift, interleave;
     int cols;                      // padded columns
@@ -40,8 +41,18 @@ BQ_DEVINL void scale_pack_block(const ScalePackParams& p, uint32_t* smem, int bl
     const int h = threadIdx.x & 63, k = k0 + 32 * h, r0 = threadIdx.x >> 6;
     const int64_t g0 = (int64_t)(n0 + r0) * per_row + (k >> p.gs_shift);
 #pragma unroll
-    for (int i = 0; i < kEach; ++i) v[i] = n0 + r0 + 4 * i < p.N && k < p.K ? __ldg(sc + (g0 + (int64_t)(4 * i) * per_row)) : 0u;
-    if (bi) {
+    for (int i = 0; i < kEach; ++i) {
+        const bool in = n0 + r0 + 4 * i < p.N && k < p.K;
+        const int64_t at = g0 + (int64_t)(4 * i) * per_row;
+        v[i] = !in ? 0u : p.mx ? __ldg(reinterpret_cast<const uint8_t*>(sc) + at) : __ldg(sc + at);
+    }
+    if (p.mx) {
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) {
+            v[i] = mx_scale_bf16(v[i]);                      // (2^-127 beyond the matrix, where the codes are 0)
+            w[i] = 0u;
+        }
+    } else if (bi) {
 #pragma unroll
         for (int i = 0; i < kEach; ++i) w[i] = n0 + r0 + 4 * i < p.N && k < p.K ? __ldg(bi + (g0 + (int64_t)(4 * i) * per_row)) : 0u;
     } else {

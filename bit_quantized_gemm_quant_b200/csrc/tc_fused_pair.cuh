@@ -134,6 +134,8 @@ __device__ __noinline__ void fp_dequantize(int left, int codes_ring, uint32_t a_
             const uint32_t w = h ? sc.y : sc.x;
             if constexpr (MODE == kModeQ4_0)
                 deq_q4_0_half(raw[h], prmt(w, w, 0x1010u), prmt(w, w, 0x3232u), wv);
+            else if constexpr (MODE == kModeMx4)
+                deq_mx4_half(raw[h], prmt(w, w, 0x1010u), wv);
             else if constexpr (MODE == kModeAff4)
                 deq_aff4_half(raw[h], prmt(w, w, 0x1010u), prmt(w, w, 0x3232u), wv);
             else

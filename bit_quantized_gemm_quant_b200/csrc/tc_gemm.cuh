@@ -36,7 +36,7 @@
 
 namespace bq {
 
-enum : int { kModeBF16 = 0, kModeQ4_0 = 1, kModeAff4 = 2, kModeAff8 = 3 };
+enum : int { kModeBF16 = 0, kModeQ4_0 = 1, kModeAff4 = 2, kModeAff8 = 3, kModeMx4 = 4 };   // kModeMx4: tc_fused_pair.cuh only
 
 template <int MODE> struct TcCfg {
     // Fused modes: kDeqGroups groups of dequant warps take k-blocks in turn.  A
