@@ -453,24 +453,32 @@ def quant_matmul_glu_backward(dh: torch.Tensor, g: torch.Tensor, u: torch.Tensor
 def mxfp4_quantize(x: torch.Tensor, stream=None):
     """bf16 or fp32 x [M][K] -> (codes u8 [M][K/2], scales float8_e8m0fnu [M][K/32]): blocks of
     32 in E2M1, two codes per byte, the first one low."""
+    if stream is None:
+        return _calls().mx_quantize(x, 4)
     with _on(stream, x, "x"):
         return _calls().mx_quantize(x, 4)
 
 
 def mxfp8_quantize(x: torch.Tensor, stream=None):
     """bf16 or fp32 x [M][K] -> (codes float8_e4m3fn [M][K], scales float8_e8m0fnu [M][K/32])."""
+    if stream is None:
+        return _calls().mx_quantize(x, 8)
     with _on(stream, x, "x"):
         return _calls().mx_quantize(x, 8)
 
 
 def mxfp4_dequantize(codes: torch.Tensor, scales: torch.Tensor, out: torch.Tensor | None = None, stream=None):
     """codes u8 [M][K/2], scales float8_e8m0fnu (or their bytes) [M][K/32] -> bf16 [M][K]."""
+    if stream is None:
+        return _calls().mx_dequantize(codes, scales, out, 4)
     with _on(stream, codes, "codes"):
         return _calls().mx_dequantize(codes, scales, out, 4)
 
 
 def mxfp8_dequantize(codes: torch.Tensor, scales: torch.Tensor, out: torch.Tensor | None = None, stream=None):
     """codes float8_e4m3fn [M][K], scales float8_e8m0fnu (or their bytes) [M][K/32] -> bf16 [M][K]."""
+    if stream is None:
+        return _calls().mx_dequantize(codes, scales, out, 8)
     with _on(stream, codes, "codes"):
         return _calls().mx_dequantize(codes, scales, out, 8)
 
@@ -479,6 +487,8 @@ def mx_matmul(xq: torch.Tensor, x_scales: torch.Tensor, wq: torch.Tensor, w_scal
               out: torch.Tensor | None = None, stream=None):
     """y[M][N] = x . W^T, bf16, for x as mxfp8_quantize (float8_e4m3fn codes) or mxfp4_quantize
     (u8 codes) gives it and W [N][K] as mxfp4_quantize does.  out shares no memory with an input."""
+    if stream is None:
+        return _calls().mx_matmul(xq, x_scales, wq, w_scales, out)
     with _on(stream, xq, "xq"):
         return _calls().mx_matmul(xq, x_scales, wq, w_scales, out)
 
@@ -486,6 +496,8 @@ def mx_matmul(xq: torch.Tensor, x_scales: torch.Tensor, wq: torch.Tensor, w_scal
 def mx_matmul_backward(dy: torch.Tensor, wq: torch.Tensor, w_scales: torch.Tensor, stream=None):
     """The gradient of mx_matmul for frozen weights (and of the activations' quantizer by the
     straight-through estimate): dx [M][K] = dy [M][N] . W, bf16."""
+    if stream is None:
+        return _calls().mx_matmul_backward(dy, wq, w_scales)
     with _on(stream, dy, "dy"):
         return _calls().mx_matmul_backward(dy, wq, w_scales)
 
@@ -509,6 +521,8 @@ def add_rms_norm(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor |
     h_out: a bf16 [M][K] tensor for h, which may be x or residual itself."""
     if quantize not in NORM_OUTS:
         raise ValueError(f"quantize: expected None, 'q8_1', 'mxfp8' or 'mxfp4', got {quantize!r}")
+    if stream is None:
+        return _calls().add_rms_norm(x, weight, residual, eps, NORM_OUTS[quantize], save_rstd, h_out)
     with _on(stream, x, "x"):
         return _calls().add_rms_norm(x, weight, residual, eps, NORM_OUTS[quantize], save_rstd, h_out)
 
@@ -518,6 +532,8 @@ def add_rms_norm_backward(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tenso
     """The gradients of add_rms_norm from dy (y's; of a quantized y by the straight-through
     estimate) and dh (what reaches h by another way, as the next residual addition's): (dx,
     dweight), bf16, dx the gradient of x and of the residual alike; dweight None unless needed."""
+    if stream is None:
+        return _calls().add_rms_norm_backward(dy, h, weight, rstd, dh, need_dweight)
     with _on(stream, dy, "dy"):
         return _calls().add_rms_norm_backward(dy, h, weight, rstd, dh, need_dweight)
 

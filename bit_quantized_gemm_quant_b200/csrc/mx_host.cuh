@@ -453,6 +453,7 @@ bq_status norm_forward(const NormParams& p, int out, const DeviceInfo& di, cudaS
 
 // CTAs of the gradient and rows of its partial sums.
 struct NormGradPlan {
+    bool few = false;              // one launch, no partial sums
     bool any = false;              // element by element
     int grid = 0;
     int64_t parts = 0;
@@ -460,9 +461,15 @@ struct NormGradPlan {
     size_t bytes = 0;
 };
 
+constexpr int64_t kNormFewRows = 512;
+
 NormGradPlan plan_norm_grad(int64_t M, int64_t K, int num_sms)
 {
     NormGradPlan pl;
+    if (M <= kNormFewRows && (K % 8 != 0 ? K <= 8192 : K <= 4096)) {
+        pl.few = true;
+        return pl;
+    }
     if (K % 8 != 0 || K > kNormMaxK) {
         pl.any = true;
         const int64_t cols = (K + 127) / 128, want = std::max<int64_t>(1, (int64_t)num_sms * 16 / cols);
@@ -490,6 +497,12 @@ bool norm_sizes_ok(int64_t M, int64_t K)
 bq_status norm_backward(const NormGradPlan& pl, const NormGradParams& p, uint16_t* dw, cudaStream_t st)
 {
     bq_status s;
+    if (pl.few) {
+        const int v = p.K % 8 == 0 ? 8 : 1;
+        const int grid = (int)p.M + (dw ? (p.K + 8 * v - 1) / (8 * v) : 0);
+        return v == 8 ? launch_pdl(rms_norm_grad_few_kernel<8>, grid, 256, 0, st, p, dw, (int)p.M)
+                      : launch_pdl(rms_norm_grad_few_kernel<1>, grid, 256, 0, st, p, dw, (int)p.M);
+    }
     if (pl.any) {
         s = launch_pdl(rms_norm_grad_any_kernel, (int)p.M, 256, 0, st, p);
         if (s == BQ_OK && dw)

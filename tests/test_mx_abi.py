@@ -94,7 +94,7 @@ def test_norm_backward(L):
     assert f(dy=None, dx=None, M=0) == f(K=0, dw=A) == OK
     size = L.add_rms_norm_backward_workspace_size
     assert size(0, 64) == size(4, 0) == 0
-    assert size(4, 64) >= 4 * 64 * 4 and size(100, 77) >= 77 * 4
+    assert size(2048, 64) >= 64 * 4 and size(2048, 77) >= 77 * 4
 
 
 def test_binding_refusals():
