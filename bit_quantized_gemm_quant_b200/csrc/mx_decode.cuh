@@ -1,9 +1,9 @@
-// mx_decode.cuh -- the product of microscaled activations and weights at decode sizes (up to 64
-// tokens), in one launch.
+// mx_decode.cuh -- the product of microscaled activations and weights at decode sizes, and for more
+// tokens where it is small, in one launch.
 //
 //   D[n][m] = sum_k W[n][k] x[m][k],  each a code times its block's power of two
 //
-// The products are mx_pair.cuh's, on single SMs: 128 rows of W x bn tokens per CTA, K dealt
+// The products are mx_pair.cuh's, on single SMs: 128 rows of W x bn (up to 64) tokens per CTA, K dealt
 // to the C CTAs of a cluster in ranges of whole stages (a stage is one 128-byte swizzle atom
 // per row: 256 elements of 4-bit activations, 128 of 8-bit ones).  The tensor cores read the packed weights, so a
 // decode step has no unpacking to do and is bound by streaming W from HBM; what counts is that
@@ -22,7 +22,7 @@
 namespace bq {
 
 constexpr int kMdThreads = 128;               // 4 warps: scales, then epilogue; between them warp 0 copies, warp 1 issues MMAs
-constexpr int kMdMaxM = 64;
+constexpr int kMdTile = 64;                   // tokens of a tile
 constexpr int kMdMaxStages = 8;
 constexpr int kMdMaxChunks = 64;              // of a CTA's range
 constexpr int kMdTmemCols = 256;              // D: 64, scales from 64: 8 per chunk
@@ -35,7 +35,7 @@ struct MdParams {
     const uint8_t* ws;         // [N][blocks]
     uint16_t* y;
     int M, N;
-    int bn;                    // a multiple of 16, at least M
+    int bn, m_tiles;           // tokens of a tile (a multiple of 16, at most 64), tiles of them
     int blocks, vec;           // K / 32; scale bytes of one load (16, 4 or 1)
     int nk, log_cluster;       // stages of K, CTAs that share them (a power of two)
     int stages;                // of the ring
@@ -103,7 +103,9 @@ mx_decode_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant
     // (From blockIdx, not from the cluster's registers: the range, and with it the MMA warp's loop and
     // operands, stay in uniform registers; else a stage took 640 clocks to issue.)
     const uint32_t csize = 1u << p.log_cluster, rank = blockIdx.x & (csize - 1u);
-    const int r0 = (int)(blockIdx.x >> p.log_cluster) * 128;
+    const int tile = (int)(blockIdx.x >> p.log_cluster);
+    const int r0 = tile / p.m_tiles * 128, m0 = tile % p.m_tiles * p.bn;
+    const int M = min(p.bn, p.M - m0);                       // tokens of this tile
     const int kb0 = (int)((int64_t)p.nk * rank >> p.log_cluster), kb1 = (int)((int64_t)p.nk * (rank + 1) >> p.log_cluster);
     const int n_stages = kb1 - kb0;                          // at least 1
 
@@ -132,7 +134,7 @@ mx_decode_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant
         const int x = (kb0 + i) * 128;                       // bytes, or elements of the spread codes
         mbar_arrive_expect_tx(full_bar(s), (XB == 4 ? kPairABytes : kPairABytes / 2) + b_bytes);
         tma_load_2d(a_base + (uint32_t)s * kPairABytes, &tm_a, full_bar(s), x, r0);
-        tma_load_2d(b_base + (uint32_t)s * b_bytes, &tm_b, full_bar(s), x, 0);
+        tma_load_2d(b_base + (uint32_t)s * b_bytes, &tm_b, full_bar(s), x, m0);
     };
 
     {
@@ -142,7 +144,7 @@ mx_decode_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant
         // the first one's before the codes are asked for
         constexpr int kBatch = 4;
         const int c0 = kb0 * kChunks, nc = n_stages * kChunks;
-        const bool live[2] = {r0 + tid < p.N, tid < p.M};
+        const bool live[2] = {r0 + tid < p.N, tid < M};
         const uint32_t dst = 16u * (uint32_t)lane + 4u * (uint32_t)warp;
         for (int g0 = c0 >> 2; 4 * g0 < c0 + nc; g0 += kBatch) {
             uint4 v[2][kBatch];
@@ -152,7 +154,7 @@ mx_decode_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant
                 for (int side = 0; side < 2; ++side)
                     v[side][i] = !live[side] || 4 * (g0 + i) >= c0 + nc ? make_uint4(0u, 0u, 0u, 0u)
                                  : side == 0 ? load_scales16(p.ws, r0 + tid, p.N, g0 + i, p.blocks, p.vec)
-                                             : load_scales16(p.xs, tid, p.M, g0 + i, p.blocks, p.vec);
+                                             : load_scales16(p.xs, m0 + tid, p.M, g0 + i, p.blocks, p.vec);
             if (warp == 0 && g0 == c0 >> 2 && elect_one())
                 for (int i = 0; i < S && i < n_stages; ++i) copy_stage(i, i);
             __syncwarp();
@@ -191,7 +193,7 @@ mx_decode_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant
                 if (!mbar_wait_warp(full_bar(s), ph)) break;
                 tc_fence_after();
                 if (elect_one()) {
-                    const uint32_t sf = tmem + (uint32_t)kMdMaxM + (uint32_t)(s * kChunks) * 8u;
+                    const uint32_t sf = tmem + (uint32_t)kMdTile + (uint32_t)(s * kChunks) * 8u;
 #pragma unroll
                     for (int c = 0; c < kChunks; ++c) {
                         scales_to_tmem(sf + 8u * c, sfa_base + 512u * (uint32_t)(i * kChunks + c));
@@ -218,32 +220,32 @@ mx_decode_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant
     const bool ok = mbar_wait_warp(done_bar, 0);
     tc_fence_after();
     if (csize > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");     // every CTA of the cluster runs
-    const int log_share = 7 - p.log_cluster, share = 1 << log_share, pitch = md_sum_pitch(p.M);
+    const int log_share = 7 - p.log_cluster, share = 1 << log_share, pitch = md_sum_pitch(p.bn);
     if (ok) {
         const uint32_t lane_addr = tmem + ((uint32_t)(32 * warp) << 16);
         const int n = r0 + tid, owner = tid >> log_share;
         const uint32_t to = csize == 1 ? 0u
                                        : map_to_cta(sum_base + (uint32_t)((((int)rank << log_share) + tid - (owner << log_share)) * pitch) * 4u,
                                                     (uint32_t)owner);
-        for (int c = 0; c < p.M; c += 16) {
+        for (int c = 0; c < M; c += 16) {
             uint32_t v[16];
             tmem_ld_32x32b_x16(lane_addr + (uint32_t)c, v);
             tmem_wait_ld();
             if (csize > 1) {
 #pragma unroll
                 for (int j = 0; j < 16; j += 4)
-                    if (c + j < p.M) st_cluster_v4(to + (uint32_t)(c + j) * 4u, v[j], v[j + 1], v[j + 2], v[j + 3]);
+                    if (c + j < M) st_cluster_v4(to + (uint32_t)(c + j) * 4u, v[j], v[j + 1], v[j + 2], v[j + 3]);
             } else {
 #pragma unroll
                 for (int j = 0; j < 16; ++j)
-                    if (n < p.N && c + j < p.M) p.y[(int64_t)(c + j) * p.N + n] = (uint16_t)f32_to_bf16_bits(__uint_as_float(v[j]));
+                    if (n < p.N && c + j < M) p.y[(int64_t)(m0 + c + j) * p.N + n] = (uint16_t)f32_to_bf16_bits(__uint_as_float(v[j]));
             }
         }
     }
     __syncwarp();
     if (csize > 1) {
         cluster_sync_all();                                  // (after a timeout the sums are not valid)
-        for (int i = tid; i < (p.M + 3) / 4 << log_share; i += kMdThreads) {
+        for (int i = tid; i < (M + 3) / 4 << log_share; i += kMdThreads) {
             const int r = i & (share - 1), m = 4 * (i >> log_share), n = r0 + ((int)rank << log_share) + r;
             float sum[4] = {0.f, 0.f, 0.f, 0.f};
             for (uint32_t q = 0; q < csize; ++q) {
@@ -255,7 +257,7 @@ mx_decode_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant
             }
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-                if (n < p.N && m + j < p.M) p.y[(int64_t)(m + j) * p.N + n] = (uint16_t)f32_to_bf16_bits(sum[j]);
+                if (n < p.N && m + j < M) p.y[(int64_t)(m0 + m + j) * p.N + n] = (uint16_t)f32_to_bf16_bits(sum[j]);
         }
     }
     tc_fence_before();

@@ -74,8 +74,10 @@ bool make_map_spread4(CUtensorMap* m, const void* ptr, int64_t rows, int64_t K, 
 constexpr int kMdMaxSmem = 116 * 1024;
 
 struct MdPlan {
-    int log_cluster = 0, stages = 0, nk = 0, range = 0;      // range: the longest, in stages
+    int bn = 16, log_cluster = 0, stages = 0, nk = 0, range = 0;      // range: the longest, in stages
     size_t smem = 0;
+    int64_t rounds = 0;
+    double cost = 0.0;
 };
 
 // Clusters of 2^l CTAs that run at once with one CTA on an SM (what the GPCs' sizes leave; a B200's
@@ -117,14 +119,14 @@ int md_clusters(int l)
 // with one CTA a tile, 8.5 with two, 13.5 with three (90 of 96 clusters fit); 2048 x 8192: 6.9 with 4, 6.0 with 8.
 bool plan_md(int64_t M, int64_t N, int64_t K, int xbits, int num_sms, int smem_optin, MdPlan* pl)
 {
-    if (M > kMdMaxM) return false;
-    const int64_t rt = (N + 127) / 128, nk = (K + mx_atom_k(xbits) - 1) / mx_atom_k(xbits);
-    const int bn = (int)((M + 15) / 16 * 16), chunks = md_chunks(xbits);
+    const int64_t mt = (M + kMdTile - 1) / kMdTile, nk = (K + mx_atom_k(xbits) - 1) / mx_atom_k(xbits);
+    const int bn = (int)(((M + mt - 1) / mt + 15) / 16 * 16), chunks = md_chunks(xbits);
+    const int64_t rt = (N + 127) / 128 * ((M + bn - 1) / bn);                 // tiles
     const int64_t room = smem_optin / 2 - 3072;                               // two CTAs on an SM
     double best = 1e300;
     for (int l = 0; l <= 3 && (1 << l) <= nk; ++l) {
         const int c = 1 << l;
-        const int64_t range = (nk + c - 1) / c, fixed = range * chunks * 1024 + (int64_t)md_sum_bytes(c, (int)M);
+        const int64_t range = (nk + c - 1) / c, fixed = range * chunks * 1024 + (int64_t)md_sum_bytes(c, bn);
         const int64_t stages = std::min<int64_t>(std::min<int64_t>(kMdMaxStages, range), (room - fixed) / md_stage_bytes(bn));
         if (range * chunks > kMdMaxChunks || room < fixed || stages < std::min<int64_t>(2, range)) continue;
         const int64_t fit = 2 * (int64_t)md_clusters(l), rounds = (rt + fit - 1) / fit;
@@ -132,6 +134,7 @@ bool plan_md(int64_t M, int64_t N, int64_t K, int xbits, int num_sms, int smem_o
         const double cost = (double)rounds * ((double)(range * (1 + per_sm)) / 2.0 + 10.0);
         if (cost >= best) continue;
         best = cost;
+        pl->rounds = rounds;
         pl->log_cluster = l;
         pl->range = (int)range;
         pl->stages = (int)stages;
@@ -139,6 +142,8 @@ bool plan_md(int64_t M, int64_t N, int64_t K, int xbits, int num_sms, int smem_o
     }
     if (best == 1e300 || rt << pl->log_cluster > INT32_MAX) return false;
     pl->nk = (int)nk;
+    pl->bn = bn;
+    pl->cost = best;
     return true;
 }
 
@@ -156,7 +161,8 @@ bq_status launch_md(int dev, const MdPlan& pl, const void* xq, const uint8_t* xs
         attr_done[dev] = true;
     }
     MdParams p;
-    p.bn = (int)((M + 15) / 16 * 16);
+    p.bn = pl.bn;
+    p.m_tiles = (int)((M + pl.bn - 1) / pl.bn);
     CUtensorMap ta, tb;
     const bool a_ok = XB == 4 ? make_map(&ta, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, wq, N, K / 2, 128, 128, CU_TENSOR_MAP_SWIZZLE_128B)
                               : make_map_spread4(&ta, wq, N, w_k, 128);
@@ -174,7 +180,7 @@ bq_status launch_md(int dev, const MdPlan& pl, const void* xq, const uint8_t* xs
     p.stages = pl.stages;
     p.range_chunks = pl.range * md_chunks(XB);
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((N + 127) / 128) << pl.log_cluster);
+    cfg.gridDim = dim3((unsigned)((N + 127) / 128 * p.m_tiles) << pl.log_cluster);
     cfg.blockDim = dim3(kMdThreads);
     cfg.dynamicSmemBytes = pl.smem;
     cfg.stream = st;
@@ -199,7 +205,7 @@ bq_status launch_md(int dev, const MdPlan& pl, const void* xq, const uint8_t* xs
 struct MxWs {
     PairPlan pl;
     MdPlan md;
-    bool decode = false;            // up to 64 tokens, one launch; else pairs of SMs
+    bool decode = false;            // the one-launch kernel; else pairs of SMs
     bool pad = false;
     int64_t k = 0;
     int chunks = 0;                 // 128-element chunks of a row, whole stages
@@ -259,7 +265,11 @@ bool plan_mx(int64_t M, int64_t N, int64_t K, int x_bits, int num_sms, int smem_
     w->pad = x_bits == 8 && K % 128 != 0;
     w->k = w->pad ? (K + 127) / 128 * 128 : K;
     w->off_w = w->pad ? up256((size_t)N * (size_t)w->k / 2) : 0u;
-    w->decode = plan_md(M, N, K, x_bits, num_sms, smem_optin, &w->md);
+    // Beyond one tile of tokens the one-launch kernel takes what it does at once and in few stages: 1000 x 1024 x
+    // 1024 8.2 us for the pairs' 6.9, which the host needs longer for; 200 x 1024 x 4096 9.3 and 11.2; 200 x 4096 x
+    // 4096, which is left to the pairs, 15.2 and 12.5.
+    w->decode = plan_md(M, N, K, x_bits, num_sms, smem_optin, &w->md) &&
+                (M <= kMdTile || (w->md.rounds == 1 && w->md.cost <= 19.0));
     w->bytes = w->off_w;
     if (w->decode) return true;
     if (!plan_mx_pair(N, M, K, x_bits, num_sms, smem_optin, &w->pl)) return false;
