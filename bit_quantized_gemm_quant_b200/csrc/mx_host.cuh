@@ -400,21 +400,23 @@ bq_status mx_gradient(const uint16_t* dy, const uint8_t* wq, const uint8_t* ws, 
 }
 
 // ------------------------------------------------------------------ norm
-// Warps a row and chunks a thread: with few rows many warps for each (its latency counts), with many a
-// warp holds up to 8 chunks a lane (fewer warps to meet and more loads in flight).
+// Warps a row and chunks a thread, as few chunks as hold the row: with few rows a chunk each (a row's
+// latency counts); with two for each SM or more up to four (fewer warps to meet, more loads in flight;
+// eight leave too few warps).  2048 rows to 8 bits with residual: 4096 wide 11.4 us with 8 warps of two chunks,
+// 11.7 with 4 of four, 13.8 with 16 of one, 13.9 with 2 of eight; 8192 wide 20.4 with 8 of four, 26.8
+// with 32 of one.
 template <typename F>
 auto norm_config(int64_t M, int64_t K, int num_sms, F&& go)
 {
     using std::integral_constant;
 #define BQ_NORM(W, C) return go(integral_constant<int, W>{}, integral_constant<int, C>{})
-    const int64_t want = (int64_t)num_sms * 8;               // warps
-    if (M >= want && K > 256) {
+    if (M >= 2 * (int64_t)num_sms && K > 256) {
         if (K <= 512) BQ_NORM(1, 2);
         if (K <= 1024) BQ_NORM(1, 4);
-        if (K <= 2048) BQ_NORM(1, 8);
-        if (K <= 4096) BQ_NORM(2, 8);
-        if (K <= 8192) BQ_NORM(4, 8);
-        BQ_NORM(8, 8);
+        if (K <= 2048) BQ_NORM(2, 4);
+        if (K <= 4096) BQ_NORM(8, 2);
+        if (K <= 8192) BQ_NORM(8, 4);
+        BQ_NORM(16, 4);
     }
     if (K <= 256) BQ_NORM(1, 1);
     if (K <= 512) BQ_NORM(2, 1);
@@ -427,19 +429,21 @@ auto norm_config(int64_t M, int64_t K, int num_sms, F&& go)
 }
 constexpr int64_t kNormMaxK = 16384;       // held in registers
 
-// The gradient's: a thread keeps three rows' chunks twice and the sums of dw.
+// The gradient's (a thread keeps three rows' chunks twice and the sums of dw) and its CTAs per SM.  2048
+// rows: 8192 wide 24.9 us with 8 warps of four chunks, 26.1 with 16 of two; 4096 wide 13.6 with two CTAs of
+// 16 of one, 14.6 with 8 of two; 8192 x 1024 13.9 with three CTAs, 16.0 with two.
 template <typename F>
 auto norm_grad_config(int64_t K, F&& go)
 {
     using std::integral_constant;
-#define BQ_NORM(W, C) return go(integral_constant<int, W>{}, integral_constant<int, C>{})
-    if (K <= 256) BQ_NORM(1, 1);
-    if (K <= 512) BQ_NORM(2, 1);
-    if (K <= 1024) BQ_NORM(4, 1);
-    if (K <= 2048) BQ_NORM(8, 1);
-    if (K <= 4096) BQ_NORM(8, 2);
-    if (K <= 8192) BQ_NORM(16, 2);
-    BQ_NORM(32, 2);
+#define BQ_NORM(W, C, PER) return go(integral_constant<int, W>{}, integral_constant<int, C>{}, integral_constant<int, PER>{})
+    if (K <= 256) BQ_NORM(1, 1, 3);
+    if (K <= 512) BQ_NORM(2, 1, 3);
+    if (K <= 1024) BQ_NORM(4, 1, 3);
+    if (K <= 2048) BQ_NORM(4, 2, 2);
+    if (K <= 4096) BQ_NORM(16, 1, 2);
+    if (K <= 8192) BQ_NORM(8, 4, 1);
+    BQ_NORM(32, 2, 1);
 #undef BQ_NORM
 }
 
@@ -487,10 +491,9 @@ NormGradPlan plan_norm_grad(int64_t M, int64_t K, int num_sms)
         pl.rows = (int)rows;
         pl.parts = (M + rows - 1) / rows;
     } else {
-        norm_grad_config(K, [&](auto w, auto) {
+        norm_grad_config(K, [&](auto w, auto, auto per) {
             constexpr int W = decltype(w)::value;
-            pl.grid = (int)std::min<int64_t>((M + norm_rows(W) - 1) / norm_rows(W),
-                                             (int64_t)num_sms * (norm_threads(W) <= 256 ? 2 : 1));
+            pl.grid = (int)std::min<int64_t>((M + norm_rows(W) - 1) / norm_rows(W), (int64_t)num_sms * decltype(per)::value);
             pl.parts = (int64_t)pl.grid * norm_rows(W);
             return 0;
         });
@@ -519,7 +522,7 @@ bq_status norm_backward(const NormGradPlan& pl, const NormGradParams& p, uint16_
             s = launch_pdl_dim(rms_norm_weight_grad_any_kernel, dim3((unsigned)((p.K + 127) / 128), (unsigned)pl.parts), 128, 0,
                                st, p, pl.rows);
     } else {
-        s = norm_grad_config(p.K, [&](auto w, auto c) {
+        s = norm_grad_config(p.K, [&](auto w, auto c, auto) {
             constexpr int W = decltype(w)::value, C = decltype(c)::value;
             return launch_pdl(rms_norm_grad_kernel<W, C>, pl.grid, norm_threads(W), 0, st, p);
         });

@@ -314,7 +314,7 @@ struct NormGradParams {
 };
 
 // CTAs walk the rows (row groups of the grid apart), the next row's loads in flight while one is
-// worked on; a thread keeps its columns' share of dw in registers until its last row.
+// worked on (not with 32 warps, whose registers hold one row's); a thread keeps its columns' share of dw in registers until its last row.
 template <int W, int C>
 __global__ void __launch_bounds__(norm_threads(W))
 rms_norm_grad_kernel(const __grid_constant__ NormGradParams p)
@@ -353,11 +353,13 @@ rms_norm_grad_kernel(const __grid_constant__ NormGradParams p)
     }
     const int64_t stride = (int64_t)gridDim.x * R;
     int64_t row = (int64_t)blockIdx.x * R + group;
+    constexpr bool kAhead = W < 32;
     Row cur, next;
-    load(cur, row);
+    if constexpr (kAhead) load(cur, row);
     int buf = 0;
     for (int64_t row0 = (int64_t)blockIdx.x * R; row0 < p.M; row0 += stride, row += stride, buf ^= 1) {
-        load(next, row + stride);
+        if constexpr (kAhead) load(next, row + stride);
+        else load(cur, row);
         const uint64_t s2 = f32x2_splat(cur.s);
         uint64_t dot2 = 0;
 #pragma unroll
@@ -398,7 +400,7 @@ rms_norm_grad_kernel(const __grid_constant__ NormGradParams p)
                 make_uint4(two(cur.d[c].x, cur.h[c].x, w[c].x, cur.r[c].x), two(cur.d[c].y, cur.h[c].y, w[c].y, cur.r[c].y),
                            two(cur.d[c].z, cur.h[c].z, w[c].z, cur.r[c].z), two(cur.d[c].w, cur.h[c].w, w[c].w, cur.r[c].w));
         }
-        cur = next;
+        if constexpr (kAhead) cur = next;
     }
     if (!p.part) return;
     float* out = p.part + ((int64_t)blockIdx.x * R + group) * p.K;
