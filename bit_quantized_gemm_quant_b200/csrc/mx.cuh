@@ -166,57 +166,83 @@ BQ_DEVINL void load8(const void* x, int64_t at, float (&v)[8])
 }
 
 // ------------------------------------------------------------------ quantize
-// A thread takes 8 elements, 4 threads a block.  Rows are whole blocks, so the matrix is one
-// run of `n` elements (a multiple of 32).  Bound by HBM.
+// A thread takes 8 elements, 4 threads a block, and kMxEach such pieces a CTA's width apart, all of whose
+// loads are in flight before the first is used.  Rows are whole blocks, so the matrix is one run of `n`
+// elements (a multiple of 32).  Bound by HBM.
+constexpr int kMxEach = 4;
+constexpr int64_t kMxSpan = 256 * 8 * kMxEach;               // elements of a CTA
+
 template <int BITS, bool F32>
 __global__ void __launch_bounds__(256)
 mx_quantize_kernel(const void* __restrict__ x, uint8_t* __restrict__ codes, uint8_t* __restrict__ scales, int64_t n)
 {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const int64_t step = (int64_t)gridDim.x * 2048;
-    for (int64_t base = (int64_t)blockIdx.x * 2048; base < n; base += step) {
-        const int64_t at = base + threadIdx.x * 8;
-        float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-        if (at < n) load8<F32>(x, at, v);
-        mx_store8<BITS>(v, codes, scales, at, at < n);
+    for (int64_t base = (int64_t)blockIdx.x * kMxSpan; base < n; base += (int64_t)gridDim.x * kMxSpan) {
+        float v[kMxEach][8];
+#pragma unroll
+        for (int i = 0; i < kMxEach; ++i) {
+            const int64_t at = base + (i * 256 + threadIdx.x) * 8;
+            if (at < n) {
+                load8<F32>(x, at, v[i]);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[i][j] = 0.0f;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kMxEach; ++i) {
+            const int64_t at = base + (i * 256 + threadIdx.x) * 8;
+            mx_store8<BITS>(v[i], codes, scales, at, at < n);
+        }
     }
 }
 
 // ------------------------------------------------------------------ dequantize
 // out = bf16_rne(X * element): exact unless it leaves bf16's range (beyond it infinity, below 2^-133 to
-// nearest even; a NaN scale gives NaN).  A thread takes 8 elements.  Bound by HBM, mostly by the writes.
-template <int BITS>
-BQ_DEVINL uint4 mx_dequant8(const uint8_t* __restrict__ codes, uint32_t byte, int64_t at)
-{
-    uint32_t o[4];
-    if constexpr (BITS == 4) {
-        const uint32_t s = mx_scale_bf16(byte) * 0x10001u;
-        e2m1x8_to_bf16(__ldg(reinterpret_cast<const uint32_t*>(codes) + (at >> 3)), o);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) o[i] = hmul2_bf16(o[i], s);
-    } else {
-        const uint2 w = __ldg(reinterpret_cast<const uint2*>(codes) + (at >> 3));
-        const float s = mx_scale(byte);
-        float v[8];
-        e4m3x2_to_f32(w.x, v[0], v[1]);
-        e4m3x2_to_f32(w.x >> 16, v[2], v[3]);
-        e4m3x2_to_f32(w.y, v[4], v[5]);
-        e4m3x2_to_f32(w.y >> 16, v[6], v[7]);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) o[i] = pack_bf16x2_rn(__fmul_rn(v[2 * i], s), __fmul_rn(v[2 * i + 1], s));
-    }
-    return make_uint4(o[0], o[1], o[2], o[3]);
-}
-
+// nearest even; a NaN scale gives NaN).  Work as in the quantizer.  Bound by HBM, mostly by the writes.
 template <int BITS>
 __global__ void __launch_bounds__(256)
-mx_dequant_kernel(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales, uint16_t* __restrict__ out, int64_t n8)
+mx_dequant_kernel(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales, uint16_t* __restrict__ out, int64_t n)
 {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    for (int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; i < n8; i += (int64_t)gridDim.x * blockDim.x)
-        reinterpret_cast<uint4*>(out)[i] = mx_dequant8<BITS>(codes, scales[i >> 2], 8 * i);
+    for (int64_t base = (int64_t)blockIdx.x * kMxSpan; base < n; base += (int64_t)gridDim.x * kMxSpan) {
+        uint2 w[kMxEach];
+        uint32_t byte[kMxEach];
+#pragma unroll
+        for (int i = 0; i < kMxEach; ++i) {
+            const int64_t at = base + (i * 256 + threadIdx.x) * 8;
+            w[i] = make_uint2(0u, 0u);
+            byte[i] = 0;
+            if (at >= n) continue;
+            if constexpr (BITS == 8) w[i] = __ldg(reinterpret_cast<const uint2*>(codes + at));
+            else w[i].x = __ldg(reinterpret_cast<const uint32_t*>(codes + at / 2));
+            byte[i] = __ldg(scales + (at >> 5));
+        }
+#pragma unroll
+        for (int i = 0; i < kMxEach; ++i) {
+            const int64_t at = base + (i * 256 + threadIdx.x) * 8;
+            if (at >= n) continue;
+            uint32_t o[4];
+            if constexpr (BITS == 4) {
+                const uint32_t s = mx_scale_bf16(byte[i]) * 0x10001u;
+                e2m1x8_to_bf16(w[i].x, o);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) o[j] = hmul2_bf16(o[j], s);
+            } else {
+                const float s = mx_scale(byte[i]);
+                float v[8];
+                e4m3x2_to_f32(w[i].x, v[0], v[1]);
+                e4m3x2_to_f32(w[i].x >> 16, v[2], v[3]);
+                e4m3x2_to_f32(w[i].y, v[4], v[5]);
+                e4m3x2_to_f32(w[i].y >> 16, v[6], v[7]);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) o[j] = pack_bf16x2_rn(__fmul_rn(v[2 * j], s), __fmul_rn(v[2 * j + 1], s));
+            }
+            *reinterpret_cast<uint4*>(out + at) = make_uint4(o[0], o[1], o[2], o[3]);
+        }
+    }
 }
 
 // Rows of 16-byte units to longer ones, zeros behind: [rows][in] to [rows][out] units.  (Codes of W for

@@ -14,6 +14,8 @@ bool all_aligned16(std::initializer_list<const void*> ps)
 }
 
 // ------------------------------------------------------------------ quantize, dequantize
+int mx_grid(int64_t n, const DeviceInfo& di) { return (int)std::min<int64_t>((n + kMxSpan - 1) / kMxSpan, (int64_t)di.num_sms * 64); }
+
 template <int BITS>
 bq_status mx_quantize(const void* x, int x_type, uint8_t* codes, uint8_t* scales, int64_t M, int64_t K, cudaStream_t st)
 {
@@ -28,7 +30,7 @@ bq_status mx_quantize(const void* x, int x_type, uint8_t* codes, uint8_t* scales
     bq_status s = current_device(&dev, &di);
     if (s != BQ_OK) return s;
     const int64_t n = M * K;
-    const int grid = grid_for(n / 8, 256, di);
+    const int grid = mx_grid(n, di);
     return x_type == BQ_TYPE_F32 ? launch_pdl(mx_quantize_kernel<BITS, true>, grid, 256, 0, st, x, codes, scales, n)
                                  : launch_pdl(mx_quantize_kernel<BITS, false>, grid, 256, 0, st, x, codes, scales, n);
 }
@@ -37,7 +39,7 @@ template <int BITS>
 bq_status launch_mx_dequant(const uint8_t* codes, const uint8_t* scales, uint16_t* out, int64_t n, const DeviceInfo& di,
                             cudaStream_t st)
 {
-    return launch_pdl(mx_dequant_kernel<BITS>, grid_for(n / 8, 256, di), 256, 0, st, codes, scales, out, n / 8);
+    return launch_pdl(mx_dequant_kernel<BITS>, mx_grid(n, di), 256, 0, st, codes, scales, out, n);
 }
 
 template <int BITS>
