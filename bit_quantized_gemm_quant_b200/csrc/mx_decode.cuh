@@ -26,6 +26,7 @@ constexpr int kMdTile = 64;                   // tokens of a tile
 constexpr int kMdMaxStages = 8;
 constexpr int kMdMaxChunks = 64;              // of a CTA's range
 constexpr int kMdTmemCols = 256;              // D: 64, scales from 64: 8 per chunk
+constexpr int kMdTmemChunks = (kMdTmemCols - kMdTile) / 8;
 
 __host__ __device__ constexpr int md_chunks(int xbits) { return mx_atom_k(xbits) / 128; }
 __host__ __device__ constexpr uint32_t md_stage_bytes(int bn) { return kPairABytes + (uint32_t)bn * 128u; }
@@ -187,17 +188,26 @@ mx_decode_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant
             const uint32_t idesc = umma_idesc_mx<XB>(128, p.bn);
             const uint64_t bd0 = umma_desc_k_sw128(b_base);
             const uint32_t desc_hi = (uint32_t)(bd0 >> 32), b_lo0 = (uint32_t)bd0, a_lo0 = (uint32_t)umma_desc_k_sw128(a_base);
+            // all scales to tensor memory while the codes arrive, where there is room for them
+            const uint32_t sf0 = tmem + (uint32_t)kMdTile;
+            const bool ahead = nc <= kMdTmemChunks;
+            auto copy_scales = [&](uint32_t to, int c) {
+                scales_to_tmem(to, sfa_base + 512u * (uint32_t)c);
+                scales_to_tmem(to + 4u, sfb_base + 512u * (uint32_t)c);
+            };
+            if (ahead && elect_one())
+                for (int c = 0; c < nc; ++c) copy_scales(sf0 + 8u * (uint32_t)c, c);
+            __syncwarp();
             int s = 0;
             uint32_t ph = 0;
             for (int i = 0; i < n_stages; ++i) {
                 if (!mbar_wait_warp(full_bar(s), ph)) break;
                 tc_fence_after();
                 if (elect_one()) {
-                    const uint32_t sf = tmem + (uint32_t)kMdTile + (uint32_t)(s * kChunks) * 8u;
+                    const uint32_t sf = sf0 + (uint32_t)((ahead ? i : s) * kChunks) * 8u;
+                    if (!ahead) {
 #pragma unroll
-                    for (int c = 0; c < kChunks; ++c) {
-                        scales_to_tmem(sf + 8u * c, sfa_base + 512u * (uint32_t)(i * kChunks + c));
-                        scales_to_tmem(sf + 8u * c + 4u, sfb_base + 512u * (uint32_t)(i * kChunks + c));
+                        for (int c = 0; c < kChunks; ++c) copy_scales(sf + 8u * c, i * kChunks + c);
                     }
                     const uint32_t al = a_lo0 + (uint32_t)s * (kPairABytes >> 4), bl = b_lo0 + (uint32_t)s * (b_bytes >> 4);
 #pragma unroll
@@ -206,7 +216,7 @@ mx_decode_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant
                         const uint32_t id = XB == 4 ? 2u * (k & 1) : (uint32_t)k;
                         umma_mx<XB>(tmem, al + 2u * k, bl + 2u * k, desc_hi, idesc | id << 4 | id << 29, at, at + 4u, i > 0 || k > 0);
                     }
-                    umma_commit(empty_bar(s));
+                    if (i + S < n_stages) umma_commit(empty_bar(s));        // the slot is filled again
                     if (i + 1 == n_stages) umma_commit(done_bar);
                 }
                 __syncwarp();
