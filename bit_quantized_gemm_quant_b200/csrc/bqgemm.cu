@@ -1730,10 +1730,10 @@ bq_status add_rms_norm(const uint16_t* x_bf16, const uint16_t* residual, const u
                        void* y, void* scales, int32_t* qsum, uint16_t* h_bf16, float* rstd, int64_t M, int64_t K,
                        bq_stream_t stream)
 {
-    if (!norm_sizes_ok(M, K)) return BQ_ERR_SHAPE;
+    if (!norm_sizes_ok(M, K) || K == 0) return BQ_ERR_SHAPE;
     if (out < BQ_NORM_BF16 || out > BQ_NORM_MXFP4 || !(eps >= 0.0f) || eps > 3.4028234e38f) return BQ_ERR_UNSUPPORTED;
     if (out != BQ_NORM_BF16 && K % 32 != 0) return BQ_ERR_SHAPE;
-    if (M == 0 || K == 0) return BQ_OK;
+    if (M == 0) return BQ_OK;
     if (!x_bf16 || !weight || !y || (out != BQ_NORM_BF16 && !scales) || (out == BQ_NORM_Q8_1 && !qsum)) return BQ_ERR_NULL;
     if (!all_aligned16({x_bf16, residual, weight, y, scales, qsum, h_bf16, rstd})) return BQ_ERR_ALIGN;
     int dev;

@@ -578,7 +578,7 @@ BQ_API size_t mx_matmul_backward_workspace_size(int64_t M, int64_t N, int64_t K)
  *                     i32 [M][K/32]; u8 [M][K] or [M][K/2] with u8 [M][K/32].  Written.
  *   h_bf16            device u16 [M][K], written, or NULL; may be x_bf16 or residual itself
  *   rstd              device f32 [M], written for the gradient, or NULL
- * No other overlap of an output with an input or another output.  K any (BQ_NORM_BF16) or a
+ * No other overlap of an output with an input or another output.  K any but 0 (BQ_NORM_BF16) or a
  * multiple of 32; M and K below 2^30.
  */
 typedef enum { BQ_NORM_BF16 = 0, BQ_NORM_Q8_1 = 1, BQ_NORM_MXFP8 = 2, BQ_NORM_MXFP4 = 3 } bq_norm_out;

@@ -71,7 +71,7 @@ def test_matmul_backward(L):
 def test_norm(L):
     def f(x=A, r=None, w=A, eps=1e-5, out=0, y=A, s=None, q=None, h=None, rstd=None, M=4, K=64):
         return L.add_rms_norm(x, r, w, eps, out, y, s, q, h, rstd, M, K, None)
-    assert f(M=-1) == f(K=-1) == f(M=2 ** 30) == f(K=2 ** 30) == SHAPE
+    assert f(M=-1) == f(K=-1) == f(M=2 ** 30) == f(K=2 ** 30) == f(K=0) == f(M=0, K=0) == SHAPE
     assert f(out=4) == f(out=-1) == f(eps=-1e-6) == f(eps=float("nan")) == f(eps=float("inf")) == UNSUPPORTED
     for out in (1, 2, 3):
         assert f(out=out, s=A, q=A, K=40) == SHAPE
@@ -80,7 +80,7 @@ def test_norm(L):
     assert f(x=None) == f(w=None) == f(y=None) == NULL
     for k in ("x", "r", "w", "y", "s", "q", "h", "rstd"):
         assert f(**{k: BAD}) == ALIGN, k
-    assert f(x=None, M=0) == f(y=None, K=0) == OK
+    assert f(x=None, y=None, M=0) == OK
 
 
 def test_norm_backward(L):
