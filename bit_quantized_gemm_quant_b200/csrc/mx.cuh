@@ -249,20 +249,38 @@ mx_dequant_kernel(const uint8_t* __restrict__ codes, const uint8_t* __restrict__
     }
 }
 
+// ------------------------------------------------------------------ longer rows
 // Rows of 16-byte units to longer ones, zeros behind: [rows][in] to [rows][out] units.  (Codes of W for
-// products whose copies want rows of whole 128 codes.)
-__global__ void __launch_bounds__(256)
-mx_pad_kernel(const uint4* __restrict__ from, uint4* __restrict__ to, int64_t rows, int in, int out)
+// products whose copies want rows of whole 128 codes.)  Blocks of 256 threads, kMxPadSpan units each.
+struct MxPadParams {
+    const uint4* from;
+    uint4* to;
+    int64_t rows;
+    int in, out;
+};
+constexpr int kMxPadSpan = 1024;
+
+BQ_DEVINL void mx_pad_block(const MxPadParams& p, int64_t block)
+{
+    uint4 v[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const int64_t i = block * kMxPadSpan + 256 * j + threadIdx.x, r = i / p.out;
+        const int c = (int)(i - r * p.out);
+        v[j] = r < p.rows && c < p.in ? ldg_stream(p.from + r * p.in + c) : make_uint4(0u, 0u, 0u, 0u);
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const int64_t i = block * kMxPadSpan + 256 * j + threadIdx.x;
+        if (i < p.rows * p.out) p.to[i] = v[j];
+    }
+}
+
+__global__ void __launch_bounds__(256) mx_pad_kernel(const __grid_constant__ MxPadParams p)
 {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const int64_t n = rows * out;
-#pragma unroll 4
-    for (int64_t i = blockIdx.x * (int64_t)256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
-        const int64_t r = i / out;
-        const int c = (int)(i - r * out);
-        to[i] = c < in ? ldg_stream(from + r * in + c) : make_uint4(0u, 0u, 0u, 0u);
-    }
+    mx_pad_block(p, blockIdx.x);
 }
 
 }  // namespace bq

@@ -266,7 +266,7 @@ bool plan_mx(int64_t M, int64_t N, int64_t K, int x_bits, int num_sms, int smem_
 {
     w->pad = x_bits == 8 && K % 128 != 0;
     w->k = w->pad ? (K + 127) / 128 * 128 : K;
-    w->off_w = w->pad ? up256((size_t)N * (size_t)w->k / 2) : 0u;
+    w->off_w = w->pad ? up256((size_t)N * (size_t)w->k / 2) + 256u : 0u;      // from the next multiple of 256 on
     // Beyond one tile of tokens the one-launch kernel takes what it does at once and in few stages: 1000 x 1024 x
     // 1024 8.2 us for the pairs' 6.9, which the host needs longer for; 200 x 1024 x 4096 9.3 and 11.2; 200 x 4096 x
     // 4096, which is left to the pairs, 15.2 and 12.5.
@@ -286,11 +286,13 @@ bool plan_mx(int64_t M, int64_t N, int64_t K, int x_bits, int num_sms, int smem_
     return true;
 }
 
-// The scales of W and x into the layout of the block-scaled product's plan.
-bq_status launch_mx_pack(const MxWs& w, const uint8_t* xs, const uint8_t* wsc, uint8_t* buf, int64_t M, int64_t N, int64_t K,
-                         cudaStream_t st)
+// The scales of W and x into the layout of the block-scaled product's plan, and W's codes into longer rows.
+bq_status launch_mx_pack(const MxWs& w, const uint8_t* xs, const uint8_t* wsc, const MxPadParams& pad, uint8_t* buf, int64_t M,
+                         int64_t N, int64_t K, cudaStream_t st)
 {
     MxPackParams p;
+    p.pad = pad;
+    p.pad_blocks = w.pad ? (pad.rows * pad.out + kMxPadSpan - 1) / kMxPadSpan : 0;
     p.blocks = (int)(K / 32);
     p.chunks = w.chunks;
     p.quads = (w.chunks + 3) / 4;
@@ -298,7 +300,7 @@ bq_status launch_mx_pack(const MxWs& w, const uint8_t* xs, const uint8_t* wsc, u
     const int groups = mx_groups(w.pl.bn), tok = w.pl.halves * w.pl.bn;
     p.side[0] = MxPackSide{wsc, buf + w.off_w, (int)N, 128, 1, (N + 255) / 256 * 2 * p.quads};
     p.side[1] = MxPackSide{xs, buf + w.off_x, (int)M, w.pl.bn, groups, (M + tok - 1) / tok * w.pl.halves * groups * p.quads};
-    const int64_t blocks = (p.side[0].items + p.side[1].items + 7) / 8;
+    const int64_t blocks = p.pad_blocks + (p.side[0].items + p.side[1].items + 7) / 8;
     return blocks > INT32_MAX ? BQ_ERR_SHAPE : launch_pdl(mx_pack_kernel, (int)blocks, 256, 0, st, p);
 }
 
@@ -370,17 +372,19 @@ bq_status mx_product(const void* xq, const uint8_t* xs, int x_bits, const uint8_
     void* buf = nullptr;
     if ((s = epi_workspace(dev, st, workspace, workspace_bytes, w.bytes, &buf)) != BQ_OK) return s;
     uint8_t* to = reinterpret_cast<uint8_t*>(buf);
-    if (w.pad) {
-        const int in = (int)(K / 32), out = (int)(w.k / 32);          // 16-byte units of a row
-        s = launch_pdl(mx_pad_kernel, grid_for(N * out / 4, 256, di), 256, 0, st, reinterpret_cast<const uint4*>(wq),
-                       reinterpret_cast<uint4*>(to), N, in, out);
-        if (s != BQ_OK) return s;
-        wq = to;
-    }
-    if (w.decode)
+    if (w.pad) to += (256u - (reinterpret_cast<uintptr_t>(to) & 255u)) & 255u;
+    const MxPadParams pad{reinterpret_cast<const uint4*>(wq), reinterpret_cast<uint4*>(to), N, (int)(K / 32), (int)(w.k / 32)};
+    if (w.pad) wq = to;
+    if (w.decode) {
+        if (w.pad) {
+            const int64_t blocks = (N * pad.out + kMxPadSpan - 1) / kMxPadSpan;
+            if (blocks > INT32_MAX) return BQ_ERR_SHAPE;
+            if ((s = launch_pdl(mx_pad_kernel, (int)blocks, 256, 0, st, pad)) != BQ_OK) return s;
+        }
         return x_bits == 8 ? launch_md<8>(dev, w.md, xq, xs, wq, w.k, ws, y, M, N, K, st)
                            : launch_md<4>(dev, w.md, xq, xs, wq, w.k, ws, y, M, N, K, st);
-    if ((s = launch_mx_pack(w, xs, ws, to, M, N, K, st)) != BQ_OK) return s;
+    }
+    if ((s = launch_mx_pack(w, xs, ws, pad, to, M, N, K, st)) != BQ_OK) return s;
     if (x_bits == 8)
         return w.pl.halves == 2 ? launch_mx_pair<8, 2>(di, dev, w, xq, wq, y, M, N, K, to, st)
                                 : launch_mx_pair<8, 1>(di, dev, w, xq, wq, y, M, N, K, to, st);

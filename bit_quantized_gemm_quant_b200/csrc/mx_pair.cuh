@@ -156,13 +156,19 @@ struct MxPackSide {
 struct MxPackParams {
     MxPackSide side[2];
     int blocks, chunks, quads, vec;
+    int64_t pad_blocks;        // the first blocks: W's codes in longer rows (else 0)
+    MxPadParams pad;
 };
 
 __global__ void __launch_bounds__(256) mx_pack_kernel(const __grid_constant__ MxPackParams p)
 {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    int64_t item = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+    if (blockIdx.x < p.pad_blocks) {
+        mx_pad_block(p.pad, blockIdx.x);
+        return;
+    }
+    int64_t item = (blockIdx.x - p.pad_blocks) * 8 + (threadIdx.x >> 5);
     const int lane = threadIdx.x & 31;
     const bool second = item >= p.side[0].items;
     const MxPackSide& q = p.side[second];
