@@ -452,7 +452,7 @@ def quant_matmul_glu_backward(dh: torch.Tensor, g: torch.Tensor, u: torch.Tensor
 # ------------------------------------------------------------ microscaled rows
 def mxfp4_quantize(x: torch.Tensor, stream=None):
     """bf16 or fp32 x [M][K] -> (codes u8 [M][K/2], scales float8_e8m0fnu [M][K/32]): blocks of
-    32 in E2M1, two codes per byte, the first one low."""
+    32 in E2M1, two codes per byte, the first one low.  Codes and scales share one allocation."""
     if stream is None:
         return _calls().mx_quantize(x, 4)
     with _on(stream, x, "x"):
@@ -460,7 +460,8 @@ def mxfp4_quantize(x: torch.Tensor, stream=None):
 
 
 def mxfp8_quantize(x: torch.Tensor, stream=None):
-    """bf16 or fp32 x [M][K] -> (codes float8_e4m3fn [M][K], scales float8_e8m0fnu [M][K/32])."""
+    """bf16 or fp32 x [M][K] -> (codes float8_e4m3fn [M][K], scales float8_e8m0fnu [M][K/32]),
+    in one allocation."""
     if stream is None:
         return _calls().mx_quantize(x, 8)
     with _on(stream, x, "x"):
@@ -518,7 +519,8 @@ def add_rms_norm(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor |
     Returns (y, h), with save_rstd (y, h, rstd fp32 [M]) for add_rms_norm_backward; h is x itself
     where there is no residual.  y is bf16, or quantized for the product that follows:
     "q8_1" (xq, dx, qsum) for quant_matmul_q8, "mxfp8" or "mxfp4" (codes, scales) for mx_matmul.
-    h_out: a bf16 [M][K] tensor for h, which may be x or residual itself."""
+    h_out: a bf16 [M][K] tensor for h, which may be x or residual itself.  Codes and their scales,
+    and h and rstd, share an allocation."""
     if quantize not in NORM_OUTS:
         raise ValueError(f"quantize: expected None, 'q8_1', 'mxfp8' or 'mxfp4', got {quantize!r}")
     if stream is None:
