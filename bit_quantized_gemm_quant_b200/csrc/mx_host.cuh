@@ -461,6 +461,9 @@ auto norm_config(int64_t M, int64_t K, int num_sms, F&& go)
 }
 constexpr int64_t kNormMaxK = 16384;       // held in registers
 
+// Elements of a row's 16-byte units: its start moves it by up to 7.
+int64_t norm_units(int64_t K) { return K % 8 == 0 ? K : K + 7; }
+
 // The gradient's (a thread keeps three rows' chunks twice and the sums of dw) and its CTAs per SM.  2048
 // rows: 8192 wide 24.9 us with 8 warps of four chunks, 26.1 with 16 of two; 4096 wide 13.6 with two CTAs of
 // 16 of one, 14.6 with 8 of two; 8192 x 1024 13.9 with three CTAs, 16.0 with two.
@@ -482,15 +485,22 @@ auto norm_grad_config(int64_t K, F&& go)
 bq_status norm_forward(const NormParams& p, int out, const DeviceInfo& di, cudaStream_t st)
 {
     const int64_t M = p.M, K = p.K;
-    if (K % 8 != 0) return launch_pdl(rms_norm_any_kernel, (int)M, 256, 0, st, p);
+    if (K % 8 != 0) {
+        if (norm_units(K) > kNormMaxK) return launch_pdl(rms_norm_any_kernel, (int)M, 256, 0, st, p);
+        return norm_config(M, norm_units(K), di.num_sms, [&](auto w, auto c) {
+            constexpr int W = decltype(w)::value, C = decltype(c)::value;
+            return launch_pdl(rms_norm_kernel<W, C, kNormBf16, true>, (int)((M + norm_rows(W) - 1) / norm_rows(W)), norm_threads(W), 0,
+                              st, p);
+        });
+    }
     auto by_out = [&](auto w, auto c) {
         constexpr int W = decltype(w)::value, C = decltype(c)::value;
         const int grid = (int)((M + norm_rows(W) - 1) / norm_rows(W));
         switch (out) {
-        case kNormQ8_1: return launch_pdl(rms_norm_kernel<W, C, kNormQ8_1>, grid, norm_threads(W), 0, st, p);
-        case kNormMx8: return launch_pdl(rms_norm_kernel<W, C, kNormMx8>, grid, norm_threads(W), 0, st, p);
-        case kNormMx4: return launch_pdl(rms_norm_kernel<W, C, kNormMx4>, grid, norm_threads(W), 0, st, p);
-        default: return launch_pdl(rms_norm_kernel<W, C, kNormBf16>, grid, norm_threads(W), 0, st, p);
+        case kNormQ8_1: return launch_pdl(rms_norm_kernel<W, C, kNormQ8_1, false>, grid, norm_threads(W), 0, st, p);
+        case kNormMx8: return launch_pdl(rms_norm_kernel<W, C, kNormMx8, false>, grid, norm_threads(W), 0, st, p);
+        case kNormMx4: return launch_pdl(rms_norm_kernel<W, C, kNormMx4, false>, grid, norm_threads(W), 0, st, p);
+        default: return launch_pdl(rms_norm_kernel<W, C, kNormBf16, false>, grid, norm_threads(W), 0, st, p);
         }
     };
     if (K > kNormMaxK) return by_out(std::integral_constant<int, 16>{}, std::integral_constant<int, 0>{});
@@ -512,21 +522,23 @@ constexpr int64_t kNormFewRows = 512;
 NormGradPlan plan_norm_grad(int64_t M, int64_t K, int num_sms)
 {
     NormGradPlan pl;
-    if (M <= kNormFewRows && (K % 8 != 0 ? K <= 8192 : K <= 4096)) {
+    if (M <= kNormFewRows && (K % 8 != 0 ? K <= 2048 : K <= 4096)) {
         pl.few = true;
         return pl;
     }
-    if (K % 8 != 0 || K > kNormMaxK) {
+    if (norm_units(K) > kNormMaxK) {
         pl.any = true;
         const int64_t cols = (K + 127) / 128, want = std::max<int64_t>(1, (int64_t)num_sms * 16 / cols);
         const int64_t rows = std::max<int64_t>(16, (M + want - 1) / want);
         pl.rows = (int)rows;
         pl.parts = (M + rows - 1) / rows;
     } else {
-        norm_grad_config(K, [&](auto w, auto, auto per) {
+        norm_grad_config(norm_units(K), [&](auto w, auto, auto per) {
             constexpr int W = decltype(w)::value;
             pl.grid = (int)std::min<int64_t>((M + norm_rows(W) - 1) / norm_rows(W), (int64_t)num_sms * decltype(per)::value);
-            pl.parts = (int64_t)pl.grid * norm_rows(W);
+            // rows that do not start on 16 bytes: those of a warp are a multiple of 8 apart
+            if (K % 8 != 0) pl.grid = (int)(((int64_t)pl.grid * norm_rows(W) + 7) / 8 * 8 / norm_rows(W));
+            pl.parts = pl.grid;
             return 0;
         });
     }
@@ -554,14 +566,14 @@ bq_status norm_backward(const NormGradPlan& pl, const NormGradParams& p, uint16_
             s = launch_pdl_dim(rms_norm_weight_grad_any_kernel, dim3((unsigned)((p.K + 127) / 128), (unsigned)pl.parts), 128, 0,
                                st, p, pl.rows);
     } else {
-        s = norm_grad_config(p.K, [&](auto w, auto c, auto) {
+        s = norm_grad_config(norm_units(p.K), [&](auto w, auto c, auto) {
             constexpr int W = decltype(w)::value, C = decltype(c)::value;
-            return launch_pdl(rms_norm_grad_kernel<W, C>, pl.grid, norm_threads(W), 0, st, p);
+            return p.K % 8 == 0 ? launch_pdl(rms_norm_grad_kernel<W, C, false>, pl.grid, norm_threads(W), 0, st, p)
+                                : launch_pdl(rms_norm_grad_kernel<W, C, true>, pl.grid, norm_threads(W), 0, st, p);
         });
     }
     if (s != BQ_OK || !dw) return s;
-    return launch_pdl_dim(epi_bias_grad_kernel, dim3((unsigned)((p.K + 31) / 32), 1u), 256, 0, st, (const float*)p.part, dw,
-                          (uint16_t*)nullptr, p.K, 1, (int)pl.parts);
+    return launch_pdl(norm_sum_kernel, (p.K + 31) / 32, 1024, 0, st, (const float*)p.part, dw, p.K, (int)pl.parts);
 }
 
 }  // namespace

@@ -10,6 +10,12 @@
 // use, 8 elements a chunk and thread, and quantizing costs the output's bytes only: a block
 // of 32 is 4 neighbouring lanes.
 //
+// Rows that do not start on 16 bytes (K no multiple of 8; SHIFT) are worked on in the 16-byte units of
+// memory that they touch, which lie alike in all operands: a row begins s = (row K) mod 8 elements into its
+// first one.  Of units that a row shares with a neighbour the other's elements are read and masked (not where the
+// call writes h over an operand, nor past the matrix's end), and written element by element; the weight is read so
+// throughout.  (Element by element throughout, 7197 x 1941's gradient took 67 us.)
+//
 // Precision.  Squares of bf16 are exact in fp32; a thread adds 8 at a time in fp32, and all
 // further sums are fp64, as is s (one Newton step from the fp32 reciprocal root).  h w is
 // exact in fp32 (8 + 8 bits), and s is used as the sum of two fp32 numbers.  For the MX types
@@ -142,9 +148,74 @@ BQ_DEVINL void row_sync(int group)
 // x + r, rounded.
 BQ_DEVINL uint32_t norm_add2(uint32_t a, uint32_t b) { return f32x2_to_bf16x2(add_f32x2(bf16x2_to_f32x2(a), bf16x2_to_f32x2(b))); }
 
-// W warps a row, C chunks of 8 elements a thread: K a multiple of 8, at most 256 W C.
-// C = 0: any multiple of 8; the second pass reads x and r (or h) again.
-template <int W, int C, int OUT>
+// One row's units of 16 bytes: element `col` (a multiple of 8) of the units is element col - s of the row.
+// strict: nothing beside the row is read.
+template <bool SHIFT>
+struct RowUnits {
+    int64_t base, total;       // where the first unit starts, the matrix's end
+    int s, K;
+    bool strict;
+
+    BQ_DEVINL RowUnits(int64_t row, int64_t M, int K_, bool strict_ = false) : base(row * K_), total(M * K_), s(0), K(K_), strict(strict_)
+    {
+        if constexpr (SHIFT) {
+            s = (int)(base & 7);
+            base -= s;
+        }
+    }
+    BQ_DEVINL int end() const { return K + s; }              // units start below it
+    BQ_DEVINL bool whole(int col) const { return !SHIFT || (col >= s && col + 8 <= K + s); }
+    BQ_DEVINL bool has(int col, int i) const { return col + i >= s && col + i < K + s; }
+
+    // The unit as it lies in memory; masked() takes the neighbours' elements out.
+    template <bool STREAM = false>
+    BQ_DEVINL uint4 load(const uint16_t* p, int col) const
+    {
+        if (whole(col) || (!strict && base + col + 8 <= total)) {
+            if constexpr (STREAM) return ldg_stream(p + base + col);
+            return *reinterpret_cast<const uint4*>(p + base + col);
+        }
+        return gather(p + base + col, col);
+    }
+    BQ_DEVINL uint4 masked(const uint4& q, int col) const
+    {
+        if (whole(col)) return q;
+        uint32_t v[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (!has(col, i)) v[i >> 1] &= i & 1 ? 0x0000FFFFu : 0xFFFF0000u;
+        return make_uint4(v[0], v[1], v[2], v[3]);
+    }
+    // The weight of a unit's elements.
+    BQ_DEVINL uint4 weight(const uint16_t* w, int col) const
+    {
+        if constexpr (!SHIFT) return ldg_cached(w + col);
+        return gather(w + col - s, col);
+    }
+    BQ_DEVINL uint4 gather(const uint16_t* p, int col) const
+    {
+        uint32_t v[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (has(col, i)) v[i >> 1] |= (uint32_t)p[i] << (16 * (i & 1));
+        return make_uint4(v[0], v[1], v[2], v[3]);
+    }
+    BQ_DEVINL void store(uint16_t* p, int col, const uint4& q) const
+    {
+        if (whole(col)) {
+            *reinterpret_cast<uint4*>(p + base + col) = q;
+            return;
+        }
+        const uint32_t v[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (has(col, i)) p[base + col + i] = (uint16_t)(v[i >> 1] >> (16 * (i & 1)));
+    }
+};
+
+// W warps a row, C chunks of 8 elements a thread: units of a row at most 32 W C.  C = 0: any number;
+// the second pass reads x and r (or h) again.  SHIFT: K no multiple of 8 (bf16 results).
+template <int W, int C, int OUT, bool SHIFT>
 __global__ void __launch_bounds__(norm_threads(W))
 rms_norm_kernel(const __grid_constant__ NormParams p)
 {
@@ -153,17 +224,17 @@ rms_norm_kernel(const __grid_constant__ NormParams p)
     __shared__ double part[R][W];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, group = warp / W, wi = warp % W;
     const int64_t row = (int64_t)blockIdx.x * R + group;
-    const int64_t at0 = row * p.K;
+    const RowUnits<SHIFT> u(row, p.M, p.K, p.h == p.x || p.h == p.res);
     const int col0 = (wi * 32 + lane) * 8, step = W * 256;
-    const int cols = row < p.M ? p.K : 0;                    // a row past the last has none
+    const int cols = row < p.M ? u.end() : 0;                // a row past the last has none
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
 
     auto load_h = [&](int col) {
-        const uint4 a = *reinterpret_cast<const uint4*>(p.x + at0 + col);
+        const uint4 a = u.masked(u.load(p.x, col), col);
         if (!p.res) return a;
-        const uint4 b = *reinterpret_cast<const uint4*>(p.res + at0 + col);
+        const uint4 b = u.masked(u.load(p.res, col), col);
         return make_uint4(norm_add2(a.x, b.x), norm_add2(a.y, b.y), norm_add2(a.z, b.z), norm_add2(a.w, b.w));
     };
     auto squares = [&](const uint4& q) {
@@ -182,8 +253,8 @@ rms_norm_kernel(const __grid_constant__ NormParams p)
 #pragma unroll
             for (int c = 0; c < C; ++c) {
                 const int col = col0 + c * step;
-                held[c] = col < cols ? *reinterpret_cast<const uint4*>(p.x + at0 + col) : zero;
-                r[c] = col < cols ? *reinterpret_cast<const uint4*>(p.res + at0 + col) : zero;
+                held[c] = col < cols ? u.load(p.x, col) : zero;
+                r[c] = col < cols ? u.load(p.res, col) : zero;
             }
 #pragma unroll
             for (int c = 0; c < C; ++c)
@@ -192,19 +263,20 @@ rms_norm_kernel(const __grid_constant__ NormParams p)
         } else {
 #pragma unroll
             for (int c = 0; c < C; ++c)
-                held[c] = col0 + c * step < cols ? *reinterpret_cast<const uint4*>(p.x + at0 + col0 + c * step) : zero;
+                held[c] = col0 + c * step < cols ? u.load(p.x, col0 + c * step) : zero;
         }
 #pragma unroll
         for (int c = 0; c < C; ++c) {
             const int col = col0 + c * step;
+            if constexpr (SHIFT) held[c] = u.masked(held[c], col);
             ss += squares(held[c]);
-            if (p.h && col < cols) *reinterpret_cast<uint4*>(p.h + at0 + col) = held[c];
+            if (p.h && col < cols) u.store(p.h, col, held[c]);
         }
     } else {
         for (int col = col0; col < cols; col += step) {
             const uint4 q = load_h(col);
             ss += squares(q);
-            if (p.h) *reinterpret_cast<uint4*>(p.h + at0 + col) = q;
+            if (p.h) u.store(p.h, col, q);
         }
     }
     ss = warp_sum(ss);
@@ -227,29 +299,29 @@ rms_norm_kernel(const __grid_constant__ NormParams p)
 
     auto emit = [&](const uint4& q, int col) {
         const bool in = col < cols;
-        const uint4 w = in ? ldg_cached(p.w + col) : zero;
+        const uint4 w = in ? u.weight(p.w, col) : zero;
         if constexpr (OUT == kNormBf16) {
             auto two = [&](uint32_t a, uint32_t b) {
                 const uint64_t v = mul_f32x2(bf16x2_to_f32x2(a), bf16x2_to_f32x2(b));
                 return f32x2_to_bf16x2(fma_f32x2(v, hi2, mul_f32x2(v, lo2)));
             };
             if (in)
-                *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(p.y) + at0 + col) =
-                    make_uint4(two(q.x, w.x), two(q.y, w.y), two(q.z, w.z), two(q.w, w.w));
+                u.store(reinterpret_cast<uint16_t*>(p.y), col,
+                        make_uint4(two(q.x, w.x), two(q.y, w.y), two(q.z, w.z), two(q.w, w.w)));
         } else if constexpr (OUT == kNormQ8_1) {
-            float v[8], u[8];
+            float v[8], g[8];
             unpack8(q, v);
-            unpack8(w, u);
+            unpack8(w, g);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = in ? norm_scaled(v[i], u[i], hi, lo) : 0.0f;
-            norm_store8<OUT>(p, v, at0 + col, in);
+            for (int i = 0; i < 8; ++i) v[i] = in ? norm_scaled(v[i], g[i], hi, lo) : 0.0f;
+            norm_store8<OUT>(p, v, u.base + col, in);
         } else {
             float v[8];
             norm_scaled_odd2(q.x, w.x, hi2, lo2, odd, v[0], v[1]);
             norm_scaled_odd2(q.y, w.y, hi2, lo2, odd, v[2], v[3]);
             norm_scaled_odd2(q.z, w.z, hi2, lo2, odd, v[4], v[5]);
             norm_scaled_odd2(q.w, w.w, hi2, lo2, odd, v[6], v[7]);
-            norm_store8<OUT>(p, v, at0 + col, in);           // (whole blocks are in or out: columns are in blocks of 32)
+            norm_store8<OUT>(p, v, u.base + col, in);           // (whole blocks are in or out: columns are in blocks of 32)
         }
     };
     if constexpr (C > 0) {
@@ -259,7 +331,7 @@ rms_norm_kernel(const __grid_constant__ NormParams p)
         // h where it is stored (this thread wrote it, possibly over x or r)
         for (int base = 0; base < p.K; base += step) {
             const int col = base + col0;
-            emit(col >= cols ? zero : p.h ? *reinterpret_cast<const uint4*>(p.h + at0 + col) : load_h(col), col);
+            emit(col >= cols ? zero : p.h ? u.masked(u.load(p.h, col), col) : load_h(col), col);
         }
     }
 }
@@ -307,7 +379,7 @@ struct NormGradParams {
     const float* rstd;
     const uint16_t* dh;        // or NULL
     uint16_t* dx;
-    float* part;               // [CTAs x rows of a CTA][K] sums of dw, or NULL
+    float* part;               // [CTAs][K] sums of dw, or NULL
     float inv_k;
     int64_t M;
     int K;
@@ -315,12 +387,13 @@ struct NormGradParams {
 
 // CTAs walk the rows (row groups of the grid apart), the next row's loads in flight while one is
 // worked on (not with 32 warps, whose registers hold one row's); a thread keeps its columns' share of dw in registers until its last row.
-template <int W, int C>
+template <int W, int C, bool SHIFT>
 __global__ void __launch_bounds__(norm_threads(W))
 rms_norm_grad_kernel(const __grid_constant__ NormGradParams p)
 {
     constexpr int R = norm_rows(W);
     __shared__ float part[2][R][W];
+    __shared__ float sums[R > 1 ? 256 * W * C : 1];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, group = warp / W, wi = warp % W;
     const int col0 = (wi * 32 + lane) * 8, step = W * 256;
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -332,27 +405,28 @@ rms_norm_grad_kernel(const __grid_constant__ NormGradParams p)
     };
     auto load = [&](Row& v, int64_t row) {
         const bool live = row < p.M;
-        const int64_t at0 = row * p.K;
+        const RowUnits<SHIFT> u(row, p.M, p.K);
 #pragma unroll
         for (int c = 0; c < C; ++c) {
             const int col = col0 + c * step;
-            const bool in = live && col < p.K;
-            v.d[c] = in ? ldg_stream(p.dy + at0 + col) : zero;
-            v.h[c] = in ? ldg_stream(p.h + at0 + col) : zero;
-            v.r[c] = in && p.dh ? ldg_stream(p.dh + at0 + col) : zero;
+            const bool in = live && col < u.end();
+            v.d[c] = in ? u.template load<true>(p.dy, col) : zero;
+            v.h[c] = in ? u.template load<true>(p.h, col) : zero;
+            v.r[c] = in && p.dh ? u.template load<true>(p.dh, col) : zero;
         }
         v.s = live ? p.rstd[row] : 0.0f;
     };
+    const int64_t stride = (int64_t)gridDim.x * R;           // (SHIFT: a multiple of 8, so a warp's rows all start alike)
+    int64_t row = (int64_t)blockIdx.x * R + group;
+    const RowUnits<SHIFT> first(row, p.M, p.K);
     uint4 w[C];
     uint64_t acc[C][4];
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-        w[c] = col0 + c * step < p.K ? ldg_cached(p.w + col0 + c * step) : zero;
+        w[c] = col0 + c * step < first.end() ? first.weight(p.w, col0 + c * step) : zero;
 #pragma unroll
         for (int i = 0; i < 4; ++i) acc[c][i] = 0;
     }
-    const int64_t stride = (int64_t)gridDim.x * R;
-    int64_t row = (int64_t)blockIdx.x * R + group;
     constexpr bool kAhead = W < 32;
     Row cur, next;
     if constexpr (kAhead) load(cur, row);
@@ -364,6 +438,10 @@ rms_norm_grad_kernel(const __grid_constant__ NormGradParams p)
         uint64_t dot2 = 0;
 #pragma unroll
         for (int c = 0; c < C; ++c) {
+            if constexpr (SHIFT) {
+                cur.d[c] = first.masked(cur.d[c], col0 + c * step);
+                cur.h[c] = first.masked(cur.h[c], col0 + c * step);
+            }
             const uint32_t dv[4] = {cur.d[c].x, cur.d[c].y, cur.d[c].z, cur.d[c].w}, hv[4] = {cur.h[c].x, cur.h[c].y, cur.h[c].z, cur.h[c].w},
                            wv[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
 #pragma unroll
@@ -386,31 +464,78 @@ rms_norm_grad_kernel(const __grid_constant__ NormGradParams p)
             }
         }
         const uint64_t coef = f32x2_splat(-(cur.s * cur.s * (dot * p.inv_k)));
-        const int64_t at0 = row * p.K;
+        const RowUnits<SHIFT> u(row, p.M, p.K);
 #pragma unroll
         for (int c = 0; c < C; ++c) {
             const int col = col0 + c * step;
-            if (!(row < p.M && col < p.K)) continue;
+            if (!(row < p.M && col < u.end())) continue;
             // s (g - h coef) + dh
             auto two = [&](uint32_t d, uint32_t h, uint32_t ww, uint32_t r) {
                 const uint64_t g = mul_f32x2(bf16x2_to_f32x2(d), bf16x2_to_f32x2(ww));             // exact
                 return f32x2_to_bf16x2(fma_f32x2(s2, fma_f32x2(bf16x2_to_f32x2(h), coef, g), bf16x2_to_f32x2(r)));
             };
-            *reinterpret_cast<uint4*>(p.dx + at0 + col) =
-                make_uint4(two(cur.d[c].x, cur.h[c].x, w[c].x, cur.r[c].x), two(cur.d[c].y, cur.h[c].y, w[c].y, cur.r[c].y),
-                           two(cur.d[c].z, cur.h[c].z, w[c].z, cur.r[c].z), two(cur.d[c].w, cur.h[c].w, w[c].w, cur.r[c].w));
+            u.store(p.dx, col,
+                    make_uint4(two(cur.d[c].x, cur.h[c].x, w[c].x, cur.r[c].x), two(cur.d[c].y, cur.h[c].y, w[c].y, cur.r[c].y),
+                               two(cur.d[c].z, cur.h[c].z, w[c].z, cur.r[c].z), two(cur.d[c].w, cur.h[c].w, w[c].w, cur.r[c].w)));
         }
         if constexpr (kAhead) cur = next;
     }
     if (!p.part) return;
-    float* out = p.part + ((int64_t)blockIdx.x * R + group) * p.K;
+    float* out = p.part + (int64_t)blockIdx.x * p.K;
+    if constexpr (R > 1) {                                   // the CTA's row groups, one after the other
+        for (int g = 0; g < R; ++g) {
+            if (group == g) {
 #pragma unroll
-    for (int c = 0; c < C; ++c) {
-        const int col = col0 + c * step;
-        if (col >= p.K) continue;
-        *reinterpret_cast<ulonglong2*>(out + col) = make_ulonglong2(acc[c][0], acc[c][1]);
-        *reinterpret_cast<ulonglong2*>(out + col + 4) = make_ulonglong2(acc[c][2], acc[c][3]);
+                for (int c = 0; c < C; ++c) {
+                    const int col = col0 + c * step;
+                    float v[8];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) f32x2_unpack(acc[c][i], v[2 * i], v[2 * i + 1]);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        if (first.has(col, i)) sums[col + i - first.s] = (g == 0 ? 0.0f : sums[col + i - first.s]) + v[i];
+                }
+            }
+            __syncthreads();
+        }
+        for (int k = threadIdx.x; k < p.K; k += norm_threads(W)) out[k] = sums[k];
+    } else {
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const int col = col0 + c * step;
+            if constexpr (SHIFT) {
+                float v[8];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) f32x2_unpack(acc[c][i], v[2 * i], v[2 * i + 1]);
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (first.has(col, i)) out[col + i - first.s] = v[i];
+            } else if (col < p.K) {
+                *reinterpret_cast<ulonglong2*>(out + col) = make_ulonglong2(acc[c][0], acc[c][1]);
+                *reinterpret_cast<ulonglong2*>(out + col + 4) = make_ulonglong2(acc[c][2], acc[c][3]);
+            }
+        }
     }
+}
+
+// dw from the CTAs' sums: 32 columns a block, whose warps take the CTAs in turn and meet in order.
+__global__ void __launch_bounds__(1024) norm_sum_kernel(const float* __restrict__ part, uint16_t* __restrict__ dw, int K, int parts)
+{
+    __shared__ float sums[32][33];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t k = (int64_t)blockIdx.x * 32 + lane;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    float s = 0.0f;
+    if (k < K) {
+#pragma unroll 8
+        for (int i = warp; i < parts; i += 32) s += part[(int64_t)i * K + k];
+    }
+    sums[warp][lane] = s;
+    __syncthreads();
+    s = warp_sum(sums[lane][warp]);                          // column `warp` of the block
+    const int64_t c = (int64_t)blockIdx.x * 32 + warp;
+    if (lane == 0 && c < K) dw[c] = (uint16_t)f32_to_bf16_bits(s);
 }
 
 // Any K: dx, one row a CTA, element by element; dy and h are read twice.
