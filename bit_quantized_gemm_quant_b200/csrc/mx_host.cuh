@@ -466,15 +466,17 @@ int64_t norm_units(int64_t K) { return K % 8 == 0 ? K : K + 7; }
 
 // The gradient's (a thread keeps three rows' chunks twice and the sums of dw) and its CTAs per SM.  2048
 // rows: 8192 wide 24.9 us with 8 warps of four chunks, 26.1 with 16 of two; 4096 wide 13.6 with two CTAs of
-// 16 of one, 14.6 with 8 of two; 8192 x 1024 13.9 with three CTAs, 16.0 with two.
+// 16 of one, 14.6 with 8 of two; 8192 x 1024 13.9 with three CTAs, 16.0 with two.  Rows that do not start on
+// 16 bytes (shift): 7197 x 1941 33.7 with 8 of one, 39.0 with 4 of two.
 template <typename F>
-auto norm_grad_config(int64_t K, F&& go)
+auto norm_grad_config(int64_t K, bool shift, F&& go)
 {
     using std::integral_constant;
 #define BQ_NORM(W, C, PER) return go(integral_constant<int, W>{}, integral_constant<int, C>{}, integral_constant<int, PER>{})
     if (K <= 256) BQ_NORM(1, 1, 3);
     if (K <= 512) BQ_NORM(2, 1, 3);
     if (K <= 1024) BQ_NORM(4, 1, 3);
+    if (shift && K <= 2048) BQ_NORM(8, 1, 3);
     if (K <= 2048) BQ_NORM(4, 2, 2);
     if (K <= 4096) BQ_NORM(16, 1, 2);
     if (K <= 8192) BQ_NORM(8, 4, 1);
@@ -533,11 +535,14 @@ NormGradPlan plan_norm_grad(int64_t M, int64_t K, int num_sms)
         pl.rows = (int)rows;
         pl.parts = (M + rows - 1) / rows;
     } else {
-        norm_grad_config(norm_units(K), [&](auto w, auto, auto per) {
+        norm_grad_config(norm_units(K), K % 8 != 0, [&](auto w, auto, auto per) {
             constexpr int W = decltype(w)::value;
             pl.grid = (int)std::min<int64_t>((M + norm_rows(W) - 1) / norm_rows(W), (int64_t)num_sms * decltype(per)::value);
             // rows that do not start on 16 bytes: those of a warp are a multiple of 8 apart
-            if (K % 8 != 0) pl.grid = (int)(((int64_t)pl.grid * norm_rows(W) + 7) / 8 * 8 / norm_rows(W));
+            if (K % 8 != 0) {
+                constexpr int kEight = 8 / norm_rows(W);      // CTAs of 8 rows
+                pl.grid = std::max(pl.grid / kEight, 1) * kEight;
+            }
             pl.parts = pl.grid;
             return 0;
         });
@@ -566,7 +571,7 @@ bq_status norm_backward(const NormGradPlan& pl, const NormGradParams& p, uint16_
             s = launch_pdl_dim(rms_norm_weight_grad_any_kernel, dim3((unsigned)((p.K + 127) / 128), (unsigned)pl.parts), 128, 0,
                                st, p, pl.rows);
     } else {
-        s = norm_grad_config(norm_units(p.K), [&](auto w, auto c, auto) {
+        s = norm_grad_config(norm_units(p.K), p.K % 8 != 0, [&](auto w, auto c, auto) {
             constexpr int W = decltype(w)::value, C = decltype(c)::value;
             return p.K % 8 == 0 ? launch_pdl(rms_norm_grad_kernel<W, C, false>, pl.grid, norm_threads(W), 0, st, p)
                                 : launch_pdl(rms_norm_grad_kernel<W, C, true>, pl.grid, norm_threads(W), 0, st, p);

@@ -167,16 +167,21 @@ struct RowUnits {
     BQ_DEVINL bool whole(int col) const { return !SHIFT || (col >= s && col + 8 <= K + s); }
     BQ_DEVINL bool has(int col, int i) const { return col + i >= s && col + i < K + s; }
 
+    BQ_DEVINL bool past(int col) const { return SHIFT && base + col + 8 > total; }      // the matrix ends in this unit
+
     // The unit as it lies in memory; masked() takes the neighbours' elements out.
-    template <bool STREAM = false>
     BQ_DEVINL uint4 load(const uint16_t* p, int col) const
     {
-        if (whole(col) || (!strict && base + col + 8 <= total)) {
-            if constexpr (STREAM) return ldg_stream(p + base + col);
-            return *reinterpret_cast<const uint4*>(p + base + col);
-        }
+        if (whole(col) || (!strict && !past(col))) return *reinterpret_cast<const uint4*>(p + base + col);
         return gather(p + base + col, col);
     }
+    // The same for loads ahead of their use: nothing of a unit that is past(), whose elements mend() fetches at the use.
+    // (A branch to them here makes the loads before it wait.)
+    BQ_DEVINL uint4 load_ahead(const uint16_t* p, int col, bool in) const
+    {
+        return in && !past(col) ? ldg_stream(p + base + col) : make_uint4(0u, 0u, 0u, 0u);
+    }
+    BQ_DEVINL uint4 mend(const uint16_t* p, int col) const { return gather(p + base + col, col); }
     BQ_DEVINL uint4 masked(const uint4& q, int col) const
     {
         if (whole(col)) return q;
@@ -410,9 +415,9 @@ rms_norm_grad_kernel(const __grid_constant__ NormGradParams p)
         for (int c = 0; c < C; ++c) {
             const int col = col0 + c * step;
             const bool in = live && col < u.end();
-            v.d[c] = in ? u.template load<true>(p.dy, col) : zero;
-            v.h[c] = in ? u.template load<true>(p.h, col) : zero;
-            v.r[c] = in && p.dh ? u.template load<true>(p.dh, col) : zero;
+            v.d[c] = u.load_ahead(p.dy, col, in);
+            v.h[c] = u.load_ahead(p.h, col, in);
+            v.r[c] = u.load_ahead(p.dh, col, in && p.dh);
         }
         v.s = live ? p.rstd[row] : 0.0f;
     };
@@ -427,18 +432,25 @@ rms_norm_grad_kernel(const __grid_constant__ NormGradParams p)
 #pragma unroll
         for (int i = 0; i < 4; ++i) acc[c][i] = 0;
     }
-    constexpr bool kAhead = W < 32;
+    constexpr bool kAhead = W * C < 64;
     Row cur, next;
     if constexpr (kAhead) load(cur, row);
     int buf = 0;
     for (int64_t row0 = (int64_t)blockIdx.x * R; row0 < p.M; row0 += stride, row += stride, buf ^= 1) {
         if constexpr (kAhead) load(next, row + stride);
         else load(cur, row);
+        const RowUnits<SHIFT> u(row, p.M, p.K);
         const uint64_t s2 = f32x2_splat(cur.s);
         uint64_t dot2 = 0;
 #pragma unroll
         for (int c = 0; c < C; ++c) {
             if constexpr (SHIFT) {
+                const int col = col0 + c * step;
+                if (row < p.M && col < u.end() && u.past(col)) {
+                    cur.d[c] = u.mend(p.dy, col);
+                    cur.h[c] = u.mend(p.h, col);
+                    if (p.dh) cur.r[c] = u.mend(p.dh, col);
+                }
                 cur.d[c] = first.masked(cur.d[c], col0 + c * step);
                 cur.h[c] = first.masked(cur.h[c], col0 + c * step);
             }
@@ -464,7 +476,6 @@ rms_norm_grad_kernel(const __grid_constant__ NormGradParams p)
             }
         }
         const uint64_t coef = f32x2_splat(-(cur.s * cur.s * (dot * p.inv_k)));
-        const RowUnits<SHIFT> u(row, p.M, p.K);
 #pragma unroll
         for (int c = 0; c < C; ++c) {
             const int col = col0 + c * step;
