@@ -191,7 +191,7 @@ bq_status launch_pair(const DeviceInfo& di, int dev, const PairPlan& pl, const u
     const unsigned grid = 2u * (unsigned)std::min<int64_t>(pl.split.tail && pl.split.dp_tiles ? pl.pairs
                                                            : pl.split.tail ? pl.split.tail_pairs : pl.tiles, pl.pairs);
     const size_t smem = std::max<size_t>(1024 + (size_t)pl.stages * pair_stage_bytes(pl.bn) + 512,
-                                         (size_t)di.max_smem_optin / 2 + 1024);   // one CTA per SM (all of TMEM)
+                                         kPairMinSmem);
     kern<<<grid, kPairThreads, smem, st>>>(ta[0], ta[1], tb[0], tb[1], p);
     bq_status s = launch_status();
     return s != BQ_OK ? s : launch_reduce<EPI>(di, pl, p, st);
@@ -415,7 +415,7 @@ bq_status launch_fused_pair(const DeviceInfo& di, int dev, const PairPlan& pl, c
     const unsigned grid = 2u * (unsigned)std::min<int64_t>(pl.split.tail && pl.split.dp_tiles ? pl.pairs
                                                            : pl.split.tail ? pl.split.tail_pairs : pl.tiles, pl.pairs);
     const size_t smem = std::max<size_t>(1024 + fp_fixed_bytes(MODE, T, pl.codes) + (size_t)pl.stages * (size_t)pl.bn * 128u + 512,
-                                         (size_t)di.max_smem_optin / 2 + 1024);   // one CTA per SM (all of TMEM)
+                                         kPairMinSmem);
     const bq_status s = launch_pdl_dim(kern, dim3(grid), kFpThreads, smem, st, ta[0], ta[1], tb[0], tb[1], p);
     return s != BQ_OK ? s : launch_reduce<EPI>(di, pl, p.q, st);
 }

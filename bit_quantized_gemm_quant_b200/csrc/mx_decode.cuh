@@ -22,6 +22,8 @@
 namespace bq {
 
 constexpr int kMdThreads = 128;               // 4 warps: scales, then epilogue; between them warp 0 copies, warp 1 issues MMAs
+constexpr uint32_t kMdMinSmem = 78 * 1024;    // shared memory asked for at least: two CTAs on an SM, never three or one of a pair
+static_assert(3 * (kMdMinSmem + 1024) > 228 * 1024 && kMdMinSmem + kPairMinSmem + 2 * 1024 > 228 * 1024, "an SM's shared memory, 1 KB a CTA the system's");
 constexpr int kMdTile = 64;                   // tokens of a tile
 constexpr int kMdMaxStages = 8;
 constexpr int kMdMaxChunks = 64;              // of a CTA's range

@@ -140,7 +140,7 @@ bool plan_md(int64_t M, int64_t N, int64_t K, int xbits, int num_sms, int smem_o
         pl->log_cluster = l;
         pl->range = (int)range;
         pl->stages = (int)stages;
-        pl->smem = std::max<size_t>((size_t)(1024 + stages * (int64_t)md_stage_bytes(bn) + fixed), 79872);
+        pl->smem = std::max<size_t>((size_t)(1024 + stages * (int64_t)md_stage_bytes(bn) + fixed), kMdMinSmem);
     }
     if (best == 1e300 || rt << pl->log_cluster > INT32_MAX) return false;
     pl->nk = (int)nk;
@@ -373,7 +373,7 @@ bq_status launch_mx_pair(const DeviceInfo& di, int dev, const MxWs& w, const voi
     const unsigned grid = 2u * (unsigned)std::min<int64_t>(pl.split.tail && pl.split.dp_tiles ? pl.pairs
                                                            : pl.split.tail ? pl.split.tail_pairs : pl.tiles, pl.pairs);
     const size_t smem = std::max<size_t>(1024 + (size_t)pl.stages * mx_stage_bytes(XB, H, pl.bn) + 512,
-                                         (size_t)di.max_smem_optin / 2 + 1024);   // one CTA per SM (all of TMEM)
+                                         kPairMinSmem);
     const bq_status s = launch_pdl_dim(kern, dim3(grid), kMxThreads, smem, st, ta, tb, tsa, tsb, p);
     return s != BQ_OK ? s : launch_reduce<kEpiPlain>(di, pl, p.q, st);
 }

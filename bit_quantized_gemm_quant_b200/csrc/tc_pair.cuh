@@ -130,6 +130,13 @@ constexpr int kPairThreads = 32 * (kPairEpiWarps + 2);
 constexpr int kPairAccCols = 256;
 constexpr uint32_t kPairABytes = 128 * 128;                  // 128 rows x 64 bf16 per CTA and stage
 
+// Shared memory that a CTA of a pair asks for at least: all of tensor memory is its own, and beside it
+// no CTA may be resident that holds tensor memory while it waits for another SM's CTA.  (Such a CTA on
+// one SM, waiting for one that this CTA keeps from its columns on another, and this CTA's partner waiting
+// for the first one's columns, would wait for each other for good.)  More than half of an SM's keeps two
+// pairs apart; this much also a pair and a cluster of mx_decode_kernel (kMdMinSmem).
+constexpr uint32_t kPairMinSmem = 156 * 1024;
+
 __host__ __device__ constexpr uint32_t pair_stage_bytes(int bn) { return kPairABytes + (uint32_t)bn * 64u; }
 
 struct PairParams {

@@ -194,6 +194,31 @@ def test_streams_at_once():
     assert torch.equal(back, bq.mxfp8_dequantize(*bq.mxfp8_quantize(x)))
 
 
+def test_products_of_every_kind_at_once():
+    """Products on clusters, on pairs of SMs, and gradients, of one stage and of many, that meet on the SMs from
+    streams of their own: each holds tensor memory, and those that wait for another SM's part keep apart."""
+    def codes(rows, k, bits, seed):
+        g = torch.Generator(device="cuda")
+        g.manual_seed(seed)
+        return _mx.random_codes(rows, k, bits, g)
+
+    sizes = [(1, 2048, 8192, 8), (16, 1024, 2048, 4), (300, 8192, 64, 4), (700, 2048, 1024, 8), (260, 4096, 4096, 4)]
+    ins = [(codes(m, k, a, i), codes(n, k, 4, 20 + i), torch.randn(m, n, device="cuda").bfloat16())
+           for i, (m, n, k, a) in enumerate(sizes)]
+    calls = [lambda i=i: bq.mx_matmul(*i[0], *i[1]) for i in ins] + [lambda i=i: bq.mx_matmul_backward(i[2], *i[1]) for i in ins[2:4]]
+    want = [c() for c in calls]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in calls]
+    got = [[] for _ in calls]
+    for _ in range(30):
+        for i, st in enumerate(streams):
+            with torch.cuda.stream(st):
+                got[i].append(calls[i]())
+    torch.cuda.synchronize()
+    for w, outs in zip(want, got):
+        assert all(torch.equal(w.view(torch.int16), o.view(torch.int16)) for o in outs)
+
+
 @pytest.mark.parametrize("M,N,K,a", [(3, 300, 1056, 8), (200, 300, 1056, 8), (300, 700, 4096, 8), (130, 260, 4096, 4),
                                      (700, 520, 1024, 4)])
 def test_workspaces_of_exactly_their_size(M, N, K, a):
