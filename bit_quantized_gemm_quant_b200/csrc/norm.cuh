@@ -593,7 +593,7 @@ rms_norm_weight_grad_any_kernel(const __grid_constant__ NormGradParams p, int ro
 
 // Few rows: dx and dw in one launch.  rstd is an input, so dw needs nothing from the rows' sums: blocks
 // of it read dy and h again (from L2) beside those of dx.  One launch and no workspace instead of two
-// and one: 333 x 2048, 8.3 us to 5.6, most of it the host's.
+// and one: 333 x 2048, 8.3 us to 4.6, most of it the host's.
 //
 // V = 8: columns in chunks of 8 (K a multiple of 8, at most 4096 in a row's registers); V = 1: any K.
 // Blocks [0, row_blocks): dx of one row; then dw of 8 V columns each, whose rows 32 groups of 8
