@@ -378,7 +378,7 @@ mx_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__
         }
     } else if (warp == kMxMmaWarp) {
         // ---------------- MMA issuer (the leader's; one elected lane issues) ----------------
-        if (rank == 0) {                                 // the whole warp, as in tc_pair.cuh
+        if (rank == 0 && elect_one()) {
             const uint32_t idesc = umma_idesc_mx<XB>(256, p.bn);
             const uint64_t bd0 = umma_desc_k_sw128(b_base);
             const uint32_t desc_hi = (uint32_t)(bd0 >> 32), b_lo0 = (uint32_t)bd0, a_lo0 = (uint32_t)umma_desc_k_sw128(a_base);
@@ -394,53 +394,49 @@ mx_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__
                 const int kb0 = u.kb0, kb1 = u.kb1;
                 const int acc0 = H == 1 ? lt & 1 : 0;
                 const uint32_t use = H == 1 ? (uint32_t)(lt >> 1) : (uint32_t)lt;
-                if (!mbar_wait_warp(tempty_bar(acc0), (use & 1u) ^ 1u)) break;
+                if (!mbar_wait(tempty_bar(acc0), (use & 1u) ^ 1u)) break;
                 for (int it = kb0; it < kb1; ++it) {
-                    if (T < S && issued >= T && !mbar_wait_warp(empty_bar(back), ph_back)) { ok = false; break; }
-                    if (!mbar_wait_warp(full_bar(s), ph)) { ok = false; break; }
-                    if (H == 2 && it == kb0 && !mbar_wait_warp(tempty_bar(1), (use & 1u) ^ 1u)) { ok = false; break; }
+                    if (T < S && issued >= T && !mbar_wait(empty_bar(back), ph_back)) { ok = false; break; }
+                    if (!mbar_wait(full_bar(s), ph)) { ok = false; break; }
+                    if (H == 2 && it == kb0 && !mbar_wait(tempty_bar(1), (use & 1u) ^ 1u)) { ok = false; break; }
                     tc_fence_after();
-                    if (elect_one()) {
-                        const uint32_t sfa = sf_tmem0 + (uint32_t)(t * sf_cols), sfb = sfa + 4u * kChunks;
-                        const uint32_t sm = sf_base + (uint32_t)s * sf_bytes;
+                    const uint32_t sfa = sf_tmem0 + (uint32_t)(t * sf_cols), sfb = sfa + 4u * kChunks;
+                    const uint32_t sm = sf_base + (uint32_t)s * sf_bytes;
 #pragma unroll
-                        for (int c = 0; c < kChunks; ++c) {
-                            scales_to_tmem_pair(sfa + 4u * c, sm + 512u * c);
+                    for (int c = 0; c < kChunks; ++c) {
+                        scales_to_tmem_pair(sfa + 4u * c, sm + 512u * c);
 #pragma unroll
-                            for (int h = 0; h < H; ++h) {
-                                const uint32_t hc = (uint32_t)(h * kChunks + c), from = sm + 512u * kChunks + 128u * group_cols * hc;
-                                scales_to_tmem_pair(sfb + group_cols * hc, from);
-                                if (groups == 2) scales_to_tmem_pair(sfb + group_cols * hc + 4u, from + 512u);
-                            }
+                        for (int h = 0; h < H; ++h) {
+                            const uint32_t hc = (uint32_t)(h * kChunks + c), from = sm + 512u * kChunks + 128u * group_cols * hc;
+                            scales_to_tmem_pair(sfb + group_cols * hc, from);
+                            if (groups == 2) scales_to_tmem_pair(sfb + group_cols * hc + 4u, from + 512u);
                         }
-                        const uint32_t al0 = a_lo0 + (uint32_t)s * (kAStage >> 4), bl0 = b_lo0 + (uint32_t)s * (b_bytes >> 3);
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            const uint32_t al = al0 + (H == 1 ? i * (kPairABytes >> 4) : 0u), bl = bl0 + i * (b_bytes >> 4);
-                            const uint32_t d = tmem_base + (uint32_t)((H == 1 ? acc0 : i) * p.bn);
-#pragma unroll
-                            for (int k = 0; k < 4; ++k) {
-                                const uint32_t c = (H == 1 ? i * (kChunks / 2) : 0) + (XB == 4 ? k >> 1 : 0);
-                                const uint32_t hc = H == 1 ? c : i * kChunks + c;
-                                const uint32_t sf = XB == 4 ? 2u * (k & 1) : (uint32_t)k;        // the first scale byte of its word
-                                umma_mx_pair<XB>(d, al + 2u * k, bl + 2u * k, desc_hi, idesc | sf << 4 | sf << 29, sfa + 4u * c,
-                                                 sfb + group_cols * hc, it > kb0 || k > 0 || (H == 1 && i > 0));
-                            }
-                            if (H == 2 && i == 0 && it + 1 == kb1) umma_commit_pair(tfull_bar(0));
-                        }
-                        umma_commit_pair(empty_bar(s));
-                        if (it + 1 == kb1) umma_commit_pair(tfull_bar(H == 1 ? acc0 : 1));
                     }
-                    __syncwarp();
+                    const uint32_t al0 = a_lo0 + (uint32_t)s * (kAStage >> 4), bl0 = b_lo0 + (uint32_t)s * (b_bytes >> 3);
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const uint32_t al = al0 + (H == 1 ? i * (kPairABytes >> 4) : 0u), bl = bl0 + i * (b_bytes >> 4);
+                        const uint32_t d = tmem_base + (uint32_t)((H == 1 ? acc0 : i) * p.bn);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const uint32_t c = (H == 1 ? i * (kChunks / 2) : 0) + (XB == 4 ? k >> 1 : 0);
+                            const uint32_t hc = H == 1 ? c : i * kChunks + c;
+                            const uint32_t sf = XB == 4 ? 2u * (k & 1) : (uint32_t)k;        // the first scale byte of its word
+                            umma_mx_pair<XB>(d, al + 2u * k, bl + 2u * k, desc_hi, idesc | sf << 4 | sf << 29, sfa + 4u * c,
+                                             sfb + group_cols * hc, it > kb0 || k > 0 || (H == 1 && i > 0));
+                        }
+                        if (H == 2 && i == 0 && it + 1 == kb1) umma_commit_pair(tfull_bar(0));
+                    }
+                    umma_commit_pair(empty_bar(s));
+                    if (it + 1 == kb1) umma_commit_pair(tfull_bar(H == 1 ? acc0 : 1));
                     ++issued;
                     if (++s == S) { s = 0; ph ^= 1u; }
                     if (++t == T) t = 0;
                     if (++back == S) { back = 0; ph_back ^= 1u; }
                 }
             }
-            if (elect_one()) umma_commit_leader(done_bar);   // nothing stays in flight past this point
-            __syncwarp();
-            mbar_wait_warp(done_bar, 0);
+            umma_commit_leader(done_bar);                // nothing stays in flight past this point
+            mbar_wait(done_bar, 0);
         }
     } else {
         // ---------------- epilogue ----------------
