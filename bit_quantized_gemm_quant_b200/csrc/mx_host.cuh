@@ -267,11 +267,11 @@ bool make_plan_mx(int64_t M, int64_t N, int64_t K, int x_bits, int num_sms, int 
     w->pad = x_bits == 8 && K % 128 != 0;
     w->k = w->pad ? (K + 127) / 128 * 128 : K;
     w->off_w = w->pad ? up256((size_t)N * (size_t)w->k / 2) + 256u : 0u;      // from the next multiple of 256 on
-    // Beyond one tile of tokens the one-launch kernel takes what it does at once and in few stages: 1000 x 1024 x
-    // 1024 8.2 us for the pairs' 6.9, which the host needs longer for; 200 x 1024 x 4096 9.3 and 11.2; 200 x 4096 x
-    // 4096, which is left to the pairs, 15.2 and 12.5.
+    // Beyond one tile of tokens the one-launch kernel takes what it does at once and in few stages.  Two tiles: 128 x
+    // 2048 x 4096, 4 bits, 7.6 us for the pairs' 8.5 (two launches); 200 x 4096 x 4096, 15.2 and 11.4.  More: 500 x 200 x
+    // 1024 5.7 and 7.4, of which the host needs most; 400 x 1024 x 2048, which is left to the pairs, 7.6 and 6.5.
     w->decode = plan_md(M, N, K, x_bits, num_sms, smem_optin, &w->md) &&
-                (M <= kMdTile || (w->md.rounds == 1 && w->md.cost <= 19.0));
+                (M <= kMdTile || (w->md.rounds == 1 && w->md.cost <= (M <= 2 * kMdTile ? 19.0 : 12.0)));
     w->bytes = w->off_w;
     if (w->decode) return true;
     if (!plan_mx_pair(N, M, K, x_bits, num_sms, smem_optin, &w->pl)) return false;
