@@ -20,7 +20,8 @@
 //     much per token, but the next unit's products wait until the epilogue has read the accumulators.
 // (With one product a stage the barriers set the pace: a turn of the loop from full to empty
 // and back, with no copies, scales or products in it, takes 330 to 450 clocks, the product at
-// 192 tokens 384.)
+// 192 tokens 384.  One lane issues throughout: 300 x 2048 x 8192 with 8-bit tokens 14.5 us, 17.1 where the
+// warp waits together and elects the lane.)
 //
 // Scales live in tensor memory as the instruction wants them: row r of an operand in lane
 // r % 32, column r / 32, a 32-bit word of the scales of 128 consecutive k (the same in all four
