@@ -251,7 +251,8 @@ mx_dequant_kernel(const uint8_t* __restrict__ codes, const uint8_t* __restrict__
 
 // ------------------------------------------------------------------ longer rows
 // Rows of 16-byte units to longer ones, zeros behind: [rows][in] to [rows][out] units.  (Codes of W for
-// products whose copies want rows of whole 128 codes.)  Blocks of 256 threads, kMxPadSpan units each.
+// products whose copies want rows of whole 128 codes.)  Blocks of 256 threads, kMxPadSpan units each,
+// of a launch with other work (mx_pack_kernel).
 struct MxPadParams {
     const uint4* from;
     uint4* to;
@@ -274,13 +275,6 @@ BQ_DEVINL void mx_pad_block(const MxPadParams& p, int64_t block)
         const int64_t i = block * kMxPadSpan + 256 * j + threadIdx.x;
         if (i < p.rows * p.out) p.to[i] = v[j];
     }
-}
-
-__global__ void __launch_bounds__(256) mx_pad_kernel(const __grid_constant__ MxPadParams p)
-{
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    mx_pad_block(p, blockIdx.x);
 }
 
 }  // namespace bq

@@ -13,6 +13,11 @@
 // for first: behind a range of codes in the memory's queues they took 3000 clocks), and the cluster's
 // CTAs write their partial products into the shared memory of the CTA that adds them, in rank order.
 //
+// 8-bit activations want the 4-bit operand in 8-byte groups with 8-byte gaps, which the tensor copy makes where rows
+// are whole 128 codes.  Elsewhere (SPREAD) the codes arrive packed, and four warps spread them over their slot of the ring,
+// a stage each.  (1 x 4096 x 4064 9.3 us, 1 x 12288 x 4064 16.1; with W copied to longer rows first, by a launch of its own, 10.1 and 19.3.  Spreading takes 1000 clocks before
+// the first product and two more waits a stage: where the copy can do it, it is ahead, 1 x 4096 x 4096 5.9 us.)
+//
 // Scales: thread t reads row t's bytes of the CTA's range (tokens: thread t token t).
 // Word of row r and chunk c (128 elements): 512 c + 16 (r % 32) + 4 (r / 32).
 #pragma once
@@ -21,7 +26,9 @@
 
 namespace bq {
 
-constexpr int kMdThreads = 128;               // 4 warps: scales, then epilogue; between them warp 0 copies, warp 1 issues MMAs
+// 4 warps: scales, then epilogue; between them warp 0 copies, warp 1 issues MMAs.  SPREAD: they spread codes in between, and
+// two more warps do that.
+__host__ __device__ constexpr int md_threads(bool spread) { return spread ? 192 : 128; }
 constexpr uint32_t kMdMinSmem = 78 * 1024;    // shared memory asked for at least: two CTAs on an SM, never three or one of a pair
 static_assert(3 * (kMdMinSmem + 1024) > 228 * 1024 && kMdMinSmem + kPairMinSmem + 2 * 1024 > 228 * 1024, "an SM's shared memory, 1 KB a CTA the system's");
 constexpr int kMdTile = 64;                   // tokens of a tile
@@ -81,16 +88,38 @@ BQ_DEVINL void st_cluster_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, 
 __host__ __device__ constexpr int md_sum_pitch(int m) { return (m + 3) / 4 * 4 + 4; }
 __host__ __device__ constexpr uint32_t md_sum_bytes(int c, int m) { return c == 1 ? 0u : 128u * (uint32_t)md_sum_pitch(m) * 4u; }
 
+// A warp spreads a stage's codes: rows of 64 packed bytes (the copy's 64-byte swizzle), the second half of the slot, to
+// rows of 128 with 8 groups of 16 codes (128-byte swizzle) all over it.
+BQ_DEVINL void md_spread(uint32_t to, int lane)
+{
+    uint4 v[4][4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+            v[q][c] = ld_shared_v4(to + kPairABytes / 2 + 64u * (uint32_t)(32 * q + lane) + 16u * (uint32_t)(c ^ ((lane >> 1) & 3)));
+    __syncwarp();                                            // every row is read
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            const uint32_t at = to + 128u * (uint32_t)(32 * q + lane);
+            st_shared_v4(at + 16u * (uint32_t)((2 * c) ^ (lane & 7)), v[q][c].x, v[q][c].y, 0u, 0u);
+            st_shared_v4(at + 16u * (uint32_t)((2 * c + 1) ^ (lane & 7)), v[q][c].z, v[q][c].w, 0u, 0u);
+        }
+}
+
 // Dynamic shared memory: ring (1024-aligned), scales of W and of the tokens (512 bytes a chunk
 // each), partial sums.
-template <int XB>
-__global__ void __launch_bounds__(kMdThreads)
+template <int XB, bool SPREAD = false>
+__global__ void __launch_bounds__(md_threads(SPREAD))
 mx_decode_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
                  const __grid_constant__ MdParams p)
 {
     constexpr int kChunks = md_chunks(XB);
     extern __shared__ uint8_t smem_raw[];
-    __shared__ __align__(8) uint64_t bars[2 * kMdMaxStages + 1];
+    constexpr int kCopier = SPREAD ? 5 : 0, kIssuer = SPREAD ? 4 : 1;
+    __shared__ __align__(8) uint64_t bars[3 * kMdMaxStages + 1];
     __shared__ uint32_t tmem_slot;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
@@ -101,7 +130,8 @@ mx_decode_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant
     const uint32_t sum_base = sfb_base + 512u * (uint32_t)p.range_chunks;
     auto full_bar = [&](int s) { return smem_u32(&bars[s]); };
     auto empty_bar = [&](int s) { return smem_u32(&bars[kMdMaxStages + s]); };
-    const uint32_t done_bar = smem_u32(&bars[2 * kMdMaxStages]);
+    auto spread_bar = [&](int s) { return smem_u32(&bars[2 * kMdMaxStages + s]); };           // SPREAD: the codes are where they belong
+    const uint32_t done_bar = smem_u32(&bars[3 * kMdMaxStages]);
 
     // (From blockIdx, not from the cluster's registers: the range, and with it the MMA warp's loop and
     // operands, stay in uniform registers; else a stage took 640 clocks to issue.)
@@ -116,6 +146,7 @@ mx_decode_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant
         for (int s = 0; s < S; ++s) {
             mbar_init(full_bar(s), 1);
             mbar_init(empty_bar(s), 1);
+            if (SPREAD) mbar_init(spread_bar(s), 1);
         }
         mbar_init(done_bar, 1);
         fence_barrier_init();
@@ -136,7 +167,8 @@ mx_decode_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant
     auto copy_stage = [&](int i, int s) {                    // stage i of the range into slot s
         const int x = (kb0 + i) * 128;                       // bytes, or elements of the spread codes
         mbar_arrive_expect_tx(full_bar(s), (XB == 4 ? kPairABytes : kPairABytes / 2) + b_bytes);
-        tma_load_2d(a_base + (uint32_t)s * kPairABytes, &tm_a, full_bar(s), x, r0);
+        if (SPREAD) tma_load_2d(a_base + (uint32_t)s * kPairABytes + kPairABytes / 2, &tm_a, full_bar(s), x / 2, r0);
+        else tma_load_2d(a_base + (uint32_t)s * kPairABytes, &tm_a, full_bar(s), x, r0);
         tma_load_2d(b_base + (uint32_t)s * b_bytes, &tm_b, full_bar(s), x, m0);
     };
 
@@ -147,7 +179,7 @@ mx_decode_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant
         // the first one's before the codes are asked for
         constexpr int kBatch = 4;
         const int c0 = kb0 * kChunks, nc = n_stages * kChunks;
-        const bool live[2] = {r0 + tid < p.N, tid < M};
+        const bool live[2] = {warp < 4 && r0 + tid < p.N, tid < M};
         const uint32_t dst = 16u * (uint32_t)lane + 4u * (uint32_t)warp;
         for (int g0 = c0 >> 2; 4 * g0 < c0 + nc; g0 += kBatch) {
             uint4 v[2][kBatch];
@@ -168,7 +200,7 @@ mx_decode_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant
                     const int c = 4 * (g0 + i) + j - c0;
                     if (c < 0 || c >= nc) continue;
 #pragma unroll
-                    for (int side = 0; side < 2; ++side) {
+                    for (int side = 0; side < 2 && warp < 4; ++side) {
                         const uint32_t w = j == 0 ? v[side][i].x : j == 1 ? v[side][i].y : j == 2 ? v[side][i].z : v[side][i].w;
                         if (side == 0 || tid < p.bn)
                             asm volatile("st.shared.u32 [%0], %1;" ::"r"((side == 0 ? sfa_base : sfb_base) + dst + 512u * (uint32_t)c), "r"(w)
@@ -178,14 +210,30 @@ mx_decode_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant
         }
         fence_proxy_async_smem();                            // the copy to tensor memory reads through the async proxy
         __syncthreads();
-        if (warp == 0) {
+        if (SPREAD && warp < 4) {
+            // ---------------- codes, spread ----------------
+            // a stage a warp, so that their waits and fences pass side by side (a slot always the same warp's: it
+            // sees every phase of the slot's barrier)
+            int s = 0;
+            uint32_t ph = 0;
+            for (int i = 0; i < n_stages; ++i) {
+                if ((s & 3) == warp) {
+                    if (!mbar_wait_warp(full_bar(s), ph)) break;
+                    md_spread(a_base + (uint32_t)s * kPairABytes, lane);
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(spread_bar(s));
+                }
+                if (++s == S) { s = 0; ph ^= 1u; }
+            }
+        } else if (warp == kCopier) {
             // ---------------- the rest of the range ----------------
             for (int i = S; i < n_stages; ++i) {
                 if (!mbar_wait_warp(empty_bar(i % S), (uint32_t)(i / S - 1) & 1u)) break;
                 if (elect_one()) copy_stage(i, i % S);
                 __syncwarp();
             }
-        } else if (warp == 1) {
+        } else if (warp == kIssuer) {
             // ---------------- MMA issuer ----------------
             const uint32_t idesc = umma_idesc_mx<XB>(128, p.bn);
             const uint64_t bd0 = umma_desc_k_sw128(b_base);
@@ -205,6 +253,7 @@ mx_decode_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant
                 int s = 0;
                 uint32_t ph = 0;
                 for (int i = 0; i < n_stages; ++i) {
+                    if (SPREAD && !mbar_wait(spread_bar(s), ph)) break;
                     if (!mbar_wait(full_bar(s), ph)) break;
                     tc_fence_after();
                     const uint32_t sf = sf0 + (uint32_t)((ahead ? i : s) * kChunks) * 8u;
@@ -233,7 +282,7 @@ mx_decode_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant
     tc_fence_after();
     if (csize > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");     // every CTA of the cluster runs
     const int log_share = 7 - p.log_cluster, share = 1 << log_share, pitch = md_sum_pitch(p.bn);
-    if (ok) {
+    if (ok && warp < 4) {
         const uint32_t lane_addr = tmem + ((uint32_t)(32 * warp) << 16);
         const int n = r0 + tid, owner = tid >> log_share;
         const uint32_t to = csize == 1 ? 0u
@@ -257,7 +306,7 @@ mx_decode_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant
     __syncwarp();
     if (csize > 1) {
         cluster_sync_all();                                  // (after a timeout the sums are not valid)
-        for (int i = tid; i < (M + 3) / 4 << log_share; i += kMdThreads) {
+        for (int i = tid; i < (M + 3) / 4 << log_share; i += md_threads(SPREAD)) {
             const int r = i & (share - 1), m = 4 * (i >> log_share), n = r0 + ((int)rank << log_share) + r;
             float sum[4] = {0.f, 0.f, 0.f, 0.f};
             for (uint32_t q = 0; q < csize; ++q) {

@@ -98,7 +98,7 @@ int md_clusters(int l)
     if (v == 0) {
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(256u << l);
-        cfg.blockDim = dim3(kMdThreads);
+        cfg.blockDim = dim3(md_threads(false));
         cfg.dynamicSmemBytes = kMdMaxSmem;
         cudaLaunchAttribute attr[1];
         attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -149,11 +149,11 @@ bool plan_md(int64_t M, int64_t N, int64_t K, int xbits, int num_sms, int smem_o
     return true;
 }
 
-template <int XB>
-bq_status launch_md(int dev, const MdPlan& pl, const void* xq, const uint8_t* xs, const uint8_t* wq, int64_t w_k,
-                    const uint8_t* wsc, uint16_t* y, int64_t M, int64_t N, int64_t K, cudaStream_t st)
+template <int XB, bool SPREAD>
+bq_status launch_md(int dev, const MdPlan& pl, const void* xq, const uint8_t* xs, const uint8_t* wq, const uint8_t* wsc,
+                    uint16_t* y, int64_t M, int64_t N, int64_t K, cudaStream_t st)
 {
-    auto kern = mx_decode_kernel<XB>;
+    auto kern = mx_decode_kernel<XB, SPREAD>;
     static bool attr_done[kMaxDevices] = {};
     if (!attr_done[dev]) {
         if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMdMaxSmem) != cudaSuccess) {
@@ -166,8 +166,9 @@ bq_status launch_md(int dev, const MdPlan& pl, const void* xq, const uint8_t* xs
     p.bn = pl.bn;
     p.m_tiles = (int)((M + pl.bn - 1) / pl.bn);
     CUtensorMap ta, tb;
-    const bool a_ok = XB == 4 ? make_map(&ta, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, wq, N, K / 2, 128, 128, CU_TENSOR_MAP_SWIZZLE_128B)
-                              : make_map_spread4(&ta, wq, N, w_k, 128);
+    const bool a_ok = XB == 4   ? make_map(&ta, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, wq, N, K / 2, 128, 128, CU_TENSOR_MAP_SWIZZLE_128B)
+                      : SPREAD  ? make_map(&ta, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, wq, N, K / 2, 128, 64, CU_TENSOR_MAP_SWIZZLE_64B)
+                                : make_map_spread4(&ta, wq, N, K, 128);
     if (!a_ok || !make_map(&tb, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, xq, M, K * XB / 8, p.bn, 128, CU_TENSOR_MAP_SWIZZLE_128B))
         return BQ_ERR_CUDA;
     p.xs = xs;
@@ -183,7 +184,7 @@ bq_status launch_md(int dev, const MdPlan& pl, const void* xq, const uint8_t* xs
     p.range_chunks = pl.range * md_chunks(XB);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)((N + 127) / 128 * p.m_tiles) << pl.log_cluster);
-    cfg.blockDim = dim3(kMdThreads);
+    cfg.blockDim = dim3(md_threads(SPREAD));
     cfg.dynamicSmemBytes = pl.smem;
     cfg.stream = st;
     cudaLaunchAttribute attr[2];
@@ -201,9 +202,9 @@ bq_status launch_md(int dev, const MdPlan& pl, const void* xq, const uint8_t* xs
     return launch_status();
 }
 
-// Workspace: W's codes in rows of whole 128 where the copies want them (K % 128 != 0 with 8-bit
-// activations; its rows have `k` elements then), and on pairs of SMs the packed scales of W and of
-// x and the partial sums of split tiles.
+// Workspace of the product on pairs of SMs: W's codes in rows of whole 128 where the copies want them (K % 128 != 0 with
+// 8-bit activations; its rows have `k` elements then), the packed scales of W and of x, and the partial sums of
+// split tiles.
 struct MxWs {
     PairPlan pl;
     MdPlan md;
@@ -264,16 +265,15 @@ bool plan_mx_pair(int64_t N, int64_t M, int64_t K, int xbits, int num_sms, int s
 
 bool make_plan_mx(int64_t M, int64_t N, int64_t K, int x_bits, int num_sms, int smem_optin, MxWs* w)
 {
-    w->pad = x_bits == 8 && K % 128 != 0;
-    w->k = w->pad ? (K + 127) / 128 * 128 : K;
-    w->off_w = w->pad ? up256((size_t)N * (size_t)w->k / 2) + 256u : 0u;      // from the next multiple of 256 on
     // Beyond one tile of tokens the one-launch kernel takes what it does at once and in few stages.  Two tiles: 128 x
     // 2048 x 4096, 4 bits, 7.6 us for the pairs' 8.5 (two launches); 200 x 4096 x 4096, 15.2 and 11.4.  More: 500 x 200 x
     // 1024 5.7 and 7.4, of which the host needs most; 400 x 1024 x 2048, which is left to the pairs, 7.6 and 6.5.
     w->decode = plan_md(M, N, K, x_bits, num_sms, smem_optin, &w->md) &&
                 (M <= kMdTile || (w->md.rounds == 1 && w->md.cost <= (M <= 2 * kMdTile ? 19.0 : 12.0)));
-    w->bytes = w->off_w;
     if (w->decode) return true;
+    w->pad = x_bits == 8 && K % 128 != 0;
+    w->k = w->pad ? (K + 127) / 128 * 128 : K;
+    w->off_w = w->pad ? up256((size_t)N * (size_t)w->k / 2) + 256u : 0u;      // from the next multiple of 256 on
     if (!plan_mx_pair(N, M, K, x_bits, num_sms, smem_optin, &w->pl)) return false;
     const int h = w->pl.halves;
     w->chunks = w->pl.split.blocks * mx_chunks(x_bits, h);
@@ -395,21 +395,16 @@ bq_status mx_product(const void* xq, const uint8_t* xs, int x_bits, const uint8_
         return cudaMemsetAsync(y, 0, (size_t)M * (size_t)N * 2u, st) == cudaSuccess ? BQ_OK : BQ_ERR_CUDA;
     MxWs w;
     if (!plan_mx(M, N, K, x_bits, di.num_sms, di.max_smem_optin, &w)) return BQ_ERR_SHAPE;
+    if (w.decode)
+        return x_bits == 4     ? launch_md<4, false>(dev, w.md, xq, xs, wq, ws, y, M, N, K, st)
+               : K % 128 == 0  ? launch_md<8, false>(dev, w.md, xq, xs, wq, ws, y, M, N, K, st)
+                               : launch_md<8, true>(dev, w.md, xq, xs, wq, ws, y, M, N, K, st);
     void* buf = nullptr;
     if ((s = epi_workspace(dev, st, workspace, workspace_bytes, w.bytes, &buf)) != BQ_OK) return s;
     uint8_t* to = reinterpret_cast<uint8_t*>(buf);
     if (w.pad) to += (256u - (reinterpret_cast<uintptr_t>(to) & 255u)) & 255u;
     const MxPadParams pad{reinterpret_cast<const uint4*>(wq), reinterpret_cast<uint4*>(to), N, (int)(K / 32), (int)(w.k / 32)};
     if (w.pad) wq = to;
-    if (w.decode) {
-        if (w.pad) {
-            const int64_t blocks = (N * pad.out + kMxPadSpan - 1) / kMxPadSpan;
-            if (blocks > INT32_MAX) return BQ_ERR_SHAPE;
-            if ((s = launch_pdl(mx_pad_kernel, (int)blocks, 256, 0, st, pad)) != BQ_OK) return s;
-        }
-        return x_bits == 8 ? launch_md<8>(dev, w.md, xq, xs, wq, w.k, ws, y, M, N, K, st)
-                           : launch_md<4>(dev, w.md, xq, xs, wq, w.k, ws, y, M, N, K, st);
-    }
     if ((s = launch_mx_pack(w, xs, ws, pad, to, M, N, K, st)) != BQ_OK) return s;
     if (x_bits == 8)
         return w.pl.halves == 2 ? launch_mx_pair<8, 2>(di, dev, w, xq, wq, y, M, N, K, to, st)
