@@ -124,7 +124,7 @@ bool plan_md(int64_t M, int64_t N, int64_t K, int xbits, int num_sms, int smem_o
     const int64_t mt = (M + kMdTile - 1) / kMdTile, nk = (K + mx_atom_k(xbits) - 1) / mx_atom_k(xbits);
     const int bn = (int)(((M + mt - 1) / mt + 15) / 16 * 16), chunks = md_chunks(xbits);
     const int64_t rt = (N + 127) / 128 * ((M + bn - 1) / bn);                 // tiles
-    const int64_t room = smem_optin / 2 - 3072;                               // two CTAs on an SM
+    const int64_t room = smem_optin / 2 - 3 * 1024;                           // two CTAs on an SM
     double best = 1e300;
     for (int l = 0; l <= 3 && (1 << l) <= nk; ++l) {
         const int c = 1 << l;
